@@ -10,10 +10,18 @@ out_dtype says otherwise, y = scale[co] * (conv + bias[co]) when the fp32
 [Cout] tensors scale / bias are given. PyTorch provides the device memory and
 the current stream; the convolution itself runs in libim2win_conv2d.so (see
 include/im2win_conv2d.h).
+
+On the features a convolution leaves, ``head`` has layer norm over the
+channels, dropout, and the softmax cross entropy of a linear classifier, with
+their gradients (include/im2win_head.h); its functions are exported here too.
 """
 from __future__ import annotations
 
 from . import _lib
+from .head import (dropout, dropout_into, layer_norm, layer_norm_into, layer_norm_backward,  # noqa: F401
+                   layer_norm_backward_into, layer_norm_workspace_size, linear_cross_entropy,
+                   linear_cross_entropy_into, linear_cross_entropy_backward,
+                   linear_cross_entropy_backward_into, linear_cross_entropy_workspace_size)
 from ._lib import (Conv2dError, Desc, Plan, ImplicitPlan, LAYOUT_CL, LAYOUT_FRAG, LAYOUT_ROW,  # noqa: F401
                    F16, F32, BF16, NCHW, NHWC, make_desc, workspace_size, plan, implicit_plan,
                    implicit_workspace_size, profile_enable, profile_read, status_string)
@@ -21,7 +29,11 @@ from ._lib import (Conv2dError, Desc, Plan, ImplicitPlan, LAYOUT_CL, LAYOUT_FRAG
 __all__ = ["conv2d", "conv2d_into", "conv2d_implicit", "conv2d_implicit_into", "pack",
            "weight_stage", "window_gemm", "describe", "plan", "implicit_plan", "workspace_size",
            "implicit_workspace_size", "implicit_gemm",
-           "Conv2dError", "profile_enable", "profile_read"]
+           "Conv2dError", "profile_enable", "profile_read",
+           "dropout", "dropout_into", "layer_norm", "layer_norm_into", "layer_norm_backward",
+           "layer_norm_backward_into", "layer_norm_workspace_size", "linear_cross_entropy",
+           "linear_cross_entropy_into", "linear_cross_entropy_backward",
+           "linear_cross_entropy_backward_into", "linear_cross_entropy_workspace_size"]
 
 
 def _dtype_code(t) -> int:

@@ -24,6 +24,7 @@ BUILDDIR = os.path.join(PKG, "_build")
 SOURCES = [
     os.path.join(CSRC, "plan.cpp"),
     os.path.join(CSRC, "api.cpp"),
+    os.path.join(CSRC, "head_api.cpp"),
     os.path.join(CSRC, "noalloc.hip"),
     os.path.join(CSRC, "kernels", "pack.hip"),
     os.path.join(CSRC, "kernels", "weight_stage.hip"),
@@ -35,6 +36,10 @@ SOURCES = [
     os.path.join(CSRC, "kernels", "conv_implicit_narrow.hip"),
     os.path.join(CSRC, "kernels", "conv_implicit_pipe.hip"),
     os.path.join(CSRC, "kernels", "conv_implicit_ksplit.hip"),
+    os.path.join(CSRC, "kernels", "dropout.hip"),
+    os.path.join(CSRC, "kernels", "layer_norm_rows.hip"),
+    os.path.join(CSRC, "kernels", "layer_norm_nchw.hip"),
+    os.path.join(CSRC, "kernels", "linear_xent.hip"),
 ]
 
 ARCH = "gfx950"
