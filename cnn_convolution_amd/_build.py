@@ -40,6 +40,8 @@ SOURCES = [
     os.path.join(CSRC, "kernels", "layer_norm_rows.hip"),
     os.path.join(CSRC, "kernels", "layer_norm_nchw.hip"),
     os.path.join(CSRC, "kernels", "linear_xent.hip"),
+    os.path.join(CSRC, "kernels", "xent_logits.hip"),
+    os.path.join(CSRC, "kernels", "xent_products.hip"),
 ]
 
 ARCH = "gfx950"

@@ -81,14 +81,21 @@ conv2d_status_t check_xent(const linear_xent_desc_t *d, XentArgs *a)
     a->ldx = d->ldx ? d->ldx : d->D;
     a->ldw = d->ldw ? d->ldw : d->D;
     a->dtype = d->dtype;
-    // the grids hold one workgroup per 64 classes or features along x and one
-    // per 64 rows or classes along y (at most 65535)
+    // tile offsets (256 rows of a stride) stay within 32 bits
     if (d->N < 0 || d->V < 1 || d->D < 1) return CONV2D_ERR_INVALID_DESC;
     if (d->N > (int64_t(1) << 22) || d->V > (int64_t(1) << 24) || d->D > (int64_t(1) << 20))
         return CONV2D_ERR_INVALID_DESC;
     if (a->ldx < d->D || a->ldw < d->D) return CONV2D_ERR_INVALID_DESC;
-    if (a->ldx > (int64_t(1) << 22) || a->ldw > (int64_t(1) << 22)) return CONV2D_ERR_INVALID_DESC;
+    if (a->ldx > (int64_t(1) << 20) || a->ldw > (int64_t(1) << 20)) return CONV2D_ERR_INVALID_DESC;
     return CONV2D_OK;
+}
+
+// rows of whole 16-byte granules are read as such; other rows are copied first
+// and need only their element's alignment
+bool rows_aligned(const void *p, int64_t D, int64_t ld, int32_t dtype)
+{
+    const int64_t es = esize(dtype), e = 16 / es;
+    return aligned(p, D % e == 0 && ld % e == 0 ? 16 : es);
 }
 
 }  // namespace
@@ -190,8 +197,8 @@ conv2d_status_t linear_xent_fwd(const linear_xent_desc_t *d, const void *x, cons
     if (d->N == 0) return CONV2D_OK;
     if (!x || !w || !target || !loss || !lse) return CONV2D_ERR_NULL_POINTER;
     if (!ws && linear_xent_fwd_workspace_size(d)) return CONV2D_ERR_WORKSPACE;
-    if (!aligned(x, esize(d->dtype)) || !aligned(w, esize(d->dtype)) || !aligned(target, 8) || !aligned(loss, 4) ||
-        !aligned(lse, 4) || !aligned(ws, 256))
+    if (!rows_aligned(x, a.D, a.ldx, a.dtype) || !rows_aligned(w, a.D, a.ldw, a.dtype) || !aligned(target, 8) ||
+        !aligned(loss, 4) || !aligned(lse, 4) || !aligned(ws, 256))
         return CONV2D_ERR_MISALIGNED;
     a.x = x;
     a.w = w;
@@ -212,7 +219,7 @@ conv2d_status_t linear_xent_bwd(const linear_xent_desc_t *d, const float *grad, 
     if (d->N > 0 && (!grad || !x || !target || !lse || !dx)) return CONV2D_ERR_NULL_POINTER;
     if (!ws && linear_xent_bwd_workspace_size(d)) return CONV2D_ERR_WORKSPACE;
     const int64_t es = esize(d->dtype);
-    if (!aligned(x, es) || !aligned(w, es) || !aligned(dx, es) || !aligned(dw, es) || !aligned(grad, 4) ||
+    if (!aligned(x, es) || !rows_aligned(w, a.D, a.ldw, a.dtype) || !aligned(dx, es) || !aligned(dw, es) || !aligned(grad, 4) ||
         !aligned(target, 8) || !aligned(lse, 4) || !aligned(ws, 256))
         return CONV2D_ERR_MISALIGNED;
     a.x = x;

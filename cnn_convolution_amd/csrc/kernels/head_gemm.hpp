@@ -1,0 +1,321 @@
+// Tiled matrix product of the linear cross entropy, out[n][m] = sum_k A[m][k]
+// B[n][k], on the matrix cores with fp32 accumulation.
+//
+// A K stage is 128 bytes of K (64 half-precision or 32 fp32 values). Both tiles
+// go from memory straight into LDS (global_load_lds_dwordx4, 1 KB per wave
+// instruction, no registers, no LDS store), NST stages deep. An operand is
+// stored in memory either with K contiguous ("rows": W and x for the logits, G
+// for dx) or with its other index contiguous ("columns": w for dx, G and x for
+// dw); its LDS image keeps that order:
+//   rows     128 bytes per row; granule g (16 bytes) of row r in slot g ^ (r & 7)
+//   columns  one K value's columns per LDS row; granule g of K row k in slot
+//            g ^ swz(k), fetched transposed by ds_read_b64_tr_b16 (lane i of a
+//            group of 16 receives column i of the four K rows the group's
+//            addresses name), fp32 by plain 4-byte reads
+// so that the fragment reads spread over all LDS banks. Either way a lane ends
+// up with the same fragment: of row (column) lane%16, half precision the 8 K
+// values 32h + 8(lane/16) .., fp32 the 4 values 16h + 4(lane/16) .., for half h
+// of the stage.
+//
+// Pipeline, one barrier per stage: the fragments of half 0 are in registers when
+// a stage begins; half 1 is read while half 0 is multiplied; then every wave's
+// reads of the stage are done and its copies of the next stage have landed
+// (barrier), the stage after that is requested into the freed buffer, and the
+// next stage's half 0 is read while half 1 is multiplied. No product waits for
+// a read issued in its own half.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "lds_dma.hpp"
+
+namespace im2win {
+
+// BM x BN tile by WM x WN waves, NST stage buffers
+template <int BM_, int BN_, int WM_, int WN_, int NST_>
+struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
+    static constexpr int waves = WM * WN, threads = waves * 64;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    static constexpr int a_bytes = BM * 128, b_bytes = BN * 128;
+    static constexpr int lds_bytes = (a_bytes + b_bytes) * NST;
+};
+
+// where granules past the end of K are read from
+__device__ __align__(16) static const uint4 zero_granule = {0, 0, 0, 0};
+
+typedef __attribute__((address_space(3))) char *lds_ptr;
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t uint32x4_t __attribute__((ext_vector_type(4)));
+
+// 16 bytes per lane from base + off (off per lane) to LDS byte address lds +
+// 16*lane
+__device__ __forceinline__ void copy_to_lds_at(const char *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+
+// one operand's tile: TB rows or columns, of which `count` exist in memory from
+// `base` on
+template <typename T, int TB, int WAVES, bool COLS>
+struct TileLoad {
+    static constexpr int E = 16 / int(sizeof(T));                 // elements per granule
+    static constexpr int KI = 128 / int(sizeof(T));               // K per stage
+    static constexpr int blocks = TB / 8, per_wave = blocks < WAVES ? 1 : blocks / WAVES;
+    static constexpr int GR = TB / E;                             // granules per K row (columns)
+    static_assert(blocks <= WAVES ? WAVES % blocks == 0 : blocks % WAVES == 0, "blocks per wave");
+    static_assert(!COLS || (GR >= 8 && GR <= 64), "columns per K row");
+
+    const char *base;        // of this tile at K = 0
+    int64_t step;            // bytes per stage
+    uint32_t off[per_wave];  // per lane, of each block
+    int64_t kstride;         // columns: bytes per K row
+
+    // columns: slot of granule g in K row k is g ^ swz(k). 16 columns are 2
+    // (half precision) or 4 granules, kept together; the K rows that one read
+    // touches (8q + 0..3 half precision, 4q fp32, q < 4) get different banks
+    static __device__ __forceinline__ int swz(int k)
+    {
+        if constexpr (sizeof(T) == 4) return ((k >> 2) & 3) * 4 & (GR - 1);
+        else if constexpr (GR == 8) return (((k >> 1) & 1) | ((k >> 3) & 1) << 1) * 2;
+        else return ((k & 3) | ((k >> 3) & 1) << 2) * 2;
+    }
+
+    static __device__ __forceinline__ int block(int wave, int i) { return (wave + WAVES * i) % blocks; }
+
+    __device__ __forceinline__ void init(const char *p, int64_t ld_bytes, int64_t first, int64_t count, int wave,
+                                         int lane)
+    {
+        kstride = ld_bytes;
+        const int n = int(count - first < TB ? count - first : TB);   // at least 1
+        if constexpr (!COLS) {
+            base = p + first * ld_bytes;
+            step = 128;
+#pragma unroll
+            for (int i = 0; i < per_wave; ++i) {
+                const int r = min(block(wave, i) * 8 + (lane >> 3), n - 1);
+                off[i] = uint32_t(r) * uint32_t(ld_bytes) + (((lane & 7) ^ (lane >> 3)) << 4);
+            }
+        } else {
+            base = p + first * int64_t(sizeof(T));
+            step = KI * ld_bytes;
+#pragma unroll
+            for (int i = 0; i < per_wave; ++i) {
+                const int k = krow(wave, lane, i);
+                off[i] = uint32_t(k) * uint32_t(ld_bytes) + uint32_t(granule(lane, k, n)) * 16;
+            }
+        }
+    }
+    static __device__ __forceinline__ int krow(int wave, int lane, int i)
+    {
+        return block(wave, i) * (64 / GR) + lane / GR;
+    }
+    // source granule of this lane in K row k; columns past the last granule
+    // read that one (n is a multiple of E: they are never stored)
+    static __device__ __forceinline__ int granule(int lane, int k, int n)
+    {
+        return min((lane % GR) ^ swz(k), n / E - 1);
+    }
+
+    __device__ __forceinline__ void issue(int64_t stage, uint32_t lds, int wave) const
+    {
+        const char *b = base + stage * step;
+#pragma unroll
+        for (int i = 0; i < per_wave; ++i)
+            copy_to_lds_at(b, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
+    }
+    // the last stage of a K that ends inside it (left < KI values): rows read
+    // zeros past it, columns repeat the last K row (the other operand has zeros
+    // there)
+    __device__ __forceinline__ void issue_tail(int64_t stage, int left, uint32_t lds, int wave, int lane) const
+    {
+        const char *b = base + stage * step;
+#pragma unroll
+        for (int i = 0; i < per_wave; ++i) {
+            const char *src;
+            if constexpr (!COLS) {
+                const bool ok = ((lane & 7) ^ (lane >> 3)) * E < left;
+                src = ok ? b + off[i] : reinterpret_cast<const char *>(&zero_granule);
+            } else {
+                const int k = krow(wave, lane, i);
+                src = b + off[i] - int64_t(max(0, k - (left - 1))) * kstride;
+            }
+            copy_to_lds(src, __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
+        }
+    }
+};
+
+// fragment addresses of one operand: byte offsets into its tile, of half 0
+template <typename T, int TB, bool COLS>
+struct FragRead {
+    static constexpr int RB = TB * int(sizeof(T));                // columns: bytes per K row
+    uint32_t o;
+    int first;               // columns: this wave's first block of 16
+
+    // first: this wave's first row or column of the tile, a multiple of 16
+    __device__ __forceinline__ void init(int f, int lane)
+    {
+        first = f / 16;
+        if constexpr (!COLS) {
+            o = uint32_t(f + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+        } else if constexpr (sizeof(T) == 2) {
+            const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);   // K row; the second read is 4 rows on
+            o = uint32_t(k) * RB + ((lane & 3) >> 1) * 16 + (lane & 1) * 8;
+            o += swizzle(k) << 4;
+        } else {
+            const int k = (lane >> 4) * 4;                        // K rows k .. k + 3
+            o = uint32_t(k) * RB + (lane & 15) * 4;
+            o += swizzle(k) << 4;
+        }
+    }
+    static __device__ __forceinline__ uint32_t swizzle(int k) { return TileLoad<T, TB, 1, true>::swz(k); }
+
+    // block i (16 rows or columns) of half h; tile: LDS address of the stage's tile
+    __device__ __forceinline__ uint4 read(lds_ptr tile, int i, int h) const
+    {
+        if constexpr (!COLS) {
+            // half 1 is granules 4 .. 7 before the swizzle: slot bit 2 flips
+            typedef __attribute__((address_space(3))) const uint32x4_t *vp;
+            return __builtin_bit_cast(uint4, *(vp)(tile + ((o ^ (h << 6)) + i * 2048)));
+        } else if constexpr (sizeof(T) == 2) {
+            const uint32_t a = (o ^ uint32_t((first + i) * 32)) + h * 32 * RB;
+            typedef __attribute__((address_space(3))) short4_t *tp;
+            const short4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(tile + a));
+            const short4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tp)(tile + a + 4 * RB));
+            const uint2 x = __builtin_bit_cast(uint2, u), y = __builtin_bit_cast(uint2, v);
+            return uint4{x.x, x.y, y.x, y.y};
+        } else {
+            typedef __attribute__((address_space(3))) const uint32_t *wp;
+            const uint32_t a = (o ^ uint32_t((first + i) * 64)) + h * 16 * RB;
+            return uint4{*(wp)(tile + a), *(wp)(tile + a + RB), *(wp)(tile + a + 2 * RB), *(wp)(tile + a + 3 * RB)};
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ floatx4_t mfma_half(const uint4 &a, const uint4 &b, floatx4_t c)
+{
+    if constexpr (sizeof(T) == 4) {
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+        return c;
+    } else {
+        return mfma16x16x32<std::is_same<T, __bf16>::value>(a, b, c);
+    }
+}
+
+struct GemmOperand {
+    const void *p;
+    int64_t ld;              // bytes between rows (rows) or K rows (columns), a multiple of 16
+    int64_t count;           // rows or columns that exist; columns: a multiple of 16 bytes' worth
+    int64_t k_end;           // K values that exist; columns repeat the last one past it
+};
+
+// acc[i][j]: 16 x 16 blocks of this wave's part of the tile; lane l holds m =
+// 16i + 4(l/16) + v and n = 16j + l%16 of it. K stages [s0, s1). extra(stage,
+// half, A fragments, acc) is called after each half's products.
+template <typename T, typename C, bool ACOLS, bool BCOLS, typename Extra>
+__device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOperand &B, int64_t m0, int64_t n0,
+                                             int s0, int s1, char *smem,
+                                             floatx4_t (&acc)[C::FM][C::FN], Extra extra)
+{
+    constexpr int KI = 128 / int(sizeof(T));
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % C::WM, wn = wave / C::WM;
+    TileLoad<T, C::BM, C::waves, ACOLS> la;
+    TileLoad<T, C::BN, C::waves, BCOLS> lb;
+    la.init(static_cast<const char *>(A.p), A.ld, m0, A.count, wave, lane);
+    lb.init(static_cast<const char *>(B.p), B.ld, n0, B.count, wave, lane);
+    FragRead<T, C::BM, ACOLS> ra;
+    FragRead<T, C::BN, BCOLS> rb;
+    ra.init(wm * (C::BM / C::WM), lane);
+    rb.init(wn * (C::BN / C::WN), lane);
+    const lds_ptr sm = (lds_ptr)smem;
+    const uint32_t sbase = uint32_t(reinterpret_cast<uintptr_t>(sm));
+    constexpr int D = decltype(la)::per_wave + decltype(lb)::per_wave;   // copies per wave per stage
+
+    // A stages first, then B stages
+    auto issue = [&](int s, int buf) {
+        const uint32_t a = sbase + buf * C::a_bytes, b = sbase + C::NST * C::a_bytes + buf * C::b_bytes;
+        const int64_t left_a = A.k_end - int64_t(s) * KI, left_b = B.k_end - int64_t(s) * KI;
+        if (left_a >= KI)
+            la.issue(s, a, wave);
+        else
+            la.issue_tail(s, int(left_a), a, wave, lane);
+        if (left_b >= KI)
+            lb.issue(s, b, wave);
+        else
+            lb.issue_tail(s, int(left_b), b, wave, lane);
+    };
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    uint4 a0[C::FM], b0[C::FN], a1[C::FM], b1[C::FN];
+    auto read = [&](int buf, int h, uint4 (&a)[C::FM], uint4 (&b)[C::FN]) {
+        const lds_ptr at = sm + buf * C::a_bytes, bt = sm + C::NST * C::a_bytes + buf * C::b_bytes;
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) b[j] = rb.read(bt, j, h);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) a[i] = ra.read(at, i, h);
+    };
+    auto multiply = [&](const uint4 (&a)[C::FM], const uint4 (&b)[C::FN]) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) acc[i][j] = mfma_half<T>(a[i], b[j], acc[i][j]);
+    };
+
+    // NST - 1 stages requested ahead; past the last stage the last one is
+    // requested again (into a buffer nothing reads any more), so that the
+    // number of copies in flight is always the same
+    const int last = s1 - 1;
+#pragma unroll
+    for (int s = 0; s < C::NST; ++s) issue(min(s0 + s, last), s);
+    wait_vm<D * (C::NST - 1)>();
+    stage_barrier();
+    read(0, 0, a0, b0);
+    int buf = 0;
+    for (int s = s0; s < s1; ++s) {
+        const int next = buf + 1 == C::NST ? 0 : buf + 1;
+        read(buf, 1, a1, b1);
+        multiply(a0, b0);
+        extra(s, 0, a0, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vm<D * (C::NST - 2)>();
+        stage_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(min(s + C::NST, last), buf);
+        read(next, 0, a0, b0);
+        multiply(a1, b1);
+        extra(s, 1, a1, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        buf = next;
+    }
+    wait_vm<0>();
+    stage_barrier();                       // the tiles' LDS is free for the epilogue
+}
+
+// workgroup -> (m, n) tile: each XCD gets a contiguous range of tiles, walked
+// in strips of 8 n tiles, so the tiles it runs at a time share their panels in
+// its L2
+__device__ __forceinline__ void strip_tile(int b, int tiles_m, int tiles_n, int &tm, int &tn)
+{
+    const int G = tiles_m * tiles_n, per = G >> 3, rem = G & 7, x = b & 7;
+    const int t = x * per + min(x, rem) + (b >> 3);
+    const int strip = t / (tiles_m * 8), r = t - strip * tiles_m * 8;
+    const int w = min(8, tiles_n - strip * 8);
+    tm = r / w;
+    tn = strip * 8 + r - tm * w;
+}
+
+}  // namespace im2win

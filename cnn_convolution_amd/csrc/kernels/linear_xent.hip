@@ -1,129 +1,23 @@
-// Softmax cross entropy of a linear classifier, logits x w^T formed tile by
-// tile and never stored: forward (loss, lse) and backward (dx, dw).
+// Softmax cross entropy of a linear classifier (im2win_head.h): the plan, the
+// small kernels, and the sequence of launches.
 //
-// Forward: each 64 classes x 64 rows tile of logits is reduced in its
-// workgroup to one (maximum, sum of exponentials around it) per row; a second
-// kernel joins a row's partials in a fixed order. Backward: pieces of the
-// classes; a piece's G = S * grad * (exp(l - lse) - [target]) goes to the
-// workspace in the type of x (S a power of two that places the largest |grad|
-// near the top of fp16's range, 1 for the other types), then dx += G w and
-// dw = G^T x.
+// Forward: one launch of logit tiles (xent_logits.hip) leaves each row's
+// (maximum, sum of exponentials) per tile of classes, a second joins them.
+// Backward, in pieces of the classes: a piece's G goes to the workspace
+// (xent_logits.hip), then dx += G w and dw = G^T x (xent_products.hip).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
-#include "../head_launch.hpp"
-#include "lds_dma.hpp"
+#include "../xent.hpp"
+#include "head_vec.hpp"
 
 namespace im2win {
 namespace {
 
-constexpr int TM = 64, TN = 64, BK = 32, kThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ floatx4_t mfma_k32(const T *a, const T *b, floatx4_t c)
-{
-    // a, b: 8 consecutive K values of this lane's row (lane group g: K 8g ..)
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-        return c;
-    } else {
-        return mfma16x16x32<std::is_same<T, __bf16>::value>(*reinterpret_cast<const uint4 *>(a),
-                                                            *reinterpret_cast<const uint4 *>(b), c);
-    }
-}
-
-struct Operand {
-    const void *p;
-    int64_t row, k;          // strides in elements
-    int64_t rows;
-};
-
-// acc[i][j]: 16x16 blocks of the workgroup's 64 x 64 tile; wave w holds rows
-// m 32*(w%2) + 16i + 4*(lane/16) + v, columns 32*(w/2) + 16j + lane%16
-template <typename T>
-__device__ __forceinline__ void tile_product(const Operand &A, const Operand &B, int64_t K, int64_t m0,
-                                             int64_t n0, floatx4_t (&acc)[2][2])
-{
-    __shared__ __align__(16) T sa[TM][BK + 16 / sizeof(T)], sb[TN][BK + 16 / sizeof(T)];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int ar = (wave & 1) * 32 + (lane & 15), br = (wave >> 1) * 32 + (lane & 15), kk = (lane >> 4) * 8;
-    const T *ap = static_cast<const T *>(A.p), *bp = static_cast<const T *>(B.p);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    for (int64_t k0 = 0; k0 < K; k0 += BK) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < TM * BK; i += kThreads) {
-            // consecutive threads along the operand's contiguous index
-            const int r = A.k == 1 ? i / BK : i % TM, k = A.k == 1 ? i % BK : i / TM;
-            const bool ok = m0 + r < A.rows && k0 + k < K;
-            sa[r][k] = ok ? ap[(m0 + r) * A.row + (k0 + k) * A.k] : T(0.f);
-        }
-        for (int i = threadIdx.x; i < TN * BK; i += kThreads) {
-            const int r = B.k == 1 ? i / BK : i % TN, k = B.k == 1 ? i % BK : i / TN;
-            const bool ok = n0 + r < B.rows && k0 + k < K;
-            sb[r][k] = ok ? bp[(n0 + r) * B.row + (k0 + k) * B.k] : T(0.f);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma_k32<T>(&sa[ar + 16 * i][kk], &sb[br + 16 * j][kk], acc[i][j]);
-    }
-}
-
 __device__ __forceinline__ bool valid_target(int64_t t, int64_t V) { return t >= 0 && t < V; }
-
-// partial (maximum, sum) of each row over this tile's classes; the target's
-// logit goes to a.loss
-template <typename T>
-__global__ __launch_bounds__(kThreads) void xent_loss_kernel(const XentArgs a, float2 *partial)
-{
-    __shared__ float2 red[2][TN];
-    const int64_t m0 = int64_t(blockIdx.x) * TM, n0 = int64_t(blockIdx.y) * TN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    floatx4_t acc[2][2];
-    tile_product<T>(Operand{a.w, a.ldw, 1, a.V}, Operand{a.x, a.ldx, 1, a.N}, a.D, m0, n0, acc);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int col = (wave >> 1) * 32 + 16 * j + (lane & 15);
-        const int64_t row = n0 + col;
-        const int64_t t = row < a.N ? a.target[row] : -1;
-        float m = -__builtin_inff(), s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t cls = m0 + (wave & 1) * 32 + 16 * i + (lane >> 4) * 4 + v;
-                if (cls < a.V) {
-                    m = fmaxf(m, acc[i][j][v]);
-                    if (cls == t) a.loss[row] = acc[i][j][v];
-                }
-            }
-        m = fmaxf(m, __shfl_xor(m, 16, 64));
-        m = fmaxf(m, __shfl_xor(m, 32, 64));
-        const float mm = m == -__builtin_inff() ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                if (m0 + (wave & 1) * 32 + 16 * i + (lane >> 4) * 4 + v < a.V) s += __expf(acc[i][j][v] - mm);
-        s += __shfl_xor(s, 16, 64);
-        s += __shfl_xor(s, 32, 64);
-        if (lane < 16) red[wave & 1][col] = float2{m, s};
-    }
-    __syncthreads();
-    if (threadIdx.x < TN && n0 + threadIdx.x < a.N) {
-        const float2 p = red[0][threadIdx.x], q = red[1][threadIdx.x];
-        const float m = fmaxf(p.x, q.x), mm = m == -__builtin_inff() ? 0.f : m;
-        partial[blockIdx.x * a.N + n0 + threadIdx.x] =
-            float2{m, p.y * __expf(p.x - mm) + q.y * __expf(q.x - mm)};
-    }
-}
 
 // one wave per row: lse over the tiles' partials, then the loss
 __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const float2 *partial, int tiles)
@@ -132,16 +26,21 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const 
     const int lane = threadIdx.x & 63;
     if (row >= a.N) return;
     float m = -__builtin_inff(), s = 0.f;
-    for (int t = lane; t < tiles; t += 64) m = fmaxf(m, partial[t * a.N + row].x);
-    for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
-    const float mm = m == -__builtin_inff() ? 0.f : m;
     for (int t = lane; t < tiles; t += 64) {
         const float2 p = partial[t * a.N + row];
-        s += p.y * __expf(p.x - mm);
+        const float n = fmaxf(m, p.x);
+        if (n == -__builtin_inff()) continue;
+        s = s * __expf(m - n) + p.y * __expf(p.x - n);
+        m = n;
     }
-    for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k, 64);
+    for (int k = 1; k < 64; k <<= 1) {
+        const float m2 = __shfl_xor(m, k, 64), s2 = __shfl_xor(s, k, 64), n = fmaxf(m, m2);
+        if (n == -__builtin_inff()) continue;
+        s = s * __expf(m - n) + s2 * __expf(m2 - n);
+        m = n;
+    }
     if (lane == 0) {
-        const float lse = mm + logf(s);
+        const float lse = m + logf(s);
         const bool ok = valid_target(a.target[row], a.V);
         a.loss[row] = ok ? lse - a.loss[row] : 0.f;
         a.lse[row] = ok ? lse : 0.f;
@@ -168,96 +67,27 @@ __global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, int
     }
 }
 
-// x with the masked rows cleared
+// rows copied to whole granules (the padding cleared), one wave per row; with
+// targets also t32 (rows up to rows_pad), and masked rows copied as zeros
 template <typename T>
-__global__ __launch_bounds__(256) void xent_rows_kernel(const XentArgs a, T *xs)
+__global__ __launch_bounds__(256) void xent_rows_kernel(const T *src, int64_t ld, int64_t rows, int64_t D, int64_t Dp,
+                                                        T *dst, const int64_t *target, int64_t V, int64_t rows_pad,
+                                                        int *t32)
 {
-    const int64_t row = blockIdx.x;
-    const bool ok = valid_target(a.target[row], a.V);
-    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-    for (int64_t d = threadIdx.x; d < a.D; d += 256) xs[row * a.D + d] = ok ? x[d] : T(0.f);
-}
-
-// G of classes v0 .. v0 + P - 1 into g [N][P]
-template <typename T>
-__global__ __launch_bounds__(kThreads) void xent_g_kernel(const XentArgs a, int64_t v0, int64_t P, T *g,
-                                                          const float *scale)
-{
-    const int64_t m0 = int64_t(blockIdx.x) * TM, n0 = int64_t(blockIdx.y) * TN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    floatx4_t acc[2][2];
-    tile_product<T>(Operand{static_cast<const T *>(a.w) + v0 * a.ldw, a.ldw, 1, P}, Operand{a.x, a.ldx, 1, a.N},
-                    a.D, m0, n0, acc);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t row = n0 + (wave >> 1) * 32 + 16 * j + (lane & 15);
-        if (row >= a.N) continue;
-        const int64_t t = a.target[row];
-        const bool ok = valid_target(t, a.V);
-        const float lse = a.lse[row], gs = a.grad[row] * scale[0];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t m = m0 + (wave & 1) * 32 + 16 * i + (lane >> 4) * 4 + v;
-                if (m >= P) continue;
-                const float q = expf(acc[i][j][v] - lse) - (v0 + m == t ? 1.f : 0.f);
-                g[row * P + m] = T(ok ? gs * q : 0.f);
-            }
+    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    constexpr int E = 16 / int(sizeof(T));
+    bool ok = row < rows;
+    if (target) {
+        const int64_t t = ok ? target[row] : -1;
+        ok = valid_target(t, V);
+        if (lane == 0 && row < rows_pad) t32[row] = ok ? int(t) : -1;
     }
-}
-
-// dx += G w for one piece into fp32 sums [N][D]
-template <typename T>
-__global__ __launch_bounds__(kThreads) void xent_dx_kernel(const XentArgs a, int64_t v0, int64_t P, const T *g,
-                                                           float *sum)
-{
-    const int64_t m0 = int64_t(blockIdx.x) * TM, n0 = int64_t(blockIdx.y) * TN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    floatx4_t acc[2][2];
-    tile_product<T>(Operand{static_cast<const T *>(a.w) + v0 * a.ldw, 1, a.ldw, a.D}, Operand{g, P, 1, a.N}, P, m0,
-                    n0, acc);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t row = n0 + (wave >> 1) * 32 + 16 * j + (lane & 15);
-        if (row >= a.N) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t m = m0 + (wave & 1) * 32 + 16 * i + (lane >> 4) * 4 + v;
-                if (m < a.D) sum[row * a.D + m] = acc[i][j][v] + (v0 ? sum[row * a.D + m] : 0.f);
-            }
-    }
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void xent_dx_out_kernel(const float *sum, int64_t n, const float *scale, T *dx)
-{
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) dx[i] = T(sum[i] * scale[1]);
-}
-
-// dw of one piece = G^T x
-template <typename T>
-__global__ __launch_bounds__(kThreads) void xent_dw_kernel(const XentArgs a, int64_t v0, int64_t P, const T *g,
-                                                           const T *xs, const float *scale)
-{
-    const int64_t m0 = int64_t(blockIdx.x) * TM, n0 = int64_t(blockIdx.y) * TN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    floatx4_t acc[2][2];
-    tile_product<T>(Operand{xs, 1, a.D, a.D}, Operand{g, 1, P, P}, a.N, m0, n0, acc);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t cls = n0 + (wave >> 1) * 32 + 16 * j + (lane & 15);
-        if (cls >= P) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t m = m0 + (wave & 1) * 32 + 16 * i + (lane >> 4) * 4 + v;
-                if (m < a.D) static_cast<T *>(a.dw)[(v0 + cls) * a.D + m] = T(acc[i][j][v] * scale[1]);
-            }
+    if (row >= rows) return;
+    for (int64_t d = lane * E; d < Dp; d += 64 * E) {
+        float f[E];
+        load_some<E>(src + row * ld + d, ok ? int(min(int64_t(E), D - d)) : 0, f);
+        store_vec<E>(dst + row * Dp + d, f);
     }
 }
 
@@ -269,14 +99,8 @@ __global__ __launch_bounds__(256) void xent_zero_kernel(T *p, int64_t n)
 }
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
 int64_t elem(int dtype) { return dtype == 0 ? 4 : 2; }
-unsigned tiles(int64_t n, int t) { return unsigned((n + t - 1) / t); }
-
-constexpr int64_t kPieceBytes = int64_t(128) << 20;   // of G
-int64_t piece_classes(int64_t N, int64_t V, int dtype)
-{
-    return std::min(round_up(V, TM), std::max<int64_t>(TM, kPieceBytes / (N * elem(dtype)) / TM * TM));
-}
 
 template <typename F>
 hipError_t with_type(int dtype, F f)
@@ -286,69 +110,246 @@ hipError_t with_type(int dtype, F f)
     return f(__bf16{});
 }
 
+struct Tile {
+    int64_t m, n;
+    int per_cu;              // workgroups a CU holds
+    double rate;             // of the CU's matrix rate when it holds that many
+};
+constexpr Tile kTiles[4] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.75}, {64, 64, 3, 0.4}, {128, 16, 2, 0.1}};
+constexpr int kCus = 256;
+// microseconds of one CU for a multiply-add count, and the least a stage takes
+// (its copies' latency)
+constexpr double kHalfRate = 4.5e6 / 2, kF32Rate = 0.55e6 / 2, kStageLatency = 0.6;
+
+// microseconds of a product of M x N outputs over `stages` K stages
+double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split, int dtype)
+{
+    const int64_t wgs = ceil_div(M, t.m) * ceil_div(N, t.n) * split;
+    const int64_t ki = 128 / elem(dtype);
+    const double rounds = double(ceil_div(wgs, int64_t(kCus) * t.per_cu));
+    // a launch of few workgroups leaves a CU fewer to run at a time
+    const double held = double(std::min<int64_t>(t.per_cu, ceil_div(wgs, kCus)));
+    const double rate = dtype == 0 ? kF32Rate : kHalfRate * t.rate;
+    const double stage = std::max(held * double(t.m * t.n * ki) / rate, kStageLatency);
+    return rounds * stage * double(ceil_div(stages, split));
+}
+
+constexpr int64_t kSlabBytes = int64_t(256) << 20;
+
+// tile and split of a product whose K may be split
+void pick_product(int64_t M, int64_t N, int64_t stages, int dtype, int *tile, int *split)
+{
+    double best = 1e30;
+    for (int t = 0; t < 3; ++t)
+        for (int sp = 1; sp <= 64; sp *= 2) {
+            if (sp > 1 && (stages / sp < 4 || int64_t(sp) * M * N * 4 > kSlabBytes)) break;
+            // the slabs are written and read once, at about 3 TB/s
+            const double us = product_us(kTiles[t], M, N, stages, sp, dtype) +
+                              (sp > 1 ? 4.0 + double(sp) * double(M) * double(N) * 8 / 3e6 : 0.0);
+            if (us < best * 0.98) {
+                best = us;
+                *tile = t;
+                *split = sp;
+            }
+        }
+}
+
+int pick_logits(int64_t M, int64_t N, int64_t stages, int dtype, bool narrow)
+{
+    if (narrow && N <= 16) return kTileNarrow;
+    double best = 1e30;
+    int tile = 0;
+    for (int t = 0; t < 3; ++t) {
+        const double us = product_us(kTiles[t], M, N, stages, 1, dtype);
+        if (us < best * 0.98) {
+            best = us;
+            tile = t;
+        }
+    }
+    return tile;
+}
+
+constexpr int64_t kPieceBytes = int64_t(256) << 20;   // of G
+
+void plan_common(XentPlan &p, int64_t D, int64_t ldx, int64_t ldw, int dtype)
+{
+    const int64_t e = 16 / elem(dtype);
+    p.Dp = round_up(D, e);
+    p.copy_x = D % e != 0 || ldx % e != 0;
+    p.copy_w = D % e != 0 || ldw % e != 0;
+}
+
+int64_t take(XentPlan &p, int64_t bytes)
+{
+    const int64_t at = p.bytes;
+    p.bytes += round_up(bytes, 256);
+    return at;
+}
+
 }  // namespace
+
+XentPlan plan_xent_fwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype)
+{
+    XentPlan p{};
+    plan_common(p, D, ldx, ldw, dtype);
+    if (N == 0) return p;
+    const int64_t es = elem(dtype);
+    p.logits_tile = pick_logits(V, N, ceil_div(p.Dp * es, 128), dtype, true);
+    p.tiles_v = ceil_div(V, kTiles[p.logits_tile].m);
+    if (p.copy_x) p.off_x = take(p, N * p.Dp * es);
+    if (p.copy_w) p.off_w = take(p, V * p.Dp * es);
+    p.off_partial = take(p, p.tiles_v * N * 8);
+    return p;
+}
+
+XentPlan plan_xent_bwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype)
+{
+    XentPlan p{};
+    plan_common(p, D, ldx, ldw, dtype);
+    p.copy_x = true;                      // the masked rows are cleared in it
+    if (N == 0) return p;
+    const int64_t es = elem(dtype), ki = 128 / es;
+    p.rows_pad = round_up(N, 256);
+    const int64_t most = std::max<int64_t>(1, kPieceBytes / (p.rows_pad * es) / 256) * 256;
+    p.piece = std::min(round_up(V, 256), most);
+    const int64_t P = std::min(V, p.piece);
+    p.logits_tile = pick_logits(P, N, ceil_div(p.Dp * es, 128), dtype, false);
+    pick_product(D, N, ceil_div(P, ki), dtype, &p.dx_tile, &p.dx_split);
+    pick_product(D, P, ceil_div(N, ki), dtype, &p.dw_tile, &p.dw_split);
+    p.dx_direct = p.dx_split == 1 && P == V;
+    p.off_scale = take(p, 8);
+    p.off_t32 = take(p, p.rows_pad * 4);
+    p.off_low = take(p, p.rows_pad * es);
+    p.off_x = take(p, N * p.Dp * es);
+    if (p.copy_w) p.off_w = take(p, V * p.Dp * es);
+    p.off_g = take(p, p.rows_pad * p.piece * es);
+    if (!p.dx_direct) p.off_dx = take(p, p.dx_split * N * D * 4);
+    if (p.dw_split > 1) p.off_dw = take(p, p.dw_split * P * D * 4);
+    return p;
+}
 
 int64_t xent_fwd_ws_bytes(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype)
 {
-    return round_up(int64_t(tiles(V, TM)) * N * 8, 256);
+    return plan_xent_fwd(N, V, D, ldx, ldw, dtype).bytes;
 }
 
 int64_t xent_bwd_ws_bytes(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype)
 {
-    if (N == 0) return 0;
-    return 256 + round_up(N * D * elem(dtype), 256) + round_up(N * D * 4, 256) +
-           round_up(N * piece_classes(N, V, dtype) * elem(dtype), 256);
+    return plan_xent_bwd(N, V, D, ldx, ldw, dtype).bytes;
 }
 
 hipError_t launch_xent_fwd(const XentArgs &a, hipStream_t s)
 {
     if (a.N == 0) return hipSuccess;
-    float2 *partial = static_cast<float2 *>(a.ws);
-    const dim3 grid(tiles(a.V, TM), tiles(a.N, TN));
-    return with_type(a.dtype, [&](auto t) {
+    const XentPlan p = plan_xent_fwd(a.N, a.V, a.D, a.ldx, a.ldw, a.dtype);
+    char *ws = static_cast<char *>(a.ws);
+    const int64_t es = elem(a.dtype);
+    LossArgs l{};
+    l.r = XentRows{a.x, a.w, a.ldx * es, a.ldw * es};
+    const hipError_t e = with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
-        hipLaunchKernelGGL((xent_loss_kernel<T>), grid, dim3(kThreads), 0, s, a, partial);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(xent_join_kernel, dim3(tiles(a.N, 4)), dim3(256), 0, s, a, partial, int(grid.x));
+        if (p.copy_x) {
+            l.r.x = ws + p.off_x;
+            l.r.ldx = p.Dp * es;
+            hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(ceil_div(a.N, 4))), dim3(256), 0, s,
+                               static_cast<const T *>(a.x), a.ldx, a.N, a.D, p.Dp,
+                               reinterpret_cast<T *>(ws + p.off_x), nullptr, a.V, 0, nullptr);
+        }
+        if (p.copy_w) {
+            l.r.w = ws + p.off_w;
+            l.r.ldw = p.Dp * es;
+            hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(ceil_div(a.V, 4))), dim3(256), 0, s,
+                               static_cast<const T *>(a.w), a.ldw, a.V, a.D, p.Dp,
+                               reinterpret_cast<T *>(ws + p.off_w), nullptr, a.V, 0, nullptr);
+        }
         return hipGetLastError();
     });
+    if (e != hipSuccess) return e;
+    l.N = a.N;
+    l.V = a.V;
+    l.Dp = p.Dp;
+    l.target = a.target;
+    l.loss = a.loss;
+    l.partial = reinterpret_cast<float2 *>(ws + p.off_partial);
+    const hipError_t e2 = launch_xent_loss(l, a.dtype, p.logits_tile, s);
+    if (e2 != hipSuccess) return e2;
+    hipLaunchKernelGGL(xent_join_kernel, dim3(unsigned(ceil_div(a.N, 4))), dim3(256), 0, s, a, l.partial,
+                       int(p.tiles_v));
+    return hipGetLastError();
 }
 
 hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
 {
-    return with_type(a.dtype, [&](auto tt) {
-        using T = decltype(tt);
-        if (a.N == 0) {
+    const XentPlan p = plan_xent_bwd(a.N, a.V, a.D, a.ldx, a.ldw, a.dtype);
+    char *ws = static_cast<char *>(a.ws);
+    const int64_t es = elem(a.dtype), ki = 128 / es;
+    if (a.N == 0)
+        return with_type(a.dtype, [&](auto t) {
+            using T = decltype(t);
             const int64_t n = a.V * a.D;
-            hipLaunchKernelGGL((xent_zero_kernel<T>), dim3(tiles(n, 256)), dim3(256), 0, s, static_cast<T *>(a.dw),
-                               n);
+            hipLaunchKernelGGL((xent_zero_kernel<T>), dim3(unsigned(ceil_div(n, 256))), dim3(256), 0, s,
+                               static_cast<T *>(a.dw), n);
             return hipGetLastError();
+        });
+    float *scale = a.dtype == 1 ? reinterpret_cast<float *>(ws + p.off_scale) : nullptr;
+    int *t32 = reinterpret_cast<int *>(ws + p.off_t32);
+    XentRows r{ws + p.off_x, a.w, p.Dp * es, a.ldw * es};
+    hipError_t e = with_type(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        if (scale) hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad, a.N, scale);
+        hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(p.rows_pad / 4)), dim3(256), 0, s,
+                           static_cast<const T *>(a.x), a.ldx, a.N, a.D, p.Dp, reinterpret_cast<T *>(ws + p.off_x),
+                           a.target, a.V, p.rows_pad, t32);
+        if (p.copy_w) {
+            r.w = ws + p.off_w;
+            r.ldw = p.Dp * es;
+            hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(ceil_div(a.V, 4))), dim3(256), 0, s,
+                               static_cast<const T *>(a.w), a.ldw, a.V, a.D, p.Dp,
+                               reinterpret_cast<T *>(ws + p.off_w), nullptr, a.V, 0, nullptr);
         }
-        char *p = static_cast<char *>(a.ws);
-        float *scale = reinterpret_cast<float *>(p);
-        p += 256;
-        T *xs = reinterpret_cast<T *>(p);
-        p += round_up(a.N * a.D * int64_t(sizeof(T)), 256);
-        float *sum = reinterpret_cast<float *>(p);
-        p += round_up(a.N * a.D * 4, 256);
-        T *g = reinterpret_cast<T *>(p);
-        hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad, a.N, scale);
-        hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, s, a, xs);
-        const int64_t step = piece_classes(a.N, a.V, a.dtype);
-        for (int64_t v0 = 0; v0 < a.V; v0 += step) {
-            const int64_t P = std::min(step, a.V - v0);
-            hipLaunchKernelGGL((xent_g_kernel<T>), dim3(tiles(P, TM), tiles(a.N, TN)), dim3(kThreads), 0, s, a, v0,
-                               P, g, scale);
-            hipLaunchKernelGGL((xent_dx_kernel<T>), dim3(tiles(a.D, TM), tiles(a.N, TN)), dim3(kThreads), 0, s, a,
-                               v0, P, g, sum);
-            hipLaunchKernelGGL((xent_dw_kernel<T>), dim3(tiles(a.D, TM), tiles(P, TN)), dim3(kThreads), 0, s, a, v0,
-                               P, g, xs, scale);
-        }
-        hipLaunchKernelGGL((xent_dx_out_kernel<T>), dim3(tiles(a.N * a.D, 256)), dim3(256), 0, s, sum, a.N * a.D,
-                           scale, static_cast<T *>(a.dx));
         return hipGetLastError();
     });
+    if (e != hipSuccess) return e;
+
+    ProductArgs dx{}, dw{};
+    dx.t32 = dw.t32 = t32;
+    dx.low = dw.low = ws + p.off_low;
+    dx.scale = dw.scale = scale;
+    dx.b = dw.b = ws + p.off_g;
+    dx.ldb = dw.ldb = p.piece * es;
+    dx.M = dw.M = a.D;
+    dx.lda = r.ldw;
+    dx.w = r.w;
+    dx.ldw = r.ldw;
+    dx.n = a.N;
+    dx.split = p.dx_split;
+    dx.slab = p.dx_direct ? nullptr : reinterpret_cast<float *>(ws + p.off_dx);
+    dx.out = a.dx;
+    dw.a = r.x;
+    dw.lda = r.ldx;
+    dw.K = dw.k_a = a.N;
+    dw.k_b = p.rows_pad;
+    dw.split = p.dw_split;
+    dw.slab = p.dw_split > 1 ? reinterpret_cast<float *>(ws + p.off_dw) : nullptr;
+    for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
+        const int64_t P = std::min(p.piece, a.V - v0);
+        GradArgs g{r, a.N, v0, P, p.Dp, t32, a.grad, a.lse, scale, ws + p.off_g, p.piece, ws + p.off_low};
+        if ((e = launch_xent_g(g, a.dtype, p.logits_tile, s)) != hipSuccess) return e;
+        dx.a = static_cast<const char *>(r.w) + v0 * r.ldw;
+        dx.K = dx.k_a = P;
+        dx.k_b = round_up(P, ki);
+        dx.add = v0 > 0;
+        // a last piece of few stages: no part without one
+        dx.split = int(std::min<int64_t>(p.dx_split, ceil_div(P, ki)));
+        if ((e = launch_xent_dx(dx, a.dtype, p.dx_tile, s)) != hipSuccess) return e;
+        dw.n = P;
+        dw.v0 = v0;
+        dw.out = static_cast<char *>(a.dw) + v0 * a.D * es;
+        if ((e = launch_xent_dw(dw, a.dtype, p.dw_tile, s)) != hipSuccess) return e;
+        if (dw.slab && (e = launch_xent_dw_join(dw, a.dtype, s)) != hipSuccess) return e;
+    }
+    dx.split = p.dx_split;
+    return dx.slab ? launch_xent_dx_join(dx, a.dtype, s) : hipSuccess;
 }
 
 }  // namespace im2win

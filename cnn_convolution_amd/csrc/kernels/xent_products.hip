@@ -1,0 +1,213 @@
+// The gradient products of the linear cross entropy, with the features along m
+// (the contiguous index of dx and dw):
+//   dx[n][d] = sum_v w[v][d] G[n][v]     G in rows, w in columns
+//   dw[v][d] = sum_n x[n][d] G[n][v]     both in columns
+// K may be split over workgroups into fp32 slabs that another kernel adds in
+// order. In half precision what rounding took from G at each row's target goes
+// back in: dx in the epilogue (+ low[n] w[target[n]]), dw as further products
+// of the stages in which a row's target is one of the wave's classes (at most
+// one more per block of 16 classes, and a block is skipped unless a
+// target falls into it).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../xent.hpp"
+#include "head_gemm.hpp"
+#include "head_vec.hpp"
+
+namespace im2win {
+namespace {
+
+template <typename T, typename C, bool DW>
+__global__ __launch_bounds__(C::threads) void xent_product_kernel(const ProductArgs a, int tiles_m, int tiles_n)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    constexpr int KI = 128 / int(sizeof(T)), KH = KI / 2;
+    constexpr bool LOW = DW && sizeof(T) == 2;
+    const int tiles = tiles_m * tiles_n;
+    const int part = blockIdx.x / tiles, b = blockIdx.x - part * tiles;
+    int tm, tn;
+    strip_tile(b, tiles_m, tiles_n, tm, tn);
+    const int64_t m0 = int64_t(tm) * C::BM, n0 = int64_t(tn) * C::BN;
+    const int nk = int((a.K + KI - 1) / KI);
+    const int s0 = int(int64_t(nk) * part / a.split), s1 = int(int64_t(nk) * (part + 1) / a.split);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    const int nw = wn * (C::BN / C::WN);
+    floatx4_t acc[C::FM][C::FN];
+
+    // the targets of a stage's rows, one per lane, loaded a stage ahead
+    int tnext = LOW ? a.t32[int64_t(s0) * KI + lane] : 0, tcur = 0;
+    const int cbase = int(a.v0 + n0) + nw;
+    auto low = [&](int s, int h, const uint4 (&af)[C::FM], floatx4_t (&c)[C::FM][C::FN]) {
+        if constexpr (LOW) {
+            if (h == 0) {
+                tcur = tnext - cbase;
+                tnext = a.t32[int64_t(min(s + 1, s1 - 1)) * KI + lane];
+            }
+            const bool in = uint32_t(tcur) < uint32_t(C::FN * 16) && (lane / KH) == h;
+            if (__ballot(in)) {
+                float lv[8];
+                load_vec<8>(static_cast<const T *>(a.low) + int64_t(s) * KI + h * KH + (lane >> 4) * 8, lv);
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) {
+                    if (!__ballot(in && (tcur >> 4) == j)) continue;
+                    T f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = __shfl(tcur, h * KH + (lane >> 4) * 8 + e, 64);
+                        f[e] = T(t == j * 16 + (lane & 15) ? lv[e] : 0.f);
+                    }
+                    const uint4 bf = *reinterpret_cast<const uint4 *>(f);
+#pragma unroll
+                    for (int i = 0; i < C::FM; ++i) c[i][j] = mfma_half<T>(af[i], bf, c[i][j]);
+                }
+            }
+        }
+    };
+    constexpr int E = 16 / int(sizeof(T));        // w's and x's rows are whole granules
+    tile_product<T, C, true, DW>(GemmOperand{a.a, a.lda, (a.M + E - 1) / E * E, a.k_a},
+                                 GemmOperand{a.b, a.ldb, DW ? a.ldb / int64_t(sizeof(T)) : a.n, a.k_b}, m0, n0, s0,
+                                 s1, smem, acc, low);
+
+    const float inv = a.scale ? a.scale[1] : 1.f;
+    const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        const int64_t row = n0 + nw + 16 * j + (lane & 15);
+        if (row >= a.n) continue;
+        int t = 0;
+        float lv = 0.f;
+        if constexpr (!DW) {
+            if (!a.slab) {
+                t = a.t32[row];
+                if (sizeof(T) == 2 && t >= 0) lv = static_cast<float>(static_cast<const T *>(a.low)[row]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+            const int64_t m = m0 + mw + i * 16;
+            const int left = int(min(int64_t(4), a.M - m));
+            if (left <= 0) continue;
+            float q[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            if (a.slab) {
+                float *o = a.slab + (int64_t(part) * a.n + row) * a.M + m;
+                if (a.add) {
+                    float p[4];
+                    load_some<4>(o, left, p);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) q[v] += p[v];
+                }
+                store_some<4>(o, left, q);
+            } else {
+                if (!DW && sizeof(T) == 2 && t >= 0) {
+                    float wv[4];
+                    load_some<4>(reinterpret_cast<const T *>(static_cast<const char *>(a.w) + t * a.ldw) + m, left,
+                                 wv);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) q[v] += lv * wv[v];
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) q[v] = t >= 0 ? q[v] * inv : 0.f;
+                store_some<4>(static_cast<T *>(a.out) + row * a.M + m, left, q);
+            }
+        }
+    }
+}
+
+// the slabs of [n][M] added in order, for dx with the rounding residual
+template <typename T, bool DW>
+__global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs a)
+{
+    const int64_t chunks = (a.M + 3) / 4, total = a.n * chunks;
+    const float inv = a.scale ? a.scale[1] : 1.f;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / chunks, m = (i - row * chunks) * 4;
+        const int left = int(min(int64_t(4), a.M - m));
+        float q[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < a.split; ++p) {
+            float f[4];
+            load_some<4>(a.slab + (int64_t(p) * a.n + row) * a.M + m, left, f);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) q[v] += f[v];
+        }
+        int t = 0;
+        if constexpr (!DW) {
+            t = a.t32[row];
+            if (sizeof(T) == 2 && t >= 0) {
+                const float lv = static_cast<float>(static_cast<const T *>(a.low)[row]);
+                float wv[4];
+                load_some<4>(reinterpret_cast<const T *>(static_cast<const char *>(a.w) + t * a.ldw) + m, left, wv);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) q[v] += lv * wv[v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) q[v] = t >= 0 ? q[v] * inv : 0.f;
+        store_some<4>(static_cast<T *>(a.out) + row * a.M + m, left, q);
+    }
+}
+
+using C256 = TileCfg<256, 256, 2, 4, 2>;
+using C128 = TileCfg<128, 128, 2, 2, 2>;
+using C64 = TileCfg<64, 64, 2, 2, 3>;
+
+template <typename T, typename C, bool DW>
+hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
+{
+    const auto kernel = xent_product_kernel<T, C, DW>;
+    const int64_t tm = (a.M + C::BM - 1) / C::BM, tn = (a.n + C::BN - 1) / C::BN;
+    if (tm * tn * a.split > INT32_MAX) return hipErrorInvalidValue;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, C::lds_bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(tm * tn * a.split)), dim3(C::threads), C::lds_bytes, s, a, int(tm),
+                       int(tn));
+    return hipGetLastError();
+}
+
+template <typename T, bool DW>
+hipError_t launch_product(const ProductArgs &a, int tile, hipStream_t s)
+{
+    switch (tile) {
+    case kTile256: return launch_tiles<T, C256, DW>(a, s);
+    case kTile128: return launch_tiles<T, C128, DW>(a, s);
+    default: return launch_tiles<T, C64, DW>(a, s);
+    }
+}
+
+template <bool DW, typename F>
+hipError_t with_type(int dtype, F f)
+{
+    if (dtype == 0) return f(float{});
+    if (dtype == 1) return f(_Float16{});
+    return f(__bf16{});
+}
+
+template <bool DW>
+hipError_t launch_join(const ProductArgs &a, int dtype, hipStream_t s)
+{
+    const int64_t total = a.n * ((a.M + 3) / 4);
+    const dim3 grid(unsigned(total / 256 + 1 < 4096 ? total / 256 + 1 : 4096));
+    return with_type<DW>(dtype, [&](auto t) {
+        hipLaunchKernelGGL((xent_join_slabs_kernel<decltype(t), DW>), grid, dim3(256), 0, s, a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+hipError_t launch_xent_dx(const ProductArgs &a, int dtype, int tile, hipStream_t s)
+{
+    return with_type<false>(dtype, [&](auto t) { return launch_product<decltype(t), false>(a, tile, s); });
+}
+
+hipError_t launch_xent_dw(const ProductArgs &a, int dtype, int tile, hipStream_t s)
+{
+    return with_type<true>(dtype, [&](auto t) { return launch_product<decltype(t), true>(a, tile, s); });
+}
+
+hipError_t launch_xent_dx_join(const ProductArgs &a, int dtype, hipStream_t s) { return launch_join<false>(a, dtype, s); }
+hipError_t launch_xent_dw_join(const ProductArgs &a, int dtype, hipStream_t s) { return launch_join<true>(a, dtype, s); }
+
+}  // namespace im2win

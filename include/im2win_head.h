@@ -119,8 +119,9 @@ conv2d_status_t layer_norm_bwd(const layer_norm_desc_t *d, const void *dy, const
  * tile by tile in fp32 and never stored; the backward pass forms them a
  * second time, in pieces of the classes, and holds one piece of G in the
  * workspace in the type of x (fp16: scaled by a power of two into the type's
- * range). dx and dw are accumulated in fp32 and rounded once. N may be 0 (dw is
- * then 0). */
+ * range; half precision: what that rounding takes from each row's target entry
+ * is added back). dx and dw are accumulated in fp32 and rounded once. N may be
+ * 0 (dw is then 0). */
 typedef struct {
     int64_t N, V, D;          /* rows, classes, features                          */
     int64_t ldx, ldw;         /* row strides of x and w in elements (0: D)        */
@@ -128,7 +129,12 @@ typedef struct {
     int32_t reserved;         /* must be 0                                        */
 } linear_xent_desc_t;
 
-/* Bytes of workspace linear_xent_fwd / linear_xent_bwd need (0 if d is
+/* Limits: N <= 2^22, V <= 2^24, D, ldx, ldw <= 2^20. Where D and the row stride
+ * are multiples of 16 bytes (8 half-precision or 4 fp32 elements) the rows are
+ * read in place and x and w must start on a 16-byte boundary (backward: w
+ * alone); other rows may start anywhere and are copied into the workspace first.
+ *
+ * Bytes of workspace linear_xent_fwd / linear_xent_bwd need (0 if d is
  * invalid, or when none is needed). */
 size_t linear_xent_fwd_workspace_size(const linear_xent_desc_t *d);
 size_t linear_xent_bwd_workspace_size(const linear_xent_desc_t *d);

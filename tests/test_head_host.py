@@ -184,7 +184,7 @@ XENT = dict(N=4, V=10, D=8, ldx=0, ldw=0, dtype=1, reserved=0)
 @pytest.mark.parametrize("bad,want", [
     (dict(N=-1), 1), (dict(V=0), 1), (dict(D=0), 1), (dict(ldx=7), 1), (dict(ldw=7), 1), (dict(reserved=2), 1),
     (dict(N=(1 << 22) + 1), 1), (dict(V=(1 << 24) + 1), 1), (dict(D=(1 << 20) + 1), 1), (dict(ldx=(1 << 22) + 1), 1),
-    (dict(dtype=3), 4),
+    (dict(ldw=(1 << 20) + 1), 1), (dict(dtype=3), 4),
 ])
 def test_linear_xent_refuses(bad, want):
     d = _head.LinearXentDesc(**{**XENT, **bad})
@@ -202,6 +202,11 @@ def test_linear_xent_pointers():
         a[i] = None
         assert _status("linear_xent_fwd", d, *a, None) == 2, i
     assert _status("linear_xent_fwd", d, P, P, P + 4, P, P, P, None) == 3
+    # rows of whole 16-byte granules start on a 16-byte boundary
+    assert _status("linear_xent_fwd", d, P + 8, P, P, P, P, P, None) == 3
+    assert _status("linear_xent_fwd", d, P, P + 8, P, P, P, P, None) == 3
+    assert _status("linear_xent_bwd", d, P, P, P + 8, P, P, P, P, P, None) == 3
+    assert _status("linear_xent_fwd", _head.LinearXentDesc(**{**XENT, "D": 7}), P, P + 1, P, P, P, P, None) == 3
     ok = [P] * 8
     for i in range(7):
         a = list(ok)
