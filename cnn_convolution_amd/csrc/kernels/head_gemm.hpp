@@ -16,13 +16,6 @@
 // up with the same fragment: of row (column) lane%16, half precision the 8 K
 // values 32h + 8(lane/16) .., fp32 the 4 values 16h + 4(lane/16) .., for half h
 // of the stage.
-//
-// Pipeline, one barrier per stage: the fragments of half 0 are in registers when
-// a stage begins; half 1 is read while half 0 is multiplied; then every wave's
-// reads of the stage are done and its copies of the next stage have landed
-// (barrier), the stage after that is requested into the freed buffer, and the
-// next stage's half 0 is read while half 1 is multiplied. No product waits for
-// a read issued in its own half.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -123,12 +116,10 @@ struct TileLoad {
         return min((lane % GR) ^ swz(k), n / E - 1);
     }
 
-    __device__ __forceinline__ void issue(int64_t stage, uint32_t lds, int wave) const
+    // copy i of this wave for the stage whose K starts at b
+    __device__ __forceinline__ void issue(const char *b, int i, uint32_t lds, int wave) const
     {
-        const char *b = base + stage * step;
-#pragma unroll
-        for (int i = 0; i < per_wave; ++i)
-            copy_to_lds_at(b, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
+        copy_to_lds_at(b, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
     }
     // the last stage of a K that ends inside it (left < KI values): rows read
     // zeros past it, columns repeat the last K row (the other operand has zeros
@@ -138,7 +129,7 @@ struct TileLoad {
         const char *b = base + stage * step;
 #pragma unroll
         for (int i = 0; i < per_wave; ++i) {
-            const char *src;
+            const char *src;                 // left >= KI: the stage is whole
             if constexpr (!COLS) {
                 const bool ok = ((lane & 7) ^ (lane >> 3)) * E < left;
                 src = ok ? b + off[i] : reinterpret_cast<const char *>(&zero_granule);
@@ -219,15 +210,37 @@ struct GemmOperand {
     int64_t k_end;           // K values that exist; columns repeat the last one past it
 };
 
+// No further products (see tile_product).
+struct NoExtra {
+    static constexpr bool any = false;
+    __device__ __forceinline__ void stage(int) {}
+    __device__ __forceinline__ void half(int, int) {}
+};
+
 // acc[i][j]: 16 x 16 blocks of this wave's part of the tile; lane l holds m =
-// 16i + 4(l/16) + v and n = 16j + l%16 of it. K stages [s0, s1). extra(stage,
-// half, A fragments, acc) is called after each half's products.
+// 16i + 4(l/16) + v and n = 16j + l%16 of it. K stages [s0, s1).
+//
+// A stage is 2 * FM steps, step t = (half t / FM, A block t % FM): FN products,
+// and between them a share of everything else, so that neither wave of a SIMD
+// issues a long run of reads or copies while the matrix core waits:
+//   A fragments are read LA steps ahead into a ring, B fragments (one set per
+//   half) two to a step ahead of their half;
+//   at step BS every read of this stage is done: the barrier that waits for
+//   them (and for the next stage's copies) frees its buffer, and the next
+//   stage's fragments are read from there on;
+//   the copies of stage s + NST into that buffer go out one share per step from
+//   BS on, into the next stage's first steps (64 KB take the CU's vector
+//   memory path 1024 cycles of a stage's 2048).
+//
+// Extra adds products of the same A fragments: extra.stage(s) before a stage,
+// extra.half(s, h) before its halves, bit j of extra.jmask whether block column j
+// has any in this half, extra.b[j] their B fragments.
 template <typename T, typename C, bool ACOLS, bool BCOLS, typename Extra>
 __device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOperand &B, int64_t m0, int64_t n0,
-                                             int s0, int s1, char *smem,
-                                             floatx4_t (&acc)[C::FM][C::FN], Extra extra)
+                                             int s0, int s1, char *smem, floatx4_t (&acc)[C::FM][C::FN],
+                                             Extra &extra)
 {
-    constexpr int KI = 128 / int(sizeof(T));
+    constexpr int KI = 128 / int(sizeof(T)), FM = C::FM, FN = C::FN, NST = C::NST;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % C::WM, wn = wave / C::WM;
     TileLoad<T, C::BM, C::waves, ACOLS> la;
@@ -240,65 +253,108 @@ __device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOpe
     rb.init(wn * (C::BN / C::WN), lane);
     const lds_ptr sm = (lds_ptr)smem;
     const uint32_t sbase = uint32_t(reinterpret_cast<uintptr_t>(sm));
-    constexpr int D = decltype(la)::per_wave + decltype(lb)::per_wave;   // copies per wave per stage
+    constexpr int UA = decltype(la)::per_wave, D = UA + decltype(lb)::per_wave;   // copies per wave and stage
 
-    // A stages first, then B stages
-    auto issue = [&](int s, int buf) {
-        const uint32_t a = sbase + buf * C::a_bytes, b = sbase + C::NST * C::a_bytes + buf * C::b_bytes;
-        const int64_t left_a = A.k_end - int64_t(s) * KI, left_b = B.k_end - int64_t(s) * KI;
-        if (left_a >= KI)
-            la.issue(s, a, wave);
-        else
-            la.issue_tail(s, int(left_a), a, wave, lane);
-        if (left_b >= KI)
-            lb.issue(s, b, wave);
-        else
-            lb.issue_tail(s, int(left_b), b, wave, lane);
-    };
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    constexpr int STEPS = 2 * FM;
+    constexpr int LA = FM >= 8 ? 5 : FM >= 4 ? 3 : 2;
+    constexpr int BS = STEPS - LA + 1;
+    constexpr int R = FM >= 8 ? 8 : 4;                        // ring of A fragments
+    constexpr int PER = (D + FM - 1) / FM;                    // copies per step
+    constexpr int TAIL = (STEPS - BS) * PER < D ? (STEPS - BS) * PER : D;   // copies that go out from BS on
+    constexpr int B1 = FM / 2 - 1;                            // first step that reads half 1's B
+    static_assert(STEPS % R == 0 && LA + 1 <= R, "ring");
 
-    uint4 a0[C::FM], b0[C::FN], a1[C::FM], b1[C::FN];
-    auto read = [&](int buf, int h, uint4 (&a)[C::FM], uint4 (&b)[C::FN]) {
-        const lds_ptr at = sm + buf * C::a_bytes, bt = sm + C::NST * C::a_bytes + buf * C::b_bytes;
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) b[j] = rb.read(bt, j, h);
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) a[i] = ra.read(at, i, h);
-    };
-    auto multiply = [&](const uint4 (&a)[C::FM], const uint4 (&b)[C::FN]) {
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j) acc[i][j] = mfma_half<T>(a[i], b[j], acc[i][j]);
-    };
-
-    // NST - 1 stages requested ahead; past the last stage the last one is
-    // requested again (into a buffer nothing reads any more), so that the
-    // number of copies in flight is always the same
+    // LDS: the A buffers first, then the B buffers
+    const int whole = int(min(A.k_end, B.k_end) / KI);        // stages that both operands fill
     const int last = s1 - 1;
+    auto request = [&](int s, int buf) {
+        const uint32_t a = sbase + buf * C::a_bytes, b = sbase + NST * C::a_bytes + buf * C::b_bytes;
+        la.issue_tail(s, int(min(A.k_end - int64_t(s) * KI, int64_t(KI))), a, wave, lane);
+        lb.issue_tail(s, int(min(B.k_end - int64_t(s) * KI, int64_t(KI))), b, wave, lane);
+    };
+    auto copy = [&](int u, int s, int buf) {                  // copy u of whole stage s
+        if (u < UA)
+            la.issue(la.base + int64_t(s) * la.step, u, sbase + buf * C::a_bytes, wave);
+        else
+            lb.issue(lb.base + int64_t(s) * lb.step, u - UA, sbase + NST * C::a_bytes + buf * C::b_bytes, wave);
+    };
 #pragma unroll
-    for (int s = 0; s < C::NST; ++s) issue(min(s0 + s, last), s);
-    wait_vm<D * (C::NST - 1)>();
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    uint4 ar[R], br[2][FN];
+    auto read_a = [&](int u, int buf) { ar[u % R] = ra.read(sm + buf * C::a_bytes, u % FM, u % STEPS / FM); };
+    auto read_b = [&](int j, int h, int buf) { br[h][j] = rb.read(sm + NST * C::a_bytes + buf * C::b_bytes, j, h); };
+
+#pragma unroll
+    for (int s = 0; s < NST; ++s)
+        if (s0 + s <= last) request(s0 + s, s);
+    if (last - s0 >= NST - 1)
+        wait_vm<D * (NST - 1)>();
+    else
+        wait_vm<0>();
     stage_barrier();
-    read(0, 0, a0, b0);
-    int buf = 0;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_b(j, 0, 0);
+#pragma unroll
+    for (int u = 0; u < LA; ++u) read_a(u, 0);
+    int buf = 0, prev = 0;
+    bool pending = false;                                     // copies TAIL .. of stage s - 1 + NST are left
     for (int s = s0; s < s1; ++s) {
-        const int next = buf + 1 == C::NST ? 0 : buf + 1;
-        read(buf, 1, a1, b1);
-        multiply(a0, b0);
-        extra(s, 0, a0, acc);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vm<D * (C::NST - 2)>();
-        stage_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        issue(min(s + C::NST, last), buf);
-        read(next, 0, a0, b0);
-        multiply(a1, b1);
-        extra(s, 1, a1, acc);
-        __builtin_amdgcn_sched_barrier(0);
+        const int next = buf + 1 == NST ? 0 : buf + 1;
+        bool now = false;
+        extra.stage(s);
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+            if (t == 0 || t == FM) extra.half(s, t / FM);
+            if (t == BS) {
+                if (NST > 2 && s + NST - 1 <= last)
+                    wait_vm<D * (NST - 2)>();
+                else
+                    wait_vm<0>();
+                stage_barrier();
+                now = s + NST <= last;
+                if (now && s + NST >= whole) {
+                    request(s + NST, buf);
+                    now = false;
+                }
+            }
+            if (t >= BS) {
+                if (now) {
+#pragma unroll
+                    for (int u = (t - BS) * PER; u < (t - BS + 1) * PER && u < TAIL; ++u) copy(u, s + NST, buf);
+                }
+            } else if (TAIL + t * PER < D) {
+                if (pending) {
+#pragma unroll
+                    for (int u = TAIL + t * PER; u < TAIL + (t + 1) * PER && u < D; ++u) copy(u, s - 1 + NST, prev);
+                }
+            }
+            // after the last stage the reads from `next` find no stage there: unused
+            if (t + LA < STEPS) read_a(t + LA, buf);
+            if (t == BS) {
+                read_a(STEPS, next);
+                read_a(STEPS + 1, next);
+            }
+            if (t > BS) read_a(t + LA, next);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if (t >= B1 && t < FM && j / 2 == t - B1) read_b(j, 1, buf);
+                if (t >= BS && j / 2 == t - BS) read_b(j, 0, next);
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[t % FM][j] = mfma_half<T>(ar[t % R], br[t / FM][j], acc[t % FM][j]);
+            if constexpr (Extra::any) {
+                if (extra.jmask)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        if ((extra.jmask >> j) & 1) acc[t % FM][j] = mfma_half<T>(ar[t % R], extra.b[j], acc[t % FM][j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        pending = now;
+        prev = buf;
         buf = next;
     }
     wait_vm<0>();

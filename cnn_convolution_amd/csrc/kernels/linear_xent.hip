@@ -220,6 +220,7 @@ XentPlan plan_xent_bwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw
     p.off_scale = take(p, 8);
     p.off_t32 = take(p, p.rows_pad * 4);
     p.off_low = take(p, p.rows_pad * es);
+    p.off_hits = take(p, p.piece / 32 * (p.rows_pad / 32));
     p.off_x = take(p, N * p.Dp * es);
     if (p.copy_w) p.off_w = take(p, V * p.Dp * es);
     p.off_g = take(p, p.rows_pad * p.piece * es);
@@ -314,6 +315,8 @@ hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
     ProductArgs dx{}, dw{};
     dx.t32 = dw.t32 = t32;
     dx.low = dw.low = ws + p.off_low;
+    dw.hits = reinterpret_cast<uint8_t *>(ws + p.off_hits);
+    dw.ldh = p.rows_pad / 32;
     dx.scale = dw.scale = scale;
     dx.b = dw.b = ws + p.off_g;
     dx.ldb = dw.ldb = p.piece * es;
@@ -333,7 +336,8 @@ hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
     dw.slab = p.dw_split > 1 ? reinterpret_cast<float *>(ws + p.off_dw) : nullptr;
     for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
         const int64_t P = std::min(p.piece, a.V - v0);
-        GradArgs g{r, a.N, v0, P, p.Dp, t32, a.grad, a.lse, scale, ws + p.off_g, p.piece, ws + p.off_low};
+        GradArgs g{r, a.N, v0, P, p.Dp, t32, a.grad, a.lse, scale, ws + p.off_g, p.piece, ws + p.off_low,
+                   reinterpret_cast<uint8_t *>(ws + p.off_hits), p.rows_pad / 32};
         if ((e = launch_xent_g(g, a.dtype, p.logits_tile, s)) != hipSuccess) return e;
         dx.a = static_cast<const char *>(r.w) + v0 * r.ldw;
         dx.K = dx.k_a = P;

@@ -33,9 +33,9 @@ __global__ __launch_bounds__(C::threads) void xent_loss_kernel(const LossArgs a,
     strip_tile(blockIdx.x, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = int64_t(tm) * C::BM, n0 = int64_t(tn) * C::BN;
     floatx4_t acc[C::FM][C::FN];
+    NoExtra none;
     tile_product<T, C, false, false>(GemmOperand{a.r.w, a.r.ldw, a.V, a.Dp}, GemmOperand{a.r.x, a.r.ldx, a.N, a.Dp},
-                                     m0, n0, 0, int((a.Dp + KI - 1) / KI), smem, acc,
-                                     [](int, int, const uint4 (&)[C::FM], auto &) {});
+                                     m0, n0, 0, int((a.Dp + KI - 1) / KI), smem, acc, none);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
     const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;      // first class of this lane in the tile
@@ -101,18 +101,33 @@ __global__ __launch_bounds__(C::threads) void xent_g_kernel(const GradArgs a, in
     strip_tile(blockIdx.x, tiles_m, tiles_n, tm, tn);
     const int64_t m0 = int64_t(tm) * C::BM, n0 = int64_t(tn) * C::BN;
     floatx4_t acc[C::FM][C::FN];
+    NoExtra none;
     const char *w = static_cast<const char *>(a.r.w) + a.v0 * a.r.ldw;
     tile_product<T, C, false, false>(GemmOperand{w, a.r.ldw, a.P, a.Dp}, GemmOperand{a.r.x, a.r.ldx, a.N, a.Dp}, m0,
-                                     n0, 0, int((a.Dp + KI - 1) / KI), smem, acc,
-                                     [](int, int, const uint4 (&)[C::FM], auto &) {});
+                                     n0, 0, int((a.Dp + KI - 1) / KI), smem, acc, none);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
     const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;
     const int left = int(min(int64_t(C::BM), a.P - m0)) - mw;
     const float S = a.scale ? a.scale[0] : 1.f;
+    const int64_t nw = n0 + wn * (C::BN / C::WN);
+    if constexpr (sizeof(T) == 2) {
+        // which 32 x 32 blocks of G hold a target
+        const int64_t cw = a.v0 + m0 + wm * (C::BM / C::WM);
+#pragma unroll
+        for (int r = 0; r < C::FN / 2; ++r) {
+            const int64_t c = a.t32[nw + 32 * r + (lane & 31)] - cw;
+#pragma unroll
+            for (int b = 0; b < C::FM / 2; ++b) {
+                const bool any = __ballot(c >= 32 * b && c < 32 * b + 32) != 0;
+                if (lane == 0)
+                    a.hits[((m0 + wm * (C::BM / C::WM)) / 32 + b) * a.ldh + nw / 32 + r] = any ? 1 : 0;
+            }
+        }
+    }
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-        const int64_t row = n0 + wn * (C::BN / C::WN) + 16 * j + (lane & 15);   // below rows_pad
+        const int64_t row = nw + 16 * j + (lane & 15);   // below rows_pad
         const int t = a.t32[row];
         const bool ok = t >= 0;
         const float gs = ok ? a.grad[row] * S : 0.f, lse = ok ? a.lse[row] : 0.f;

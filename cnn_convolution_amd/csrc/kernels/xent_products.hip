@@ -19,12 +19,67 @@
 namespace im2win {
 namespace {
 
+// dw: the products that add low[n] x[n] to the target's class of each row n
+template <typename T, typename C>
+struct LowExtra {
+    static constexpr bool any = true;
+    static constexpr int KI = 128 / int(sizeof(T)), KH = KI / 2;
+    const ProductArgs &a;
+    int64_t c0;              // first class of this wave, relative to the piece
+    int s0, nk, lane;
+    uint32_t hit = 0;        // bit s & 31: a target of stage s's rows is one of this wave's classes
+    uint32_t jmask = 0;      // of this half: the block columns with one
+    uint4 b[C::FN];
+
+    // hits of 32 stages at a time: lane l < 32 takes stage l for the first 32
+    // classes, the others for the second 32 of a wave of 64 classes
+    __device__ __forceinline__ void stage(int s)
+    {
+        if ((s & 31) != 0 && s != s0) return;
+        uint64_t all = 0;
+#pragma unroll
+        for (int q = 0; q < (C::FN + 3) / 4; ++q) {
+            const int64_t st = (s & ~31) + (lane & 31);
+            const bool in = (lane >> 5) * 2 + q * 4 < C::FN && st < nk;
+            uint32_t v = 0;
+            if (in) {
+                const uint8_t *p = a.hits + (c0 / 32 + q * 2 + (lane >> 5)) * a.ldh + st * 2;
+                v = p[0] | p[1];
+            }
+            all |= __ballot(v != 0);
+        }
+        hit = uint32_t(all) | uint32_t(all >> 32);
+    }
+    __device__ __forceinline__ void half(int s, int h)
+    {
+        jmask = 0;
+        if (__builtin_expect(!((hit >> (s & 31)) & 1), 1)) return;
+        const int64_t r0 = int64_t(s) * KI;
+        const int t = a.t32[r0 + lane] - int(a.v0 + c0);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            if (__ballot((lane / KH) == h && t >= 0 && (t >> 4) == j)) jmask |= 1u << j;
+        if (!jmask) return;
+        float lv[8];
+        load_vec<8>(static_cast<const T *>(a.low) + r0 + h * KH + (lane >> 4) * 8, lv);
+        int te[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) te[e] = __shfl(t, h * KH + (lane >> 4) * 8 + e, 64);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            T f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = T(te[e] == j * 16 + (lane & 15) ? lv[e] : 0.f);
+            b[j] = *reinterpret_cast<const uint4 *>(f);
+        }
+    }
+};
+
 template <typename T, typename C, bool DW>
 __global__ __launch_bounds__(C::threads) void xent_product_kernel(const ProductArgs a, int tiles_m, int tiles_n)
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    constexpr int KI = 128 / int(sizeof(T)), KH = KI / 2;
-    constexpr bool LOW = DW && sizeof(T) == 2;
+    constexpr int KI = 128 / int(sizeof(T));
     const int tiles = tiles_m * tiles_n;
     const int part = blockIdx.x / tiles, b = blockIdx.x - part * tiles;
     int tm, tn;
@@ -36,39 +91,16 @@ __global__ __launch_bounds__(C::threads) void xent_product_kernel(const ProductA
     const int nw = wn * (C::BN / C::WN);
     floatx4_t acc[C::FM][C::FN];
 
-    // the targets of a stage's rows, one per lane, loaded a stage ahead
-    int tnext = LOW ? a.t32[int64_t(s0) * KI + lane] : 0, tcur = 0;
-    const int cbase = int(a.v0 + n0) + nw;
-    auto low = [&](int s, int h, const uint4 (&af)[C::FM], floatx4_t (&c)[C::FM][C::FN]) {
-        if constexpr (LOW) {
-            if (h == 0) {
-                tcur = tnext - cbase;
-                tnext = a.t32[int64_t(min(s + 1, s1 - 1)) * KI + lane];
-            }
-            const bool in = uint32_t(tcur) < uint32_t(C::FN * 16) && (lane / KH) == h;
-            if (__ballot(in)) {
-                float lv[8];
-                load_vec<8>(static_cast<const T *>(a.low) + int64_t(s) * KI + h * KH + (lane >> 4) * 8, lv);
-#pragma unroll
-                for (int j = 0; j < C::FN; ++j) {
-                    if (!__ballot(in && (tcur >> 4) == j)) continue;
-                    T f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int t = __shfl(tcur, h * KH + (lane >> 4) * 8 + e, 64);
-                        f[e] = T(t == j * 16 + (lane & 15) ? lv[e] : 0.f);
-                    }
-                    const uint4 bf = *reinterpret_cast<const uint4 *>(f);
-#pragma unroll
-                    for (int i = 0; i < C::FM; ++i) c[i][j] = mfma_half<T>(af[i], bf, c[i][j]);
-                }
-            }
-        }
-    };
     constexpr int E = 16 / int(sizeof(T));        // w's and x's rows are whole granules
-    tile_product<T, C, true, DW>(GemmOperand{a.a, a.lda, (a.M + E - 1) / E * E, a.k_a},
-                                 GemmOperand{a.b, a.ldb, DW ? a.ldb / int64_t(sizeof(T)) : a.n, a.k_b}, m0, n0, s0,
-                                 s1, smem, acc, low);
+    const GemmOperand A{a.a, a.lda, (a.M + E - 1) / E * E, a.k_a};
+    const GemmOperand B{a.b, a.ldb, DW ? a.ldb / int64_t(sizeof(T)) : a.n, a.k_b};
+    if constexpr (DW && sizeof(T) == 2) {
+        LowExtra<T, C> low{a, n0 + nw, s0, nk, lane};
+        tile_product<T, C, true, DW>(A, B, m0, n0, s0, s1, smem, acc, low);
+    } else {
+        NoExtra none;
+        tile_product<T, C, true, DW>(A, B, m0, n0, s0, s1, smem, acc, none);
+    }
 
     const float inv = a.scale ? a.scale[1] : 1.f;
     const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;

@@ -22,7 +22,7 @@ struct XentPlan {
     int64_t rows_pad;        // rows of G
     int dx_tile, dx_split, dw_tile, dw_split;
     bool dx_direct;          // one piece and no split: dx straight from the product
-    int64_t off_scale, off_t32, off_low, off_x, off_w, off_partial, off_g, off_dx, off_dw, bytes;
+    int64_t off_scale, off_t32, off_low, off_hits, off_x, off_w, off_partial, off_g, off_dx, off_dw, bytes;
 };
 XentPlan plan_xent_fwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype);
 XentPlan plan_xent_bwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype);
@@ -50,6 +50,8 @@ struct GradArgs {
     void *g;                 // [rows_pad][ldg]
     int64_t ldg;
     void *low;               // [N]: what rounding took from G at the target (half precision)
+    uint8_t *hits;           // [piece / 32][rows_pad / 32]: whether a target lies in that block of G
+    int64_t ldh;
 };
 hipError_t launch_xent_g(const GradArgs &a, int dtype, int tile, hipStream_t s);
 
@@ -65,6 +67,8 @@ struct ProductArgs {
     const float *scale;      // scale[1]: 1/S, or null
     const int *t32;
     const void *low;
+    const uint8_t *hits;     // dw
+    int64_t ldh;
     int64_t v0;              // dw: first class of the piece
     const void *w;           // dx: for the rounding residual
     int64_t ldw;             // bytes
