@@ -212,9 +212,10 @@ struct GemmOperand {
 
 // No further products (see tile_product).
 struct NoExtra {
-    static constexpr bool any = false;
-    __device__ __forceinline__ void stage(int) {}
-    __device__ __forceinline__ void half(int, int) {}
+    template <typename R, typename A>
+    __device__ __forceinline__ void run(int, R, A &)
+    {
+    }
 };
 
 // acc[i][j]: 16 x 16 blocks of this wave's part of the tile; lane l holds m =
@@ -232,9 +233,8 @@ struct NoExtra {
 //   BS on, into the next stage's first steps (64 KB take the CU's vector
 //   memory path 1024 cycles of a stage's 2048).
 //
-// Extra adds products of the same A fragments: extra.stage(s) before a stage,
-// extra.half(s, h) before its halves, bit j of extra.jmask whether block column j
-// has any in this half, extra.b[j] their B fragments.
+// extra.run(s, read, acc) may add products of stage s's A fragments, read(i, h)
+// for block i of half h.
 template <typename T, typename C, bool ACOLS, bool BCOLS, typename Extra>
 __device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOperand &B, int64_t m0, int64_t n0,
                                              int s0, int s1, char *smem, floatx4_t (&acc)[C::FM][C::FN],
@@ -304,10 +304,9 @@ __device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOpe
     for (int s = s0; s < s1; ++s) {
         const int next = buf + 1 == NST ? 0 : buf + 1;
         bool now = false;
-        extra.stage(s);
+        extra.run(s, [&](int i, int h) { return ra.read(sm + buf * C::a_bytes, i, h); }, acc);
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
-            if (t == 0 || t == FM) extra.half(s, t / FM);
             if (t == BS) {
                 if (NST > 2 && s + NST - 1 <= last)
                     wait_vm<D * (NST - 2)>();
@@ -345,12 +344,6 @@ __device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOpe
             }
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[t % FM][j] = mfma_half<T>(ar[t % R], br[t / FM][j], acc[t % FM][j]);
-            if constexpr (Extra::any) {
-                if (extra.jmask)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        if ((extra.jmask >> j) & 1) acc[t % FM][j] = mfma_half<T>(ar[t % R], extra.b[j], acc[t % FM][j]);
-            }
             __builtin_amdgcn_sched_barrier(0);
         }
         pending = now;

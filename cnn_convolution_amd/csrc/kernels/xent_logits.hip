@@ -74,7 +74,8 @@ __global__ __launch_bounds__(C::threads) void xent_loss_kernel(const LossArgs a,
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) s += fast_exp(acc[i][j][v] - mm);
+            for (int v = 0; v < 4; ++v)
+                s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, mm * -kLog2e));
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
         if (lane < 16) red[wm * C::BN + col] = float2{m, s};
@@ -125,26 +126,44 @@ __global__ __launch_bounds__(C::threads) void xent_g_kernel(const GradArgs a, in
             }
         }
     }
+    const bool edge = m0 + C::BM > a.P;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
         const int64_t row = nw + 16 * j + (lane & 15);   // below rows_pad
         const int t = a.t32[row];
         const bool ok = t >= 0;
-        const float gs = ok ? a.grad[row] * S : 0.f, lse = ok ? a.lse[row] : 0.f;
-        const int64_t tl = ok ? t - a.v0 - m0 - mw : -1;
+        const float gs = ok ? a.grad[row] * S : 0.f, c = ok ? a.lse[row] * -kLog2e : 0.f;
         T *g = static_cast<T *>(a.g) + row * a.ldg + m0 + mw;
+        // exp(l - lse) as one fma and exp2: the rounding of lse * log2(e) is of
+        // the size of lse's own
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                acc[i][j][v] = gs * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, c));
+        if (__ballot(!ok) || edge) {
+            // masked rows and classes past the end: selected away, never multiplied
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = ok && i * 16 + v < left ? acc[i][j][v] : 0.f;
+        }
+        const int64_t tl = ok ? t - a.v0 - m0 - mw : -1;
+        if (__ballot(tl >= 0 && tl < C::FM * 16 && (tl & 15) < 4)) {
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (tl == i * 16 + v) {
+                        acc[i][j][v] -= gs;
+                        if constexpr (sizeof(T) == 2)
+                            static_cast<T *>(a.low)[row] =
+                                T(acc[i][j][v] - static_cast<float>(T(acc[i][j][v])));
+                    }
+        }
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
-            float q[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const bool hit = tl == i * 16 + v;
-                const float p = fast_exp(acc[i][j][v] - lse);
-                // a masked row's product may be NaN: selected away, never multiplied
-                q[v] = ok && i * 16 + v < left ? gs * (hit ? p - 1.f : p) : 0.f;
-                if (sizeof(T) == 2 && hit && i * 16 + v < left)
-                    static_cast<T *>(a.low)[row] = T(q[v] - static_cast<float>(T(q[v])));
-            }
+            const float q[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
             store_vec<4>(g + i * 16, q);
         }
     }

@@ -22,20 +22,16 @@ namespace {
 // dw: the products that add low[n] x[n] to the target's class of each row n
 template <typename T, typename C>
 struct LowExtra {
-    static constexpr bool any = true;
     static constexpr int KI = 128 / int(sizeof(T)), KH = KI / 2;
     const ProductArgs &a;
     int64_t c0;              // first class of this wave, relative to the piece
     int s0, nk, lane;
     uint32_t hit = 0;        // bit s & 31: a target of stage s's rows is one of this wave's classes
-    uint32_t jmask = 0;      // of this half: the block columns with one
-    uint4 b[C::FN];
 
     // hits of 32 stages at a time: lane l < 32 takes stage l for the first 32
     // classes, the others for the second 32 of a wave of 64 classes
-    __device__ __forceinline__ void stage(int s)
+    __device__ __forceinline__ void load_hits(int s)
     {
-        if ((s & 31) != 0 && s != s0) return;
         uint64_t all = 0;
 #pragma unroll
         for (int q = 0; q < (C::FN + 3) / 4; ++q) {
@@ -50,27 +46,31 @@ struct LowExtra {
         }
         hit = uint32_t(all) | uint32_t(all >> 32);
     }
-    __device__ __forceinline__ void half(int s, int h)
+    template <typename R>
+    __device__ __forceinline__ void run(int s, R read, floatx4_t (&acc)[C::FM][C::FN])
     {
-        jmask = 0;
+        if ((s & 31) == 0 || s == s0) load_hits(s);
         if (__builtin_expect(!((hit >> (s & 31)) & 1), 1)) return;
         const int64_t r0 = int64_t(s) * KI;
         const int t = a.t32[r0 + lane] - int(a.v0 + c0);
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-            if (__ballot((lane / KH) == h && t >= 0 && (t >> 4) == j)) jmask |= 1u << j;
-        if (!jmask) return;
-        float lv[8];
-        load_vec<8>(static_cast<const T *>(a.low) + r0 + h * KH + (lane >> 4) * 8, lv);
-        int te[8];
+        for (int h = 0; h < 2; ++h) {
+            if (!__ballot((lane / KH) == h && t >= 0 && t < C::FN * 16)) continue;
+            float lv[8];
+            load_vec<8>(static_cast<const T *>(a.low) + r0 + h * KH + (lane >> 4) * 8, lv);
+            int te[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) te[e] = __shfl(t, h * KH + (lane >> 4) * 8 + e, 64);
+            for (int e = 0; e < 8; ++e) te[e] = __shfl(t, h * KH + (lane >> 4) * 8 + e, 64);
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-            T f[8];
+            for (int j = 0; j < C::FN; ++j) {
+                if (!__ballot((lane / KH) == h && t >= 0 && (t >> 4) == j)) continue;
+                T f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = T(te[e] == j * 16 + (lane & 15) ? lv[e] : 0.f);
-            b[j] = *reinterpret_cast<const uint4 *>(f);
+                for (int e = 0; e < 8; ++e) f[e] = T(te[e] == j * 16 + (lane & 15) ? lv[e] : 0.f);
+                const uint4 b = *reinterpret_cast<const uint4 *>(f);
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i) acc[i][j] = mfma_half<T>(read(i, h), b, acc[i][j]);
+            }
         }
     }
 };
