@@ -22,9 +22,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T *x, T *y, int64_t 
         const int m = int(min(int64_t(8), n - b * 8));
         float f[8];
         load_some<8>(x + b * 8, m, f);
-        const uint32_t keep = keep_bits(uint64_t(b), d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (keep >> e) & 1 ? f[e] * d.scale : 0.f;
+        drop_block(uint64_t(b), d, f);
         store_some<8>(y + b * 8, m, f);
     }
 }

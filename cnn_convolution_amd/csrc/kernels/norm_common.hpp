@@ -33,18 +33,15 @@ hipError_t with_norm_types(int dtype, int y_dtype, F f)
 template <int K>
 __device__ __forceinline__ void drop_run(int64_t first, const DropSpec &d, float (&f)[K])
 {
+    if constexpr (K == 8) {
+        if ((first & 7) == 0) {
+            drop_block(uint64_t(first) >> 3, d, f);
+            return;
+        }
+    }
     const uint32_t keep = keep_run<K>(first, d);
 #pragma unroll
     for (int e = 0; e < K; ++e) f[e] = (keep >> e) & 1 ? f[e] * d.scale : 0.f;
-}
-
-// sum over the L lanes (a power of two) of an aligned group
-template <int L>
-__device__ __forceinline__ float lane_sum(float v)
-{
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m, 64);
-    return v;
 }
 
 // dweight, dbias from the blocks' partial sums [rows][2][C], in a fixed order
