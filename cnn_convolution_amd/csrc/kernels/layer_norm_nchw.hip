@@ -55,15 +55,42 @@ __device__ __forceinline__ void store_pos(T *p, int left, const float (&f)[4])
     }
 }
 
+// Elements of an image are addressed as its (wave-uniform) base and a 32-bit
+// byte offset per lane: half the registers of a pointer per channel. The images
+// these kernels take are below 4 GB.
+template <typename T>
+__device__ __forceinline__ const T *at_offset(const T *base, uint32_t elems)
+{
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + elems * uint32_t(sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ T *at_offset(T *base, uint32_t elems)
+{
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(base) + elems * uint32_t(sizeof(T)));
+}
+
+// where positions p .. p + 3 of a channel are read from, and how far that is
+// before p (see load_row)
+struct Window {
+    uint32_t at;
+    int shift;
+    __device__ __forceinline__ Window(int64_t p, int64_t P)
+    {
+        const int64_t q = p < P - 4 ? p : P - 4;
+        at = uint32_t(q);
+        shift = int(p - q < 4 ? p - q : 4);
+    }
+};
+
 // WAVES waves, 4 * WAVES channel groups; EXACT: P is a multiple of 4
 template <typename TX, typename TY, int WAVES, int KR, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArgs a, int tiles_p)
 {
     constexpr int G = WAVES * 4;
-    __shared__ __align__(16) float red[2][2][WAVES][kPos];    // slot, (mean, squares)
+    __shared__ __align__(16) float red[2][WAVES][kPos];    // mean, squares
     const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, wave = threadIdx.x >> 6, C = a.C;
     const float fc = float(C);
-    const int64_t tiles = a.N * tiles_p;
+    const uint32_t P = uint32_t(a.P);
     float w[KR], b[KR];
 #pragma unroll
     for (int i = 0; i < KR; ++i) {
@@ -78,72 +105,85 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
         for (int i = 0; i < KR; ++i) n += max(0, min(4, C - i * G - q * 4));
         return float(n);
     };
-    int slot = 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const TilePos at(t, tiles_p, l, a);
-        const TX *x = static_cast<const TX *>(a.x) + at.base;
-        TY *y = static_cast<TY *>(a.out) + at.base + at.p;
-        // channels past the last read that one and count nowhere
-        Raw<TX, 4> q[KR];
+    const TilePos at(blockIdx.x, tiles_p, l, a);
+    const TX *x = static_cast<const TX *>(a.x) + at.base;
+    TY *y = static_cast<TY *>(a.out) + at.base;
+    const Window win(at.p, a.P);
+    // channels past the last read that one and count nowhere
+    Raw<TX, 4> q[KR];
 #pragma unroll
-        for (int i = 0; i < KR; ++i) q[i] = load_row<TX, 4, EXACT>(x + min(g + i * G, C - 1) * a.P, at.p, a.P);
-        float v[KR][4], mean[4] = {}, sq[4] = {};
+    for (int i = 0; i < KR; ++i)
+        q[i] = load_raw<TX, 4>(at_offset(x, uint32_t(min(g + i * G, C - 1)) * P + win.at));
+    if constexpr (!EXACT)
 #pragma unroll
-        for (int i = 0; i < KR; ++i)
+        for (int i = 0; i < KR; ++i) shift_down(q[i], win.shift);
+    float v[KR][4], mean[4] = {}, sq[4] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[i][e] = element(q[i], e);
-                mean[e] += g + i * G < C ? v[i][e] : 0.f;
-            }
-        // a wave's own mean and squared deviations, joined with one barrier:
-        // sum (x - mean)^2 = sum_w [Q_w + n_w (mean_w - mean)^2]
-        wave_chan_sum(mean);
-        const float nw = fmaxf(count(wave), 1.f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mean[e] /= nw;
-#pragma unroll
-        for (int i = 0; i < KR; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float d = v[i][e] - mean[e];
-                sq[e] += g + i * G < C ? d * d : 0.f;
-            }
-        wave_chan_sum(sq);
-        if ((threadIdx.x & 48) == 0)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                red[slot][0][wave][l * 4 + e] = mean[e];
-                red[slot][1][wave][l * 4 + e] = sq[e];
-            }
-        __syncthreads();
-        float rstd[4];
+    for (int i = 0; i < KR; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float m = 0.f, s = 0.f;
-#pragma unroll
-            for (int k = 0; k < WAVES; ++k) m += red[slot][0][k][l * 4 + e] * count(k);
-            m /= fc;
-#pragma unroll
-            for (int k = 0; k < WAVES; ++k) {
-                const float d = red[slot][0][k][l * 4 + e] - m;
-                s += red[slot][1][k][l * 4 + e] + count(k) * d * d;
-            }
-            mean[e] = m;
-            rstd[e] = 1.f / sqrtf(s / fc + a.eps);
+            v[i][e] = element(q[i], e);
+            mean[e] += g + i * G < C ? v[i][e] : 0.f;
         }
-        slot ^= 1;                             // a wave that is ahead writes the other slot
+    // a wave's own mean and squared deviations, joined with one barrier:
+    // sum (x - mean)^2 = sum_w [Q_w + n_w (mean_w - mean)^2]
+    wave_chan_sum(mean);
+    const float nw = fmaxf(count(wave), 1.f);
 #pragma unroll
-        for (int i = 0; i < KR; ++i) {
-            const int c = g + i * G;
+    for (int e = 0; e < 4; ++e) mean[e] /= nw;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = (v[i][e] - mean[e]) * rstd[e] * w[i] + b[i];
-            if (a.drop.threshold) drop_run<4>(at.base + c * a.P + at.p, a.drop, v[i]);
-            store_pos<EXACT>(y + c * a.P, c < C ? at.left : 0, v[i]);
+    for (int i = 0; i < KR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float d = v[i][e] - mean[e];
+            sq[e] += g + i * G < C ? d * d : 0.f;
         }
-        if (g == 0 && a.mean) {
-            store_some<4>(a.mean + at.n * a.P + at.p, at.left, mean);
-            store_some<4>(a.rstd + at.n * a.P + at.p, at.left, rstd);
+    wave_chan_sum(sq);
+    if ((threadIdx.x & 48) == 0)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            red[0][wave][l * 4 + e] = mean[e];
+            red[1][wave][l * 4 + e] = sq[e];
         }
+    __syncthreads();
+    float rstd[4], m[4] = {}, s[4] = {};
+#pragma unroll 4
+    for (int k = 0; k < WAVES; ++k) {
+        const float4 u = *reinterpret_cast<const float4 *>(&red[0][k][l * 4]);
+        const float n = count(k);
+        m[0] += u.x * n;
+        m[1] += u.y * n;
+        m[2] += u.z * n;
+        m[3] += u.w * n;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] /= fc;
+#pragma unroll 4
+    for (int k = 0; k < WAVES; ++k) {
+        const float4 u = *reinterpret_cast<const float4 *>(&red[0][k][l * 4]);
+        const float4 q2 = *reinterpret_cast<const float4 *>(&red[1][k][l * 4]);
+        const float n = count(k);
+        s[0] += q2.x + n * (u.x - m[0]) * (u.x - m[0]);
+        s[1] += q2.y + n * (u.y - m[1]) * (u.y - m[1]);
+        s[2] += q2.z + n * (u.z - m[2]) * (u.z - m[2]);
+        s[3] += q2.w + n * (u.w - m[3]) * (u.w - m[3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        mean[e] = m[e];
+        rstd[e] = 1.f / sqrtf(s[e] / fc + a.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < KR; ++i) {
+        const int c = g + i * G;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = (v[i][e] - mean[e]) * rstd[e] * w[i] + b[i];
+        if (a.drop.threshold) drop_run<4>(at.base + c * a.P + at.p, a.drop, v[i]);
+        store_pos<EXACT>(at_offset(y, c * P + uint32_t(at.p)), c < C ? at.left : 0, v[i]);
+    }
+    if (g == 0 && a.mean) {
+        store_some<4>(a.mean + at.n * a.P + at.p, at.left, mean);
+        store_some<4>(a.rstd + at.n * a.P + at.p, at.left, rstd);
     }
 }
 
@@ -164,26 +204,36 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
     int slot = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const TilePos at(t, tiles_p, l, a);
+        // opaque, so that no offset of a channel is kept in registers over the tiles
+        uint32_t P = uint32_t(a.P);
+        asm volatile("" : "+s"(P));
         const TX *x = static_cast<const TX *>(a.x) + at.base;
         const TY *dy = static_cast<const TY *>(a.dy) + at.base;
-        TX *dx = static_cast<TX *>(a.out) + at.base + at.p;
+        TX *dx = static_cast<TX *>(a.out) + at.base;
+        const Window win(at.p, a.P);
         const Raw<float, 4> rm = load_row<float, 4, EXACT>(a.mean + at.n * a.P, at.p, a.P);
         const Raw<float, 4> rr = load_row<float, 4, EXACT>(a.rstd + at.n * a.P, at.p, a.P);
         Raw<TX, 4> qx[KR];
         Raw<TY, 4> qy[KR];
 #pragma unroll
         for (int i = 0; i < KR; ++i) {
-            const int64_t row = min(g + i * G, C - 1) * a.P;
-            qx[i] = load_row<TX, 4, EXACT>(x + row, at.p, a.P);
-            qy[i] = load_row<TY, 4, EXACT>(dy + row, at.p, a.P);
+            const uint32_t o = uint32_t(min(g + i * G, C - 1)) * P + win.at;
+            qx[i] = load_raw<TX, 4>(at_offset(x, o));
+            qy[i] = load_raw<TY, 4>(at_offset(dy, o));
         }
+        if constexpr (!EXACT)
+#pragma unroll
+            for (int i = 0; i < KR; ++i) {
+                shift_down(qx[i], win.shift);
+                shift_down(qy[i], win.shift);
+            }
         float h[KR][4], z[KR][4], s1[4] = {}, s2[4] = {};
 #pragma unroll
         for (int i = 0; i < KR; ++i) {
             const int c = g + i * G;
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[i][e] = element(qy[i], e);
-            if (a.drop.threshold) drop_run<4>(at.base + c * a.P + at.p, a.drop, z[i]);
+            if (a.drop.threshold) drop_run<4>(at.base + uint32_t(c) * P + at.p, a.drop, z[i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool in = c < C && (EXACT ? 0 < at.left : e < at.left);
@@ -206,13 +256,22 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
             }
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s1[e] = s2[e] = 0.f;
+        for (int e = 0; e < 4; ++e) s1[e] = s2[e] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < WAVES; ++k) {
+            const float4 u = *reinterpret_cast<const float4 *>(&red[slot][0][k][l * 4]);
+            const float4 q = *reinterpret_cast<const float4 *>(&red[slot][1][k][l * 4]);
+            s1[0] += u.x;
+            s1[1] += u.y;
+            s1[2] += u.z;
+            s1[3] += u.w;
+            s2[0] += q.x;
+            s2[1] += q.y;
+            s2[2] += q.z;
+            s2[3] += q.w;
+        }
 #pragma unroll
-            for (int k = 0; k < WAVES; ++k) {
-                s1[e] += red[slot][0][k][l * 4 + e];
-                s2[e] += red[slot][1][k][l * 4 + e];
-            }
+        for (int e = 0; e < 4; ++e) {
             s1[e] /= fc;
             s2[e] /= fc;
         }
@@ -223,7 +282,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
             float o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = element(rr, e) * (z[i][e] - s1[e] - h[i][e] * s2[e]);
-            store_pos<EXACT>(dx + c * a.P, c < C ? at.left : 0, o);
+            store_pos<EXACT>(at_offset(dx, c * P + uint32_t(at.p)), c < C ? at.left : 0, o);
         }
     }
     if (!a.partial) return;
@@ -385,7 +444,7 @@ struct Hold {
 };
 Hold hold_of(int64_t C, int64_t P)
 {
-    if (P < 4) return {0, 0};
+    if (P < 4 || C * P >= int64_t(1) << 30) return {0, 0};
     if (C <= 64) return {4, 4};
     if (C <= 128) return {4, 8};
     if (C <= 256) return {8, 8};
@@ -419,19 +478,20 @@ int64_t norm_nchw_partials(int64_t N, int64_t C, int64_t P)
 hipError_t launch_norm_nchw_fwd(const NormArgs &a, hipStream_t s)
 {
     const Hold h = hold_of(a.C, a.P);
-    const dim3 grid(unsigned(std::min(tiles_of(a.N, a.P), kMaxBlocksFwd)));
+    const int64_t tiles = tiles_of(a.N, a.P);
     const int tiles_p = int((a.P + kPos - 1) / kPos);
     return with_norm_types(a.dtype, a.y_dtype, [&](auto tx, auto ty) {
         using TX = typename decltype(tx)::type;
         using TY = typename decltype(ty)::type;
-        if (!h.kr) {
+        if (!h.kr || tiles > INT32_MAX) {
+            const dim3 grid(unsigned(std::min(tiles, kMaxBlocksFwd)));
             hipLaunchKernelGGL((norm_nchw_fwd_wide_kernel<TX, TY>), grid, dim3(kWide), 0, s, a, tiles_p);
             return hipGetLastError();
         }
         return with_hold(h, a.P % 4 == 0, [&](auto w, auto k, auto exact) {
             constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value;
-            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, decltype(exact)::value>), grid,
-                               dim3(WAVES * 64), 0, s, a, tiles_p);
+            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, decltype(exact)::value>),
+                               dim3(unsigned(tiles)), dim3(WAVES * 64), 0, s, a, tiles_p);
             return hipGetLastError();
         });
     });
