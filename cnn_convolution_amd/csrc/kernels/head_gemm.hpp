@@ -27,15 +27,20 @@
 
 namespace im2win {
 
-// BM x BN tile by WM x WN waves, NST stage buffers
-template <int BM_, int BN_, int WM_, int WN_, int NST_>
+// BM x BN tile by WM x WN waves, NST stage buffers; per_cu: workgroups that a CU
+// holds (LDS), and that a launch has for each
+template <int BM_, int BN_, int WM_, int WN_, int NST_, int PER_CU>
 struct TileCfg {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
-    static constexpr int waves = WM * WN, threads = waves * 64;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, per_cu = PER_CU;
+    static constexpr int waves = WM * WN, threads = waves * 64, per_simd = waves * PER_CU / 4;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
     static constexpr int a_bytes = BM * 128, b_bytes = BN * 128;
     static constexpr int lds_bytes = (a_bytes + b_bytes) * NST;
 };
+using C256 = TileCfg<256, 256, 2, 4, 2, 1>;
+using C128 = TileCfg<128, 128, 2, 2, 2, 2>;
+using C64 = TileCfg<64, 64, 2, 2, 3, 3>;
+using CNarrow = TileCfg<128, 16, 4, 1, 4, 2>;
 
 // where granules past the end of K are read from
 __device__ __align__(16) static const uint4 zero_granule = {0, 0, 0, 0};
@@ -218,8 +223,11 @@ struct NoExtra {
     }
 };
 
-// acc[i][j]: 16 x 16 blocks of this wave's part of the tile; lane l holds m =
-// 16i + 4(l/16) + v and n = 16j + l%16 of it. K stages [s0, s1).
+// The product of one tile after another, acc[i][j]: 16 x 16 blocks of this wave's
+// part of the tile; lane l holds m = 16i + 4(l/16) + v and n = 16j + l%16 of it.
+// start() requests the first stages, run() multiplies; between a tile's run()
+// and its epilogue the next tile is started, so its first stages arrive while
+// the epilogue works on registers.
 //
 // A stage is 2 * FM steps, step t = (half t / FM, A block t % FM): FN products,
 // and between them a share of everything else, so that neither wave of a SIMD
@@ -232,126 +240,168 @@ struct NoExtra {
 //   the copies of stage s + NST into that buffer go out one share per step from
 //   BS on, into the next stage's first steps (64 KB take the CU's vector
 //   memory path 1024 cycles of a stage's 2048).
-//
-// extra.run(s, read, acc) may add products of stage s's A fragments, read(i, h)
-// for block i of half h.
-template <typename T, typename C, bool ACOLS, bool BCOLS, typename Extra>
-__device__ __forceinline__ void tile_product(const GemmOperand &A, const GemmOperand &B, int64_t m0, int64_t n0,
-                                             int s0, int s1, char *smem, floatx4_t (&acc)[C::FM][C::FN],
-                                             Extra &extra)
-{
-    constexpr int KI = 128 / int(sizeof(T)), FM = C::FM, FN = C::FN, NST = C::NST;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % C::WM, wn = wave / C::WM;
-    TileLoad<T, C::BM, C::waves, ACOLS> la;
-    TileLoad<T, C::BN, C::waves, BCOLS> lb;
-    la.init(static_cast<const char *>(A.p), A.ld, m0, A.count, wave, lane);
-    lb.init(static_cast<const char *>(B.p), B.ld, n0, B.count, wave, lane);
-    FragRead<T, C::BM, ACOLS> ra;
-    FragRead<T, C::BN, BCOLS> rb;
-    ra.init(wm * (C::BM / C::WM), lane);
-    rb.init(wn * (C::BN / C::WN), lane);
-    const lds_ptr sm = (lds_ptr)smem;
-    const uint32_t sbase = uint32_t(reinterpret_cast<uintptr_t>(sm));
-    constexpr int UA = decltype(la)::per_wave, D = UA + decltype(lb)::per_wave;   // copies per wave and stage
-
-    constexpr int STEPS = 2 * FM;
-    constexpr int LA = FM >= 8 ? 5 : FM >= 4 ? 3 : 2;
-    constexpr int BS = STEPS - LA + 1;
-    constexpr int R = FM >= 8 ? 8 : 4;                        // ring of A fragments
-    constexpr int PER = (D + FM - 1) / FM;                    // copies per step
-    constexpr int TAIL = (STEPS - BS) * PER < D ? (STEPS - BS) * PER : D;   // copies that go out from BS on
-    constexpr int B1 = FM / 2 - 1;                            // first step that reads half 1's B
+// 256 x 256 tiles, bf16: 1.36 us per 64-wide stage, 1540 TFLOP/s (without the
+// copies 1700, without the LDS reads 1580: what is left is issue and power).
+template <typename T, typename C, bool ACOLS, bool BCOLS>
+struct TilePipe {
+    static constexpr int KI = 128 / int(sizeof(T)), FM = C::FM, FN = C::FN, NST = C::NST;
+    static constexpr int STEPS = 2 * FM;
+    static constexpr int LA = FM >= 8 ? 4 : FM >= 4 ? 3 : 2;
+    static constexpr int BS = STEPS - LA + 1;
+    static constexpr int R = FM >= 8 ? 8 : 4;                 // ring of A fragments
+    static constexpr int B1 = FM / 2 - 1;                     // first step that reads half 1's B
     static_assert(STEPS % R == 0 && LA + 1 <= R, "ring");
 
-    // LDS: the A buffers first, then the B buffers
-    const int whole = int(min(A.k_end, B.k_end) / KI);        // stages that both operands fill
-    const int last = s1 - 1;
-    auto request = [&](int s, int buf) {
+    const int lane, wave;
+    const lds_ptr sm;        // the A buffers first, then the B buffers
+    const uint32_t sbase;
+    TileLoad<T, C::BM, C::waves, ACOLS> la;
+    TileLoad<T, C::BN, C::waves, BCOLS> lb;
+    FragRead<T, C::BM, ACOLS> ra;
+    FragRead<T, C::BN, BCOLS> rb;
+    int64_t a_end, b_end;    // K values of either operand
+    int s0, s1;              // K stages [s0, s1)
+
+    static constexpr int UA = decltype(la)::per_wave, D = UA + decltype(lb)::per_wave;   // copies per wave and stage
+    static constexpr int PER = (D + FM - 1) / FM;             // copies per step
+    static constexpr int TAIL = (STEPS - BS) * PER < D ? (STEPS - BS) * PER : D;   // copies that go out from BS on
+
+    __device__ __forceinline__ TilePipe(char *smem)
+        : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), sm((lds_ptr)smem),
+          sbase(uint32_t(reinterpret_cast<uintptr_t>(sm)))
+    {
+        ra.init(wave % C::WM * (C::BM / C::WM), lane);
+        rb.init(wave / C::WM * (C::BN / C::WN), lane);
+    }
+
+    __device__ __forceinline__ void request(int s, int buf)
+    {
         const uint32_t a = sbase + buf * C::a_bytes, b = sbase + NST * C::a_bytes + buf * C::b_bytes;
-        la.issue_tail(s, int(min(A.k_end - int64_t(s) * KI, int64_t(KI))), a, wave, lane);
-        lb.issue_tail(s, int(min(B.k_end - int64_t(s) * KI, int64_t(KI))), b, wave, lane);
-    };
-    auto copy = [&](int u, int s, int buf) {                  // copy u of whole stage s
+        la.issue_tail(s, int(min(a_end - int64_t(s) * KI, int64_t(KI))), a, wave, lane);
+        lb.issue_tail(s, int(min(b_end - int64_t(s) * KI, int64_t(KI))), b, wave, lane);
+    }
+    __device__ __forceinline__ void copy(int u, int s, int buf)      // copy u of whole stage s
+    {
         if (u < UA)
             la.issue(la.base + int64_t(s) * la.step, u, sbase + buf * C::a_bytes, wave);
         else
             lb.issue(lb.base + int64_t(s) * lb.step, u - UA, sbase + NST * C::a_bytes + buf * C::b_bytes, wave);
-    };
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-
-    uint4 ar[R], br[2][FN];
-    auto read_a = [&](int u, int buf) { ar[u % R] = ra.read(sm + buf * C::a_bytes, u % FM, u % STEPS / FM); };
-    auto read_b = [&](int j, int h, int buf) { br[h][j] = rb.read(sm + NST * C::a_bytes + buf * C::b_bytes, j, h); };
-
-#pragma unroll
-    for (int s = 0; s < NST; ++s)
-        if (s0 + s <= last) request(s0 + s, s);
-    if (last - s0 >= NST - 1)
-        wait_vm<D * (NST - 1)>();
-    else
-        wait_vm<0>();
-    stage_barrier();
-#pragma unroll
-    for (int j = 0; j < FN; ++j) read_b(j, 0, 0);
-#pragma unroll
-    for (int u = 0; u < LA; ++u) read_a(u, 0);
-    int buf = 0, prev = 0;
-    bool pending = false;                                     // copies TAIL .. of stage s - 1 + NST are left
-    for (int s = s0; s < s1; ++s) {
-        const int next = buf + 1 == NST ? 0 : buf + 1;
-        bool now = false;
-        extra.run(s, [&](int i, int h) { return ra.read(sm + buf * C::a_bytes, i, h); }, acc);
-#pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-            if (t == BS) {
-                if (NST > 2 && s + NST - 1 <= last)
-                    wait_vm<D * (NST - 2)>();
-                else
-                    wait_vm<0>();
-                stage_barrier();
-                now = s + NST <= last;
-                if (now && s + NST >= whole) {
-                    request(s + NST, buf);
-                    now = false;
-                }
-            }
-            if (t >= BS) {
-                if (now) {
-#pragma unroll
-                    for (int u = (t - BS) * PER; u < (t - BS + 1) * PER && u < TAIL; ++u) copy(u, s + NST, buf);
-                }
-            } else if (TAIL + t * PER < D) {
-                if (pending) {
-#pragma unroll
-                    for (int u = TAIL + t * PER; u < TAIL + (t + 1) * PER && u < D; ++u) copy(u, s - 1 + NST, prev);
-                }
-            }
-            // after the last stage the reads from `next` find no stage there: unused
-            if (t + LA < STEPS) read_a(t + LA, buf);
-            if (t == BS) {
-                read_a(STEPS, next);
-                read_a(STEPS + 1, next);
-            }
-            if (t > BS) read_a(t + LA, next);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if (t >= B1 && t < FM && j / 2 == t - B1) read_b(j, 1, buf);
-                if (t >= BS && j / 2 == t - BS) read_b(j, 0, next);
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[t % FM][j] = mfma_half<T>(ar[t % R], br[t / FM][j], acc[t % FM][j]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        pending = now;
-        prev = buf;
-        buf = next;
     }
-    wait_vm<0>();
-    stage_barrier();                       // the tiles' LDS is free for the epilogue
+
+    // The buffers are free (run() has ended or not begun).
+    __device__ __forceinline__ void start(const GemmOperand &A, const GemmOperand &B, int64_t m0, int64_t n0,
+                                          int first, int end)
+    {
+        s0 = first;
+        s1 = end;
+        a_end = A.k_end;
+        b_end = B.k_end;
+        la.init(static_cast<const char *>(A.p), A.ld, m0, A.count, wave, lane);
+        lb.init(static_cast<const char *>(B.p), B.ld, n0, B.count, wave, lane);
+#pragma unroll
+        for (int s = 0; s < NST; ++s)
+            if (s0 + s < s1) request(s0 + s, s);
+    }
+
+    // since: vector memory operations that each wave is known to have issued
+    // since start() (no more than it has). extra.run(s, read, acc) may add products
+    // of stage s's A fragments, read(i, h) for block i of half h.
+    template <int SINCE, typename Extra>
+    __device__ __forceinline__ void run(bool since, floatx4_t (&acc)[C::FM][C::FN], Extra &extra)
+    {
+        const int whole = int(min(a_end, b_end) / KI);        // stages that both operands fill
+        const int last = s1 - 1;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+        uint4 ar[R], br[2][FN];
+        auto read_a = [&](int u, int buf) { ar[u % R] = ra.read(sm + buf * C::a_bytes, u % FM, u % STEPS / FM); };
+        auto read_b = [&](int j, int h, int buf) { br[h][j] = rb.read(sm + NST * C::a_bytes + buf * C::b_bytes, j, h); };
+
+        static_assert(D * (NST - 1) + SINCE < 64, "wait count");
+        if (last - s0 < NST - 1)
+            wait_vm<0>();
+        else if (SINCE > 0 && since)
+            wait_vm<D * (NST - 1) + SINCE>();
+        else
+            wait_vm<D * (NST - 1)>();
+        stage_barrier();
+#pragma unroll
+        for (int j = 0; j < FN; ++j) read_b(j, 0, 0);
+#pragma unroll
+        for (int u = 0; u < LA; ++u) read_a(u, 0);
+        int buf = 0, prev = 0;
+        bool pending = false;                                 // copies TAIL .. of stage s - 1 + NST are left
+        for (int s = s0; s < s1; ++s) {
+            const int next = buf + 1 == NST ? 0 : buf + 1;
+            bool now = false;
+            extra.run(s, [&](int i, int h) { return ra.read(sm + buf * C::a_bytes, i, h); }, acc);
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+                if (t == BS) {
+                    if (NST > 2 && s + NST - 1 <= last)
+                        wait_vm<D * (NST - 2)>();
+                    else
+                        wait_vm<0>();
+                    stage_barrier();
+                    now = s + NST <= last;
+                    if (now && s + NST >= whole) {
+                        request(s + NST, buf);
+                        now = false;
+                    }
+                }
+                if (t >= BS) {
+                    if (now) {
+#pragma unroll
+                        for (int u = (t - BS) * PER; u < (t - BS + 1) * PER && u < TAIL; ++u) copy(u, s + NST, buf);
+                    }
+                } else if (TAIL + t * PER < D) {
+                    if (pending) {
+#pragma unroll
+                        for (int u = TAIL + t * PER; u < TAIL + (t + 1) * PER && u < D; ++u)
+                            copy(u, s - 1 + NST, prev);
+                    }
+                }
+                // after the last stage the reads from `next` find no stage there: unused
+                if (t + LA < STEPS) read_a(t + LA, buf);
+                if (t == BS) {
+                    read_a(STEPS, next);
+                    read_a(STEPS + 1, next);
+                }
+                if (t > BS) read_a(t + LA, next);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    if (t >= B1 && t < FM && j / 2 == t - B1) read_b(j, 1, buf);
+                    if (t >= BS && j / 2 == t - BS) read_b(j, 0, next);
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[t % FM][j] = mfma_half<T>(ar[t % R], br[t / FM][j], acc[t % FM][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            pending = now;
+            prev = buf;
+            buf = next;
+        }
+        wait_vm<0>();
+        stage_barrier();                   // no wave reads the buffers any more
+    }
+};
+
+// 8 consecutive values of m per lane instead of 4: blocks i and i + 1 of a column
+// exchanged between neighbouring rows of 16 lanes, so that a half-precision store
+// is 16 bytes. Afterwards lane row q holds m = 16(i + q%2) + 8(q/2) .. + 7.
+template <typename T>
+__device__ __forceinline__ uint4 pair_blocks(const floatx4_t &a, const floatx4_t &b)
+{
+    typedef T pair __attribute__((ext_vector_type(2)));
+    const auto pack = [](float u, float v) {
+        return __builtin_bit_cast(uint32_t, pair{static_cast<T>(u), static_cast<T>(v)});
+    };
+    const auto x = __builtin_amdgcn_permlane16_swap(pack(a[0], a[1]), pack(b[0], b[1]), false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(pack(a[2], a[3]), pack(b[2], b[3]), false, false);
+    return uint4{x[0], y[0], x[1], y[1]};
 }
 
 // workgroup -> (m, n) tile: each XCD gets a contiguous range of tiles, walked

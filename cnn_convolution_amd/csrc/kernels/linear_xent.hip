@@ -110,28 +110,36 @@ hipError_t with_type(int dtype, F f)
     return f(__bf16{});
 }
 
+// Time of one launch, from measurements of each tile shape (bf16 and fp32,
+// 8192 x 16384 outputs over K 512 .. 4096, and single workgroups over K 8192):
+// microseconds of a K stage with 1, 2, .. workgroups on a CU, and what a
+// workgroup adds per tile. Half precision at K = 512, 1024, 4096 (TFLOP/s):
+// 256 x 256 1079, 1168, 1418; 128 x 128 881, 984, 1163; 64 x 64 576, 669, 725;
+// a lone 64 x 64 workgroup takes 0.30 us a stage, 128 x 128 0.69, 256 x 256 1.28.
 struct Tile {
     int64_t m, n;
     int per_cu;              // workgroups a CU holds
-    double rate;             // of the CU's matrix rate when it holds that many
+    double half[3], f32[3];  // us per stage with 1, 2, 3 of them
+    double fixed;            // us per tile before its epilogue
 };
-constexpr Tile kTiles[4] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.75}, {64, 64, 3, 0.4}, {128, 16, 2, 0.1}};
+constexpr Tile kTiles[3] = {{256, 256, 1, {1.42, 0, 0}, {7.3, 0, 0}, 4.3},
+                            {128, 128, 2, {0.69, 0.88, 0}, {1.9, 3.7, 0}, 2.7},
+                            {64, 64, 3, {0.30, 0.42, 0.53}, {0.60, 1.0, 1.45}, 1.3}};
 constexpr int kCus = 256;
-// microseconds of one CU for a multiply-add count, and the least a stage takes
-// (its copies' latency)
-constexpr double kHalfRate = 4.5e6 / 2, kF32Rate = 0.55e6 / 2, kStageLatency = 0.6;
 
-// microseconds of a product of M x N outputs over `stages` K stages
-double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split, int dtype)
+// microseconds of a product of M x N outputs over `stages` K stages that leaves
+// out_bytes per output
+double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split, int dtype, int out_bytes)
 {
     const int64_t wgs = ceil_div(M, t.m) * ceil_div(N, t.n) * split;
-    const int64_t ki = 128 / elem(dtype);
-    const double rounds = double(ceil_div(wgs, int64_t(kCus) * t.per_cu));
-    // a launch of few workgroups leaves a CU fewer to run at a time
-    const double held = double(std::min<int64_t>(t.per_cu, ceil_div(wgs, kCus)));
-    const double rate = dtype == 0 ? kF32Rate : kHalfRate * t.rate;
-    const double stage = std::max(held * double(t.m * t.n * ki) / rate, kStageLatency);
-    return rounds * stage * double(ceil_div(stages, split));
+    const int held = int(std::min<int64_t>(t.per_cu, ceil_div(wgs, kCus)));
+    const double rounds = double(ceil_div(wgs, int64_t(kCus) * held));
+    const double stage = (dtype == 0 ? t.f32 : t.half)[held - 1];
+    // an epilogue: 7 us for 65536 exponentials on a CU, or its stores at a CU's
+    // share of the memory bandwidth; half of it hidden by a neighbour's products
+    const double outputs = double(held * t.m * t.n);
+    const double epilogue = std::max(outputs * 7.0 / 65536, outputs * out_bytes / 2e4) * (held > 1 ? 0.5 : 1.0);
+    return rounds * (stage * double(ceil_div(stages, split)) + t.fixed + epilogue);
 }
 
 constexpr int64_t kSlabBytes = int64_t(256) << 20;
@@ -143,9 +151,9 @@ void pick_product(int64_t M, int64_t N, int64_t stages, int dtype, int *tile, in
     for (int t = 0; t < 3; ++t)
         for (int sp = 1; sp <= 64; sp *= 2) {
             if (sp > 1 && (stages / sp < 4 || int64_t(sp) * M * N * 4 > kSlabBytes)) break;
-            // the slabs are written and read once, at about 3 TB/s
-            const double us = product_us(kTiles[t], M, N, stages, sp, dtype) +
-                              (sp > 1 ? 4.0 + double(sp) * double(M) * double(N) * 8 / 3e6 : 0.0);
+            // the slabs are read once more, at about 3 TB/s, by a launch of their own
+            const double us = product_us(kTiles[t], M, N, stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
+                              (sp > 1 ? 5.0 + double(sp) * double(M) * double(N) * 4 / 3e6 : 0.0);
             if (us < best * 0.98) {
                 best = us;
                 *tile = t;
@@ -160,7 +168,7 @@ int pick_logits(int64_t M, int64_t N, int64_t stages, int dtype, bool narrow)
     double best = 1e30;
     int tile = 0;
     for (int t = 0; t < 3; ++t) {
-        const double us = product_us(kTiles[t], M, N, stages, 1, dtype);
+        const double us = product_us(kTiles[t], M, N, stages, 1, dtype, narrow ? 0 : int(elem(dtype)));
         if (us < best * 0.98) {
             best = us;
             tile = t;
@@ -195,7 +203,7 @@ XentPlan plan_xent_fwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw
     if (N == 0) return p;
     const int64_t es = elem(dtype);
     p.logits_tile = pick_logits(V, N, ceil_div(p.Dp * es, 128), dtype, true);
-    p.tiles_v = ceil_div(V, kTiles[p.logits_tile].m);
+    p.tiles_v = ceil_div(V, p.logits_tile == kTileNarrow ? 128 : kTiles[p.logits_tile].m);
     if (p.copy_x) p.off_x = take(p, N * p.Dp * es);
     if (p.copy_w) p.off_w = take(p, V * p.Dp * es);
     p.off_partial = take(p, p.tiles_v * N * 8);

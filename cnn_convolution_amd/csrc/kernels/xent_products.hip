@@ -10,6 +10,7 @@
 // target falls into it).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../xent.hpp"
@@ -76,93 +77,155 @@ struct LowExtra {
 };
 
 template <typename T, typename C, bool DW>
-__global__ __launch_bounds__(C::threads) void xent_product_kernel(const ProductArgs a, int tiles_m, int tiles_n)
+__global__ __launch_bounds__(C::threads, C::per_simd) void xent_product_kernel(const ProductArgs a, int tiles_m, int tiles_n)
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    constexpr int KI = 128 / int(sizeof(T));
-    const int tiles = tiles_m * tiles_n;
-    const int part = blockIdx.x / tiles, b = blockIdx.x - part * tiles;
-    int tm, tn;
-    strip_tile(b, tiles_m, tiles_n, tm, tn);
-    const int64_t m0 = int64_t(tm) * C::BM, n0 = int64_t(tn) * C::BN;
+    constexpr int KI = 128 / int(sizeof(T)), E = 16 / int(sizeof(T));   // w's and x's rows are whole granules
+    constexpr bool HALF = sizeof(T) == 2;
+    constexpr int STORES = HALF ? C::FM * C::FN / 2 : C::FM * C::FN;    // of a wave and whole tile, at least
+    const int tiles = tiles_m * tiles_n, all = tiles * a.split;
     const int nk = int((a.K + KI - 1) / KI);
-    const int s0 = int(int64_t(nk) * part / a.split), s1 = int(int64_t(nk) * (part + 1) / a.split);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
-    const int nw = wn * (C::BN / C::WN);
-    floatx4_t acc[C::FM][C::FN];
-
-    constexpr int E = 16 / int(sizeof(T));        // w's and x's rows are whole granules
+    const int mw = wm * (C::BM / C::WM), nw = wn * (C::BN / C::WN);
+    const float inv = a.scale ? a.scale[1] : 1.f;
     const GemmOperand A{a.a, a.lda, (a.M + E - 1) / E * E, a.k_a};
     const GemmOperand B{a.b, a.ldb, DW ? a.ldb / int64_t(sizeof(T)) : a.n, a.k_b};
-    if constexpr (DW && sizeof(T) == 2) {
-        LowExtra<T, C> low{a, n0 + nw, s0, nk, lane};
-        tile_product<T, C, true, DW>(A, B, m0, n0, s0, s1, smem, acc, low);
-    } else {
-        NoExtra none;
-        tile_product<T, C, true, DW>(A, B, m0, n0, s0, s1, smem, acc, none);
-    }
-
-    const float inv = a.scale ? a.scale[1] : 1.f;
-    const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-        const int64_t row = n0 + nw + 16 * j + (lane & 15);
-        if (row >= a.n) continue;
-        int t = 0;
-        float lv = 0.f;
-        if constexpr (!DW) {
-            if (!a.slab) {
-                t = a.t32[row];
-                if (sizeof(T) == 2 && t >= 0) lv = static_cast<float>(static_cast<const T *>(a.low)[row]);
-            }
+    TilePipe<T, C, true, DW> pipe(smem);
+    int part = 0;
+    int64_t m0 = 0, n0 = 0;
+    auto start = [&](int t) {
+        int tm, tn;
+        part = t / tiles;
+        strip_tile(t - part * tiles, tiles_m, tiles_n, tm, tn);
+        m0 = int64_t(tm) * C::BM;
+        n0 = int64_t(tn) * C::BN;
+        pipe.start(A, B, m0, n0, int(int64_t(nk) * part / a.split), int(int64_t(nk) * (part + 1) / a.split));
+    };
+    // dw in half precision has no registers left for the next tile's addresses: its
+    // launch has a workgroup for every tile
+    constexpr bool ONE = DW && HALF;
+    start(blockIdx.x);
+    bool stored = false;                       // the last epilogue stored a whole tile
+    for (int t = blockIdx.x; t < all; t += ONE ? all : int(gridDim.x)) {
+        const int cur = part;
+        const int64_t mt = m0 + mw, nt = n0 + nw;
+        floatx4_t acc[C::FM][C::FN];
+        if constexpr (DW && HALF) {
+            LowExtra<T, C> low{a, nt, pipe.s0, nk, lane};
+            pipe.template run<STORES>(stored, acc, low);
+        } else {
+            NoExtra none;
+            pipe.template run<STORES>(stored, acc, none);
         }
+        if constexpr (!ONE) {
+            stored = m0 + C::BM <= a.M && n0 + C::BN <= a.n;
+            if (t + int(gridDim.x) < all) start(t + gridDim.x);
+        }
+
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            const int64_t m = m0 + mw + i * 16;
-            const int left = int(min(int64_t(4), a.M - m));
-            if (left <= 0) continue;
-            float q[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        for (int j = 0; j < C::FN; ++j) {
+            const int64_t row = nt + 16 * j + (lane & 15);
+            if (row >= a.n) continue;
             if (a.slab) {
-                float *o = a.slab + (int64_t(part) * a.n + row) * a.M + m;
-                if (a.add) {
-                    float p[4];
-                    load_some<4>(o, left, p);
+                float *o = a.slab + (int64_t(cur) * a.n + row) * a.M;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) q[v] += p[v];
+                for (int i = 0; i < C::FM; ++i) {
+                    const int64_t m = mt + i * 16 + (lane >> 4) * 4, left = a.M - m;
+                    if (left <= 0) continue;
+                    float q[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    if (a.add) {
+                        float p[4];
+                        load_some<4>(o + m, left, p);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) q[v] += p[v];
+                    }
+                    store_some<4>(o + m, left, q);
                 }
-                store_some<4>(o, left, q);
-            } else {
-                if (!DW && sizeof(T) == 2 && t >= 0) {
+                continue;
+            }
+            int tgt = 0;
+            float lv = 0.f;
+            if constexpr (!DW) {
+                tgt = a.t32[row];
+                if (HALF && tgt >= 0) lv = static_cast<float>(static_cast<const T *>(a.low)[row]);
+            }
+            const T *wt = reinterpret_cast<const T *>(static_cast<const char *>(a.w) + tgt * a.ldw);
+            T *o = static_cast<T *>(a.out) + row * a.M;
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                if (!DW && HALF && tgt >= 0) {
+                    const int64_t m = mt + i * 16 + (lane >> 4) * 4;
                     float wv[4];
-                    load_some<4>(reinterpret_cast<const T *>(static_cast<const char *>(a.w) + t * a.ldw) + m, left,
-                                 wv);
+                    load_some<4>(wt + m, a.M - m, wv);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) q[v] += lv * wv[v];
+                    for (int v = 0; v < 4; ++v) acc[i][j][v] += lv * wv[v];
                 }
 #pragma unroll
-                for (int v = 0; v < 4; ++v) q[v] = t >= 0 ? q[v] * inv : 0.f;
-                store_some<4>(static_cast<T *>(a.out) + row * a.M + m, left, q);
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = tgt >= 0 ? acc[i][j][v] * inv : 0.f;
+            }
+            if constexpr (HALF) {
+                const int64_t m8 = mt + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+#pragma unroll
+                for (int i = 0; i < C::FM; i += 2) {
+                    const uint4 q = pair_blocks<T>(acc[i][j], acc[i + 1][j]);
+                    store_some_raw(o + m8 + i * 16, a.M - m8 - i * 16, __builtin_bit_cast(Raw<T, 8>, q));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i) {
+                    const int64_t m = mt + i * 16 + (lane >> 4) * 4;
+                    const float q[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    store_some<4>(o + m, a.M - m, q);
+                }
             }
         }
     }
 }
 
-// the slabs of [n][M] added in order, for dx with the rounding residual
-template <typename T, bool DW>
+// The slabs of [n][M] added in a fixed order, for dx with the rounding residual:
+// a workgroup takes 256 / Q chunks of 4 outputs, Q threads a chunk, thread q slabs
+// q, q + Q, .. (few outputs and many slabs would leave most of the chip idle)
+template <typename T, bool DW, int Q>
 __global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs a)
 {
+    __shared__ float4 sum[Q > 1 ? 256 : 1];
+    constexpr int CH = 256 / Q;
     const int64_t chunks = (a.M + 3) / 4, total = a.n * chunks;
     const float inv = a.scale ? a.scale[1] : 1.f;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-        const int64_t row = i / chunks, m = (i - row * chunks) * 4;
-        const int left = int(min(int64_t(4), a.M - m));
-        float q[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int p = 0; p < a.split; ++p) {
-            float f[4];
-            load_some<4>(a.slab + (int64_t(p) * a.n + row) * a.M + m, left, f);
+    const int k = threadIdx.x % CH, q = threadIdx.x / CH;
+    for (int64_t i0 = int64_t(blockIdx.x) * CH; i0 < total; i0 += int64_t(gridDim.x) * CH) {
+        const int64_t i = min(i0 + k, total - 1);
+        const int64_t row = i / chunks, m = (i - row * chunks) * 4, left = a.M - m;
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        const float *src = a.slab + row * a.M + m;
+        const int64_t step = a.n * a.M;
+        if (left >= 4) {
+#pragma unroll 4
+            for (int p = q; p < a.split; p += Q) {
+                float g[4];
+                load_vec<4>(src + p * step, g);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) q[v] += f[v];
+                for (int v = 0; v < 4; ++v) f[v] += g[v];
+            }
+        } else {
+            for (int p = q; p < a.split; p += Q)
+                for (int v = 0; v < left; ++v) f[v] += src[p * step + v];
         }
+        if constexpr (Q > 1) {
+            __syncthreads();
+            sum[threadIdx.x] = float4{f[0], f[1], f[2], f[3]};
+            __syncthreads();
+            if (q > 0) continue;
+#pragma unroll
+            for (int p = 1; p < Q; ++p) {
+                const float4 g = sum[p * CH + k];
+                f[0] += g.x;
+                f[1] += g.y;
+                f[2] += g.z;
+                f[3] += g.w;
+            }
+        }
+        if (i0 + k >= total) continue;
         int t = 0;
         if constexpr (!DW) {
             t = a.t32[row];
@@ -171,18 +234,14 @@ __global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs 
                 float wv[4];
                 load_some<4>(reinterpret_cast<const T *>(static_cast<const char *>(a.w) + t * a.ldw) + m, left, wv);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) q[v] += lv * wv[v];
+                for (int v = 0; v < 4; ++v) f[v] += lv * wv[v];
             }
         }
 #pragma unroll
-        for (int v = 0; v < 4; ++v) q[v] = t >= 0 ? q[v] * inv : 0.f;
-        store_some<4>(static_cast<T *>(a.out) + row * a.M + m, left, q);
+        for (int v = 0; v < 4; ++v) f[v] = t >= 0 ? f[v] * inv : 0.f;
+        store_some<4>(static_cast<T *>(a.out) + row * a.M + m, left, f);
     }
 }
-
-using C256 = TileCfg<256, 256, 2, 4, 2>;
-using C128 = TileCfg<128, 128, 2, 2, 2>;
-using C64 = TileCfg<64, 64, 2, 2, 3>;
 
 template <typename T, typename C, bool DW>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
@@ -190,11 +249,12 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
     const auto kernel = xent_product_kernel<T, C, DW>;
     const int64_t tm = (a.M + C::BM - 1) / C::BM, tn = (a.n + C::BN - 1) / C::BN;
     if (tm * tn * a.split > INT32_MAX) return hipErrorInvalidValue;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, C::lds_bytes);
+    static std::atomic<uint64_t> allowed{0};
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(unsigned(tm * tn * a.split)), dim3(C::threads), C::lds_bytes, s, a, int(tm),
-                       int(tn));
+    const int64_t all = tm * tn * a.split;
+    const int64_t grid = DW && sizeof(T) == 2 ? all : std::min(all, int64_t(C::per_cu) * 256);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), C::lds_bytes, s, a, int(tm), int(tn));
     return hipGetLastError();
 }
 
@@ -220,9 +280,14 @@ template <bool DW>
 hipError_t launch_join(const ProductArgs &a, int dtype, hipStream_t s)
 {
     const int64_t total = a.n * ((a.M + 3) / 4);
-    const dim3 grid(unsigned(total / 256 + 1 < 4096 ? total / 256 + 1 : 4096));
     return with_type<DW>(dtype, [&](auto t) {
-        hipLaunchKernelGGL((xent_join_slabs_kernel<decltype(t), DW>), grid, dim3(256), 0, s, a);
+        if (a.split >= 8 && total < 65536) {
+            const dim3 grid(unsigned((total + 15) / 16));
+            hipLaunchKernelGGL((xent_join_slabs_kernel<decltype(t), DW, 16>), grid, dim3(256), 0, s, a);
+        } else {
+            const dim3 grid(unsigned(std::min<int64_t>((total + 255) / 256, 8192)));
+            hipLaunchKernelGGL((xent_join_slabs_kernel<decltype(t), DW, 1>), grid, dim3(256), 0, s, a);
+        }
         return hipGetLastError();
     });
 }

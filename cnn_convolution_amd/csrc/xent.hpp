@@ -3,11 +3,26 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "head_launch.hpp"
 
 namespace im2win {
+
+// lets `kernel` take `bytes` of dynamic LDS on the current device, once per
+// device (`done` has a bit for each)
+inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    const hipError_t e2 = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e2 == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e2;
+}
 
 // tile shapes of the products (classes or features x rows or classes)
 enum XentTile { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileNarrow = 3 };
