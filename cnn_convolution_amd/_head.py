@@ -53,11 +53,21 @@ def lib() -> ctypes.CDLL:
     return _bound
 
 
+_functions = {}
+
+
+def _function(name):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    return f
+
+
 def call(name: str, desc, *args) -> None:
-    st = getattr(lib(), name)(ctypes.byref(desc), *args)
+    st = _function(name)(desc, *args)
     if st != 0:
         raise _lib.Conv2dError(st, name)
 
 
 def size(name: str, desc) -> int:
-    return int(getattr(lib(), name)(ctypes.byref(desc)))
+    return _function(name)(desc)

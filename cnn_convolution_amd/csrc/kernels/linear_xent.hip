@@ -47,17 +47,18 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const 
     }
 }
 
-// S: the power of two with S * max |grad| in [2^14, 2^15]
-__global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, int64_t N, float *scale)
+// S: the power of two with S * max |grad| in [2^14, 2^15], by one workgroup
+template <int THREADS>
+__device__ __forceinline__ void grad_scale(const float *grad, int64_t N, float *scale)
 {
-    __shared__ float red[16];
+    __shared__ float red[THREADS / 64];
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < N; i += 1024) m = fmaxf(m, fabsf(grad[i]));
+    for (int64_t i = threadIdx.x; i < N; i += THREADS) m = fmaxf(m, fabsf(grad[i]));
     for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w]);
+        for (int w = 1; w < THREADS / 64; ++w) m = fmaxf(m, red[w]);
         int e = 0;
         const bool ok = m > 0.f && m < __builtin_inff();
         if (ok) (void)frexpf(m, &e);
@@ -67,13 +68,23 @@ __global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, int
     }
 }
 
+__global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, int64_t N, float *scale)
+{
+    grad_scale<1024>(grad, N, scale);
+}
+
 // rows copied to whole granules (the padding cleared), one wave per row; with
-// targets also t32 (rows up to rows_pad), and masked rows copied as zeros
+// targets also t32 (rows up to rows_pad), and masked rows copied as zeros; with
+// grad the last workgroup finds the scale instead
 template <typename T>
 __global__ __launch_bounds__(256) void xent_rows_kernel(const T *src, int64_t ld, int64_t rows, int64_t D, int64_t Dp,
                                                         T *dst, const int64_t *target, int64_t V, int64_t rows_pad,
-                                                        int *t32)
+                                                        int *t32, const float *grad, float *scale)
 {
+    if (grad && blockIdx.x == gridDim.x - 1) {
+        grad_scale<256>(grad, rows, scale);
+        return;
+    }
     const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     constexpr int E = 16 / int(sizeof(T));
@@ -262,14 +273,14 @@ hipError_t launch_xent_fwd(const XentArgs &a, hipStream_t s)
             l.r.ldx = p.Dp * es;
             hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(ceil_div(a.N, 4))), dim3(256), 0, s,
                                static_cast<const T *>(a.x), a.ldx, a.N, a.D, p.Dp,
-                               reinterpret_cast<T *>(ws + p.off_x), nullptr, a.V, 0, nullptr);
+                               reinterpret_cast<T *>(ws + p.off_x), nullptr, a.V, 0, nullptr, nullptr, nullptr);
         }
         if (p.copy_w) {
             l.r.w = ws + p.off_w;
             l.r.ldw = p.Dp * es;
             hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(ceil_div(a.V, 4))), dim3(256), 0, s,
                                static_cast<const T *>(a.w), a.ldw, a.V, a.D, p.Dp,
-                               reinterpret_cast<T *>(ws + p.off_w), nullptr, a.V, 0, nullptr);
+                               reinterpret_cast<T *>(ws + p.off_w), nullptr, a.V, 0, nullptr, nullptr, nullptr);
         }
         return hipGetLastError();
     });
@@ -305,16 +316,18 @@ hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
     XentRows r{ws + p.off_x, a.w, p.Dp * es, a.ldw * es};
     hipError_t e = with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
-        if (scale) hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad, a.N, scale);
-        hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(p.rows_pad / 4)), dim3(256), 0, s,
+        // a workgroup of the copy has time for some tens of thousands of gradients
+        const bool with_rows = scale && a.N <= 32768;
+        if (scale && !with_rows) hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad, a.N, scale);
+        hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(p.rows_pad / 4 + (with_rows ? 1 : 0))), dim3(256), 0, s,
                            static_cast<const T *>(a.x), a.ldx, a.N, a.D, p.Dp, reinterpret_cast<T *>(ws + p.off_x),
-                           a.target, a.V, p.rows_pad, t32);
+                           a.target, a.V, p.rows_pad, t32, with_rows ? a.grad : nullptr, scale);
         if (p.copy_w) {
             r.w = ws + p.off_w;
             r.ldw = p.Dp * es;
             hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(ceil_div(a.V, 4))), dim3(256), 0, s,
                                static_cast<const T *>(a.w), a.ldw, a.V, a.D, p.Dp,
-                               reinterpret_cast<T *>(ws + p.off_w), nullptr, a.V, 0, nullptr);
+                               reinterpret_cast<T *>(ws + p.off_w), nullptr, a.V, 0, nullptr, nullptr, nullptr);
         }
         return hipGetLastError();
     });
@@ -353,15 +366,23 @@ hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
         dx.add = v0 > 0;
         // a last piece of few stages: no part without one
         dx.split = int(std::min<int64_t>(p.dx_split, ceil_div(P, ki)));
-        if ((e = launch_xent_dx(dx, a.dtype, p.dx_tile, s)) != hipSuccess) return e;
         dw.n = P;
         dw.v0 = v0;
         dw.out = static_cast<char *>(a.dw) + v0 * a.D * es;
-        if ((e = launch_xent_dw(dw, a.dtype, p.dw_tile, s)) != hipSuccess) return e;
-        if (dw.slab && (e = launch_xent_dw_join(dw, a.dtype, s)) != hipSuccess) return e;
+        if (p.dx_tile == kTile64 && p.dw_tile == kTile64) {
+            if ((e = launch_xent_both(dx, dw, a.dtype, s)) != hipSuccess) return e;
+        } else {
+            if ((e = launch_xent_dx(dx, a.dtype, p.dx_tile, s)) != hipSuccess) return e;
+            if ((e = launch_xent_dw(dw, a.dtype, p.dw_tile, s)) != hipSuccess) return e;
+        }
+        const bool done = v0 + P == a.V;
+        dx.split = p.dx_split;
+        if (dw.slab || (done && dx.slab)) {
+            e = launch_xent_join(done && dx.slab ? &dx : nullptr, dw.slab ? &dw : nullptr, a.dtype, s);
+            if (e != hipSuccess) return e;
+        }
     }
-    dx.split = p.dx_split;
-    return dx.slab ? launch_xent_dx_join(dx, a.dtype, s) : hipSuccess;
+    return hipSuccess;
 }
 
 }  // namespace im2win

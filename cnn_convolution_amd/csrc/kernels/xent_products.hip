@@ -76,10 +76,11 @@ struct LowExtra {
     }
 };
 
+// tiles begin, begin + step, .. of one product
 template <typename T, typename C, bool DW>
-__global__ __launch_bounds__(C::threads, C::per_simd) void xent_product_kernel(const ProductArgs a, int tiles_m, int tiles_n)
+__device__ __forceinline__ void product_tiles(const ProductArgs &a, int tiles_m, int tiles_n, int begin, int step,
+                                              char *smem)
 {
-    extern __shared__ __attribute__((aligned(16))) char smem[];
     constexpr int KI = 128 / int(sizeof(T)), E = 16 / int(sizeof(T));   // w's and x's rows are whole granules
     constexpr bool HALF = sizeof(T) == 2;
     constexpr int STORES = HALF ? C::FM * C::FN / 2 : C::FM * C::FN;    // of a wave and whole tile, at least
@@ -104,9 +105,9 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_product_kernel(c
     // dw in half precision has no registers left for the next tile's addresses: its
     // launch has a workgroup for every tile
     constexpr bool ONE = DW && HALF;
-    start(blockIdx.x);
+    start(begin);
     bool stored = false;                       // the last epilogue stored a whole tile
-    for (int t = blockIdx.x; t < all; t += ONE ? all : int(gridDim.x)) {
+    for (int t = begin; t < all; t += ONE ? all : step) {
         const int cur = part;
         const int64_t mt = m0 + mw, nt = n0 + nw;
         floatx4_t acc[C::FM][C::FN];
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_product_kernel(c
         }
         if constexpr (!ONE) {
             stored = m0 + C::BM <= a.M && n0 + C::BN <= a.n;
-            if (t + int(gridDim.x) < all) start(t + gridDim.x);
+            if (t + step < all) start(t + step);
         }
 
 #pragma unroll
@@ -182,18 +183,39 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_product_kernel(c
     }
 }
 
+template <typename T, typename C, bool DW>
+__global__ __launch_bounds__(C::threads, C::per_simd) void xent_product_kernel(const ProductArgs a, int tiles_m,
+                                                                               int tiles_n)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    product_tiles<T, C, DW>(a, tiles_m, tiles_n, blockIdx.x, gridDim.x, smem);
+}
+
+// dx and dw of a small step in one launch, a workgroup per tile: neither fills the
+// chip and both need only G
+template <typename T, typename C>
+__global__ __launch_bounds__(C::threads, C::per_simd) void xent_both_kernel(const ProductArgs dx, const ProductArgs dw,
+                                                                            int dx_m, int dx_n, int dw_m, int dw_n)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int n = dx_m * dx_n * dx.split, b = blockIdx.x;
+    if (b < n)
+        product_tiles<T, C, false>(dx, dx_m, dx_n, b, n, smem);
+    else
+        product_tiles<T, C, true>(dw, dw_m, dw_n, b - n, dw_m * dw_n * dw.split, smem);
+}
+
 // The slabs of [n][M] added in a fixed order, for dx with the rounding residual:
 // a workgroup takes 256 / Q chunks of 4 outputs, Q threads a chunk, thread q slabs
 // q, q + Q, .. (few outputs and many slabs would leave most of the chip idle)
 template <typename T, bool DW, int Q>
-__global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs a)
+__device__ __forceinline__ void join_slabs(const ProductArgs &a, int block, int blocks, float4 *sum)
 {
-    __shared__ float4 sum[Q > 1 ? 256 : 1];
     constexpr int CH = 256 / Q;
     const int64_t chunks = (a.M + 3) / 4, total = a.n * chunks;
     const float inv = a.scale ? a.scale[1] : 1.f;
     const int k = threadIdx.x % CH, q = threadIdx.x / CH;
-    for (int64_t i0 = int64_t(blockIdx.x) * CH; i0 < total; i0 += int64_t(gridDim.x) * CH) {
+    for (int64_t i0 = int64_t(block) * CH; i0 < total; i0 += int64_t(blocks) * CH) {
         const int64_t i = min(i0 + k, total - 1);
         const int64_t row = i / chunks, m = (i - row * chunks) * 4, left = a.M - m;
         float f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -243,6 +265,17 @@ __global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs 
     }
 }
 
+template <typename T, int Q>
+__global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs dx, const ProductArgs dw, int dx_blocks)
+{
+    __shared__ float4 sum[Q > 1 ? 256 : 1];
+    const int b = blockIdx.x;
+    if (b < dx_blocks)
+        join_slabs<T, false, Q>(dx, b, dx_blocks, sum);
+    else
+        join_slabs<T, true, Q>(dw, b - dx_blocks, gridDim.x - dx_blocks, sum);
+}
+
 template <typename T, typename C, bool DW>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
 {
@@ -268,7 +301,7 @@ hipError_t launch_product(const ProductArgs &a, int tile, hipStream_t s)
     }
 }
 
-template <bool DW, typename F>
+template <typename F>
 hipError_t with_type(int dtype, F f)
 {
     if (dtype == 0) return f(float{});
@@ -276,35 +309,60 @@ hipError_t with_type(int dtype, F f)
     return f(__bf16{});
 }
 
-template <bool DW>
-hipError_t launch_join(const ProductArgs &a, int dtype, hipStream_t s)
-{
-    const int64_t total = a.n * ((a.M + 3) / 4);
-    return with_type<DW>(dtype, [&](auto t) {
-        if (a.split >= 8 && total < 65536) {
-            const dim3 grid(unsigned((total + 15) / 16));
-            hipLaunchKernelGGL((xent_join_slabs_kernel<decltype(t), DW, 16>), grid, dim3(256), 0, s, a);
-        } else {
-            const dim3 grid(unsigned(std::min<int64_t>((total + 255) / 256, 8192)));
-            hipLaunchKernelGGL((xent_join_slabs_kernel<decltype(t), DW, 1>), grid, dim3(256), 0, s, a);
-        }
-        return hipGetLastError();
-    });
-}
-
 }  // namespace
 
 hipError_t launch_xent_dx(const ProductArgs &a, int dtype, int tile, hipStream_t s)
 {
-    return with_type<false>(dtype, [&](auto t) { return launch_product<decltype(t), false>(a, tile, s); });
+    return with_type(dtype, [&](auto t) { return launch_product<decltype(t), false>(a, tile, s); });
 }
 
 hipError_t launch_xent_dw(const ProductArgs &a, int dtype, int tile, hipStream_t s)
 {
-    return with_type<true>(dtype, [&](auto t) { return launch_product<decltype(t), true>(a, tile, s); });
+    return with_type(dtype, [&](auto t) { return launch_product<decltype(t), true>(a, tile, s); });
 }
 
-hipError_t launch_xent_dx_join(const ProductArgs &a, int dtype, hipStream_t s) { return launch_join<false>(a, dtype, s); }
-hipError_t launch_xent_dw_join(const ProductArgs &a, int dtype, hipStream_t s) { return launch_join<true>(a, dtype, s); }
+hipError_t launch_xent_both(const ProductArgs &dx, const ProductArgs &dw, int dtype, hipStream_t s)
+{
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        using C = C64;
+        const auto kernel = xent_both_kernel<T, C>;
+        const int64_t xm = (dx.M + C::BM - 1) / C::BM, xn = (dx.n + C::BN - 1) / C::BN;
+        const int64_t wm = (dw.M + C::BM - 1) / C::BM, wn = (dw.n + C::BN - 1) / C::BN;
+        const int64_t grid = xm * xn * dx.split + wm * wn * dw.split;
+        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        static std::atomic<uint64_t> allowed{0};
+        const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), C::lds_bytes, s, dx, dw, int(xm), int(xn),
+                           int(wm), int(wn));
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_xent_join(const ProductArgs *dx, const ProductArgs *dw, int dtype, hipStream_t s)
+{
+    int64_t blocks[2] = {0, 0}, most = 0;
+    bool few = true;
+    const ProductArgs *all[2] = {dx, dw};
+    for (int k = 0; k < 2; ++k)
+        if (all[k]) {
+            blocks[k] = all[k]->n * ((all[k]->M + 3) / 4);      // chunks of 4 outputs
+            most = std::max(most, blocks[k]);
+            few = few && all[k]->split >= 8;
+        }
+    few = few && most < 65536;
+    for (int64_t &b : blocks) b = std::min<int64_t>(few ? (b + 15) / 16 : (b + 255) / 256, 8192);
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        const ProductArgs none{}, &x = dx ? *dx : none, &w = dw ? *dw : none;
+        const dim3 grid(unsigned(blocks[0] + blocks[1]));
+        if (few)
+            hipLaunchKernelGGL((xent_join_slabs_kernel<T, 16>), grid, dim3(256), 0, s, x, w, int(blocks[0]));
+        else
+            hipLaunchKernelGGL((xent_join_slabs_kernel<T, 1>), grid, dim3(256), 0, s, x, w, int(blocks[0]));
+        return hipGetLastError();
+    });
+}
 
 }  // namespace im2win

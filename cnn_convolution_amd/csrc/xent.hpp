@@ -90,8 +90,9 @@ struct ProductArgs {
 };
 hipError_t launch_xent_dx(const ProductArgs &a, int dtype, int tile, hipStream_t s);
 hipError_t launch_xent_dw(const ProductArgs &a, int dtype, int tile, hipStream_t s);
-// the slabs added, in order, into out
-hipError_t launch_xent_dx_join(const ProductArgs &a, int dtype, hipStream_t s);
-hipError_t launch_xent_dw_join(const ProductArgs &a, int dtype, hipStream_t s);
+// both with 64 x 64 tiles
+hipError_t launch_xent_both(const ProductArgs &dx, const ProductArgs &dw, int dtype, hipStream_t s);
+// the slabs added, in order, into out; either may be null
+hipError_t launch_xent_join(const ProductArgs *dx, const ProductArgs *dw, int dtype, hipStream_t s);
 
 }  // namespace im2win

@@ -22,54 +22,63 @@ __all__ = ["dropout", "dropout_into", "layer_norm", "layer_norm_into", "layer_no
            "linear_cross_entropy_workspace_size"]
 
 _codes = None
+_raw_stream = None
+
+
+def _torch_names() -> None:
+    """What the calls below need of torch, looked up once."""
+    global _codes, _raw_stream, _F32, _I64
+    import torch
+    _F32, _I64 = torch.float32, torch.int64
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _codes = {torch.float32: _lib.F32, torch.float16: _lib.F16, torch.bfloat16: _lib.BF16}
 
 
 def _code(dtype) -> int:
-    global _codes
     if _codes is None:
-        import torch
-        _codes = {torch.float32: _lib.F32, torch.float16: _lib.F16, torch.bfloat16: _lib.BF16}
+        _torch_names()
     try:
         return _codes[dtype]
     except KeyError:
         raise TypeError(f"unsupported dtype {dtype}") from None
 
 
-def _stream(t) -> int:
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _device(t, name, like=None):
+def _device(t, name) -> int:
+    """The device index of a device tensor."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} must be on the device of x")
+    return t.get_device()
 
 
-def _vector(t, name, n, like, dtype="torch.float32"):
-    """The pointer of a contiguous vector of n elements (None stays None)."""
+def _vector(t, name, n, dev, dtype=None):
+    """The pointer of a contiguous vector of n elements, fp32 unless said (None
+    stays None)."""
     if t is None:
         return None
-    _device(t, name, like)
-    if str(t.dtype) != dtype or t.numel() != n or not t.is_contiguous():
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on the device of x")
+    dtype = dtype or _F32
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
     return t.data_ptr()
 
 
-def _contiguous(t, name, shape, dtype, like):
-    _device(t, name, like)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+def _contiguous(t, name, shape, dtype, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on the device of x")
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _workspace(ws, need, like):
+def _workspace(ws, need, dev):
     if need == 0:
         return None
     if ws is None:
-        raise ValueError(f"a workspace of {need} bytes is needed")
-    _device(ws, "ws", like)
+        raise ValueError(f"a workspace (ws) of {need} bytes is needed")
+    if ws.get_device() != dev:
+        raise ValueError("ws must be a device tensor on the device of x")
     if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws must be contiguous with at least {need} bytes")
     return ws.data_ptr()
@@ -84,12 +93,12 @@ def _bytes(n, like):
 
 def dropout_into(x, y, p: float, seed: int, offset: int = 0) -> None:
     """y = dropout(x), both contiguous (y may be x)."""
-    _device(x, "x")
+    dev = _device(x, "x")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    out = _contiguous(y, "y", x.shape, x.dtype, x)
     d = DropoutDesc(x.numel(), _code(x.dtype), 0, p, seed, offset)
-    _head.call("dropout_fwd", d, x.data_ptr(), out, _stream(x))
+    out = _contiguous(y, "y", x.shape, x.dtype, dev)
+    _head.call("dropout_fwd", d, x.data_ptr(), out, _raw_stream(dev))
 
 
 def dropout(x, p: float, seed: int, offset: int = 0):
@@ -130,49 +139,49 @@ def _rows(t, name):
 
 
 def _norm_desc(x, layout, y_dtype, eps, dropout_p, seed, offset):
-    """(descriptor, shape of mean and rstd)"""
+    """(descriptor, number of positions)"""
     lay = _lib.NCHW if layout == "nchw" else _lib.NHWC if layout == "nhwc" else layout
     if lay not in (_lib.NCHW, _lib.NHWC):
         raise ValueError(f"unknown layout {layout!r}")
     if lay == _lib.NHWC:
         N, C, ldx = _rows(x, "x")
-        P, stat = 1, tuple(x.shape[:-1])
+        P = 1
     else:
         if x.dim() < 3:
             raise ValueError("an nchw x has at least three dimensions")
         if not x.is_contiguous():
             raise ValueError("an nchw x must be contiguous")
         N, C, ldx = x.shape[0], x.shape[1], 0
-        stat = (N,) + tuple(x.shape[2:])
         P = 1
         for n in x.shape[2:]:
             P *= n
     return LayerNormDesc(N, C, P, ldx, 0, 0, _code(x.dtype), _code(y_dtype), lay, 0, eps, dropout_p, seed,
-                         offset), stat
+                         offset), N * P
 
 
-def _row_stride(d, t, name, shape, dtype, like):
+def _row_stride(d, t, name, shape, dtype, dev):
     """The row stride of y, dy or dx (0 for nchw)."""
-    _device(t, name, like)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on the device of x")
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
-    if d.layout == _lib.NHWC:
-        return _rows(t, name)[2]
-    if not t.is_contiguous():
+    if t.is_contiguous():
+        return 0
+    if d.layout != _lib.NHWC:
         raise ValueError(f"an nchw {name} must be contiguous")
-    return 0
+    return _rows(t, name)[2]
 
 
 def layer_norm_into(x, weight, bias, y, mean, rstd, eps: float = 1e-5, *, layout="nhwc", dropout_p: float = 0.0,
                     seed: int = 0, offset: int = 0) -> None:
     """Enqueue y, mean, rstd = layer_norm(x); weight, bias may be None, and mean
     and rstd both None when no backward pass follows."""
-    _device(x, "x")
-    d, stat = _norm_desc(x, layout, y.dtype, eps, dropout_p, seed, offset)
-    d.ldy = _row_stride(d, y, "y", x.shape, y.dtype, x)
-    n = d.N * d.P
-    _head.call("layer_norm_fwd", d, x.data_ptr(), _vector(weight, "weight", d.C, x), _vector(bias, "bias", d.C, x),
-               y.data_ptr(), _vector(mean, "mean", n, x), _vector(rstd, "rstd", n, x), _stream(x))
+    dev = _device(x, "x")
+    d, n = _norm_desc(x, layout, y.dtype, eps, dropout_p, seed, offset)
+    d.ldy = _row_stride(d, y, "y", x.shape, y.dtype, dev)
+    C = d.C
+    _head.call("layer_norm_fwd", d, x.data_ptr(), _vector(weight, "weight", C, dev), _vector(bias, "bias", C, dev),
+               y.data_ptr(), _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev), _raw_stream(dev))
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, layout="nhwc", out_dtype=None,
@@ -183,7 +192,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, layout="nhwc", o
     import torch
     _device(x, "x")
     odt = x.dtype if out_dtype is None else out_dtype
-    _, stat = _norm_desc(x, layout, odt, eps, dropout_p, seed, offset)
+    d, _ = _norm_desc(x, layout, odt, eps, dropout_p, seed, offset)
+    stat = x.shape[:-1] if d.layout == _lib.NHWC else x.shape[:1] + x.shape[2:]
     y = torch.empty(x.shape, dtype=odt, device=x.device)
     mean = torch.empty(stat, dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
@@ -202,16 +212,16 @@ def layer_norm_backward_into(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, 
                              dropout_p: float = 0.0, seed: int = 0, offset: int = 0) -> None:
     """Enqueue the gradients of layer_norm; dweight and dbias may both be None
     (then ws may be None too)."""
-    _device(x, "x")
-    d, stat = _norm_desc(x, layout, dy.dtype, 0.0, dropout_p, seed, offset)
-    d.ldy = _row_stride(d, dy, "dy", x.shape, dy.dtype, x)
-    d.lddx = _row_stride(d, dx, "dx", x.shape, x.dtype, x)
-    n = d.N * d.P
+    dev = _device(x, "x")
+    d, n = _norm_desc(x, layout, dy.dtype, 0.0, dropout_p, seed, offset)
+    d.ldy = _row_stride(d, dy, "dy", x.shape, dy.dtype, dev)
+    d.lddx = _row_stride(d, dx, "dx", x.shape, x.dtype, dev)
+    C = d.C
     need = _head.size("layer_norm_bwd_workspace_size", d) if dweight is not None else 0
-    _head.call("layer_norm_bwd", d, dy.data_ptr(), x.data_ptr(), _vector(weight, "weight", d.C, x),
-               _vector(mean, "mean", n, x), _vector(rstd, "rstd", n, x), dx.data_ptr(),
-               _vector(dweight, "dweight", d.C, x), _vector(dbias, "dbias", d.C, x), _workspace(ws, need, x),
-               _stream(x))
+    _head.call("layer_norm_bwd", d, dy.data_ptr(), x.data_ptr(), _vector(weight, "weight", C, dev),
+               _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev), dx.data_ptr(),
+               _vector(dweight, "dweight", C, dev), _vector(dbias, "dbias", C, dev), _workspace(ws, need, dev),
+               _raw_stream(dev))
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, layout="nhwc", dropout_p: float = 0.0, seed: int = 0,
@@ -235,9 +245,18 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, layout="nhwc", dropout_p: 
 def _xent_desc(x, w):
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError("x must be [N][D] and w [V][D]")
-    if x.dtype != w.dtype:
+    if x.dtype is not w.dtype:
         raise TypeError("x and w must share a dtype")
-    return LinearXentDesc(x.shape[0], w.shape[0], x.shape[1], _rows(x, "x")[2], _rows(w, "w")[2], _code(x.dtype), 0)
+    N, D = x.shape
+    return LinearXentDesc(N, w.shape[0], D, D if x.is_contiguous() else _rows(x, "x")[2],
+                          D if w.is_contiguous() else _rows(w, "w")[2], _code(x.dtype), 0)
+
+
+def _same_device(x, w) -> int:
+    dev = _device(x, "x")
+    if w.get_device() != dev:
+        raise ValueError("w must be a device tensor on the device of x")
+    return dev
 
 
 def linear_cross_entropy_workspace_size(x, w, *, backward: bool = False) -> int:
@@ -250,12 +269,12 @@ def linear_cross_entropy_workspace_size(x, w, *, backward: bool = False) -> int:
 
 def linear_cross_entropy_into(x, w, target, loss, lse, ws) -> None:
     """Enqueue loss, lse = linear_cross_entropy(x, w, target)."""
-    _device(x, "x")
-    _device(w, "w", x)
+    dev = _same_device(x, w)
     d = _xent_desc(x, w)
-    _head.call("linear_xent_fwd", d, x.data_ptr(), w.data_ptr(), _vector(target, "target", d.N, x, "torch.int64"),
-               _vector(loss, "loss", d.N, x), _vector(lse, "lse", d.N, x),
-               _workspace(ws, _head.size("linear_xent_fwd_workspace_size", d), x), _stream(x))
+    N = x.shape[0]
+    _head.call("linear_xent_fwd", d, x.data_ptr(), w.data_ptr(), _vector(target, "target", N, dev, _I64),
+               _vector(loss, "loss", N, dev), _vector(lse, "lse", N, dev),
+               _workspace(ws, _head.size("linear_xent_fwd_workspace_size", d), dev), _raw_stream(dev))
 
 
 def linear_cross_entropy(x, w, target):
@@ -272,13 +291,13 @@ def linear_cross_entropy(x, w, target):
 def linear_cross_entropy_backward_into(grad, x, w, target, lse, dx, dw, ws) -> None:
     """Enqueue the gradients of linear_cross_entropy for the per-row gradient
     grad (fp32 [N]) of its loss."""
-    _device(x, "x")
-    _device(w, "w", x)
+    dev = _same_device(x, w)
     d = _xent_desc(x, w)
-    _head.call("linear_xent_bwd", d, _vector(grad, "grad", d.N, x), x.data_ptr(), w.data_ptr(),
-               _vector(target, "target", d.N, x, "torch.int64"), _vector(lse, "lse", d.N, x),
-               _contiguous(dx, "dx", x.shape, x.dtype, x), _contiguous(dw, "dw", w.shape, w.dtype, x),
-               _workspace(ws, _head.size("linear_xent_bwd_workspace_size", d), x), _stream(x))
+    N = x.shape[0]
+    _head.call("linear_xent_bwd", d, _vector(grad, "grad", N, dev), x.data_ptr(), w.data_ptr(),
+               _vector(target, "target", N, dev, _I64), _vector(lse, "lse", N, dev),
+               _contiguous(dx, "dx", x.shape, x.dtype, dev), _contiguous(dw, "dw", w.shape, w.dtype, dev),
+               _workspace(ws, _head.size("linear_xent_bwd_workspace_size", d), dev), _raw_stream(dev))
 
 
 def linear_cross_entropy_backward(grad, x, w, target, lse):
