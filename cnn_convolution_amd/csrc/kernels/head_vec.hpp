@@ -43,6 +43,15 @@ __device__ __forceinline__ float element(const Raw<T, K> &r, int e)
     return static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(e & 1 ? u >> 16 : u)));
 }
 
+// all elements kept (mask ~0) or cleared (mask 0): as a mask, for a choice between
+// values may become a branch
+template <typename T, int K>
+__device__ __forceinline__ void keep_if(Raw<T, K> &r, uint32_t mask)
+{
+#pragma unroll
+    for (int i = 0; i < Raw<T, K>::ND; ++i) r.d[i] &= mask;
+}
+
 // r moved down by s elements (s >= 0), zeros moving in
 template <typename T, int K>
 __device__ __forceinline__ void shift_down(Raw<T, K> &r, int s)
@@ -118,7 +127,7 @@ __device__ __forceinline__ void store_raw(T *p, const Raw<T, K> &r)
 // Waits for the loads of r. Loads and stores return in order, and behind a
 // branch the compiler cannot count the stores: a wait for loads that come
 // before such stores would wait for the stores too, so prefetched loads are
-// waited for ahead of them.
+// waited for ahead of them. (The values become opaque to the compiler here.)
 template <typename T, int K>
 __device__ __forceinline__ void arrive(Raw<T, K> &r)
 {

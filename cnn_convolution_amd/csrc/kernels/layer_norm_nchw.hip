@@ -17,13 +17,14 @@
 namespace im2win {
 namespace {
 
-constexpr int kPosLanes = 16, kPos = 64;
+constexpr int kPosLanes = 16, kPos = 64;       // lanes, and positions of a tile of 4 per lane
 
 // v[e] over the lanes of a wave that hold the same positions
-__device__ __forceinline__ void wave_chan_sum(float (&v)[4])
+template <int PV>
+__device__ __forceinline__ void wave_chan_sum(float (&v)[PV])
 {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < PV; ++e) {
         const uint32_t u = __float_as_uint(v[e]);
         const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
         const uint32_t w = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
@@ -32,26 +33,27 @@ __device__ __forceinline__ void wave_chan_sum(float (&v)[4])
     }
 }
 
-// where this thread's tile lies
+// where this thread's positions lie, PV of them per lane
+template <int PV>
 struct TilePos {
     int64_t n, p, base;      // image, first position, offset of channel 0 there
     int left;                // positions that exist (<= 0: none)
     __device__ __forceinline__ TilePos(int64_t t, int tiles_p, int l, const NormArgs &a)
     {
         n = t / tiles_p;
-        p = (t - n * tiles_p) * kPos + l * 4;
-        left = int(min(int64_t(4), a.P - p));
+        p = (t - n * tiles_p) * (kPosLanes * PV) + l * PV;
+        left = int(min(int64_t(PV), a.P - p));
         base = n * a.C * a.P;
     }
 };
 
-template <bool EXACT, typename T>
-__device__ __forceinline__ void store_pos(T *p, int left, const float (&f)[4])
+template <bool EXACT, int PV, typename T>
+__device__ __forceinline__ void store_pos(T *p, int left, const float (&f)[PV])
 {
     if constexpr (EXACT) {
-        if (left > 0) store_vec<4>(p, f);
+        if (left > 0) store_vec<PV>(p, f);
     } else {
-        store_some<4>(p, left, f);
+        store_some<PV>(p, left, f);
     }
 }
 
@@ -69,25 +71,26 @@ __device__ __forceinline__ T *at_offset(T *base, uint32_t elems)
     return reinterpret_cast<T *>(reinterpret_cast<char *>(base) + elems * uint32_t(sizeof(T)));
 }
 
-// where positions p .. p + 3 of a channel are read from, and how far that is
+// where positions p .. p + PV - 1 of a channel are read from, and how far that is
 // before p (see load_row)
+template <int PV>
 struct Window {
     uint32_t at;
     int shift;
     __device__ __forceinline__ Window(int64_t p, int64_t P)
     {
-        const int64_t q = p < P - 4 ? p : P - 4;
+        const int64_t q = p < P - PV ? p : P - PV;
         at = uint32_t(q);
-        shift = int(p - q < 4 ? p - q : 4);
+        shift = int(p - q < PV ? p - q : PV);
     }
 };
 
-// WAVES waves, 4 * WAVES channel groups; EXACT: P is a multiple of 4
-template <typename TX, typename TY, int WAVES, int KR, bool EXACT>
+// WAVES waves, 4 * WAVES channel groups; EXACT: P is a multiple of PV
+template <typename TX, typename TY, int WAVES, int KR, int PV, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArgs a, int tiles_p)
 {
     constexpr int G = WAVES * 4;
-    __shared__ __align__(16) float red[2][WAVES][kPos];    // mean, squares
+    __shared__ __align__(16) float red[2][WAVES][kPosLanes * PV];    // mean, squares
     const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, wave = threadIdx.x >> 6, C = a.C;
     const float fc = float(C);
     const uint32_t P = uint32_t(a.P);
@@ -105,23 +108,23 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
         for (int i = 0; i < KR; ++i) n += max(0, min(4, C - i * G - q * 4));
         return float(n);
     };
-    const TilePos at(blockIdx.x, tiles_p, l, a);
+    const TilePos<PV> at(blockIdx.x, tiles_p, l, a);
     const TX *x = static_cast<const TX *>(a.x) + at.base;
     TY *y = static_cast<TY *>(a.out) + at.base;
-    const Window win(at.p, a.P);
+    const Window<PV> win(at.p, a.P);
     // channels past the last read that one and count nowhere
-    Raw<TX, 4> q[KR];
+    Raw<TX, PV> q[KR];
 #pragma unroll
     for (int i = 0; i < KR; ++i)
-        q[i] = load_raw<TX, 4>(at_offset(x, uint32_t(min(g + i * G, C - 1)) * P + win.at));
+        q[i] = load_raw<TX, PV>(at_offset(x, uint32_t(min(g + i * G, C - 1)) * P + win.at));
     if constexpr (!EXACT)
 #pragma unroll
         for (int i = 0; i < KR; ++i) shift_down(q[i], win.shift);
-    float v[KR][4], mean[4] = {}, sq[4] = {};
+    float v[KR][PV], mean[PV] = {}, sq[PV] = {};
 #pragma unroll
     for (int i = 0; i < KR; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PV; ++e) {
             v[i][e] = element(q[i], e);
             mean[e] += g + i * G < C ? v[i][e] : 0.f;
         }
@@ -130,46 +133,42 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
     wave_chan_sum(mean);
     const float nw = fmaxf(count(wave), 1.f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) mean[e] /= nw;
+    for (int e = 0; e < PV; ++e) mean[e] /= nw;
 #pragma unroll
     for (int i = 0; i < KR; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PV; ++e) {
             const float d = v[i][e] - mean[e];
             sq[e] += g + i * G < C ? d * d : 0.f;
         }
     wave_chan_sum(sq);
     if ((threadIdx.x & 48) == 0)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            red[0][wave][l * 4 + e] = mean[e];
-            red[1][wave][l * 4 + e] = sq[e];
+        for (int e = 0; e < PV; ++e) {
+            red[0][wave][l * PV + e] = mean[e];
+            red[1][wave][l * PV + e] = sq[e];
         }
     __syncthreads();
-    float rstd[4], m[4] = {}, s[4] = {};
+    float rstd[PV], m[PV] = {}, s[PV] = {};
 #pragma unroll 4
     for (int k = 0; k < WAVES; ++k) {
-        const float4 u = *reinterpret_cast<const float4 *>(&red[0][k][l * 4]);
         const float n = count(k);
-        m[0] += u.x * n;
-        m[1] += u.y * n;
-        m[2] += u.z * n;
-        m[3] += u.w * n;
+#pragma unroll
+        for (int e = 0; e < PV; ++e) m[e] += red[0][k][l * PV + e] * n;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] /= fc;
+    for (int e = 0; e < PV; ++e) m[e] /= fc;
 #pragma unroll 4
     for (int k = 0; k < WAVES; ++k) {
-        const float4 u = *reinterpret_cast<const float4 *>(&red[0][k][l * 4]);
-        const float4 q2 = *reinterpret_cast<const float4 *>(&red[1][k][l * 4]);
         const float n = count(k);
-        s[0] += q2.x + n * (u.x - m[0]) * (u.x - m[0]);
-        s[1] += q2.y + n * (u.y - m[1]) * (u.y - m[1]);
-        s[2] += q2.z + n * (u.z - m[2]) * (u.z - m[2]);
-        s[3] += q2.w + n * (u.w - m[3]) * (u.w - m[3]);
+#pragma unroll
+        for (int e = 0; e < PV; ++e) {
+            const float d = red[0][k][l * PV + e] - m[e];
+            s[e] += red[1][k][l * PV + e] + n * d * d;
+        }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < PV; ++e) {
         mean[e] = m[e];
         rstd[e] = 1.f / sqrtf(s[e] / fc + a.eps);
     }
@@ -177,21 +176,21 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
     for (int i = 0; i < KR; ++i) {
         const int c = g + i * G;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[i][e] = (v[i][e] - mean[e]) * rstd[e] * w[i] + b[i];
-        if (a.drop.threshold) drop_run<4>(at.base + c * a.P + at.p, a.drop, v[i]);
+        for (int e = 0; e < PV; ++e) v[i][e] = (v[i][e] - mean[e]) * rstd[e] * w[i] + b[i];
+        if (a.drop.threshold) drop_run<PV>(at.base + c * a.P + at.p, a.drop, v[i]);
         store_pos<EXACT>(at_offset(y, c * P + uint32_t(at.p)), c < C ? at.left : 0, v[i]);
     }
     if (g == 0 && a.mean) {
-        store_some<4>(a.mean + at.n * a.P + at.p, at.left, mean);
-        store_some<4>(a.rstd + at.n * a.P + at.p, at.left, rstd);
+        store_some<PV>(a.mean + at.n * a.P + at.p, at.left, mean);
+        store_some<PV>(a.rstd + at.n * a.P + at.p, at.left, rstd);
     }
 }
 
-template <typename TX, typename TY, int WAVES, int KR, bool EXACT>
+template <typename TX, typename TY, int WAVES, int KR, int PV, bool EXACT, bool DROP>
 __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArgs a, int tiles_p)
 {
     constexpr int G = WAVES * 4;
-    __shared__ __align__(16) float red[2][2][WAVES][kPos];
+    __shared__ __align__(16) float red[2][2][WAVES][kPosLanes * PV];
     const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, wave = threadIdx.x >> 6, C = a.C;
     const float fc = float(C);
     const int64_t tiles = a.N * tiles_p;
@@ -203,23 +202,23 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
     }
     int slot = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const TilePos at(t, tiles_p, l, a);
+        const TilePos<PV> at(t, tiles_p, l, a);
         // opaque, so that no offset of a channel is kept in registers over the tiles
         uint32_t P = uint32_t(a.P);
         asm volatile("" : "+s"(P));
         const TX *x = static_cast<const TX *>(a.x) + at.base;
         const TY *dy = static_cast<const TY *>(a.dy) + at.base;
         TX *dx = static_cast<TX *>(a.out) + at.base;
-        const Window win(at.p, a.P);
-        const Raw<float, 4> rm = load_row<float, 4, EXACT>(a.mean + at.n * a.P, at.p, a.P);
-        const Raw<float, 4> rr = load_row<float, 4, EXACT>(a.rstd + at.n * a.P, at.p, a.P);
-        Raw<TX, 4> qx[KR];
-        Raw<TY, 4> qy[KR];
+        const Window<PV> win(at.p, a.P);
+        Raw<float, PV> rm = load_row<float, PV, EXACT>(a.mean + at.n * a.P, at.p, a.P);
+        Raw<float, PV> rr = load_row<float, PV, EXACT>(a.rstd + at.n * a.P, at.p, a.P);
+        Raw<TX, PV> qx[KR];
+        Raw<TY, PV> qy[KR];
 #pragma unroll
         for (int i = 0; i < KR; ++i) {
             const uint32_t o = uint32_t(min(g + i * G, C - 1)) * P + win.at;
-            qx[i] = load_raw<TX, 4>(at_offset(x, o));
-            qy[i] = load_raw<TY, 4>(at_offset(dy, o));
+            qx[i] = load_raw<TX, PV>(at_offset(x, o));
+            qy[i] = load_raw<TY, PV>(at_offset(dy, o));
         }
         if constexpr (!EXACT)
 #pragma unroll
@@ -227,51 +226,66 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
                 shift_down(qx[i], win.shift);
                 shift_down(qy[i], win.shift);
             }
-        float h[KR][4], z[KR][4], s1[4] = {}, s2[4] = {};
+        // a position past the end has mean, rstd and dy 0, a channel past the last
+        // dy 0: they add nothing (not EXACT: the shift has cleared the positions)
+        const uint32_t pos = !EXACT || at.left > 0 ? ~0u : 0u;
+        keep_if(rm, pos);
+        keep_if(rr, pos);
+#pragma unroll
+        for (int i = 0; i < KR; ++i) keep_if(qy[i], g + i * G < C ? pos : 0u);
+        // xhat and dz of channel i: formed from the raw values in both passes, which
+        // takes half the registers of keeping them; a dropout mask is kept (a bit)
+        constexpr int KW = 32 / PV;                // channels per word
+        uint32_t keep[(KR + KW - 1) / KW] = {};
+        auto form = [&](int i, float (&h)[PV], float (&z)[PV]) {
+#pragma unroll
+            for (int e = 0; e < PV; ++e) {
+                h[e] = (element(qx[i], e) - element(rm, e)) * element(rr, e);
+                z[e] = element(qy[i], e);
+                if constexpr (DROP) z[e] = (keep[i / KW] >> (i % KW * PV + e)) & 1 ? z[e] * a.drop.scale : 0.f;
+            }
+        };
+        if constexpr (DROP)
+#pragma unroll
+            for (int i = 0; i < KR; ++i) {
+                keep[i / KW] |= (keep_run<PV>(at.base + uint32_t(g + i * G) * P + at.p, a.drop) & ((1u << PV) - 1))
+                                << (i % KW * PV);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        float s1[PV] = {}, s2[PV] = {};
 #pragma unroll
         for (int i = 0; i < KR; ++i) {
-            const int c = g + i * G;
+            float h[PV], z[PV];
+            form(i, h, z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[i][e] = element(qy[i], e);
-            if (a.drop.threshold) drop_run<4>(at.base + uint32_t(c) * P + at.p, a.drop, z[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool in = c < C && (EXACT ? 0 < at.left : e < at.left);
-                h[i][e] = in ? (element(qx[i], e) - element(rm, e)) * element(rr, e) : 0.f;
-                z[i][e] = in ? z[i][e] : 0.f;
-                dw[i] += z[i][e] * h[i][e];
-                db[i] += z[i][e];
-                z[i][e] *= w[i];
-                s1[e] += z[i][e];
-                s2[e] += z[i][e] * h[i][e];
+            for (int e = 0; e < PV; ++e) {
+                dw[i] += z[e] * h[e];
+                db[i] += z[e];
+                s1[e] += z[e] * w[i];
+                s2[e] += z[e] * w[i] * h[e];
             }
+            __builtin_amdgcn_sched_barrier(0);     // one channel's values at a time
         }
         wave_chan_sum(s1);
         wave_chan_sum(s2);
         if ((threadIdx.x & 48) == 0)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                red[slot][0][wave][l * 4 + e] = s1[e];
-                red[slot][1][wave][l * 4 + e] = s2[e];
+            for (int e = 0; e < PV; ++e) {
+                red[slot][0][wave][l * PV + e] = s1[e];
+                red[slot][1][wave][l * PV + e] = s2[e];
             }
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s1[e] = s2[e] = 0.f;
+        for (int e = 0; e < PV; ++e) s1[e] = s2[e] = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < WAVES; ++k) {
-            const float4 u = *reinterpret_cast<const float4 *>(&red[slot][0][k][l * 4]);
-            const float4 q = *reinterpret_cast<const float4 *>(&red[slot][1][k][l * 4]);
-            s1[0] += u.x;
-            s1[1] += u.y;
-            s1[2] += u.z;
-            s1[3] += u.w;
-            s2[0] += q.x;
-            s2[1] += q.y;
-            s2[2] += q.z;
-            s2[3] += q.w;
-        }
+        for (int k = 0; k < WAVES; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < PV; ++e) {
+                s1[e] += red[slot][0][k][l * PV + e];
+                s2[e] += red[slot][1][k][l * PV + e];
+            }
+#pragma unroll
+        for (int e = 0; e < PV; ++e) {
             s1[e] /= fc;
             s2[e] /= fc;
         }
@@ -279,10 +293,14 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
 #pragma unroll
         for (int i = 0; i < KR; ++i) {
             const int c = g + i * G;
-            float o[4];
+            float o[PV], h[PV], z[PV];
+            arrive(qx[i]);                     // opaque: formed anew, not kept since the first pass
+            arrive(qy[i]);
+            form(i, h, z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = element(rr, e) * (z[i][e] - s1[e] - h[i][e] * s2[e]);
+            for (int e = 0; e < PV; ++e) o[e] = element(rr, e) * (z[e] * w[i] - s1[e] - h[e] * s2[e]);
             store_pos<EXACT>(at_offset(dx, c * P + uint32_t(at.p)), c < C ? at.left : 0, o);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!a.partial) return;
@@ -316,6 +334,19 @@ __device__ __forceinline__ void chan_sum(float (&v)[4], float (*red)[kPos])
     }
 }
 
+// positions p .. p + 3 of a channel's row of P, zeros past its end
+template <typename T>
+__device__ __forceinline__ void load_pos(const T *row, int64_t p, int64_t P, float (&f)[4])
+{
+    if (P >= 4) {                              // wave-uniform
+        const Raw<T, 4> r = load_row<T, 4, false>(row, p, P);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = element(r, e);
+    } else {
+        load_some<4>(row + p, P - p, f);
+    }
+}
+
 // any number of channels and positions: the tile is read again for each pass
 template <typename TX, typename TY>
 __global__ __launch_bounds__(kWide) void norm_nchw_fwd_wide_kernel(const NormArgs a, int tiles_p)
@@ -324,20 +355,22 @@ __global__ __launch_bounds__(kWide) void norm_nchw_fwd_wide_kernel(const NormArg
     const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, C = a.C;
     const float fc = float(C);
     for (int64_t t = blockIdx.x; t < a.N * tiles_p; t += gridDim.x) {
-        const TilePos at(t, tiles_p, l, a);
-        const TX *x = static_cast<const TX *>(a.x) + at.base + at.p;
+        const TilePos<4> at(t, tiles_p, l, a);
+        const TX *x = static_cast<const TX *>(a.x) + at.base;
         TY *y = static_cast<TY *>(a.out) + at.base + at.p;
         float v[4], mean[4] = {}, var[4] = {}, rstd[4];
+#pragma unroll 4
         for (int c = g; c < C; c += kWideGroups) {
-            load_some<4>(x + c * a.P, at.left, v);
+            load_pos(x + c * a.P, at.p, a.P, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) mean[e] += v[e];
         }
         chan_sum(mean, red);
 #pragma unroll
         for (int e = 0; e < 4; ++e) mean[e] /= fc;
+#pragma unroll 4
         for (int c = g; c < C; c += kWideGroups) {
-            load_some<4>(x + c * a.P, at.left, v);
+            load_pos(x + c * a.P, at.p, a.P, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) var[e] += (v[e] - mean[e]) * (v[e] - mean[e]);
         }
@@ -348,9 +381,10 @@ __global__ __launch_bounds__(kWide) void norm_nchw_fwd_wide_kernel(const NormArg
             store_some<4>(a.mean + at.n * a.P + at.p, at.left, mean);
             store_some<4>(a.rstd + at.n * a.P + at.p, at.left, rstd);
         }
+#pragma unroll 4
         for (int c = g; c < C; c += kWideGroups) {
             const float w = a.weight ? a.weight[c] : 1.f, b = a.bias ? a.bias[c] : 0.f;
-            load_some<4>(x + c * a.P, at.left, v);
+            load_pos(x + c * a.P, at.p, a.P, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = (v[e] - mean[e]) * rstd[e] * w + b;
             if (a.drop.threshold) drop_run<4>(at.base + c * a.P + at.p, a.drop, v);
@@ -366,17 +400,17 @@ __global__ __launch_bounds__(kWide) void norm_nchw_bwd_wide_kernel(const NormArg
     const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, C = a.C;
     const float fc = float(C);
     for (int64_t t = blockIdx.x; t < a.N * tiles_p; t += gridDim.x) {
-        const TilePos at(t, tiles_p, l, a);
-        const TX *x = static_cast<const TX *>(a.x) + at.base + at.p;
-        const TY *dy = static_cast<const TY *>(a.dy) + at.base + at.p;
+        const TilePos<4> at(t, tiles_p, l, a);
+        const TX *x = static_cast<const TX *>(a.x) + at.base;
+        const TY *dy = static_cast<const TY *>(a.dy) + at.base;
         TX *dx = static_cast<TX *>(a.out) + at.base + at.p;
         float mean[4], rstd[4], h[4], z[4], s1[4] = {}, s2[4] = {};
         load_some<4>(a.mean + at.n * a.P + at.p, at.left, mean);
         load_some<4>(a.rstd + at.n * a.P + at.p, at.left, rstd);
         auto load = [&](int c) {                       // xhat and dz * weight
             const float w = a.weight ? a.weight[c] : 1.f;
-            load_some<4>(x + c * a.P, at.left, h);
-            load_some<4>(dy + c * a.P, at.left, z);
+            load_pos(x + c * a.P, at.p, a.P, h);
+            load_pos(dy + c * a.P, at.p, a.P, z);
             if (a.drop.threshold) drop_run<4>(at.base + c * a.P + at.p, a.drop, z);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -384,6 +418,7 @@ __global__ __launch_bounds__(kWide) void norm_nchw_bwd_wide_kernel(const NormArg
                 z[e] *= w;
             }
         };
+#pragma unroll 4
         for (int c = g; c < C; c += kWideGroups) {
             load(c);
 #pragma unroll
@@ -394,6 +429,7 @@ __global__ __launch_bounds__(kWide) void norm_nchw_bwd_wide_kernel(const NormArg
         }
         chan_sum(s1, red);
         chan_sum(s2, red);
+#pragma unroll 4
         for (int c = g; c < C; c += kWideGroups) {
             load(c);
 #pragma unroll
@@ -414,17 +450,16 @@ __global__ __launch_bounds__(256) void norm_planes_kernel(const NormArgs a)
     for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
         const int64_t base = (n * C + c) * a.P;
         for (int64_t p = l * 4; p < a.P; p += 256) {
-            const int left = int(min(int64_t(4), a.P - p));
             float h[4], z[4], mean[4], rstd[4];
-            load_some<4>(static_cast<const TX *>(a.x) + base + p, left, h);
-            load_some<4>(static_cast<const TY *>(a.dy) + base + p, left, z);
-            load_some<4>(a.mean + n * a.P + p, left, mean);
-            load_some<4>(a.rstd + n * a.P + p, left, rstd);
+            load_pos(static_cast<const TX *>(a.x) + base, p, a.P, h);
+            load_pos(static_cast<const TY *>(a.dy) + base, p, a.P, z);
+            load_pos(a.mean + n * a.P, p, a.P, mean);
+            load_pos(a.rstd + n * a.P, p, a.P, rstd);
             if (a.drop.threshold) drop_run<4>(base + p, a.drop, z);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                dw += e < left ? z[e] * (h[e] - mean[e]) * rstd[e] : 0.f;
-                db += e < left ? z[e] : 0.f;
+                dw += z[e] * (h[e] - mean[e]) * rstd[e];   // 0 past the end
+                db += z[e];
             }
         }
     }
@@ -436,62 +471,69 @@ __global__ __launch_bounds__(256) void norm_planes_kernel(const NormArgs a)
     }
 }
 
-// Waves per workgroup and channels per thread: channels in registers, as few as
-// hold them all, since fewer registers mean more tiles in flight; kr 0: read
-// again for each pass
+// Waves per workgroup, channels per thread and positions per lane: channels in
+// registers, as few as hold them all, since fewer registers mean more tiles in
+// flight; past 256 channels half the positions (16 channels of 4 positions
+// do not fit the registers backward: 384 channels of 56 x 56, bf16, 50 images
+// took 246 us); kr 0: read again for each pass
 struct Hold {
-    int waves, kr;
+    int waves, kr, pv;
 };
 Hold hold_of(int64_t C, int64_t P)
 {
-    if (P < 4 || C * P >= int64_t(1) << 30) return {0, 0};
-    if (C <= 64) return {4, 4};
-    if (C <= 128) return {4, 8};
-    if (C <= 256) return {8, 8};
-    if (C <= 512) return {8, 16};
-    return {0, 0};
+    if (P < 4 || C * P >= int64_t(1) << 30) return {0, 0, 4};
+    if (C <= 64) return {4, 4, 4};
+    if (C <= 128) return {4, 8, 4};
+    if (C <= 256) return {8, 8, 4};
+    if (C <= 512) return {8, 16, 2};
+    return {0, 0, 4};
 }
 
 template <typename F>
-hipError_t with_hold(const Hold &h, bool exact, F f)
+hipError_t with_hold(const Hold &h, int64_t P, F f)
 {
     using std::integral_constant;
-    const auto call = [&](auto w, auto k) { return exact ? f(w, k, std::true_type{}) : f(w, k, std::false_type{}); };
-    if (h.waves == 4 && h.kr == 4) return call(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-    if (h.waves == 4) return call(integral_constant<int, 4>{}, integral_constant<int, 8>{});
-    if (h.kr == 8) return call(integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    return call(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    const auto call = [&](auto w, auto k, auto v) {
+        return P % decltype(v)::value == 0 ? f(w, k, v, std::true_type{}) : f(w, k, v, std::false_type{});
+    };
+    const integral_constant<int, 4> four{};
+    const integral_constant<int, 8> eight{};
+    if (h.waves == 4 && h.kr == 4) return call(four, four, four);
+    if (h.waves == 4) return call(four, eight, four);
+    if (h.kr == 8) return call(eight, eight, four);
+    return call(eight, integral_constant<int, 16>{}, integral_constant<int, 2>{});
 }
 
 constexpr int64_t kMaxBlocksFwd = 4096, kMaxBlocksBwd = 512, kImageSplits = 16;
 
-int64_t tiles_of(int64_t N, int64_t P) { return N * ((P + kPos - 1) / kPos); }
+int64_t tiles_of_image(int64_t P, const Hold &h) { return (P + kPosLanes * h.pv - 1) / (kPosLanes * h.pv); }
 
 }  // namespace
 
 int64_t norm_nchw_partials(int64_t N, int64_t C, int64_t P)
 {
-    if (!hold_of(C, P).kr) return kImageSplits;
-    return std::max<int64_t>(1, std::min(tiles_of(N, P), kMaxBlocksBwd));
+    const Hold h = hold_of(C, P);
+    if (!h.kr) return kImageSplits;
+    return std::max<int64_t>(1, std::min(N * tiles_of_image(P, h), kMaxBlocksBwd));
 }
 
 hipError_t launch_norm_nchw_fwd(const NormArgs &a, hipStream_t s)
 {
     const Hold h = hold_of(a.C, a.P);
-    const int64_t tiles = tiles_of(a.N, a.P);
-    const int tiles_p = int((a.P + kPos - 1) / kPos);
+    const int64_t tiles_p = tiles_of_image(a.P, h), tiles = a.N * tiles_p;
     return with_norm_types(a.dtype, a.y_dtype, [&](auto tx, auto ty) {
         using TX = typename decltype(tx)::type;
         using TY = typename decltype(ty)::type;
-        if (!h.kr || tiles > INT32_MAX) {
+        if (!h.kr) {
             const dim3 grid(unsigned(std::min(tiles, kMaxBlocksFwd)));
-            hipLaunchKernelGGL((norm_nchw_fwd_wide_kernel<TX, TY>), grid, dim3(kWide), 0, s, a, tiles_p);
+            hipLaunchKernelGGL((norm_nchw_fwd_wide_kernel<TX, TY>), grid, dim3(kWide), 0, s, a, int(tiles_p));
             return hipGetLastError();
         }
-        return with_hold(h, a.P % 4 == 0, [&](auto w, auto k, auto exact) {
-            constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value;
-            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, decltype(exact)::value>),
-                               dim3(unsigned(tiles)), dim3(WAVES * 64), 0, s, a, tiles_p);
+        if (tiles > INT32_MAX) return hipErrorInvalidValue;     // a.N < 2^31 images of few positions: not reached
+        return with_hold(h, a.P, [&](auto w, auto k, auto v, auto exact) {
+            constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value, PV = decltype(v)::value;
+            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, PV, decltype(exact)::value>),
+                               dim3(unsigned(tiles)), dim3(WAVES * 64), 0, s, a, int(tiles_p));
             return hipGetLastError();
         });
     });
@@ -501,18 +543,24 @@ hipError_t launch_norm_nchw_bwd(const NormArgs &a, hipStream_t s)
 {
     const Hold h = hold_of(a.C, a.P);
     const int64_t blocks = norm_nchw_partials(a.N, a.C, a.P);
-    const int tiles_p = int((a.P + kPos - 1) / kPos);
+    const int tiles_p = int(tiles_of_image(a.P, h));
     hipError_t e = with_norm_types(a.dtype, a.y_dtype, [&](auto tx, auto ty) {
         using TX = typename decltype(tx)::type;
         using TY = typename decltype(ty)::type;
         if (h.kr)
-            return with_hold(h, a.P % 4 == 0, [&](auto w, auto k, auto exact) {
-                constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value;
-                hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, decltype(exact)::value>),
-                                   dim3(unsigned(blocks)), dim3(WAVES * 64), 0, s, a, tiles_p);
+            return with_hold(h, a.P, [&](auto w, auto k, auto v, auto exact) {
+                constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value, PV = decltype(v)::value;
+                constexpr bool EXACT = decltype(exact)::value;
+                const dim3 grid{unsigned(blocks)};
+                if (a.drop.threshold)
+                    hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, PV, EXACT, true>), grid,
+                                       dim3(WAVES * 64), 0, s, a, tiles_p);
+                else
+                    hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, PV, EXACT, false>), grid,
+                                       dim3(WAVES * 64), 0, s, a, tiles_p);
                 return hipGetLastError();
             });
-        const dim3 grid(unsigned(std::max<int64_t>(1, std::min(tiles_of(a.N, a.P), kMaxBlocksFwd))));
+        const dim3 grid(unsigned(std::max<int64_t>(1, std::min(a.N * tiles_p, kMaxBlocksFwd))));
         hipLaunchKernelGGL((norm_nchw_bwd_wide_kernel<TX, TY>), grid, dim3(kWide), 0, s, a, tiles_p);
         const hipError_t e1 = hipGetLastError();
         if (e1 != hipSuccess || !a.partial) return e1;
