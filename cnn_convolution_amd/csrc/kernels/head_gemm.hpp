@@ -42,6 +42,27 @@ using C128 = TileCfg<128, 128, 2, 2, 2, 2>;
 using C64 = TileCfg<64, 64, 2, 2, 3, 3>;
 using CNarrow = TileCfg<128, 16, 4, 1, 4, 2>;
 
+// A whole 32 x 32 tile per wave, the four waves of a workgroup each with a quarter
+// of K and stage buffers of its own (no barriers); for launches that could not
+// fill the chip otherwise and whose K cannot be split over workgroups. Epi: how
+// the waves hold the tile once their sums are joined.
+struct C32K : TileCfg<32, 32, 1, 1, 4, 1> {
+    using Wave = TileCfg<32, 32, 1, 1, 4, 1>;
+    using Epi = TileCfg<32, 32, 2, 2, 4, 1>;
+    static constexpr int groups = 4, threads = 256, per_simd = 1;
+    static constexpr int lds_bytes = Wave::lds_bytes * groups;
+};
+template <typename C>
+constexpr bool kSplitWaves = std::is_same<C, C32K>::value;
+template <typename C>
+struct EpiOf {
+    using type = C;
+};
+template <>
+struct EpiOf<C32K> {
+    using type = C32K::Epi;
+};
+
 // where granules past the end of K are read from
 __device__ __align__(16) static const uint4 zero_granule = {0, 0, 0, 0};
 
@@ -91,7 +112,8 @@ struct TileLoad {
                                          int lane)
     {
         kstride = ld_bytes;
-        const int n = int(count - first < TB ? count - first : TB);   // at least 1
+        if constexpr (!COLS) first = first < count ? first : count - 1;   // a tile of padding alone
+        const int n = int(count - first < TB ? count - first : TB);       // at least 1
         if constexpr (!COLS) {
             base = p + first * ld_bytes;
             step = 128;
@@ -266,12 +288,27 @@ struct TilePipe {
     static constexpr int PER = (D + FM - 1) / FM;             // copies per step
     static constexpr int TAIL = (STEPS - BS) * PER < D ? (STEPS - BS) * PER : D;   // copies that go out from BS on
 
+    static constexpr bool SOLO = kSplitWaves<C>;              // a wave by itself
+
     __device__ __forceinline__ TilePipe(char *smem)
-        : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), sm((lds_ptr)smem),
-          sbase(uint32_t(reinterpret_cast<uintptr_t>(sm)))
+        : lane(threadIdx.x & 63), wave(SOLO ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+          sm((lds_ptr)(SOLO ? smem + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (C::a_bytes + C::b_bytes) * NST
+                            : smem)),
+          sbase(__builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>(sm))))
     {
         ra.init(wave % C::WM * (C::BM / C::WM), lane);
         rb.init(wave / C::WM * (C::BN / C::WN), lane);
+    }
+
+    static __device__ __forceinline__ void sync()
+    {
+        if constexpr (SOLO) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0) only
+            asm volatile("" ::: "memory");
+        } else {
+            stage_barrier();
+        }
     }
 
     __device__ __forceinline__ void request(int s, int buf)
@@ -327,7 +364,7 @@ struct TilePipe {
             wait_vm<D * (NST - 1) + SINCE>();
         else
             wait_vm<D * (NST - 1)>();
-        stage_barrier();
+        sync();
 #pragma unroll
         for (int j = 0; j < FN; ++j) read_b(j, 0, 0);
 #pragma unroll
@@ -345,7 +382,7 @@ struct TilePipe {
                         wait_vm<D * (NST - 2)>();
                     else
                         wait_vm<0>();
-                    stage_barrier();
+                    sync();
                     now = s + NST <= last;
                     if (now && s + NST >= whole) {
                         request(s + NST, buf);
@@ -385,9 +422,29 @@ struct TilePipe {
             buf = next;
         }
         wait_vm<0>();
-        stage_barrier();                   // no wave reads the buffers any more
+        sync();                   // no wave reads the buffers any more
     }
 };
+
+// The four waves' sums of C32K's tile added in order: on return wave w holds block
+// (w % 2, w / 2) as its one block. smem: the stage buffers, no longer in use.
+template <typename C>
+__device__ __forceinline__ void join_waves(char *smem, const floatx4_t (&acc)[C::FM][C::FN], floatx4_t (&out)[1][1])
+{
+    floatx4_t *part = reinterpret_cast<floatx4_t *>(smem);    // [wave][block][lane], a wave's own buffers first
+    constexpr int STRIDE = C::Wave::lds_bytes / int(sizeof(floatx4_t));
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) part[wave * STRIDE + (j * 2 + i) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    floatx4_t t = part[wave * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) t += part[w * STRIDE + wave * 64 + lane];
+    out[0][0] = t;
+    __syncthreads();                           // the buffers may be written again
+}
 
 // 8 consecutive values of m per lane instead of 4: blocks i and i + 1 of a column
 // exchanged between neighbouring rows of 16 lanes, so that a half-precision store

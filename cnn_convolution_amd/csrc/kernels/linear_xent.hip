@@ -133,9 +133,10 @@ struct Tile {
     double half[3], f32[3];  // us per stage with 1, 2, 3 of them
     double fixed;            // us per tile before its epilogue
 };
-constexpr Tile kTiles[3] = {{256, 256, 1, {1.42, 0, 0}, {7.3, 0, 0}, 4.3},
+constexpr Tile kShapes[4] = {{256, 256, 1, {1.42, 0, 0}, {7.3, 0, 0}, 4.3},
                             {128, 128, 2, {0.69, 0.88, 0}, {1.9, 3.7, 0}, 2.7},
-                            {64, 64, 3, {0.30, 0.42, 0.53}, {0.60, 1.0, 1.45}, 1.3}};
+                            {64, 64, 3, {0.30, 0.42, 0.53}, {0.60, 1.0, 1.45}, 1.3},
+                            {32, 32, 1, {0.28, 0, 0}, {0.60, 0, 0}, 2.5}};   // K over four waves
 constexpr int kCus = 256;
 
 // microseconds of a product of M x N outputs over `stages` K stages that leaves
@@ -163,7 +164,7 @@ void pick_product(int64_t M, int64_t N, int64_t stages, int dtype, int *tile, in
         for (int sp = 1; sp <= 64; sp *= 2) {
             if (sp > 1 && (stages / sp < 4 || int64_t(sp) * M * N * 4 > kSlabBytes)) break;
             // the slabs are read once more, at about 3 TB/s, by a launch of their own
-            const double us = product_us(kTiles[t], M, N, stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
+            const double us = product_us(kShapes[t], M, N, stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
                               (sp > 1 ? 5.0 + double(sp) * double(M) * double(N) * 4 / 3e6 : 0.0);
             if (us < best * 0.98) {
                 best = us;
@@ -178,8 +179,9 @@ int pick_logits(int64_t M, int64_t N, int64_t stages, int dtype, bool narrow)
     if (narrow && N <= 16) return kTileNarrow;
     double best = 1e30;
     int tile = 0;
-    for (int t = 0; t < 3; ++t) {
-        const double us = product_us(kTiles[t], M, N, stages, 1, dtype, narrow ? 0 : int(elem(dtype)));
+    for (int t = 0; t < 4; ++t) {
+        const int64_t own = t == kTile32K ? ceil_div(stages, 4) : stages;
+        const double us = product_us(kShapes[t], M, N, own, 1, dtype, narrow ? 0 : int(elem(dtype)));
         if (us < best * 0.98) {
             best = us;
             tile = t;
@@ -214,7 +216,7 @@ XentPlan plan_xent_fwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw
     if (N == 0) return p;
     const int64_t es = elem(dtype);
     p.logits_tile = pick_logits(V, N, ceil_div(p.Dp * es, 128), dtype, true);
-    p.tiles_v = ceil_div(V, p.logits_tile == kTileNarrow ? 128 : kTiles[p.logits_tile].m);
+    p.tiles_v = ceil_div(V, p.logits_tile == kTileNarrow ? 128 : kShapes[p.logits_tile].m);
     if (p.copy_x) p.off_x = take(p, N * p.Dp * es);
     if (p.copy_w) p.off_w = take(p, V * p.Dp * es);
     p.off_partial = take(p, p.tiles_v * N * 8);

@@ -45,56 +45,75 @@ struct LogitTiles {
         strip_tile(t, tiles_m, tiles_n, tm, tn);
         m0 = int64_t(tm) * C::BM;
         n0 = int64_t(tn) * C::BN;
-        pipe.start(w, x, m0, n0, 0, stages);
+        if constexpr (kSplitWaves<C>) {
+            const int q = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            pipe.start(w, x, m0, n0, stages * q / C::groups, stages * (q + 1) / C::groups);
+        } else {
+            pipe.start(w, x, m0, n0, 0, stages);
+        }
+    }
+    // the tile's logits as the epilogue's waves hold them; `next` tiles are
+    // started meanwhile where the buffers allow it
+    template <int SINCE, typename E>
+    __device__ __forceinline__ void run(bool since, int next, char *smem, floatx4_t (&out)[E::FM][E::FN])
+    {
+        NoExtra none;
+        if constexpr (kSplitWaves<C>) {
+            floatx4_t acc[C::FM][C::FN];
+            pipe.template run<0>(false, acc, none);
+            join_waves<C>(smem, acc, out);
+        } else {
+            pipe.template run<SINCE>(since, out, none);
+        }
+        if (next < tiles_m * tiles_n) start(next);
     }
 };
 
 template <typename T, typename C>
 __global__ __launch_bounds__(C::threads, C::per_simd) void xent_loss_kernel(const LossArgs a, int tiles_m, int tiles_n)
 {
+    using E = typename EpiOf<C>::type;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     float2 *red = reinterpret_cast<float2 *>(smem + C::lds_bytes);   // [WM][BN], beside the stage buffers
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
-    const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;      // first class of this lane in the tile
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % E::WM, wn = wave / E::WM;
+    const int mw = wm * (E::BM / E::WM) + (lane >> 4) * 4;      // first class of this lane in the tile
     const int tiles = tiles_m * tiles_n;
     LogitTiles<T, C> lt(smem, a.r, 0, a.V, a.N, a.Dp, tiles_m, tiles_n);
-    NoExtra none;
     lt.start(blockIdx.x);
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t m0 = lt.m0, n0 = lt.n0;
-        const int left = int(min(int64_t(C::BM), a.V - m0)) - mw;   // classes of this lane that exist
+        const int left = int(min(int64_t(E::BM), a.V - m0)) - mw;   // classes of this lane that exist
         // the rows' targets among this lane's classes 16i + v, loaded ahead
-        int64_t target[C::FN];
+        int64_t target[E::FN];
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-            target[j] = a.target[min(n0 + wn * (C::BN / C::WN) + 16 * j + (lane & 15), a.N - 1)];
-        floatx4_t acc[C::FM][C::FN];
-        lt.pipe.template run<0>(false, acc, none);
-        if (tile + int(gridDim.x) < tiles) lt.start(tile + gridDim.x);
+        for (int j = 0; j < E::FN; ++j)
+            target[j] = a.target[min(n0 + wn * (E::BN / E::WN) + 16 * j + (lane & 15), a.N - 1)];
+        floatx4_t acc[E::FM][E::FN];
+        lt.template run<0, E>(false, tile + int(gridDim.x), smem, acc);
 
-        if (m0 + C::BM > a.V) {
+        if (m0 + E::BM > a.V) {
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
+            for (int i = 0; i < E::FM; ++i)
 #pragma unroll
-                for (int j = 0; j < C::FN; ++j)
+                for (int j = 0; j < E::FN; ++j)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         if (i * 16 + v >= left) acc[i][j][v] = -__builtin_inff();
         }
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-            const int col = wn * (C::BN / C::WN) + 16 * j + (lane & 15);
+        for (int j = 0; j < E::FN; ++j) {
+            const int col = wn * (E::BN / E::WN) + 16 * j + (lane & 15);
             const int64_t row = n0 + col, t = row < a.N ? target[j] - m0 - mw : -1;
-            if (__ballot(t >= 0 && t < C::FM * 16 && t < left && (t & 15) < 4)) {
+            if (__ballot(t >= 0 && t < E::FM * 16 && t < left && (t & 15) < 4)) {
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i)
+                for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         if (t == i * 16 + v && i * 16 + v < left) a.loss[row] = acc[i][j][v];
             }
             float m = acc[0][j][0];
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
+            for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) m = fmaxf(m, acc[i][j][v]);
             m = fmaxf(m, __shfl_xor(m, 16, 64));
@@ -102,26 +121,26 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_loss_kernel(cons
             const float mm = m == -__builtin_inff() ? 0.f : m;      // no class here: exp(-inf) = 0 below
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
+            for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, mm * -kLog2e));
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
-            if (lane < 16) red[wm * C::BN + col] = float2{m, s};
+            if (lane < 16) red[wm * E::BN + col] = float2{m, s};
         }
         // LDS accesses alone are waited for: the next tile's copies stay in flight.
         // The next writes to red come after the barriers of the next run().
         stage_barrier();
-        for (int col = threadIdx.x; col < C::BN && n0 + col < a.N; col += C::threads) {
+        for (int col = threadIdx.x; col < E::BN && n0 + col < a.N; col += C::threads) {
             float m = red[col].x;
 #pragma unroll
-            for (int w = 1; w < C::WM; ++w) m = fmaxf(m, red[w * C::BN + col].x);
+            for (int w = 1; w < E::WM; ++w) m = fmaxf(m, red[w * E::BN + col].x);
             const float mm = m == -__builtin_inff() ? 0.f : m;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < C::WM; ++w) s += red[w * C::BN + col].y * fast_exp(red[w * C::BN + col].x - mm);
-            a.partial[m0 / C::BM * a.N + n0 + col] = float2{m, s};
+            for (int w = 0; w < E::WM; ++w) s += red[w * E::BN + col].y * fast_exp(red[w * E::BN + col].x - mm);
+            a.partial[m0 / E::BM * a.N + n0 + col] = float2{m, s};
         }
     }
 }
@@ -129,50 +148,56 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_loss_kernel(cons
 template <typename T, typename C>
 __global__ __launch_bounds__(C::threads, C::per_simd) void xent_g_kernel(const GradArgs a, int tiles_m, int tiles_n)
 {
+    using E = typename EpiOf<C>::type;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    constexpr int STORES = sizeof(T) == 2 ? C::FM * C::FN / 2 : C::FM * C::FN;   // of a wave and tile
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
-    const int mw = wm * (C::BM / C::WM) + (lane >> 4) * 4;
+    constexpr bool PAIRS = sizeof(T) == 2 && E::FM % 2 == 0;
+    constexpr int STORES = PAIRS ? E::FM * E::FN / 2 : E::FM * E::FN;   // of a wave and tile
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % E::WM, wn = wave / E::WM;
+    const int mw = wm * (E::BM / E::WM) + (lane >> 4) * 4;
     const int tiles = tiles_m * tiles_n;
     const float S = a.scale ? a.scale[0] : 1.f;
     LogitTiles<T, C> lt(smem, a.r, a.v0, a.P, a.N, a.Dp, tiles_m, tiles_n);
-    NoExtra none;
     lt.start(blockIdx.x);
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t m0 = lt.m0, n0 = lt.n0, nw = n0 + wn * (C::BN / C::WN);
-        const int left = int(min(int64_t(C::BM), a.P - m0)) - mw;
+        const int64_t m0 = lt.m0, n0 = lt.n0, nw = n0 + wn * (E::BN / E::WN);
+        const int left = int(min(int64_t(E::BM), a.P - m0)) - mw;
         // of the rows of this lane's columns (below rows_pad), loaded ahead
-        int target[C::FN];
-        float grad[C::FN], lse[C::FN];
+        int target[E::FN];
+        float grad[E::FN], lse[E::FN];
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
+        for (int j = 0; j < E::FN; ++j) {
             const int64_t row = nw + 16 * j + (lane & 15), in = min(row, a.N - 1);
             target[j] = a.t32[row];
             grad[j] = a.grad[in];
             lse[j] = a.lse[in];
         }
-        floatx4_t acc[C::FM][C::FN];
-        lt.pipe.template run<STORES>(tile != int(blockIdx.x), acc, none);
-        if (tile + int(gridDim.x) < tiles) lt.start(tile + gridDim.x);
+        floatx4_t acc[E::FM][E::FN];
+        lt.template run<STORES, E>(tile != int(blockIdx.x), tile + int(gridDim.x), smem, acc);
 
         if constexpr (sizeof(T) == 2) {
             // which 32 x 32 blocks of G hold a target
-            const int64_t cw = a.v0 + m0 + wm * (C::BM / C::WM);
+            const int64_t cw = a.v0 + m0 + wm * (E::BM / E::WM);
+            if constexpr (E::FM == 1) {
+                // one block per workgroup: every wave sees its 32 rows
+                const int64_t c = a.t32[n0 + (lane & 31)] - a.v0 - m0;
+                const bool any = __ballot(c >= 0 && c < 32) != 0;
+                if (threadIdx.x == 0) a.hits[m0 / 32 * a.ldh + n0 / 32] = any ? 1 : 0;
+            }
 #pragma unroll
-            for (int r = 0; r < C::FN / 2; ++r) {
+            for (int r = 0; r < E::FN / 2; ++r) {
                 const int64_t c0 = target[2 * r] - cw, c1 = target[2 * r + 1] - cw;
 #pragma unroll
-                for (int b = 0; b < C::FM / 2; ++b) {
+                for (int b = 0; b < E::FM / 2; ++b) {
                     const bool any = __ballot((c0 >= 32 * b && c0 < 32 * b + 32) ||
                                               (c1 >= 32 * b && c1 < 32 * b + 32)) != 0;
                     if (lane == 0)
-                        a.hits[((m0 + wm * (C::BM / C::WM)) / 32 + b) * a.ldh + nw / 32 + r] = any ? 1 : 0;
+                        a.hits[((m0 + wm * (E::BM / E::WM)) / 32 + b) * a.ldh + nw / 32 + r] = any ? 1 : 0;
                 }
             }
         }
-        const bool edge = m0 + C::BM > a.P;
+        const bool edge = m0 + E::BM > a.P;
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
+        for (int j = 0; j < E::FN; ++j) {
             const int64_t row = nw + 16 * j + (lane & 15);
             const int t = target[j];
             const bool ok = t >= 0;
@@ -180,21 +205,21 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_g_kernel(const G
             // exp(l - lse) as one fma and exp2: the rounding of lse * log2(e) is of
             // the size of lse's own
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
+            for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     acc[i][j][v] = gs * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, c));
             if (__ballot(!ok) || edge) {
                 // masked rows and classes past the end: selected away, never multiplied
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i)
+                for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) acc[i][j][v] = ok && i * 16 + v < left ? acc[i][j][v] : 0.f;
             }
             const int64_t tl = ok ? t - a.v0 - m0 - mw : -1;
-            if (__ballot(tl >= 0 && tl < C::FM * 16 && (tl & 15) < 4)) {
+            if (__ballot(tl >= 0 && tl < E::FM * 16 && (tl & 15) < 4)) {
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i)
+                for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         if (tl == i * 16 + v) {
@@ -205,15 +230,17 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_g_kernel(const G
                         }
             }
             T *g = static_cast<T *>(a.g) + row * a.ldg + m0;
-            if constexpr (sizeof(T) == 2) {
-                const int m8 = wm * (C::BM / C::WM) + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+            if constexpr (PAIRS) {
+                const int m8 = wm * (E::BM / E::WM) + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
 #pragma unroll
-                for (int i = 0; i < C::FM; i += 2) *reinterpret_cast<uint4 *>(g + m8 + i * 16) =
+                for (int i = 0; i < E::FM; i += 2) *reinterpret_cast<uint4 *>(g + m8 + i * 16) =
                     pair_blocks<T>(acc[i][j], acc[i + 1][j]);
             } else {
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i)
-                    *reinterpret_cast<floatx4_t *>(g + mw + i * 16) = acc[i][j];
+                for (int i = 0; i < E::FM; ++i) {
+                    const float q[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    store_vec<4>(g + mw + i * 16, q);
+                }
             }
         }
     }
@@ -226,7 +253,8 @@ hipError_t launch_tiles(K kernel, int lds, std::atomic<uint64_t> &allowed, const
     if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), lds, allowed);
     if (e != hipSuccess) return e;
-    const int64_t grid = std::min(tm * tn, int64_t(C::per_cu) * 256);
+    // C32K joins its waves in the stage buffers: a workgroup per tile
+    const int64_t grid = kSplitWaves<C> ? tm * tn : std::min(tm * tn, int64_t(C::per_cu) * 256);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), lds, s, a, int(tm), int(tn));
     return hipGetLastError();
 }
@@ -234,10 +262,12 @@ hipError_t launch_tiles(K kernel, int lds, std::atomic<uint64_t> &allowed, const
 template <typename T>
 hipError_t loss_tile(const LossArgs &a, int tile, hipStream_t s)
 {
-    static std::atomic<uint64_t> allowed[4];
+    static std::atomic<uint64_t> allowed[kTiles];
     switch (tile) {
     case kTile256: return launch_tiles<C256>(xent_loss_kernel<T, C256>, C256::lds_bytes + C256::WM * C256::BN * 8, allowed[kTile256], a, a.V, a.N, s);
     case kTile128: return launch_tiles<C128>(xent_loss_kernel<T, C128>, C128::lds_bytes + C128::WM * C128::BN * 8, allowed[kTile128], a, a.V, a.N, s);
+    case kTile32K:
+        return launch_tiles<C32K>(xent_loss_kernel<T, C32K>, C32K::lds_bytes + 2 * 32 * 8, allowed[kTile32K], a, a.V, a.N, s);
     case kTile64: return launch_tiles<C64>(xent_loss_kernel<T, C64>, C64::lds_bytes + C64::WM * C64::BN * 8, allowed[kTile64], a, a.V, a.N, s);
     default: return launch_tiles<CNarrow>(xent_loss_kernel<T, CNarrow>, CNarrow::lds_bytes + CNarrow::WM * CNarrow::BN * 8, allowed[kTileNarrow], a, a.V, a.N, s);
     }
@@ -246,10 +276,14 @@ hipError_t loss_tile(const LossArgs &a, int tile, hipStream_t s)
 template <typename T>
 hipError_t g_tile(const GradArgs &a, int tile, hipStream_t s)
 {
-    static std::atomic<uint64_t> allowed[4];
+    static std::atomic<uint64_t> allowed[kTiles];
     switch (tile) {
     case kTile256: return launch_tiles<C256>(xent_g_kernel<T, C256>, C256::lds_bytes, allowed[kTile256], a, a.P, a.N, s);
     case kTile128: return launch_tiles<C128>(xent_g_kernel<T, C128>, C128::lds_bytes, allowed[kTile128], a, a.P, a.N, s);
+    case kTile32K:
+        // the products read G in whole stages of 64: the padding is written too
+        return launch_tiles<C32K>(xent_g_kernel<T, C32K>, C32K::lds_bytes, allowed[kTile32K], a, (a.P + 63) / 64 * 64,
+                                  (a.N + 63) / 64 * 64, s);
     default: return launch_tiles<C64>(xent_g_kernel<T, C64>, C64::lds_bytes, allowed[kTile64], a, a.P, a.N, s);
     }
 }
