@@ -367,6 +367,15 @@ def test_linear_cross_entropy_in_several_pieces(N, V, D, dt):
     _check_xent(*_xent_case(N, V, D, dt, seed=1), dt, ref_dev=DEV, what="pieces")
 
 
+@pytest.mark.parametrize("N,V,D", [(2100, 9000, 520), (3000, 40, 200), (2500, 130, 264), (16, 40000, 264),
+                                   (700, 33000, 260), (1, 70001, 136), (200, 100, 4096), (33, 300, 2500)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_linear_cross_entropy_tile_shapes(N, V, D, dt):
+    """Many tiles per workgroup, targets in every block of G, few rows against
+    many classes, long K split over workgroups and over waves."""
+    _check_xent(*_xent_case(N, V, D, dt, seed=N), dt, ref_dev=DEV, what="tiles")
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 def test_linear_cross_entropy_strided_and_unaligned(dt):
     N, V, D = 70, 300, 104
@@ -553,6 +562,21 @@ def test_workspace_contents_are_never_read_before_written(dt):
         conv.linear_cross_entropy_backward_into(up, x, w, t, lse, dx, dw, ws)
         outs.append([loss, lse, dx, dw])
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_example_head_learns(dt):
+    """The example's head on frozen convolution features: the held-out loss falls
+    from about log(classes) well below it."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_head.py")
+    spec = importlib.util.spec_from_file_location("train_head", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses, before, after = mod.train(steps=60, classes=200, dtype=TYPES[dt])
+    _say(f"example {dt}: {before:.3f} -> {after:.3f}, last steps {losses[-3:]}")
+    assert all(np.isfinite(losses)) and before > 4.0 and after < 0.5 * before
 
 
 def test_python_refusals():
