@@ -28,7 +28,7 @@
 namespace im2win {
 
 // BM x BN tile by WM x WN waves, NST stage buffers; per_cu: workgroups that a CU
-// holds (LDS), and that a launch has for each
+// holds (LDS)
 template <int BM_, int BN_, int WM_, int WN_, int NST_, int PER_CU>
 struct TileCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, per_cu = PER_CU;
@@ -40,7 +40,18 @@ struct TileCfg {
 using C256 = TileCfg<256, 256, 2, 4, 2, 1>;
 using C128 = TileCfg<128, 128, 2, 2, 2, 2>;
 using C64 = TileCfg<64, 64, 2, 2, 3, 3>;
+using C64x32 = TileCfg<64, 32, 2, 2, 3, 4>;
 using CNarrow = TileCfg<128, 16, 4, 1, 4, 2>;
+
+// Workgroups of a launch over `tiles` tiles. Where a CU holds one workgroup, as many
+// as CUs, each taking every grid-th tile and starting the next one's copies
+// before its epilogue; where it holds several, one per tile: a neighbour's
+// products cover the epilogue, and the CUs that finish first take what is left.
+template <typename C>
+inline int64_t grid_of(int64_t tiles)
+{
+    return C::per_cu == 1 && tiles > 256 ? 256 : tiles;
+}
 
 // A whole 32 x 32 tile per wave, the four waves of a workgroup each with a quarter
 // of K and stage buffers of its own (no barriers); for launches that could not

@@ -130,28 +130,32 @@ hipError_t with_type(int dtype, F f)
 struct Tile {
     int64_t m, n;
     int per_cu;              // workgroups a CU holds
-    double half[3], f32[3];  // us per stage with 1, 2, 3 of them
+    double half[4], f32[4];  // us per stage with 1, 2, .. of them
     double fixed;            // us per tile before its epilogue
 };
-constexpr Tile kShapes[4] = {{256, 256, 1, {1.42, 0, 0}, {7.3, 0, 0}, 4.3},
-                            {128, 128, 2, {0.69, 0.88, 0}, {1.9, 3.7, 0}, 2.7},
-                            {64, 64, 3, {0.30, 0.42, 0.53}, {0.60, 1.0, 1.45}, 1.3},
-                            {32, 32, 1, {0.28, 0, 0}, {0.60, 0, 0}, 2.5}};   // K over four waves
-constexpr int kCus = 256;
+constexpr Tile kShapes[5] = {{256, 256, 1, {1.42}, {7.3}, 4.3},
+                             {128, 128, 2, {0.69, 0.88}, {1.9, 3.7}, 2.7},
+                             {64, 64, 3, {0.30, 0.42, 0.53}, {0.48, 0.93, 1.4}, 1.3},
+                             {32, 32, 1, {0.28}, {0.60}, 2.5},              // K over four waves
+                             {64, 32, 4, {0.25, 0.30, 0.36, 0.42}, {0.30, 0.50, 0.73, 0.95}, 1.3}};
+constexpr int64_t kCus = 256;
 
 // microseconds of a product of M x N outputs over `stages` K stages that leaves
 // out_bytes per output
 double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split, int dtype, int out_bytes)
 {
     const int64_t wgs = ceil_div(M, t.m) * ceil_div(N, t.n) * split;
-    const int held = int(std::min<int64_t>(t.per_cu, ceil_div(wgs, kCus)));
-    const double rounds = double(ceil_div(wgs, int64_t(kCus) * held));
-    const double stage = (dtype == 0 ? t.f32 : t.half)[held - 1];
-    // an epilogue: 7 us for 65536 exponentials on a CU, or its stores at a CU's
-    // share of the memory bandwidth; half of it hidden by a neighbour's products
-    const double outputs = double(held * t.m * t.n);
-    const double epilogue = std::max(outputs * 7.0 / 65536, outputs * out_bytes / 2e4) * (held > 1 ? 0.5 : 1.0);
-    return rounds * (stage * double(ceil_div(stages, split)) + t.fixed + epilogue);
+    const int64_t of_cu = ceil_div(wgs, kCus);                    // the busiest CU's
+    const auto held_us = [&](int64_t held) {
+        if (held == 0) return 0.0;
+        const double stage = (dtype == 0 ? t.f32 : t.half)[held - 1];
+        // an epilogue: 7 us for 65536 exponentials on a CU, or its stores at a CU's
+        // share of the memory bandwidth; half of it hidden by a neighbour's products
+        const double outputs = double(held * t.m * t.n);
+        const double epilogue = std::max(outputs * 7.0 / 65536, outputs * out_bytes / 2e4) * (held > 1 ? 0.5 : 1.0);
+        return stage * double(ceil_div(stages, split)) + t.fixed + epilogue;
+    };
+    return double(of_cu / t.per_cu) * held_us(t.per_cu) + held_us(of_cu % t.per_cu);
 }
 
 constexpr int64_t kSlabBytes = int64_t(256) << 20;
@@ -179,7 +183,7 @@ int pick_logits(int64_t M, int64_t N, int64_t stages, int dtype, bool narrow)
     if (narrow && N <= 16) return kTileNarrow;
     double best = 1e30;
     int tile = 0;
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 5; ++t) {
         const int64_t own = t == kTile32K ? ceil_div(stages, 4) : stages;
         const double us = product_us(kShapes[t], M, N, own, 1, dtype, narrow ? 0 : int(elem(dtype)));
         if (us < best * 0.98) {

@@ -177,11 +177,13 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_g_kernel(const G
         if constexpr (sizeof(T) == 2) {
             // which 32 x 32 blocks of G hold a target
             const int64_t cw = a.v0 + m0 + wm * (E::BM / E::WM);
-            if constexpr (E::FM == 1) {
-                // one block per workgroup: every wave sees its 32 rows
-                const int64_t c = a.t32[n0 + (lane & 31)] - a.v0 - m0;
+            if constexpr (E::FN == 1) {
+                // a block's rows are shared by waves: each sees all 32 of them, the
+                // first wave of each block of classes writes
+                static_assert(E::BN == 32 && (E::FM == 1 || E::FM == 2), "one block of rows");
+                const int64_t b32 = m0 + wm * (E::BM / E::WM) / 32 * 32, c = a.t32[n0 + (lane & 31)] - a.v0 - b32;
                 const bool any = __ballot(c >= 0 && c < 32) != 0;
-                if (threadIdx.x == 0) a.hits[m0 / 32 * a.ldh + n0 / 32] = any ? 1 : 0;
+                if (lane == 0 && wn == 0) a.hits[b32 / 32 * a.ldh + n0 / 32] = any ? 1 : 0;
             }
 #pragma unroll
             for (int r = 0; r < E::FN / 2; ++r) {
@@ -254,7 +256,7 @@ hipError_t launch_tiles(K kernel, int lds, std::atomic<uint64_t> &allowed, const
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), lds, allowed);
     if (e != hipSuccess) return e;
     // C32K joins its waves in the stage buffers: a workgroup per tile
-    const int64_t grid = kSplitWaves<C> ? tm * tn : std::min(tm * tn, int64_t(C::per_cu) * 256);
+    const int64_t grid = kSplitWaves<C> ? tm * tn : grid_of<C>(tm * tn);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), lds, s, a, int(tm), int(tn));
     return hipGetLastError();
 }
@@ -266,6 +268,9 @@ hipError_t loss_tile(const LossArgs &a, int tile, hipStream_t s)
     switch (tile) {
     case kTile256: return launch_tiles<C256>(xent_loss_kernel<T, C256>, C256::lds_bytes + C256::WM * C256::BN * 8, allowed[kTile256], a, a.V, a.N, s);
     case kTile128: return launch_tiles<C128>(xent_loss_kernel<T, C128>, C128::lds_bytes + C128::WM * C128::BN * 8, allowed[kTile128], a, a.V, a.N, s);
+    case kTile64x32:
+        return launch_tiles<C64x32>(xent_loss_kernel<T, C64x32>, C64x32::lds_bytes + 2 * 32 * 8, allowed[kTile64x32], a, a.V,
+                                    a.N, s);
     case kTile32K:
         return launch_tiles<C32K>(xent_loss_kernel<T, C32K>, C32K::lds_bytes + 2 * 32 * 8, allowed[kTile32K], a, a.V, a.N, s);
     case kTile64: return launch_tiles<C64>(xent_loss_kernel<T, C64>, C64::lds_bytes + C64::WM * C64::BN * 8, allowed[kTile64], a, a.V, a.N, s);
@@ -284,6 +289,9 @@ hipError_t g_tile(const GradArgs &a, int tile, hipStream_t s)
         // the products read G in whole stages of 64: the padding is written too
         return launch_tiles<C32K>(xent_g_kernel<T, C32K>, C32K::lds_bytes, allowed[kTile32K], a, (a.P + 63) / 64 * 64,
                                   (a.N + 63) / 64 * 64, s);
+    case kTile64x32:
+        return launch_tiles<C64x32>(xent_g_kernel<T, C64x32>, C64x32::lds_bytes, allowed[kTile64x32], a, a.P,
+                                    (a.N + 63) / 64 * 64, s);
     default: return launch_tiles<C64>(xent_g_kernel<T, C64>, C64::lds_bytes, allowed[kTile64], a, a.P, a.N, s);
     }
 }

@@ -286,7 +286,7 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
     if (e != hipSuccess) return e;
     const int64_t all = tm * tn * a.split;
-    const int64_t grid = DW && sizeof(T) == 2 ? all : std::min(all, int64_t(C::per_cu) * 256);
+    const int64_t grid = DW && sizeof(T) == 2 ? all : grid_of<C>(all);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), C::lds_bytes, s, a, int(tm), int(tn));
     return hipGetLastError();
 }

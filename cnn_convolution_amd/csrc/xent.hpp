@@ -25,7 +25,7 @@ inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t>
 }
 
 // tile shapes of the products (classes or features x rows or classes)
-enum XentTile { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32K = 3, kTileNarrow = 4, kTiles = 5 };
+enum XentTile { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32K = 3, kTile64x32 = 4, kTileNarrow = 5, kTiles = 6 };
 
 // What a call does, from its sizes alone. Offsets are into the workspace.
 struct XentPlan {
