@@ -41,16 +41,21 @@ using C256 = TileCfg<256, 256, 2, 4, 2, 1>;
 using C128 = TileCfg<128, 128, 2, 2, 2, 2>;
 using C64 = TileCfg<64, 64, 2, 2, 3, 3>;
 using C64x32 = TileCfg<64, 32, 2, 2, 3, 4>;
+// for few rows, bound by the one read of W: four buffers in flight beat eight (1 row,
+// 65536 x 2048 bf16 61.6 us, with eight 67.5; half as wide with two waves 65.3)
 using CNarrow = TileCfg<128, 16, 4, 1, 4, 2>;
 
-// Workgroups of a launch over `tiles` tiles. Where a CU holds one workgroup, as many
-// as CUs, each taking every grid-th tile and starting the next one's copies
-// before its epilogue; where it holds several, one per tile: a neighbour's
-// products cover the epilogue, and the CUs that finish first take what is left.
+// Workgroups of a launch over `tiles` tiles of `stages` K stages. Where a CU holds
+// one workgroup, or the tiles are short, as many as the chip holds, each taking
+// every grid-th tile and starting the next one's copies before its epilogue; else
+// one per tile: a neighbour's products cover the epilogue, and the CUs that
+// finish first take what is left. (dw of 69 rows, 64798 classes, 256 features, whose
+// tiles have two stages: 103 us with a workgroup per tile, 90 so.)
 template <typename C>
-inline int64_t grid_of(int64_t tiles)
+inline int64_t grid_of(int64_t tiles, int64_t stages)
 {
-    return C::per_cu == 1 && tiles > 256 ? 256 : tiles;
+    const int64_t held = int64_t(C::per_cu) * 256;
+    return (C::per_cu == 1 || stages <= 4) && tiles > held ? held : tiles;
 }
 
 // A whole 32 x 32 tile per wave, the four waves of a workgroup each with a quarter

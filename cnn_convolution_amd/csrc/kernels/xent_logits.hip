@@ -249,14 +249,15 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_g_kernel(const G
 }
 
 template <typename C, typename K, typename A>
-hipError_t launch_tiles(K kernel, int lds, std::atomic<uint64_t> &allowed, const A &a, int64_t M, int64_t N, hipStream_t s)
+hipError_t launch_tiles(K kernel, int lds, std::atomic<uint64_t> &allowed, const A &a, int64_t stages,
+                        int64_t M, int64_t N, hipStream_t s)
 {
     const int64_t tm = (M + C::BM - 1) / C::BM, tn = (N + C::BN - 1) / C::BN;
     if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), lds, allowed);
     if (e != hipSuccess) return e;
     // C32K joins its waves in the stage buffers: a workgroup per tile
-    const int64_t grid = kSplitWaves<C> ? tm * tn : grid_of<C>(tm * tn);
+    const int64_t grid = kSplitWaves<C> ? tm * tn : grid_of<C>(tm * tn, stages);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), lds, s, a, int(tm), int(tn));
     return hipGetLastError();
 }
@@ -265,16 +266,17 @@ template <typename T>
 hipError_t loss_tile(const LossArgs &a, int tile, hipStream_t s)
 {
     static std::atomic<uint64_t> allowed[kTiles];
+    const int64_t stages = (a.Dp * int64_t(sizeof(T)) + 127) / 128;
     switch (tile) {
-    case kTile256: return launch_tiles<C256>(xent_loss_kernel<T, C256>, C256::lds_bytes + C256::WM * C256::BN * 8, allowed[kTile256], a, a.V, a.N, s);
-    case kTile128: return launch_tiles<C128>(xent_loss_kernel<T, C128>, C128::lds_bytes + C128::WM * C128::BN * 8, allowed[kTile128], a, a.V, a.N, s);
+    case kTile256: return launch_tiles<C256>(xent_loss_kernel<T, C256>, C256::lds_bytes + C256::WM * C256::BN * 8, allowed[kTile256], a, stages, a.V, a.N, s);
+    case kTile128: return launch_tiles<C128>(xent_loss_kernel<T, C128>, C128::lds_bytes + C128::WM * C128::BN * 8, allowed[kTile128], a, stages, a.V, a.N, s);
     case kTile64x32:
-        return launch_tiles<C64x32>(xent_loss_kernel<T, C64x32>, C64x32::lds_bytes + 2 * 32 * 8, allowed[kTile64x32], a, a.V,
+        return launch_tiles<C64x32>(xent_loss_kernel<T, C64x32>, C64x32::lds_bytes + 2 * 32 * 8, allowed[kTile64x32], a, stages, a.V,
                                     a.N, s);
     case kTile32K:
-        return launch_tiles<C32K>(xent_loss_kernel<T, C32K>, C32K::lds_bytes + 2 * 32 * 8, allowed[kTile32K], a, a.V, a.N, s);
-    case kTile64: return launch_tiles<C64>(xent_loss_kernel<T, C64>, C64::lds_bytes + C64::WM * C64::BN * 8, allowed[kTile64], a, a.V, a.N, s);
-    default: return launch_tiles<CNarrow>(xent_loss_kernel<T, CNarrow>, CNarrow::lds_bytes + CNarrow::WM * CNarrow::BN * 8, allowed[kTileNarrow], a, a.V, a.N, s);
+        return launch_tiles<C32K>(xent_loss_kernel<T, C32K>, C32K::lds_bytes + 2 * 32 * 8, allowed[kTile32K], a, stages, a.V, a.N, s);
+    case kTile64: return launch_tiles<C64>(xent_loss_kernel<T, C64>, C64::lds_bytes + C64::WM * C64::BN * 8, allowed[kTile64], a, stages, a.V, a.N, s);
+    default: return launch_tiles<CNarrow>(xent_loss_kernel<T, CNarrow>, CNarrow::lds_bytes + CNarrow::WM * CNarrow::BN * 8, allowed[kTileNarrow], a, stages, a.V, a.N, s);
     }
 }
 
@@ -282,17 +284,18 @@ template <typename T>
 hipError_t g_tile(const GradArgs &a, int tile, hipStream_t s)
 {
     static std::atomic<uint64_t> allowed[kTiles];
+    const int64_t stages = (a.Dp * int64_t(sizeof(T)) + 127) / 128;
     switch (tile) {
-    case kTile256: return launch_tiles<C256>(xent_g_kernel<T, C256>, C256::lds_bytes, allowed[kTile256], a, a.P, a.N, s);
-    case kTile128: return launch_tiles<C128>(xent_g_kernel<T, C128>, C128::lds_bytes, allowed[kTile128], a, a.P, a.N, s);
+    case kTile256: return launch_tiles<C256>(xent_g_kernel<T, C256>, C256::lds_bytes, allowed[kTile256], a, stages, a.P, a.N, s);
+    case kTile128: return launch_tiles<C128>(xent_g_kernel<T, C128>, C128::lds_bytes, allowed[kTile128], a, stages, a.P, a.N, s);
     case kTile32K:
         // the products read G in whole stages of 64: the padding is written too
-        return launch_tiles<C32K>(xent_g_kernel<T, C32K>, C32K::lds_bytes, allowed[kTile32K], a, (a.P + 63) / 64 * 64,
+        return launch_tiles<C32K>(xent_g_kernel<T, C32K>, C32K::lds_bytes, allowed[kTile32K], a, stages, (a.P + 63) / 64 * 64,
                                   (a.N + 63) / 64 * 64, s);
     case kTile64x32:
-        return launch_tiles<C64x32>(xent_g_kernel<T, C64x32>, C64x32::lds_bytes, allowed[kTile64x32], a, a.P,
+        return launch_tiles<C64x32>(xent_g_kernel<T, C64x32>, C64x32::lds_bytes, allowed[kTile64x32], a, stages, a.P,
                                     (a.N + 63) / 64 * 64, s);
-    default: return launch_tiles<C64>(xent_g_kernel<T, C64>, C64::lds_bytes, allowed[kTile64], a, a.P, a.N, s);
+    default: return launch_tiles<C64>(xent_g_kernel<T, C64>, C64::lds_bytes, allowed[kTile64], a, stages, a.P, a.N, s);
     }
 }
 

@@ -102,9 +102,9 @@ __device__ __forceinline__ void product_tiles(const ProductArgs &a, int tiles_m,
         n0 = int64_t(tn) * C::BN;
         pipe.start(A, B, m0, n0, int(int64_t(nk) * part / a.split), int(int64_t(nk) * (part + 1) / a.split));
     };
-    // dw in half precision has no registers left for the next tile's addresses: its
-    // launch has a workgroup for every tile
-    constexpr bool ONE = DW && HALF;
+    // dw in half precision with the largest tile has no registers left for the next
+    // tile's addresses: its launch has a workgroup for every tile
+    constexpr bool ONE = DW && HALF && C::FM == 8;
     start(begin);
     bool stored = false;                       // the last epilogue stored a whole tile
     for (int t = begin; t < all; t += ONE ? all : step) {
@@ -286,7 +286,8 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
     if (e != hipSuccess) return e;
     const int64_t all = tm * tn * a.split;
-    const int64_t grid = DW && sizeof(T) == 2 ? all : grid_of<C>(all);
+    const int64_t stages = (a.K * int64_t(sizeof(T)) + 127) / 128 / a.split;
+    const int64_t grid = DW && sizeof(T) == 2 && C::FM == 8 ? all : grid_of<C>(all, stages);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), C::lds_bytes, s, a, int(tm), int(tn));
     return hipGetLastError();
 }
