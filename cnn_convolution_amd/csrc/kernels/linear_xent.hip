@@ -142,13 +142,14 @@ constexpr int64_t kCus = 256;
 
 // microseconds of a product of M x N outputs over `stages` K stages that leaves
 // out_bytes per output
-double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split, int dtype, int out_bytes)
+double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split, int dtype, int out_bytes,
+                  double hit_us = 0.0)
 {
     const int64_t wgs = ceil_div(M, t.m) * ceil_div(N, t.n) * split;
     const int64_t of_cu = ceil_div(wgs, kCus);                    // the busiest CU's
     const auto held_us = [&](int64_t held) {
         if (held == 0) return 0.0;
-        const double stage = (dtype == 0 ? t.f32 : t.half)[held - 1];
+        const double stage = (dtype == 0 ? t.f32 : t.half)[held - 1] + hit_us;
         // an epilogue: 7 us for 65536 exponentials on a CU, or its stores at a CU's
         // share of the memory bandwidth; half of it hidden by a neighbour's products
         const double outputs = double(held * t.m * t.n);
@@ -161,14 +162,17 @@ double product_us(const Tile &t, int64_t M, int64_t N, int64_t stages, int split
 constexpr int64_t kSlabBytes = int64_t(256) << 20;
 
 // tile and split of a product whose K may be split
-void pick_product(int64_t M, int64_t N, int64_t stages, int dtype, int *tile, int *split)
+void pick_product(int64_t M, int64_t N, int64_t stages, int dtype, int64_t classes, int *tile, int *split)
 {
     double best = 1e30;
-    for (int t = 0; t < 3; ++t)
+    for (int t = 0; t < 3; ++t) {
+        // dw in half precision: a stage of 64 rows with a target among a wave's 64
+        // (tiles of 64: 32) classes takes about 0.9 us more
+        const double hits = classes && dtype ? std::min(1.0, 64.0 * (kShapes[t].n == 64 ? 32 : 64) / double(classes)) : 0.0;
         for (int sp = 1; sp <= 64; sp *= 2) {
             if (sp > 1 && (stages / sp < 4 || int64_t(sp) * M * N * 4 > kSlabBytes)) break;
             // the slabs are read once more, at about 3 TB/s, by a launch of their own
-            const double us = product_us(kShapes[t], M, N, stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
+            const double us = product_us(kShapes[t], M, N, stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype)), 0.9 * hits) +
                               (sp > 1 ? 5.0 + double(sp) * double(M) * double(N) * 4 / 3e6 : 0.0);
             if (us < best * 0.98) {
                 best = us;
@@ -176,6 +180,7 @@ void pick_product(int64_t M, int64_t N, int64_t stages, int dtype, int *tile, in
                 *split = sp;
             }
         }
+    }
 }
 
 int pick_logits(int64_t M, int64_t N, int64_t stages, int dtype, bool narrow)
@@ -239,8 +244,8 @@ XentPlan plan_xent_bwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw
     p.piece = std::min(round_up(V, 256), most);
     const int64_t P = std::min(V, p.piece);
     p.logits_tile = pick_logits(P, N, ceil_div(p.Dp * es, 128), dtype, false);
-    pick_product(D, N, ceil_div(P, ki), dtype, &p.dx_tile, &p.dx_split);
-    pick_product(D, P, ceil_div(N, ki), dtype, &p.dw_tile, &p.dw_split);
+    pick_product(D, N, ceil_div(P, ki), dtype, 0, &p.dx_tile, &p.dx_split);
+    pick_product(D, P, ceil_div(N, ki), dtype, V, &p.dw_tile, &p.dw_split);
     p.dx_direct = p.dx_split == 1 && P == V;
     p.off_scale = take(p, 8);
     p.off_t32 = take(p, p.rows_pad * 4);
