@@ -1,12 +1,14 @@
 // Layer norm over the channels of NCHW feature maps: forward and backward.
 // Bound by HBM like the row kernels; here a position's channels are P elements
-// apart, so a workgroup takes a tile of 64 consecutive positions of one image
-// and all its channels. Thread (g, l) holds positions 4l .. 4l+3 (one vector
-// load per channel, 16 lanes reading consecutive memory) of KR channels g, g +
-// groups, ...; a wave adds its channels in registers, the waves' sums meet in
-// LDS. Backward, a thread's share of dweight and dbias stays in registers over
-// all tiles the workgroup takes. Maps of more than 512 channels, or fewer than 4
-// positions, are read again for each pass.
+// apart, so a workgroup takes a tile of consecutive positions of one image and
+// all its channels. Thread (g, l) holds PV positions from PV l on (one vector load
+// per channel, PL lanes reading consecutive memory) of KR channels g, g + groups,
+// ...; a wave adds its channels in registers, the waves' sums meet in LDS.
+// Backward, a thread's share of dweight and dbias stays in registers over all
+// tiles the workgroup takes. Maps of more than 1024 channels, or fewer than 4
+// positions, are read again for each pass. Forward 64 channels of 56 x 56, 32
+// images, fp32 to fp16 11.5 us (3.4 TB/s: one wave of tiles); backward 256 channels
+// of 56 x 56, 64 images, fp32 124 us (5.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -19,8 +21,8 @@ namespace {
 
 constexpr int kPosLanes = 16, kPos = 64;       // lanes, and positions of a tile of 4 per lane
 
-// v[e] over the lanes of a wave that hold the same positions
-template <int PV>
+// v[e] over the lanes of a wave that hold the same positions, every PL-th
+template <int PV, int PL = kPosLanes>
 __device__ __forceinline__ void wave_chan_sum(float (&v)[PV])
 {
 #pragma unroll
@@ -30,18 +32,20 @@ __device__ __forceinline__ void wave_chan_sum(float (&v)[PV])
         const uint32_t w = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
         const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
         v[e] = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+        if constexpr (PL == 8)                     // lane i and i + 8 of 16: a rotation by 8
+            v[e] += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v[e]), 0x128, 0xf, 0xf, true));
     }
 }
 
-// where this thread's positions lie, PV of them per lane
-template <int PV>
+// where this thread's positions lie, PV of them per lane, PL lanes a channel
+template <int PV, int PL = kPosLanes>
 struct TilePos {
     int64_t n, p, base;      // image, first position, offset of channel 0 there
     int left;                // positions that exist (<= 0: none)
     __device__ __forceinline__ TilePos(int64_t t, int tiles_p, int l, const NormArgs &a)
     {
         n = t / tiles_p;
-        p = (t - n * tiles_p) * (kPosLanes * PV) + l * PV;
+        p = (t - n * tiles_p) * (PL * PV) + l * PV;
         left = int(min(int64_t(PV), a.P - p));
         base = n * a.C * a.P;
     }
@@ -85,13 +89,62 @@ struct Window {
     }
 };
 
-// WAVES waves, 4 * WAVES channel groups; EXACT: P is a multiple of PV
-template <typename TX, typename TY, int WAVES, int KR, int PV, bool EXACT>
+// Dropout of a tile: the blocks of 16 * PV positions of KR channels overlap from
+// lane to lane, so the lanes of a channel group make each block once and pass
+// the kept bits through LDS (a Philox block per lane and channel, or two where P
+// is no multiple of 4, is what these kernels waited for: 384 channels of 7 x 7,
+// 2354 images, f16 backward 264 us, so 176; with P a multiple of 4 it is even,
+// 164 channels of 56 x 56, 97 images forward 93 and 101).
+template <int KR, int PV, int PL = kPosLanes>
+struct TileDrop {
+    static constexpr int BLOCKS = PL * PV / 8 + 1;                    // that a channel's positions may touch
+    static constexpr int ROUNDS = (KR * BLOCKS + PL - 1) / PL;
+    static constexpr int KW = 32 / PV, WORDS = (KR + KW - 1) / KW;    // channels per word of kept bits
+    static constexpr int BYTES = ROUNDS * PL + 4;                     // of a group
+    uint32_t keep[WORDS];
+
+    // the kept bits of channels g, g + G, ..; e0: the tile's first element in channel 0
+    __device__ __forceinline__ void make(uint8_t *bytes, int64_t e0, uint32_t P, int G, const DropSpec &d)
+    {
+        const int l = threadIdx.x % PL, g = threadIdx.x / PL;
+        uint8_t *mine = bytes + g * BYTES;
+        __builtin_amdgcn_sched_barrier(0);         // between the loads and their first use
+        before();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int job = r * PL + l, i = job / BLOCKS;
+            const uint64_t e = uint64_t(e0 + uint32_t(g + i * G) * int64_t(P));
+            mine[job] = uint8_t(keep_bits((e >> 3) + (job - i * BLOCKS), d));
+        }
+        before();
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) keep[k] = 0;
+#pragma unroll
+        for (int i = 0; i < KR; ++i) {
+            const uint32_t o = (uint32_t(e0 + uint32_t(g + i * G) * int64_t(P)) & 7) + l * PV;
+            const uint8_t *b = mine + i * BLOCKS + (o >> 3);
+            keep[i / KW] |= ((b[0] | b[1] << 8) >> (o & 7) & ((1u << PV) - 1)) << (i % KW * PV);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ bool kept(int i, int e) const { return (keep[i / KW] >> (i % KW * PV + e)) & 1; }
+
+private:
+    // a group lies within a wave, whose LDS accesses are in order
+    static __device__ __forceinline__ void before()
+    {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+};
+
+// WAVES waves, 64 / PL * WAVES channel groups; EXACT: P is a multiple of PV
+template <typename TX, typename TY, int WAVES, int KR, int PV, int PL, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArgs a, int tiles_p)
 {
-    constexpr int G = WAVES * 4;
-    __shared__ __align__(16) float red[2][WAVES][kPosLanes * PV];    // mean, squares
-    const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, wave = threadIdx.x >> 6, C = a.C;
+    constexpr int GW = 64 / PL, G = WAVES * GW;
+    __shared__ __align__(16) float red[2][WAVES][PL * PV];    // mean, squares
+    const int l = threadIdx.x % PL, g = threadIdx.x / PL, wave = threadIdx.x >> 6, C = a.C;
     const float fc = float(C);
     const uint32_t P = uint32_t(a.P);
     float w[KR], b[KR];
@@ -105,18 +158,21 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
     auto count = [&](int q) {
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < KR; ++i) n += max(0, min(4, C - i * G - q * 4));
+        for (int i = 0; i < KR; ++i) n += max(0, min(GW, C - i * G - q * GW));
         return float(n);
     };
-    const TilePos<PV> at(blockIdx.x, tiles_p, l, a);
+    const TilePos<PV, PL> at(blockIdx.x, tiles_p, l, a);
     const TX *x = static_cast<const TX *>(a.x) + at.base;
     TY *y = static_cast<TY *>(a.out) + at.base;
     const Window<PV> win(at.p, a.P);
+    TileDrop<KR, PV, PL> drop;
+    __shared__ uint8_t bytes[G * TileDrop<KR, PV, PL>::BYTES];
     // channels past the last read that one and count nowhere
     Raw<TX, PV> q[KR];
 #pragma unroll
     for (int i = 0; i < KR; ++i)
         q[i] = load_raw<TX, PV>(at_offset(x, uint32_t(min(g + i * G, C - 1)) * P + win.at));
+    if (a.drop.threshold) drop.make(bytes, at.base + at.p - l * PV, P, G, a.drop);
     if constexpr (!EXACT)
 #pragma unroll
         for (int i = 0; i < KR; ++i) shift_down(q[i], win.shift);
@@ -130,7 +186,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
         }
     // a wave's own mean and squared deviations, joined with one barrier:
     // sum (x - mean)^2 = sum_w [Q_w + n_w (mean_w - mean)^2]
-    wave_chan_sum(mean);
+    wave_chan_sum<PV, PL>(mean);
     const float nw = fmaxf(count(wave), 1.f);
 #pragma unroll
     for (int e = 0; e < PV; ++e) mean[e] /= nw;
@@ -141,8 +197,8 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
             const float d = v[i][e] - mean[e];
             sq[e] += g + i * G < C ? d * d : 0.f;
         }
-    wave_chan_sum(sq);
-    if ((threadIdx.x & 48) == 0)
+    wave_chan_sum<PV, PL>(sq);
+    if ((threadIdx.x & 63) < PL)
 #pragma unroll
         for (int e = 0; e < PV; ++e) {
             red[0][wave][l * PV + e] = mean[e];
@@ -177,7 +233,9 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
         const int c = g + i * G;
 #pragma unroll
         for (int e = 0; e < PV; ++e) v[i][e] = (v[i][e] - mean[e]) * rstd[e] * w[i] + b[i];
-        if (a.drop.threshold) drop_run<PV>(at.base + c * a.P + at.p, a.drop, v[i]);
+        if (a.drop.threshold)
+#pragma unroll
+            for (int e = 0; e < PV; ++e) v[i][e] = drop.kept(i, e) ? v[i][e] * a.drop.scale : 0.f;
         store_pos<EXACT>(at_offset(y, c * P + uint32_t(at.p)), c < C ? at.left : 0, v[i]);
     }
     if (g == 0 && a.mean) {
@@ -186,12 +244,12 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
     }
 }
 
-template <typename TX, typename TY, int WAVES, int KR, int PV, bool EXACT, bool DROP>
+template <typename TX, typename TY, int WAVES, int KR, int PV, int PL, bool EXACT, bool DROP>
 __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArgs a, int tiles_p)
 {
-    constexpr int G = WAVES * 4;
-    __shared__ __align__(16) float red[2][2][WAVES][kPosLanes * PV];
-    const int l = threadIdx.x % kPosLanes, g = threadIdx.x / kPosLanes, wave = threadIdx.x >> 6, C = a.C;
+    constexpr int G = WAVES * 64 / PL;
+    __shared__ __align__(16) float red[2][2][WAVES][PL * PV];
+    const int l = threadIdx.x % PL, g = threadIdx.x / PL, wave = threadIdx.x >> 6, C = a.C;
     const float fc = float(C);
     const int64_t tiles = a.N * tiles_p;
     float w[KR], dw[KR], db[KR];
@@ -201,8 +259,10 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
         dw[i] = db[i] = 0.f;
     }
     int slot = 0;
+    TileDrop<KR, PV, PL> drop;
+    __shared__ uint8_t bytes[DROP ? G * TileDrop<KR, PV, PL>::BYTES : 1];
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const TilePos<PV> at(t, tiles_p, l, a);
+        const TilePos<PV, PL> at(t, tiles_p, l, a);
         // opaque, so that no offset of a channel is kept in registers over the tiles
         uint32_t P = uint32_t(a.P);
         asm volatile("" : "+s"(P));
@@ -220,6 +280,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
             qx[i] = load_raw<TX, PV>(at_offset(x, o));
             qy[i] = load_raw<TY, PV>(at_offset(dy, o));
         }
+        if constexpr (DROP) drop.make(bytes, at.base + at.p - l * PV, P, G, a.drop);
         if constexpr (!EXACT)
 #pragma unroll
             for (int i = 0; i < KR; ++i) {
@@ -235,23 +296,14 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
         for (int i = 0; i < KR; ++i) keep_if(qy[i], g + i * G < C ? pos : 0u);
         // xhat and dz of channel i: formed from the raw values in both passes, which
         // takes half the registers of keeping them; a dropout mask is kept (a bit)
-        constexpr int KW = 32 / PV;                // channels per word
-        uint32_t keep[(KR + KW - 1) / KW] = {};
         auto form = [&](int i, float (&h)[PV], float (&z)[PV]) {
 #pragma unroll
             for (int e = 0; e < PV; ++e) {
                 h[e] = (element(qx[i], e) - element(rm, e)) * element(rr, e);
                 z[e] = element(qy[i], e);
-                if constexpr (DROP) z[e] = (keep[i / KW] >> (i % KW * PV + e)) & 1 ? z[e] * a.drop.scale : 0.f;
+                if constexpr (DROP) z[e] = drop.kept(i, e) ? z[e] * a.drop.scale : 0.f;
             }
         };
-        if constexpr (DROP)
-#pragma unroll
-            for (int i = 0; i < KR; ++i) {
-                keep[i / KW] |= (keep_run<PV>(at.base + uint32_t(g + i * G) * P + at.p, a.drop) & ((1u << PV) - 1))
-                                << (i % KW * PV);
-                __builtin_amdgcn_sched_barrier(0);
-            }
         float s1[PV] = {}, s2[PV] = {};
 #pragma unroll
         for (int i = 0; i < KR; ++i) {
@@ -266,9 +318,9 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
             }
             __builtin_amdgcn_sched_barrier(0);     // one channel's values at a time
         }
-        wave_chan_sum(s1);
-        wave_chan_sum(s2);
-        if ((threadIdx.x & 48) == 0)
+        wave_chan_sum<PV, PL>(s1);
+        wave_chan_sum<PV, PL>(s2);
+        if ((threadIdx.x & 63) < PL)
 #pragma unroll
             for (int e = 0; e < PV; ++e) {
                 red[slot][0][wave][l * PV + e] = s1[e];
@@ -306,7 +358,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_bwd_kernel(const NormArg
     if (!a.partial) return;
 #pragma unroll
     for (int i = 0; i < KR; ++i) {
-        const float u = lane_sum<kPosLanes>(dw[i]), v = lane_sum<kPosLanes>(db[i]);
+        const float u = lane_sum<PL>(dw[i]), v = lane_sum<PL>(db[i]);
         const int c = g + i * G;
         if (l == 0 && c < C) {
             a.partial[(int64_t(blockIdx.x) * 2 + 0) * C + c] = u;
@@ -471,42 +523,46 @@ __global__ __launch_bounds__(256) void norm_planes_kernel(const NormArgs a)
     }
 }
 
-// Waves per workgroup, channels per thread and positions per lane: channels in
-// registers, as few as hold them all, since fewer registers mean more tiles in
-// flight; past 256 channels half the positions (16 channels of 4 positions
-// do not fit the registers backward: 384 channels of 56 x 56, bf16, 50 images
-// took 246 us); kr 0: read again for each pass
+// Waves per workgroup, channels per thread, positions per lane and lanes per
+// channel: channels in registers, as few as hold them all, since fewer registers
+// mean more tiles in flight; kr 0: read again for each pass. Past 256 channels
+// half the positions (16 channels of 4 positions do not fit the registers
+// backward: 384 channels of 56 x 56, bf16, 50 images took 246 us, so 114). Past 512
+// half the lanes (744 channels of 56 x 56, 5 images, bf16: backward 71 us when read
+// again, 44 so, 16 waves spill; forward 33, 27, 32).
 struct Hold {
-    int waves, kr, pv;
+    int waves, kr, pv, pl;
 };
 Hold hold_of(int64_t C, int64_t P)
 {
-    if (P < 4 || C * P >= int64_t(1) << 30) return {0, 0, 4};
-    if (C <= 64) return {4, 4, 4};
-    if (C <= 128) return {4, 8, 4};
-    if (C <= 256) return {8, 8, 4};
-    if (C <= 512) return {8, 16, 2};
-    return {0, 0, 4};
+    if (P < 4 || C > 1024 || C * P >= int64_t(1) << 30) return {0, 0, 4, 16};
+    if (C <= 64) return {4, 4, 4, 16};
+    if (C <= 128) return {4, 8, 4, 16};
+    if (C <= 256) return {8, 8, 4, 16};
+    if (C <= 512) return {8, 16, 2, 16};
+    return {8, 16, 2, 8};
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// f(waves, channels, positions, lanes, exact)
 template <typename F>
 hipError_t with_hold(const Hold &h, int64_t P, F f)
 {
-    using std::integral_constant;
-    const auto call = [&](auto w, auto k, auto v) {
-        return P % decltype(v)::value == 0 ? f(w, k, v, std::true_type{}) : f(w, k, v, std::false_type{});
+    const auto call = [&](auto w, auto k, auto v, auto l) {
+        return P % decltype(v)::value == 0 ? f(w, k, v, l, std::true_type{}) : f(w, k, v, l, std::false_type{});
     };
-    const integral_constant<int, 4> four{};
-    const integral_constant<int, 8> eight{};
-    if (h.waves == 4 && h.kr == 4) return call(four, four, four);
-    if (h.waves == 4) return call(four, eight, four);
-    if (h.kr == 8) return call(eight, eight, four);
-    return call(eight, integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    if (h.waves == 4 && h.kr == 4) return call(Int<4>{}, Int<4>{}, Int<4>{}, Int<16>{});
+    if (h.waves == 4) return call(Int<4>{}, Int<8>{}, Int<4>{}, Int<16>{});
+    if (h.kr == 8) return call(Int<8>{}, Int<8>{}, Int<4>{}, Int<16>{});
+    if (h.pl == 16) return call(Int<8>{}, Int<16>{}, Int<2>{}, Int<16>{});
+    return call(Int<8>{}, Int<16>{}, Int<2>{}, Int<8>{});
 }
 
 constexpr int64_t kMaxBlocksFwd = 4096, kMaxBlocksBwd = 512, kImageSplits = 16;
 
-int64_t tiles_of_image(int64_t P, const Hold &h) { return (P + kPosLanes * h.pv - 1) / (kPosLanes * h.pv); }
+int64_t tiles_of_image(int64_t P, const Hold &h) { return (P + h.pl * h.pv - 1) / (h.pl * h.pv); }
 
 }  // namespace
 
@@ -530,9 +586,10 @@ hipError_t launch_norm_nchw_fwd(const NormArgs &a, hipStream_t s)
             return hipGetLastError();
         }
         if (tiles > INT32_MAX) return hipErrorInvalidValue;     // a.N < 2^31 images of few positions: not reached
-        return with_hold(h, a.P, [&](auto w, auto k, auto v, auto exact) {
+        return with_hold(h, a.P, [&](auto w, auto k, auto v, auto l, auto exact) {
             constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value, PV = decltype(v)::value;
-            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, PV, decltype(exact)::value>),
+            constexpr int PL = decltype(l)::value;
+            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, PV, PL, decltype(exact)::value>),
                                dim3(unsigned(tiles)), dim3(WAVES * 64), 0, s, a, int(tiles_p));
             return hipGetLastError();
         });
@@ -548,15 +605,16 @@ hipError_t launch_norm_nchw_bwd(const NormArgs &a, hipStream_t s)
         using TX = typename decltype(tx)::type;
         using TY = typename decltype(ty)::type;
         if (h.kr)
-            return with_hold(h, a.P, [&](auto w, auto k, auto v, auto exact) {
+            return with_hold(h, a.P, [&](auto w, auto k, auto v, auto l, auto exact) {
                 constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value, PV = decltype(v)::value;
+                constexpr int PL = decltype(l)::value;
                 constexpr bool EXACT = decltype(exact)::value;
                 const dim3 grid{unsigned(blocks)};
                 if (a.drop.threshold)
-                    hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, PV, EXACT, true>), grid,
+                    hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, PV, PL, EXACT, true>), grid,
                                        dim3(WAVES * 64), 0, s, a, tiles_p);
                 else
-                    hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, PV, EXACT, false>), grid,
+                    hipLaunchKernelGGL((norm_nchw_bwd_kernel<TX, TY, WAVES, KR, PV, PL, EXACT, false>), grid,
                                        dim3(WAVES * 64), 0, s, a, tiles_p);
                 return hipGetLastError();
             });

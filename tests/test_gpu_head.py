@@ -296,6 +296,33 @@ def test_fused_dropout_equals_dropout_of_the_norm():
     assert torch.equal(conv.layer_norm(x, layout="nchw", dropout_p=0.3, seed=5)[0], conv.dropout(y, 0.3, 5))
 
 
+# channels on both sides of each number that a kernel holds, positions that are and
+# are not whole tiles, vectors and 8-element blocks; the third has more tiles than
+# workgroups
+@pytest.mark.parametrize("N,C,P", [(3, 36, 49), (2, 64, 196), (601, 70, 26), (3, 129, 47), (2, 257, 64), (5, 512, 33),
+                                   (3, 513, 49), (40, 700, 98), (2, 1024, 17), (2, 1025, 21), (7, 300, 3), (4, 90, 4)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_fused_dropout_of_feature_maps(N, C, P, dt):
+    _say(f"layer norm nchw dropout {N} {C} {P} {dt}")
+    g = torch.Generator(device=DEV).manual_seed(N + C + P)
+    x = torch.randn(N, C, P, generator=g, device=DEV).to(TYPES[dt])
+    dy = torch.randn(N, C, P, generator=g, device=DEV)
+    w, b = torch.randn(C, generator=g, device=DEV), torch.randn(C, generator=g, device=DEV)
+    y, mean, rstd = conv.layer_norm(x.float(), w, b, layout="nchw")
+    kw = {"layout": "nchw", "dropout_p": 0.3, "seed": 11, "offset": 3}
+    assert torch.equal(conv.layer_norm(x.float(), w, b, **kw)[0], conv.dropout(y, 0.3, 11, 3))
+    got = conv.layer_norm_backward(dy, x.float(), w, mean, rstd, **kw)
+    want = conv.layer_norm_backward(conv.dropout(dy, 0.3, 11, 3), x.float(), w, mean, rstd, layout="nchw")
+    # the same fp32 formula twice: sums of up to 16016 terms in one order or another,
+    # 16016 U < 2e-3 of the terms' magnitudes, in practice far less; a wrong mask is O(1)
+    for a, c in zip(got, want):
+        assert (a - c).abs().max().item() <= 1e-4 * c.abs().max().item()
+    if dt == "bf16":
+        yb = conv.layer_norm(x, w, b, layout="nchw")[0]
+        yd = conv.layer_norm(x, w, b, **kw)[0]
+        assert torch.equal(yd == 0, (conv.dropout(yb, 0.3, 11, 3) == 0))
+
+
 # ---- linear cross entropy ----------------------------------------------------------------
 
 def _xent_case(N, V, D, dt, seed, spread=2.0):
@@ -374,6 +401,13 @@ def test_linear_cross_entropy_tile_shapes(N, V, D, dt):
     """Many tiles per workgroup, targets in every block of G, few rows against
     many classes, long K split over workgroups and over waves."""
     _check_xent(*_xent_case(N, V, D, dt, seed=N), dt, ref_dev=DEV, what="tiles")
+
+
+@pytest.mark.parametrize("N,V,D", [(1601, 208, 376), (2300, 384, 1000), (2300, 384, 2600), (4099, 5, 48), (129, 33, 2048)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_linear_cross_entropy_with_few_classes(N, V, D, dt):
+    """Every stage of rows then has a target among every wave's classes."""
+    _check_xent(*_xent_case(N, V, D, dt, seed=9), dt, ref_dev=DEV, what="few classes")
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
