@@ -7,6 +7,10 @@
 //             the type of x, and what that rounding took from the target's
 //             entry: G's largest entry of a row is usually that one, and its
 //             error alone would be the same relative error in all of dx and dw.
+// Bound by the matrix cores (many rows) or by the one read of w (few). 8192 rows,
+// 131072 classes, 4096 features, bf16: the losses in 6.2 ms, 1410 TFLOP/s (the
+// library's plain product of these operands 1450), G of 16384 classes 0.80 ms,
+// 1370; 1 row, 65536 classes, 2048 features 61 us, 4.4 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
