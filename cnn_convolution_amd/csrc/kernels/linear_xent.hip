@@ -42,7 +42,8 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const 
     if (lane == 0) {
         const float lse = m + logf(s);
         const bool ok = valid_target(a.target[row], a.V);
-        a.loss[row] = ok ? lse - a.loss[row] : 0.f;
+        // a small loss of large logits: the maximum cancels before the rounding of lse
+        a.loss[row] = ok ? logf(s) + (m - a.loss[row]) : 0.f;
         a.lse[row] = ok ? lse : 0.f;
     }
 }

@@ -28,6 +28,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // exp(a) for a <= 0 or moderate: one multiplication and the hardware's exp2
 __device__ __forceinline__ float fast_exp(float a) { return __builtin_amdgcn_exp2f(a * kLog2e); }
 
+// exp(l - b) as exp2(fma(l, log2 e, -b log2 e)), one fma per logit: the rounding of
+// b log2 e (3e-6 of the result for b = 40) is the same for a row's logits, and this
+// factor takes it out again once per row
+__device__ __forceinline__ float rounding_of(float b)
+{
+    return __builtin_amdgcn_exp2f(-__builtin_fmaf(b, kLog2e, b * -kLog2e));
+}
+
 // the tile pipelines of the logits: w's and x's rows are whole granules; a
 // workgroup takes every gridDim.x-th tile
 template <typename T, typename C>
@@ -131,6 +139,7 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_loss_kernel(cons
                     s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, mm * -kLog2e));
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
+            s *= rounding_of(mm);
             if (lane < 16) red[wm * E::BN + col] = float2{m, s};
         }
         // LDS accesses alone are waited for: the next tile's copies stay in flight.
@@ -208,13 +217,12 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void xent_g_kernel(const G
             const int t = target[j];
             const bool ok = t >= 0;
             const float gs = ok ? grad[j] * S : 0.f, c = ok ? lse[j] * -kLog2e : 0.f;
-            // exp(l - lse) as one fma and exp2: the rounding of lse * log2(e) is of
-            // the size of lse's own
+            const float ps = ok ? gs * rounding_of(lse[j]) : 0.f;
 #pragma unroll
             for (int i = 0; i < E::FM; ++i)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    acc[i][j][v] = gs * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, c));
+                    acc[i][j][v] = ps * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][v], kLog2e, c));
             if (__ballot(!ok) || edge) {
                 // masked rows and classes past the end: selected away, never multiplied
 #pragma unroll

@@ -481,6 +481,21 @@ def test_large_logits(scale):
         _check_xent((x.float() * scale).to(x.dtype), w, t, up, dt, what=f"x {scale}", rel=False)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_small_losses_of_large_logits(dt):
+    """Logits a for the target and a - 16 for 99 others, all exact: the loss,
+    log(1 + 99 exp(-16)), is far below the spacing of fp32 numbers near a."""
+    a = torch.tensor([1000.0, 992.0, 512.0, 64.0])
+    x = torch.stack([a, a - 16], 1).to(TYPES[dt]).to(DEV)
+    w = torch.zeros(100, 2)
+    w[0, 0], w[1:, 1] = 1, 1
+    loss, lse = conv.linear_cross_entropy(x, w.to(TYPES[dt]).to(DEV), torch.zeros(4, dtype=torch.int64, device=DEV))
+    # a sum of exponentials near 1 by at most 40 additions, its logarithm, a subtraction
+    want = float(np.log1p(99 * np.exp(-16.0)))
+    assert (loss.cpu().double() - want).abs().max().item() <= 44 * U
+    assert ((lse.cpu().double() - a.double() - want).abs() <= 2 * U * a.double()).all()
+
+
 def test_zero_gradient_rows():
     x, w, t, up = _xent_case(33, 500, 64, "f16", seed=8)
     loss, lse = conv.linear_cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV))
