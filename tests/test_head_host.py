@@ -1,5 +1,5 @@
 """Training-head operators without a GPU: the header against the binding, the
-checker's generator against published values, its gradients against
+oracle's generator against published values, its gradients against
 differences, refusals of bad descriptors, and workspace sizes."""
 import ctypes
 import os
@@ -83,7 +83,7 @@ def _differences(f, x, h=1e-6):
     return g
 
 
-def test_checker_layer_norm_gradient_against_differences():
+def test_oracle_layer_norm_gradient_against_differences():
     g = torch.Generator().manual_seed(1)
     for dim, shape in ((1, (3, 5)), (1, (2, 4, 3))):
         x = torch.randn(shape, generator=g, dtype=torch.float64)
@@ -101,7 +101,7 @@ def test_checker_layer_norm_gradient_against_differences():
             assert torch.allclose(a, _differences(f, v), rtol=1e-6, atol=1e-7)
 
 
-def test_checker_cross_entropy_gradient_against_differences():
+def test_oracle_cross_entropy_gradient_against_differences():
     g = torch.Generator().manual_seed(2)
     x = torch.randn((4, 3), generator=g, dtype=torch.float64)
     w = torch.randn((6, 3), generator=g, dtype=torch.float64)
