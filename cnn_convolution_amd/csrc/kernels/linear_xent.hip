@@ -19,6 +19,18 @@ namespace {
 
 __device__ __forceinline__ bool valid_target(int64_t t, int64_t V) { return t >= 0 && t < V; }
 
+// (m, s) joined by (m2, s2). A part without a class, or of classes at -infinity
+// alone, has the sum 0 and adds nothing. NaN is in a part's sum only: fmaxf passes it
+// over, and a tile of NaN classes and padding has the maximum -infinity, so it is by
+// the sum that a part is left out.
+__device__ __forceinline__ void join_part(float &m, float &s, float m2, float s2)
+{
+    if (s2 == 0.f) return;
+    const float n = fmaxf(m, m2);
+    s = (s == 0.f ? 0.f : s * __expf(m - n)) + s2 * __expf(m2 - n);
+    m = n;
+}
+
 // one wave per row: lse over the tiles' partials, then the loss
 __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const float2 *partial, int tiles)
 {
@@ -28,16 +40,11 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const 
     float m = -__builtin_inff(), s = 0.f;
     for (int t = lane; t < tiles; t += 64) {
         const float2 p = partial[t * a.N + row];
-        const float n = fmaxf(m, p.x);
-        if (n == -__builtin_inff()) continue;
-        s = s * __expf(m - n) + p.y * __expf(p.x - n);
-        m = n;
+        join_part(m, s, p.x, p.y);
     }
     for (int k = 1; k < 64; k <<= 1) {
-        const float m2 = __shfl_xor(m, k, 64), s2 = __shfl_xor(s, k, 64), n = fmaxf(m, m2);
-        if (n == -__builtin_inff()) continue;
-        s = s * __expf(m - n) + s2 * __expf(m2 - n);
-        m = n;
+        const float m2 = __shfl_xor(m, k, 64), s2 = __shfl_xor(s, k, 64);
+        join_part(m, s, m2, s2);
     }
     if (lane == 0) {
         const float lse = m + logf(s);

@@ -1,0 +1,61 @@
+"""Training-head kernels where they are easiest to get wrong: NaN logits, what
+masked rows hold, logits of 10^9, roundings that have to cancel, very many
+rows, and launches wider than one grid. Bounds as in test_gpu_head.py: u = 2^-24
+is the unit roundoff of fp32, uo that of the stored type."""
+import numpy as np
+import pytest
+import torch
+
+import cnn_convolution_amd as conv
+from cnn_convolution_amd import _lib
+from oracle import head as ref
+from test_gpu_head import DEV, SUB, TYPES, U, UO, _check_xent, _close, _say, _xent_case
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    _lib.lib()
+
+
+def _ulp_half(v, dt):
+    """Half the spacing of the type's numbers at v (float64 in, float64 out)."""
+    e = torch.frexp(v.abs())[1].double()               # |v| in [2^(e-1), 2^e)
+    return torch.clamp(torch.exp2(e - 1) * UO[dt], min=SUB[dt])
+
+
+@pytest.mark.parametrize("N", [1, 16, 40, 300])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_nan_weights_reach_every_loss(N, dt):
+    """NaN in the weights of one class, or of all classes of a tile: every unmasked
+    row's lse and loss are NaN, wherever its target lies; masked rows stay 0.
+    257 classes leave the last one alone in a tile of 32, 64, 128 or 256."""
+    for V, lo, hi in ((257, 256, 257), (600, 0, 256), (600, 256, 512), (1025, 1024, 1025), (70, 69, 70)):
+        _say(f"NaN weights N={N} V={V} classes {lo}..{hi} {dt}")
+        x, w, _, _ = _xent_case(N, V, 72, dt, seed=N + V)
+        w[lo:hi, 5] = NAN
+        t = torch.full((N,), 0 if lo else V - 1, dtype=torch.int64)
+        if N > 3:
+            t[3] = -1
+        loss, lse = (v.cpu() for v in conv.linear_cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV)))
+        ok = t >= 0
+        assert bool(torch.isnan(lse[ok]).all()), "lse"
+        assert bool(torch.isnan(loss[ok]).all()), "loss"
+        assert not loss[~ok].any() and not lse[~ok].any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_nan_features_reach_loss_and_lse_of_their_row_alone(dt):
+    for N, V in ((1, 300), (9, 257), (40, 100), (300, 2000)):
+        x, w, t, _ = _xent_case(N, V, 64, dt, seed=6)
+        k = N // 2
+        t[k] = 3
+        x[k, 5] = NAN
+        loss, lse = (v.cpu() for v in conv.linear_cross_entropy(x.to(DEV), w.to(DEV), t.to(DEV)))
+        for v in (loss, lse):
+            bad = torch.isnan(v)
+            assert bad[k] and int(bad.sum()) == 1, (N, V, int(bad.sum()))
