@@ -55,20 +55,26 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs a, const 
     }
 }
 
-// S: the power of two with S * max |grad| in [2^14, 2^15], by one workgroup
+// S: the power of two with S * max |grad| in [2^14, 2^15], by one workgroup. The
+// maximum is over the rows that have a gradient: a masked row's grad may hold
+// anything, and an infinite (or NaN) one is its own row's affair.
 template <int THREADS>
-__device__ __forceinline__ void grad_scale(const float *grad, int64_t N, float *scale)
+__device__ __forceinline__ void grad_scale(const float *grad, const int64_t *target, int64_t V, int64_t N,
+                                           float *scale)
 {
     __shared__ float red[THREADS / 64];
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < N; i += THREADS) m = fmaxf(m, fabsf(grad[i]));
+    for (int64_t i = threadIdx.x; i < N; i += THREADS) {
+        const float g = fabsf(grad[i]);
+        if (valid_target(target[i], V) && g < __builtin_inff()) m = fmaxf(m, g);
+    }
     for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < THREADS / 64; ++w) m = fmaxf(m, red[w]);
         int e = 0;
-        const bool ok = m > 0.f && m < __builtin_inff();
+        const bool ok = m > 0.f;
         if (ok) (void)frexpf(m, &e);
         e = max(-100, min(100, 15 - e));
         scale[0] = ok ? ldexpf(1.f, e) : 1.f;
@@ -76,9 +82,10 @@ __device__ __forceinline__ void grad_scale(const float *grad, int64_t N, float *
     }
 }
 
-__global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, int64_t N, float *scale)
+__global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, const int64_t *target, int64_t V,
+                                                         int64_t N, float *scale)
 {
-    grad_scale<1024>(grad, N, scale);
+    grad_scale<1024>(grad, target, V, N, scale);
 }
 
 // rows copied to whole granules (the padding cleared), one wave per row; with
@@ -90,7 +97,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const T *src, int64_t ld
                                                         int *t32, const float *grad, float *scale)
 {
     if (grad && blockIdx.x == gridDim.x - 1) {
-        grad_scale<256>(grad, rows, scale);
+        grad_scale<256>(grad, target, V, rows, scale);
         return;
     }
     const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -337,7 +344,8 @@ hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
         using T = decltype(t);
         // a workgroup of the copy has time for some tens of thousands of gradients
         const bool with_rows = scale && a.N <= 32768;
-        if (scale && !with_rows) hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad, a.N, scale);
+        if (scale && !with_rows)
+            hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad, a.target, a.V, a.N, scale);
         hipLaunchKernelGGL((xent_rows_kernel<T>), dim3(unsigned(p.rows_pad / 4 + (with_rows ? 1 : 0))), dim3(256), 0, s,
                            static_cast<const T *>(a.x), a.ldx, a.N, a.D, p.Dp, reinterpret_cast<T *>(ws + p.off_x),
                            a.target, a.V, p.rows_pad, t32, with_rows ? a.grad : nullptr, scale);

@@ -59,3 +59,40 @@ def test_nan_features_reach_loss_and_lse_of_their_row_alone(dt):
         for v in (loss, lse):
             bad = torch.isnan(v)
             assert bad[k] and int(bad.sum()) == 1, (N, V, int(bad.sum()))
+
+
+# ---- what a gradient of one row does to the others -------------------------------------------
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("value", [INF, -INF, 1e30, NAN])
+@pytest.mark.parametrize("N", [70, 40000])
+def test_gradients_of_masked_rows_change_nothing(dt, value, N):
+    x, w, t, up = _xent_case(N, 20, 24, dt, seed=3)
+    up *= 1e-6                                          # small against the type: the common scale counts
+    t[10], t[N - 1] = -1, 20
+    args = [v.to(DEV) for v in (x, w, t)]
+    _, lse = conv.linear_cross_entropy(*args)
+    got = []
+    for g in (0.0, value):
+        up[10] = up[N - 1] = g
+        got.append(conv.linear_cross_entropy_backward(up.to(DEV), *args, lse))
+    for a, b, name in zip(*got, ("dx", "dw")):
+        assert torch.equal(a, b), name
+    assert bool(got[0][1].any())
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_an_infinite_gradient_stays_in_its_row(dt):
+    x, w, t, up = _xent_case(70, 20, 24, dt, seed=3)
+    up *= 1e-6
+    t[10] = 4
+    args = [v.to(DEV) for v in (x, w, t)]
+    _, lse = conv.linear_cross_entropy(*args)
+    rest = torch.arange(70) != 10
+    got = []
+    for g in (0.0, INF):
+        up[10] = g
+        got.append(conv.linear_cross_entropy_backward(up.to(DEV), *args, lse)[0].cpu())
+    assert torch.equal(got[0][rest], got[1][rest]) and bool(got[0][rest].any())
+    assert not bool(torch.isfinite(got[1][10]).all())
