@@ -96,3 +96,37 @@ def test_an_infinite_gradient_stays_in_its_row(dt):
         got.append(conv.linear_cross_entropy_backward(up.to(DEV), *args, lse)[0].cpu())
     assert torch.equal(got[0][rest], got[1][rest]) and bool(got[0][rest].any())
     assert not bool(torch.isfinite(got[1][10]).all())
+
+
+# ---- logits far beyond fp32's integers ------------------------------------------------------
+
+
+@pytest.mark.parametrize("N", [3, 40, 600])
+@pytest.mark.parametrize("dt,exps", [("f32", (15, 20, 26, 31, 34, 60, 100)), ("bf16", (15, 20, 26, 31, 34, 60, 100)),
+                                     ("f16", (15, 20, 26, 34))])
+def test_equal_logits_of_any_size(N, dt, exps):
+    """All logits equal 77/64 * 2^e exactly: the loss is log V for every e. From 2^31 on
+    lse rounds to the logit itself, so that exp(l - lse) = 1 and the gradients are
+    small integers times powers of two."""
+    V, D = 100, 64
+    for e in exps:
+        _say(f"equal logits 2^{e} N={N} {dt}")
+        a, b = 2.0 ** ((e - 6) // 2), 77 / 64 * 2.0 ** (e - 6 - (e - 6) // 2)
+        x = torch.full((N, D), a).to(TYPES[dt]).to(DEV)
+        w = torch.full((V, D), b).to(TYPES[dt]).to(DEV)
+        t = torch.zeros(N, dtype=torch.int64, device=DEV)
+        loss, lse = conv.linear_cross_entropy(x, w, t)
+        # V exponentials of 0 in a chain of at most V / 64 + 64, logarithm and subtraction
+        _close(loss, torch.full((N,), np.log(V), dtype=torch.float64), torch.tensor((V / 64 + 64 + 44) * U), "loss")
+        want = 77 / 64 * 2.0 ** e + np.log(V)
+        assert ((lse.cpu().double() - want).abs() <= 2 * U * want + 2e-5).all()
+        if e < 31:
+            continue
+        assert bool((lse == 77 / 64 * 2.0 ** e).all())
+        up = torch.full((N,), 2.0 ** -10, device=DEV)
+        dx, dw = conv.linear_cross_entropy_backward(up, x, w, t, lse)
+        dx0 = torch.full((N, D), 99 * 2.0 ** -10 * b, dtype=torch.float64)
+        _close(dx, dx0, _ulp_half(dx0, dt) + 2 * V * U * dx0, "dx")
+        dw0 = torch.full((V, D), N * 2.0 ** -10 * a, dtype=torch.float64)
+        dw0[0] = 0
+        _close(dw, dw0, _ulp_half(dw0, dt) + 2 * N * U * dw0, "dw")
