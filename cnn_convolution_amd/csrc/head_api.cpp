@@ -12,7 +12,7 @@ using namespace im2win;
 
 namespace {
 
-constexpr int64_t kMaxDim = int64_t(1) << 31;      // of one size: tile counts stay within a grid
+constexpr int64_t kMaxDim = int64_t(1) << 31;      // of one size
 constexpr int64_t kMaxElems = int64_t(1) << 40;    // of one tensor: byte offsets stay within 64 bits
 
 bool type_ok(int32_t t) { return t == CONV2D_F32 || t == CONV2D_F16 || t == CONV2D_BF16; }

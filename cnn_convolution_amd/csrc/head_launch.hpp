@@ -10,6 +10,11 @@
 
 namespace im2win {
 
+// Workgroups of `threads` that one launch may have: a grid of 2^32 threads or more is
+// run modulo 2^32, without an error. Kernels with more to do stride over the rest
+// or are launched in parts.
+constexpr int64_t max_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 // Dropout over elements numbered in 64 bits (see im2win_head.h): element i is
 // kept when its 16-bit number is at least `threshold` (0: everything is kept)
 // and multiplied by `scale`.

@@ -138,9 +138,10 @@ private:
     }
 };
 
-// WAVES waves, 64 / PL * WAVES channel groups; EXACT: P is a multiple of PV
+// One tile, first + blockIdx.x. WAVES waves, 64 / PL * WAVES channel groups; EXACT: P is
+// a multiple of PV
 template <typename TX, typename TY, int WAVES, int KR, int PV, int PL, bool EXACT>
-__global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArgs a, int tiles_p)
+__global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArgs a, int tiles_p, int64_t first)
 {
     constexpr int GW = 64 / PL, G = WAVES * GW;
     __shared__ __align__(16) float red[2][WAVES][PL * PV];    // mean, squares
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_nchw_fwd_kernel(const NormArg
         for (int i = 0; i < KR; ++i) n += max(0, min(GW, C - i * G - q * GW));
         return float(n);
     };
-    const TilePos<PV, PL> at(blockIdx.x, tiles_p, l, a);
+    const TilePos<PV, PL> at(first + blockIdx.x, tiles_p, l, a);
     const TX *x = static_cast<const TX *>(a.x) + at.base;
     TY *y = static_cast<TY *>(a.out) + at.base;
     const Window<PV> win(at.p, a.P);
@@ -585,12 +586,14 @@ hipError_t launch_norm_nchw_fwd(const NormArgs &a, hipStream_t s)
             hipLaunchKernelGGL((norm_nchw_fwd_wide_kernel<TX, TY>), grid, dim3(kWide), 0, s, a, int(tiles_p));
             return hipGetLastError();
         }
-        if (tiles > INT32_MAX) return hipErrorInvalidValue;     // a.N < 2^31 images of few positions: not reached
         return with_hold(h, a.P, [&](auto w, auto k, auto v, auto l, auto exact) {
             constexpr int WAVES = decltype(w)::value, KR = decltype(k)::value, PV = decltype(v)::value;
             constexpr int PL = decltype(l)::value;
-            hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, PV, PL, decltype(exact)::value>),
-                               dim3(unsigned(tiles)), dim3(WAVES * 64), 0, s, a, int(tiles_p));
+            constexpr int64_t most = max_groups(WAVES * 64);
+            for (int64_t first = 0; first < tiles; first += most)
+                hipLaunchKernelGGL((norm_nchw_fwd_kernel<TX, TY, WAVES, KR, PV, PL, decltype(exact)::value>),
+                                   dim3(unsigned(std::min(tiles - first, most))), dim3(WAVES * 64), 0, s, a,
+                                   int(tiles_p), first);
             return hipGetLastError();
         });
     });

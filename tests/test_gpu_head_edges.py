@@ -130,3 +130,21 @@ def test_equal_logits_of_any_size(N, dt, exps):
         dw0 = torch.full((V, D), N * 2.0 ** -10 * a, dtype=torch.float64)
         dw0[0] = 0
         _close(dw, dw0, _ulp_half(dw0, dt) + 2 * N * U * dw0, "dw")
+
+
+# ---- wider than a launch ----------------------------------------------------------------------
+
+
+def test_more_feature_maps_than_workgroups_of_a_launch():
+    """2^24 + 5 maps of 2 x 2 positions are as many tiles of 256 threads: more
+    than the 2^32 threads of a launch."""
+    N, C = (1 << 24) + 5, 2
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(N, C, 4, generator=g, device=DEV).half()
+    w, b = torch.tensor([1.5, -0.5], device=DEV), torch.tensor([0.25, 1.0], device=DEV)
+    kw = dict(layout="nchw", dropout_p=0.25, seed=3)
+    y, mean, rstd = conv.layer_norm(x, w, b, **kw)
+    # element 8 i begins map i: a half's own blocks begin at its first map
+    for lo, hi in ((0, N // 2), (N // 2, N)):
+        yh, mh, rh = conv.layer_norm(x[lo:hi], w, b, offset=lo, **kw)
+        assert torch.equal(y[lo:hi], yh) and torch.equal(mean[lo:hi], mh) and torch.equal(rstd[lo:hi], rh)
