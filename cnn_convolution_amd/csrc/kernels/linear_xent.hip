@@ -120,8 +120,8 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const T *src, int64_t ld
 template <typename T>
 __global__ __launch_bounds__(256) void xent_zero_kernel(T *p, int64_t n)
 {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) p[i] = T(0.f);
+    const int64_t step = int64_t(gridDim.x) * 256;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) p[i] = T(0.f);
 }
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -333,8 +333,9 @@ hipError_t launch_xent_bwd(const XentArgs &a, hipStream_t s)
         return with_type(a.dtype, [&](auto t) {
             using T = decltype(t);
             const int64_t n = a.V * a.D;
-            hipLaunchKernelGGL((xent_zero_kernel<T>), dim3(unsigned(ceil_div(n, 256))), dim3(256), 0, s,
-                               static_cast<T *>(a.dw), n);
+            const int64_t groups = std::min(ceil_div(n, 256), max_groups(256));
+            hipLaunchKernelGGL((xent_zero_kernel<T>), dim3(unsigned(groups)), dim3(256), 0, s, static_cast<T *>(a.dw),
+                               n);
             return hipGetLastError();
         });
     float *scale = a.dtype == 1 ? reinterpret_cast<float *>(ws + p.off_scale) : nullptr;

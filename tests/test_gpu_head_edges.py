@@ -148,3 +148,13 @@ def test_more_feature_maps_than_workgroups_of_a_launch():
     for lo, hi in ((0, N // 2), (N // 2, N)):
         yh, mh, rh = conv.layer_norm(x[lo:hi], w, b, offset=lo, **kw)
         assert torch.equal(y[lo:hi], yh) and torch.equal(mean[lo:hi], mh) and torch.equal(rstd[lo:hi], rh)
+
+
+def test_weight_gradient_of_no_rows_beyond_a_launch():
+    V, D = (1 << 16) + 1, 1 << 16
+    w = torch.empty(V, D, dtype=torch.bfloat16, device=DEV)
+    dw = torch.ones_like(w)
+    x = torch.empty(0, D, dtype=torch.bfloat16, device=DEV)
+    z, e = torch.empty(0, dtype=torch.int64, device=DEV), torch.empty(0, device=DEV)
+    conv.linear_cross_entropy_backward_into(e, x, w, z, e, torch.empty_like(x), dw, None)
+    assert not bool(dw.any())
