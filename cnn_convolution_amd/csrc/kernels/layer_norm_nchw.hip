@@ -497,30 +497,31 @@ __global__ __launch_bounds__(kWide) void norm_nchw_bwd_wide_kernel(const NormArg
 template <typename TX, typename TY>
 __global__ __launch_bounds__(256) void norm_planes_kernel(const NormArgs a)
 {
-    const int c = blockIdx.x * 4 + (threadIdx.x >> 6), l = threadIdx.x & 63, C = a.C;
-    if (c >= C) return;
-    float dw = 0.f, db = 0.f;
-    for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
-        const int64_t base = (n * C + c) * a.P;
-        for (int64_t p = l * 4; p < a.P; p += 256) {
-            float h[4], z[4], mean[4], rstd[4];
-            load_pos(static_cast<const TX *>(a.x) + base, p, a.P, h);
-            load_pos(static_cast<const TY *>(a.dy) + base, p, a.P, z);
-            load_pos(a.mean + n * a.P, p, a.P, mean);
-            load_pos(a.rstd + n * a.P, p, a.P, rstd);
-            if (a.drop.threshold) drop_run<4>(base + p, a.drop, z);
+    const int l = threadIdx.x & 63, C = a.C;
+    for (int c = blockIdx.x * 4 + (threadIdx.x >> 6); c < C; c += gridDim.x * 4) {
+        float dw = 0.f, db = 0.f;
+        for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
+            const int64_t base = (n * C + c) * a.P;
+            for (int64_t p = l * 4; p < a.P; p += 256) {
+                float h[4], z[4], mean[4], rstd[4];
+                load_pos(static_cast<const TX *>(a.x) + base, p, a.P, h);
+                load_pos(static_cast<const TY *>(a.dy) + base, p, a.P, z);
+                load_pos(a.mean + n * a.P, p, a.P, mean);
+                load_pos(a.rstd + n * a.P, p, a.P, rstd);
+                if (a.drop.threshold) drop_run<4>(base + p, a.drop, z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dw += z[e] * (h[e] - mean[e]) * rstd[e];   // 0 past the end
-                db += z[e];
+                for (int e = 0; e < 4; ++e) {
+                    dw += z[e] * (h[e] - mean[e]) * rstd[e];   // 0 past the end
+                    db += z[e];
+                }
             }
         }
-    }
-    dw = lane_sum<64>(dw);
-    db = lane_sum<64>(db);
-    if (l == 0) {
-        a.partial[(int64_t(blockIdx.y) * 2 + 0) * C + c] = dw;
-        a.partial[(int64_t(blockIdx.y) * 2 + 1) * C + c] = db;
+        dw = lane_sum<64>(dw);
+        db = lane_sum<64>(db);
+        if (l == 0) {
+            a.partial[(int64_t(blockIdx.y) * 2 + 0) * C + c] = dw;
+            a.partial[(int64_t(blockIdx.y) * 2 + 1) * C + c] = db;
+        }
     }
 }
 
@@ -625,8 +626,8 @@ hipError_t launch_norm_nchw_bwd(const NormArgs &a, hipStream_t s)
         hipLaunchKernelGGL((norm_nchw_bwd_wide_kernel<TX, TY>), grid, dim3(kWide), 0, s, a, tiles_p);
         const hipError_t e1 = hipGetLastError();
         if (e1 != hipSuccess || !a.partial) return e1;
-        hipLaunchKernelGGL((norm_planes_kernel<TX, TY>), dim3(unsigned((a.C + 3) / 4), unsigned(blocks)),
-                           dim3(256), 0, s, a);
+        const int64_t groups = std::min<int64_t>((int64_t(a.C) + 3) / 4, max_groups(256));
+        hipLaunchKernelGGL((norm_planes_kernel<TX, TY>), dim3(unsigned(groups), unsigned(blocks)), dim3(256), 0, s, a);
         return hipGetLastError();
     });
     if (e != hipSuccess || !a.partial) return e;

@@ -446,18 +446,21 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *partial,
 {
     __shared__ float part[64][17];
     const int col = threadIdx.x & 15, g = threadIdx.x >> 4;
-    const int64_t k = int64_t(blockIdx.x) * 16 + col;
-    float t = 0.f;
-    if (k < 2 * int64_t(C))
+    // the next columns' part[0] is written by the threads that read this one's
+    for (int64_t k0 = int64_t(blockIdx.x) * 16; k0 < 2 * int64_t(C); k0 += int64_t(gridDim.x) * 16) {
+        const int64_t k = k0 + col;
+        float t = 0.f;
+        if (k < 2 * int64_t(C))
 #pragma unroll 4
-        for (int r = g; r < rows; r += 64) t += partial[int64_t(r) * 2 * C + k];
-    part[g][col] = t;
-    __syncthreads();
-    for (int m = 32; m > 0; m >>= 1) {
-        if (g < m) part[g][col] += part[g + m][col];
+            for (int r = g; r < rows; r += 64) t += partial[int64_t(r) * 2 * C + k];
+        part[g][col] = t;
         __syncthreads();
+        for (int m = 32; m > 0; m >>= 1) {
+            if (g < m) part[g][col] += part[g + m][col];
+            __syncthreads();
+        }
+        if (g == 0 && k < 2 * int64_t(C)) (k < C ? dweight : dbias)[k < C ? k : k - C] = part[0][col];
     }
-    if (g == 0 && k < 2 * int64_t(C)) (k < C ? dweight : dbias)[k < C ? k : k - C] = part[0][col];
 }
 
 // The group that holds a row of C channels: as few lanes per row as keep it to
@@ -588,8 +591,9 @@ hipError_t launch_norm_rows_bwd(const NormArgs &a, hipStream_t s)
 hipError_t launch_norm_reduce(const float *partial, int64_t rows, int C, float *dweight, float *dbias,
                               hipStream_t s)
 {
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3(unsigned((2 * int64_t(C) + 15) / 16)), dim3(1024), 0, s,
-                       partial, int(rows), C, dweight, dbias);
+    const int64_t groups = std::min((2 * int64_t(C) + 15) / 16, max_groups(1024));
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3(unsigned(groups)), dim3(1024), 0, s, partial, int(rows), C, dweight,
+                       dbias);
     return hipGetLastError();
 }
 

@@ -158,3 +158,20 @@ def test_weight_gradient_of_no_rows_beyond_a_launch():
     z, e = torch.empty(0, dtype=torch.int64, device=DEV), torch.empty(0, device=DEV)
     conv.linear_cross_entropy_backward_into(e, x, w, z, e, torch.empty_like(x), dw, None)
     assert not bool(dw.any())
+
+
+@pytest.mark.parametrize("layout,C", [("nhwc", (1 << 25) + 8), ("nchw", (1 << 26) + 4)])
+def test_weight_gradients_of_more_channels_than_a_launch(layout, C):
+    """One position of very many channels: the reductions of dweight and dbias."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    shape = (1, C) if layout == "nhwc" else (1, C, 1)
+    x = torch.randn(shape, generator=g, device=DEV).half()
+    dy = torch.randn(shape, generator=g, device=DEV).half()
+    mean, rstd = torch.full((1,), 0.5, device=DEV), torch.full((1,), 2.0, device=DEV)
+    if layout == "nchw":
+        mean, rstd = mean.view(1, 1), rstd.view(1, 1)
+    _, dw, db = conv.layer_norm_backward(dy, x, None, mean, rstd, layout=layout)
+    want = dy.float().reshape(-1) * ((x.float().reshape(-1) - 0.5) * 2.0)
+    # two products and a subtraction, rounded once each
+    assert bool(((dw - want).abs() <= 4 * U * (want.abs() + dy.float().reshape(-1).abs())).all())
+    assert torch.equal(db, dy.float().reshape(-1))
