@@ -20,9 +20,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
+#include "../head_launch.hpp"
 #include "lds_dma.hpp"
 
 namespace im2win {
@@ -45,6 +47,10 @@ using C64x32 = TileCfg<64, 32, 2, 2, 3, 4>;
 // 65536 x 2048 bf16 61.6 us, with eight 67.5; half as wide with two waves 65.3)
 using CNarrow = TileCfg<128, 16, 4, 1, 4, 2>;
 
+// Tiles of a launch at most: a tile's number plus a grid stays within an int. 2^22
+// rows by 2^24 classes are that many tiles of 256 x 256.
+constexpr int64_t kMaxTiles = int64_t(1) << 30;
+
 // Workgroups of a launch over `tiles` tiles of `stages` K stages. Where a CU holds
 // one workgroup, or the tiles are short, as many as the chip holds, each taking
 // every grid-th tile and starting the next one's copies before its epilogue; else
@@ -55,7 +61,7 @@ template <typename C>
 inline int64_t grid_of(int64_t tiles, int64_t stages)
 {
     const int64_t held = int64_t(C::per_cu) * 256;
-    return (C::per_cu == 1 || stages <= 4) && tiles > held ? held : tiles;
+    return (C::per_cu == 1 || stages <= 4) && tiles > held ? held : std::min(tiles, max_groups(C::threads));
 }
 
 // A whole 32 x 32 tile per wave, the four waves of a workgroup each with a quarter

@@ -287,11 +287,11 @@ hipError_t launch_tiles(K kernel, int lds, std::atomic<uint64_t> &allowed, const
                         int64_t M, int64_t N, hipStream_t s)
 {
     const int64_t tm = (M + C::BM - 1) / C::BM, tn = (N + C::BN - 1) / C::BN;
-    if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    if (tm * tn > kMaxTiles) return hipErrorInvalidValue;
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), lds, allowed);
     if (e != hipSuccess) return e;
     // C32K joins its waves in the stage buffers: a workgroup per tile
-    const int64_t grid = kSplitWaves<C> ? tm * tn : grid_of<C>(tm * tn, stages);
+    const int64_t grid = kSplitWaves<C> ? std::min(tm * tn, max_groups(C::threads)) : grid_of<C>(tm * tn, stages);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), lds, s, a, int(tm), int(tn));
     return hipGetLastError();
 }

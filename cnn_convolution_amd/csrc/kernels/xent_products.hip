@@ -307,15 +307,15 @@ __global__ __launch_bounds__(256) void xent_join_slabs_kernel(const ProductArgs 
 template <typename T, typename C, bool DW>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t s)
 {
+    constexpr bool ONE = DW && sizeof(T) == 2 && C::FM == 8;    // a workgroup for every tile
     const auto kernel = xent_product_kernel<T, C, DW>;
-    const int64_t tm = (a.M + C::BM - 1) / C::BM, tn = (a.n + C::BN - 1) / C::BN;
-    if (tm * tn * a.split > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t tm = (a.M + C::BM - 1) / C::BM, tn = (a.n + C::BN - 1) / C::BN, all = tm * tn * a.split;
+    if (all > (ONE ? max_groups(C::threads) : kMaxTiles)) return hipErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
     if (e != hipSuccess) return e;
-    const int64_t all = tm * tn * a.split;
     const int64_t stages = (a.K * int64_t(sizeof(T)) + 127) / 128 / a.split;
-    const int64_t grid = DW && sizeof(T) == 2 && C::FM == 8 ? all : grid_of<C>(all, stages);
+    const int64_t grid = ONE ? all : grid_of<C>(all, stages);
     hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(C::threads), C::lds_bytes, s, a, int(tm), int(tn));
     return hipGetLastError();
 }
@@ -359,7 +359,7 @@ hipError_t launch_xent_both(const ProductArgs &dx, const ProductArgs &dw, int dt
         const int64_t xm = (dx.M + C::BM - 1) / C::BM, xn = (dx.n + C::BN - 1) / C::BN;
         const int64_t wm = (dw.M + C::BM - 1) / C::BM, wn = (dw.n + C::BN - 1) / C::BN;
         const int64_t grid = xm * xn * dx.split + wm * wn * dw.split;
-        if (grid > INT32_MAX) return hipErrorInvalidValue;
+        if (grid > max_groups(C::threads)) return hipErrorInvalidValue;
         static std::atomic<uint64_t> allowed{0};
         const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
         if (e != hipSuccess) return e;

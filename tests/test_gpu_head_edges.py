@@ -175,3 +175,23 @@ def test_weight_gradients_of_more_channels_than_a_launch(layout, C):
     # two products and a subtraction, rounded once each
     assert bool(((dw - want).abs() <= 4 * U * (want.abs() + dy.float().reshape(-1).abs())).all())
     assert torch.equal(db, dy.float().reshape(-1))
+
+
+def test_more_logit_tiles_than_workgroups_of_a_launch():
+    """2^22 rows by 65536 classes: 2^24 tiles of 128 x 128 with 256 threads, which is a
+    grid of 2^32. Rows across the whole range against the definition."""
+    N, V, D = 1 << 22, 65536, 320
+    g = torch.Generator(device=DEV).manual_seed(3)
+    w = (torch.randn(V, D, generator=g, device=DEV) * 0.1).bfloat16()
+    x = torch.randn(N, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    t = torch.randint(0, V, (N,), generator=g, device=DEV)
+    loss, lse = conv.linear_cross_entropy(x, w, t)
+    assert bool(torch.isfinite(loss).all()) and bool((lse > 0).all())
+    rows = torch.cat([torch.arange(500, device=DEV), torch.randint(0, N, (1000,), generator=g, device=DEV),
+                      torch.arange(N - 500, N, device=DEV)])
+    xs, ts = x[rows], t[rows]
+    l0, s0 = ref.cross_entropy(xs, w, ts)
+    dl = 2 * (D + 1) * U * (xs.double().abs() @ w.double().abs().t()).amax(1)
+    tol = 2 * dl + (V / 64 + 108) * U + 4 * U * (2 * s0.abs() + l0.abs())
+    _close(loss[rows], l0, tol, "loss")
+    _close(lse[rows], s0, tol, "lse")
