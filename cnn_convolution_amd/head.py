@@ -8,8 +8,9 @@ with its gradient (definitions in include/im2win_head.h).
     dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd, dropout_p=0.1, seed=step)
 
 Every operator has an ``_into`` form that takes the caller's outputs and
-workspace. All work is enqueued on the current stream of x's device; the
-kernels are in the HIP library, PyTorch provides device memory and streams.
+workspace. All work is enqueued on the current stream of x's device, whichever
+device is current; the kernels are in the HIP library, PyTorch provides device
+memory and streams.
 """
 from __future__ import annotations
 
@@ -23,15 +24,17 @@ __all__ = ["dropout", "dropout_into", "layer_norm", "layer_norm_into", "layer_no
 
 _codes = None
 _raw_stream = None
+_current_device = None
 
 
 def _torch_names() -> None:
     """What the calls below need of torch, looked up once."""
-    global _codes, _raw_stream, _F32, _I64
+    global _codes, _raw_stream, _current_device, _F32, _I64
     import torch
     _F32, _I64 = torch.float32, torch.int64
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _codes = {torch.float32: _lib.F32, torch.float16: _lib.F16, torch.bfloat16: _lib.BF16}
 
 
@@ -49,6 +52,22 @@ def _device(t, name) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     return t.get_device()
+
+
+def _device_guard(dev):
+    import torch
+    return torch.cuda.device(dev)
+
+
+def _enqueue(dev, name, desc, *args) -> None:
+    """The library's call on the current stream of device dev. A launch goes to
+    the current device, and a device's default stream is the null stream on
+    every device: dev has to be the current one."""
+    if _current_device() == dev:
+        _head.call(name, desc, *args, _raw_stream(dev))
+    else:
+        with _device_guard(dev):
+            _head.call(name, desc, *args, _raw_stream(dev))
 
 
 def _vector(t, name, n, dev, dtype=None):
@@ -98,7 +117,7 @@ def dropout_into(x, y, p: float, seed: int, offset: int = 0) -> None:
         raise ValueError("x must be contiguous")
     d = DropoutDesc(x.numel(), _code(x.dtype), 0, p, seed, offset)
     out = _contiguous(y, "y", x.shape, x.dtype, dev)
-    _head.call("dropout_fwd", d, x.data_ptr(), out, _raw_stream(dev))
+    _enqueue(dev, "dropout_fwd", d, x.data_ptr(), out)
 
 
 def dropout(x, p: float, seed: int, offset: int = 0):
@@ -180,8 +199,8 @@ def layer_norm_into(x, weight, bias, y, mean, rstd, eps: float = 1e-5, *, layout
     d, n = _norm_desc(x, layout, y.dtype, eps, dropout_p, seed, offset)
     d.ldy = _row_stride(d, y, "y", x.shape, y.dtype, dev)
     C = d.C
-    _head.call("layer_norm_fwd", d, x.data_ptr(), _vector(weight, "weight", C, dev), _vector(bias, "bias", C, dev),
-               y.data_ptr(), _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev), _raw_stream(dev))
+    _enqueue(dev, "layer_norm_fwd", d, x.data_ptr(), _vector(weight, "weight", C, dev), _vector(bias, "bias", C, dev),
+             y.data_ptr(), _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev))
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, *, layout="nhwc", out_dtype=None,
@@ -218,10 +237,9 @@ def layer_norm_backward_into(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, 
     d.lddx = _row_stride(d, dx, "dx", x.shape, x.dtype, dev)
     C = d.C
     need = _head.size("layer_norm_bwd_workspace_size", d) if dweight is not None else 0
-    _head.call("layer_norm_bwd", d, dy.data_ptr(), x.data_ptr(), _vector(weight, "weight", C, dev),
-               _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev), dx.data_ptr(),
-               _vector(dweight, "dweight", C, dev), _vector(dbias, "dbias", C, dev), _workspace(ws, need, dev),
-               _raw_stream(dev))
+    _enqueue(dev, "layer_norm_bwd", d, dy.data_ptr(), x.data_ptr(), _vector(weight, "weight", C, dev),
+             _vector(mean, "mean", n, dev), _vector(rstd, "rstd", n, dev), dx.data_ptr(),
+             _vector(dweight, "dweight", C, dev), _vector(dbias, "dbias", C, dev), _workspace(ws, need, dev))
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, layout="nhwc", dropout_p: float = 0.0, seed: int = 0,
@@ -272,9 +290,9 @@ def linear_cross_entropy_into(x, w, target, loss, lse, ws) -> None:
     dev = _same_device(x, w)
     d = _xent_desc(x, w)
     N = x.shape[0]
-    _head.call("linear_xent_fwd", d, x.data_ptr(), w.data_ptr(), _vector(target, "target", N, dev, _I64),
-               _vector(loss, "loss", N, dev), _vector(lse, "lse", N, dev),
-               _workspace(ws, _head.size("linear_xent_fwd_workspace_size", d), dev), _raw_stream(dev))
+    _enqueue(dev, "linear_xent_fwd", d, x.data_ptr(), w.data_ptr(), _vector(target, "target", N, dev, _I64),
+             _vector(loss, "loss", N, dev), _vector(lse, "lse", N, dev),
+             _workspace(ws, _head.size("linear_xent_fwd_workspace_size", d), dev))
 
 
 def linear_cross_entropy(x, w, target):
@@ -294,10 +312,10 @@ def linear_cross_entropy_backward_into(grad, x, w, target, lse, dx, dw, ws) -> N
     dev = _same_device(x, w)
     d = _xent_desc(x, w)
     N = x.shape[0]
-    _head.call("linear_xent_bwd", d, _vector(grad, "grad", N, dev), x.data_ptr(), w.data_ptr(),
-               _vector(target, "target", N, dev, _I64), _vector(lse, "lse", N, dev),
-               _contiguous(dx, "dx", x.shape, x.dtype, dev), _contiguous(dw, "dw", w.shape, w.dtype, dev),
-               _workspace(ws, _head.size("linear_xent_bwd_workspace_size", d), dev), _raw_stream(dev))
+    _enqueue(dev, "linear_xent_bwd", d, _vector(grad, "grad", N, dev), x.data_ptr(), w.data_ptr(),
+             _vector(target, "target", N, dev, _I64), _vector(lse, "lse", N, dev),
+             _contiguous(dx, "dx", x.shape, x.dtype, dev), _contiguous(dw, "dw", w.shape, w.dtype, dev),
+             _workspace(ws, _head.size("linear_xent_bwd_workspace_size", d), dev))
 
 
 def linear_cross_entropy_backward(grad, x, w, target, lse):

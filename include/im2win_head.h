@@ -14,8 +14,9 @@
  *                                       x w^T, which are never stored
  *
  * Pointers are DEVICE pointers the caller allocates and owns; `stream` is a
- * hipStream_t passed as void* (NULL: the default stream). All work is enqueued
- * on `stream`; the calls return without synchronising, allocate nothing and
+ * hipStream_t passed as void* (NULL: the default stream). The current device has
+ * to be the one the pointers and the stream belong to. All work is enqueued on
+ * `stream`; the calls return without synchronising, allocate nothing and
  * keep no state. Every argument is validated before anything is enqueued; on an
  * error nothing is launched and no output is touched (CONV2D_ERR_HIP: launches
  * of earlier steps of the same call may have been enqueued). Tensors need the
