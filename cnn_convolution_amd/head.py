@@ -277,6 +277,16 @@ def _same_device(x, w) -> int:
     return dev
 
 
+def _row_start(t, name, D, ld):
+    """The pointer of rows of D elements, ld apart: whole 16-byte granules are read
+    in place and start on one, other rows are copied first and start anywhere."""
+    p, size = t.data_ptr(), t.element_size()
+    if p % 16 and D * size % 16 == 0 and ld * size % 16 == 0:
+        raise ValueError(f"{name} must start on a 16-byte boundary, its rows being whole 16-byte pieces "
+                         f"(a view that does not can be cloned)")
+    return p
+
+
 def linear_cross_entropy_workspace_size(x, w, *, backward: bool = False) -> int:
     """Bytes of workspace of linear_cross_entropy_into, or with ``backward`` of
     both that and linear_cross_entropy_backward_into."""
@@ -286,11 +296,13 @@ def linear_cross_entropy_workspace_size(x, w, *, backward: bool = False) -> int:
 
 
 def linear_cross_entropy_into(x, w, target, loss, lse, ws) -> None:
-    """Enqueue loss, lse = linear_cross_entropy(x, w, target)."""
+    """Enqueue loss, lse = linear_cross_entropy(x, w, target). x and w whose rows and
+    row strides are multiples of 16 bytes have to start on a 16-byte boundary."""
     dev = _same_device(x, w)
     d = _xent_desc(x, w)
     N = x.shape[0]
-    _enqueue(dev, "linear_xent_fwd", d, x.data_ptr(), w.data_ptr(), _vector(target, "target", N, dev, _I64),
+    _enqueue(dev, "linear_xent_fwd", d, _row_start(x, "x", d.D, d.ldx), _row_start(w, "w", d.D, d.ldw),
+             _vector(target, "target", N, dev, _I64),
              _vector(loss, "loss", N, dev), _vector(lse, "lse", N, dev),
              _workspace(ws, _head.size("linear_xent_fwd_workspace_size", d), dev))
 
@@ -298,7 +310,8 @@ def linear_cross_entropy_into(x, w, target, loss, lse, ws) -> None:
 def linear_cross_entropy(x, w, target):
     """Softmax cross entropy of the logits x w^T (never stored) with int64
     targets: per-row (loss, lse) in fp32. Rows whose target is outside [0, V)
-    are masked: both are 0."""
+    are masked: both are 0. x and w whose rows and row strides are multiples of
+    16 bytes have to start on a 16-byte boundary."""
     import torch
     loss = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
     lse = torch.empty_like(loss)
@@ -308,12 +321,13 @@ def linear_cross_entropy(x, w, target):
 
 def linear_cross_entropy_backward_into(grad, x, w, target, lse, dx, dw, ws) -> None:
     """Enqueue the gradients of linear_cross_entropy for the per-row gradient
-    grad (fp32 [N]) of its loss."""
+    grad (fp32 [N]) of its loss. w as in linear_cross_entropy_into; x may start
+    anywhere."""
     dev = _same_device(x, w)
     d = _xent_desc(x, w)
     N = x.shape[0]
-    _enqueue(dev, "linear_xent_bwd", d, _vector(grad, "grad", N, dev), x.data_ptr(), w.data_ptr(),
-             _vector(target, "target", N, dev, _I64), _vector(lse, "lse", N, dev),
+    _enqueue(dev, "linear_xent_bwd", d, _vector(grad, "grad", N, dev), x.data_ptr(),
+             _row_start(w, "w", d.D, d.ldw), _vector(target, "target", N, dev, _I64), _vector(lse, "lse", N, dev),
              _contiguous(dx, "dx", x.shape, x.dtype, dev), _contiguous(dw, "dw", w.shape, w.dtype, dev),
              _workspace(ws, _head.size("linear_xent_bwd_workspace_size", d), dev))
 

@@ -195,3 +195,19 @@ def test_more_logit_tiles_than_workgroups_of_a_launch():
     tol = 2 * dl + (V / 64 + 108) * U + 4 * U * (2 * s0.abs() + l0.abs())
     _close(loss[rows], l0, tol, "loss")
     _close(lse[rows], s0, tol, "lse")
+
+
+def test_views_that_start_off_a_granule_are_refused_by_name():
+    """Rows of whole 16-byte granules are read in place and have to start on one."""
+    x = torch.zeros(4, 64, dtype=torch.float16, device=DEV)
+    w = torch.zeros(5, 64, dtype=torch.float16, device=DEV)
+    t = torch.zeros(4, dtype=torch.int64, device=DEV)
+    for a, b, name in ((x[:, 4:36], w[:, :32], "x"), (x[:, :32], w[:, 4:36], "w")):
+        with pytest.raises(ValueError, match=f"^{name} must start on a 16-byte boundary"):
+            conv.linear_cross_entropy(a, b, t)
+    loss, lse = conv.linear_cross_entropy(x[:, :32], w[:, :32], t)
+    with pytest.raises(ValueError, match="^w must start on a 16-byte boundary"):
+        conv.linear_cross_entropy_backward(loss, x[:, :32], w[:, 4:36], t, lse)
+    conv.linear_cross_entropy_backward(loss, x[:, 4:36], w[:, :32], t, lse)
+    # rows that are copied first start anywhere
+    conv.linear_cross_entropy(x[:, 3:34], w[:, 1:32], t)
