@@ -174,6 +174,8 @@ def _norm_desc(x, layout, y_dtype, eps, dropout_p, seed, offset):
         P = 1
         for n in x.shape[2:]:
             P *= n
+        if P == 0:                                  # maps without positions: nothing to normalise
+            N, P = 0, 1
     return LayerNormDesc(N, C, P, ldx, 0, 0, _code(x.dtype), _code(y_dtype), lay, 0, eps, dropout_p, seed,
                          offset), N * P
 

@@ -211,3 +211,13 @@ def test_views_that_start_off_a_granule_are_refused_by_name():
     conv.linear_cross_entropy_backward(loss, x[:, 4:36], w[:, :32], t, lse)
     # rows that are copied first start anywhere
     conv.linear_cross_entropy(x[:, 3:34], w[:, 1:32], t)
+
+
+def test_nchw_maps_without_positions():
+    w = torch.ones(16, device=DEV)
+    for shape in ((2, 16, 0), (2, 16, 0, 7)):
+        x = torch.empty(shape, device=DEV)
+        y, mean, rstd = conv.layer_norm(x, w, layout="nchw")
+        assert y.shape == shape and mean.numel() == 0
+        dx, dw, db = conv.layer_norm_backward(x, x, w, mean, rstd, layout="nchw")
+        assert dx.shape == shape and not dw.any() and not db.any()
