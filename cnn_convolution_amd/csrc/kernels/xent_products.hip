@@ -7,7 +7,10 @@
 // back in: dx in the epilogue (+ low[n] w[target[n]]), dw as further products
 // of the stages in which a row's target is one of the wave's classes (at most
 // one more per block of 16 classes, and a block is skipped unless a
-// target falls into it). Bound by the matrix cores: with 8192 rows, a piece of 16384
+// target falls into it). What it took from a row's other entries, summed, goes into dx
+// times the part c that the class weights share: the roundings then multiply w - c,
+// and an offset of all classes cancels as it should, for sum_v G is 0 (30 classes that
+// share 64 times their spread, bf16: dx was off by 0.4 of its size). Bound by the matrix cores: with 8192 rows, a piece of 16384
 // classes and 4096 features, bf16, dx takes 0.82 ms (1340 TFLOP/s) and dw 0.94 ms
 // (1170; 0.90 without hits: both operands come through transposed reads, two for
 // each one of rows, and with a workgroup per tile nothing covers a tile's first
@@ -104,6 +107,47 @@ struct LowExtra {
     }
 };
 
+// dx: acc += rest * shared for this part's share of the blocks of classes. A lane's column is
+// row n of dx; the four lanes of a column take every fourth block.
+template <typename C>
+__device__ __forceinline__ void add_rest(const ProductArgs &a, int part, int64_t m0, int64_t n0, int lane,
+                                         floatx4_t (&acc)[C::FM][C::FN])
+{
+    // nothing shared (weights of either sign, the usual case): nothing to add
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        float c[4];
+        load_vec<4>(a.shared + m0 + i * 16 + (lane >> 4) * 4, c);
+        any |= c[0] != 0.f || c[1] != 0.f || c[2] != 0.f || c[3] != 0.f;
+    }
+    if (!__ballot(any)) return;
+    const int begin = int(int64_t(a.blocks) * part / a.split), end = int(int64_t(a.blocks) * (part + 1) / a.split);
+    float rest[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) rest[j] = 0.f;
+    const float *p = a.rest + n0 + (lane & 15);          // rows below ldr, a multiple of 256
+#pragma unroll 2
+    for (int b = begin + (lane >> 4); b < end; b += 4)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) rest[j] += p[b * a.ldr + 16 * j];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        rest[j] += __shfl_xor(rest[j], 16, 64);
+        rest[j] += __shfl_xor(rest[j], 32, 64);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        float c[4];
+        load_vec<4>(a.shared + m0 + i * 16 + (lane >> 4) * 4, c);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] += rest[j] * c[v];
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // tiles begin, begin + step, .. of one product
 template <typename T, typename C, bool DW>
 __device__ __forceinline__ void product_tiles(const ProductArgs &a, int tiles_m, int tiles_n, int begin, int step,
@@ -146,6 +190,7 @@ __device__ __forceinline__ void product_tiles(const ProductArgs &a, int tiles_m,
             NoExtra none;
             pipe.template run<STORES>(stored, acc, none);
         }
+        if constexpr (HALF && !DW) add_rest<C>(a, part, mt, nt, lane, acc);
         if constexpr (!ONE) {
             stored = m0 + C::BM <= a.M && n0 + C::BN <= a.n;
             if (t + step < all) start(t + step);

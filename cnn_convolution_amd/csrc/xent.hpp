@@ -37,7 +37,8 @@ struct XentPlan {
     int64_t rows_pad;        // rows of G
     int dx_tile, dx_split, dw_tile, dw_split;
     bool dx_direct;          // one piece and no split: dx straight from the product
-    int64_t off_scale, off_t32, off_low, off_hits, off_x, off_w, off_partial, off_g, off_dx, off_dw, bytes;
+    int64_t off_scale, off_t32, off_low, off_hits, off_rest, off_shared, off_some, off_x, off_w, off_partial, off_g,
+        off_dx, off_dw, bytes;
 };
 XentPlan plan_xent_fwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype);
 XentPlan plan_xent_bwd(int64_t N, int64_t V, int64_t D, int64_t ldx, int64_t ldw, int dtype);
@@ -67,7 +68,13 @@ struct GradArgs {
     void *low;               // [N]: what rounding took from G at the target (half precision)
     uint8_t *hits;           // [piece / 32][rows_pad / 32]: whether a target lies in that block of G
     int64_t ldh;
+    float *rest;             // [rest_blocks][ldr]: what rounding took from the other entries (half precision)
+    int64_t ldr;
+    const int *some;         // [somes]: whether the class weights share anything in 256 features; else no rest
+    int somes;
 };
+// blocks of classes of `rest` that G of P classes leaves: one per wave and tile
+int64_t rest_blocks(int tile, int64_t P);
 hipError_t launch_xent_g(const GradArgs &a, int dtype, int tile, hipStream_t s);
 
 struct ProductArgs {
@@ -87,6 +94,10 @@ struct ProductArgs {
     int64_t v0;              // dw: first class of the piece
     const void *w;           // dx: for the rounding residual
     int64_t ldw;             // bytes
+    const float *rest;       // dx in half precision: [blocks][ldr]
+    int64_t ldr;
+    int blocks;
+    const float *shared;     // ... and [M rounded up to 256]: what the rows of w share
 };
 hipError_t launch_xent_dx(const ProductArgs &a, int dtype, int tile, hipStream_t s);
 hipError_t launch_xent_dw(const ProductArgs &a, int dtype, int tile, hipStream_t s);

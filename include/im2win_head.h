@@ -120,8 +120,9 @@ conv2d_status_t layer_norm_bwd(const layer_norm_desc_t *d, const void *dy, const
  * tile by tile in fp32 and never stored; the backward pass forms them a
  * second time, in pieces of the classes, and holds one piece of G in the
  * workspace in the type of x (fp16: scaled by a power of two into the type's
- * range; half precision: what that rounding takes from each row's target entry
- * is added back). dx and dw are accumulated in fp32 and rounded once. N may be
+ * range, which the largest finite grad of an unmasked row decides; half
+ * precision: what that rounding takes from each row's target entry is added
+ * back, and an offset that the class weights share still cancels in dx). dx and dw are accumulated in fp32 and rounded once. N may be
  * 0 (dw is then 0). */
 typedef struct {
     int64_t N, V, D;          /* rows, classes, features                          */

@@ -221,3 +221,68 @@ def test_nchw_maps_without_positions():
         assert y.shape == shape and mean.numel() == 0
         dx, dw, db = conv.layer_norm_backward(x, x, w, mean, rstd, layout="nchw")
         assert dx.shape == shape and not dw.any() and not db.any()
+
+
+# ---- roundings of the gradient of the logits ---------------------------------------------------
+
+
+@pytest.mark.parametrize("N,V,D", [(64, 30, 256), (300, 30, 100), (2100, 1700, 520), (16, 40000, 136), (5, 120, 1032),
+                                   (700, 240, 72), (4100, 33000, 128), (40, 30, 101)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_an_offset_that_all_classes_share_cancels(N, V, D, dt):
+    """sum_v G = 0 in every row, so a vector that all class weights share is not in
+    dx. All logits are 0 here (x = 0) and every entry of G but the target's is 1/V,
+    rounded the same way: unless G's roundings are made to cancel as G does, dx is
+    off by that rounding times the offset. Bound: uo of G on the weights less
+    their offset, the fp32 sums on the weights themselves, half a spacing of dx."""
+    _say(f"shared offset N={N} V={V} D={D} {dt}")
+    g = torch.Generator(device=DEV).manual_seed(N + V)
+    off = torch.randn(1, D, generator=g, device=DEV)
+    w = (torch.randn(V, D, generator=g, device=DEV) + 64.0 * off).to(TYPES[dt])
+    x = torch.zeros(N, D, dtype=TYPES[dt], device=DEV)
+    t = torch.randint(0, V, (N,), generator=g, device=DEV)
+    up = torch.ones(N, device=DEV)
+    _, lse = conv.linear_cross_entropy(x, w, t)
+    dx, _ = conv.linear_cross_entropy_backward(up, x, w, t, lse)
+    wd = w.double()
+    mean = wd.mean(0, keepdim=True)
+    dev = (wd - mean).abs()
+    # G row by row: 1/V, and 1/V - 1 at the target; what the kernel takes as shared
+    # lies within the spread of the class weights, feature by feature
+    dx0 = mean - wd[t]
+    uo = UO[dt] if dt != "f32" else 0.0
+    rough = (dev.mean(0) + dev.amax(0)) * (uo * 1.01) + 2 * uo * uo * dev[t]
+    # p's own error, (4 + |lse|) U of the type's fp32, times the offset; sums of V terms
+    fine = (2 * (V / 64 + 64) + 48 + np.log(V)) * U * (wd.abs().mean(0) + wd.abs()[t]) if dt != "f32" else \
+        (2 * (V + 8) + 48) * U * (wd.abs().mean(0) + wd.abs()[t])
+    _close(dx, dx0, rough + fine + _ulp_half(dx0, dt), "dx")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("N,V", [(512, 21), (512, 100), (600, 3000)])
+def test_shared_offset_of_trained_weights(N, V, dt):
+    """The same with rows that have logits: the relative L2 error of dx stays within
+    that of rounding dx and G's entries on the centred weights."""
+    D = 256
+    g = torch.Generator(device=DEV).manual_seed(V)
+    w = (torch.randn(V, D, generator=g, device=DEV) + 64.0 * torch.randn(1, D, generator=g, device=DEV)) / 8
+    t = torch.randint(0, V, (N,), generator=g, device=DEV)
+    x = torch.randn(N, D, generator=g, device=DEV) / 16
+    x -= (x @ w.mean(0, keepdim=True).t()) @ w.mean(0, keepdim=True) / w.mean(0).norm() ** 2    # logits of order 1
+    x, w = x.to(TYPES[dt]), w.to(TYPES[dt])
+    up = torch.ones(N, device=DEV)
+    _, lse = conv.linear_cross_entropy(x, w, t)
+    dx, _ = conv.linear_cross_entropy_backward(up, x, w, t, lse)
+    dx0, _, G = ref.cross_entropy_grad(up, x, w, t)
+    far = G.abs()
+    far[torch.arange(N, device=DEV), t] = 0
+    wd = w.double()
+    dev = (wd - wd.mean(0)).norm(dim=1)
+    most = (wd - wd.mean(0)).abs().amax(0).norm()       # the mean against what is taken as shared
+    logit = 2 * (D + 1) * U * (x.double().abs() @ wd.abs().t()).amax()         # p's relative error, all classes alike
+    bound = UO[dt] * ((far @ dev + far.sum(1) * most) + dx0.norm(dim=1)) + \
+        2 * logit * far.sum(1) * most + (2 * (V + 56) * U + 4 * U * (1 + lse.double().abs())) * (G.abs() @ wd.norm(dim=1))
+    err = (dx.double() - dx0).norm(dim=1)
+    _say(f"offset {N} {V} {dt}: relative L2 {((dx.double() - dx0).norm() / dx0.norm()).item():.2e}, "
+         f"worst share of the bound {(err / bound).max().item():.2f}")
+    assert bool((err <= bound).all())
