@@ -286,3 +286,52 @@ def test_shared_offset_of_trained_weights(N, V, dt):
     _say(f"offset {N} {V} {dt}: relative L2 {((dx.double() - dx0).norm() / dx0.norm()).item():.2e}, "
          f"worst share of the bound {(err / bound).max().item():.2f}")
     assert bool((err <= bound).all())
+
+
+@pytest.mark.parametrize("N,D,dt,V", [(64, 256, "bf16", 512), (300, 100, "bf16", 512), (2100, 520, "bf16", 512),
+                                      (5000, 64, "bf16", 512), (64, 256, "f16", 4096), (2100, 136, "f16", 4096)])
+def test_rounding_at_the_target_is_taken_back(N, D, dt, V):
+    """With all logits 0, G is 1/V but at the target, where 1 - 1/V lies halfway
+    between two numbers of the type. dx (from x = 0) and dw (from w = 0) have to be as
+    good as with an unrounded G: half a spacing of the result, the fp32 sums'
+    bounds, and the rounding of the target's remainder, uo / V of each row's
+    contribution. The rounding itself, 1 / V, is a multiple of those."""
+    _say(f"target rounding N={N} V={V} D={D} {dt}")
+    g = torch.Generator(device=DEV).manual_seed(N)
+    t = torch.randint(0, V, (N,), generator=g, device=DEV)
+    up = torch.full((N,), 1.0, device=DEV)
+    a = torch.randn(N, D, generator=g, device=DEV).to(TYPES[dt])
+    b = torch.randn(V, D, generator=g, device=DEV).to(TYPES[dt])
+    for x, w in ((torch.zeros_like(a), b), (a, torch.zeros_like(b))):
+        _, lse = conv.linear_cross_entropy(x, w, t)
+        dx, dw = conv.linear_cross_entropy_backward(up, x, w, t, lse)
+        dx0, dw0, G = ref.cross_entropy_grad(up, x, w, t)
+        far = G.abs()
+        far[torch.arange(N, device=DEV), t] = 0         # exact in the type up to p's fp32 error
+        X, W = x.double().abs(), w.double().abs()
+        tol = _ulp_half(dx0, dt) + 2 * (V + 56) * U * (G.abs() @ W) + UO[dt] / V * W[t]
+        _close(dx, dx0, tol, "dx")
+        hit = torch.zeros(V, D, dtype=torch.float64, device=DEV).index_add_(0, t, X)
+        tol = _ulp_half(dw0, dt) + 2 * (N + 56) * U * (G.abs().t() @ X) + UO[dt] / V * hit
+        _close(dw, dw0, tol, "dw")
+
+
+# ---- rows in numbers ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,V,D", [(100352, 21, 256), (100352, 150, 256), (40001, 9, 24)])
+def test_pixels_of_a_batch(N, V, D, dt):
+    """As many rows as a batch has pixels, few classes; the largest row gradient
+    comes late in the array."""
+    x, w, t, up = _xent_case(N, V, D, dt, seed=V)
+    up[N - 2] *= 50.0
+    t[N - 2] = 1
+    _check_xent(x, w, t, up, dt, ref_dev=DEV, what="pixels")
+
+
+def test_row_weights_of_a_millionth_in_fp16():
+    """Scaled into fp16's range, G keeps its digits; dx and dw below 2^-14 lose theirs
+    in their own storage alone."""
+    x, w, t, up = _xent_case(64, 1000, 128, "f16", seed=10)
+    _check_xent(x, w, t, up * 1e-6, "f16", what="row weights of 1e-6", rel=False)
