@@ -55,8 +55,10 @@ constexpr int64_t kMaxTiles = int64_t(1) << 30;
 // one workgroup, or the tiles are short, as many as the chip holds, each taking
 // every grid-th tile and starting the next one's copies before its epilogue; else
 // one per tile: a neighbour's products cover the epilogue, and the CUs that
-// finish first take what is left. (dw of 69 rows, 64798 classes, 256 features, whose
-// tiles have two stages: 103 us with a workgroup per tile, 90 so.)
+// finish first take what is left. (A step with a workgroup per tile and so, 64798
+// classes, 256 features, bf16: 69 rows, dw in two stages, 73.6 and 72.7 us; 200 rows, four
+// stages, 109.1 and 106.0; 400 rows, logits in four, 158.5 and 154.1. More stages: no
+// difference with 6, 8 or 16 as the limit.)
 template <typename C>
 inline int64_t grid_of(int64_t tiles, int64_t stages)
 {

@@ -562,6 +562,13 @@ hipError_t with_hold(const Hold &h, int64_t P, F f)
     return call(Int<8>{}, Int<16>{}, Int<2>{}, Int<8>{});
 }
 
+// Workgroups of the re-reading kernels (1024 to 8192 measure the same: 32 images of 1100
+// channels, 28 x 28, bf16, forward 58.6 us) and of the backward one that holds its
+// tile, each with a row of partial sums (256 channels of 56 x 56, 64 images, fp32: 121.8,
+// 124.3 and 126.9 us with 256, 512 and 1024; 64 channels, 32 images, fp16: 19.4, 15.3 and
+// 14.9); parts of the images for the re-reading dweight and dbias (1100 channels of 28 x 28,
+// 32 images, bf16: 184, 177 and 177 us with 8, 16 and 32; 2000 images of 7 x 7, fp16: 1513, 1383
+// and 1344).
 constexpr int64_t kMaxBlocksFwd = 4096, kMaxBlocksBwd = 512, kImageSplits = 16;
 
 int64_t tiles_of_image(int64_t P, const Hold &h) { return (P + h.pl * h.pv - 1) / (h.pl * h.pv); }

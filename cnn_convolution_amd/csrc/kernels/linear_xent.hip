@@ -276,7 +276,9 @@ int pick_logits(int64_t M, int64_t N, int64_t stages, int dtype, bool narrow)
     return tile;
 }
 
-constexpr int64_t kPieceBytes = int64_t(256) << 20;   // of G
+// Of G, but never less than 256 classes: with more than 2^18 rows (2^19 in half
+// precision) a piece is those 256, 4 GB at 2^22 rows of fp32.
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
 void plan_common(XentPlan &p, int64_t D, int64_t ldx, int64_t ldw, int dtype)
 {

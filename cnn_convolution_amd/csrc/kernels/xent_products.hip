@@ -414,6 +414,12 @@ hipError_t launch_xent_both(const ProductArgs &dx, const ProductArgs &dw, int dt
     });
 }
 
+// 16 threads a chunk for 8 slabs and more of fewer than 65536 chunks: 69 rows, 64798
+// classes, 256 features, bf16, dx in 64 slabs: step 76.7 us with a thread a chunk, 72.2 so; 64
+// rows, 30000 classes, 1024 features, fp16, 16384 chunks 82.0 and 80.9. With few slabs or many
+// chunks a thread a chunk fills the chip as well: 300 rows, 40000 classes, 1024 features,
+// bf16, 76800 chunks, 199.0 so and 201.1 with 16. (In between it costs 1 us: 300 rows, 5000
+// classes, 512 features, fp32 86.3 and 87.5.)
 hipError_t launch_xent_join(const ProductArgs *dx, const ProductArgs *dw, int dtype, hipStream_t s)
 {
     int64_t blocks[2] = {0, 0}, most = 0;
