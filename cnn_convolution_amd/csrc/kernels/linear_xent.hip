@@ -20,14 +20,14 @@ namespace {
 __device__ __forceinline__ bool valid_target(int64_t t, int64_t V) { return t >= 0 && t < V; }
 
 // (m, s) joined by (m2, s2). A part without a class, or of classes at -infinity
-// alone, has the sum 0 and adds nothing. NaN is in a part's sum only: fmaxf passes it
-// over, and a tile of NaN classes and padding has the maximum -infinity, so it is by
-// the sum that a part is left out.
+// alone, is (-infinity, 0) and adds nothing. NaN is in a part's sum only: fmaxf passes
+// it over, and a tile of NaN classes and padding has the maximum -infinity, so it is
+// by the sum that a part is left out (as a choice, not a branch: the next part's load
+// would be waited for behind it).
 __device__ __forceinline__ void join_part(float &m, float &s, float m2, float s2)
 {
-    if (s2 == 0.f) return;
-    const float n = fmaxf(m, m2);
-    s = (s == 0.f ? 0.f : s * __expf(m - n)) + s2 * __expf(m2 - n);
+    const float n = fmaxf(m, m2), a = s * __expf(m - n), b = s2 * __expf(m2 - n);
+    s = (s == 0.f ? 0.f : a) + (s2 == 0.f ? 0.f : b);
     m = n;
 }
 
