@@ -8,13 +8,13 @@
 // of the stages in which a row's target is one of the wave's classes (at most
 // one more per block of 16 classes, and a block is skipped unless a
 // target falls into it). What it took from a row's other entries, summed, goes into dx
-// times the part c that the class weights share: the roundings then multiply w - c,
-// and an offset of all classes cancels as it should, for sum_v G is 0 (30 classes that
-// share 64 times their spread, bf16: dx was off by 0.4 of its size). Bound by the matrix cores: with 8192 rows, a piece of 16384
-// classes and 4096 features, bf16, dx takes 0.82 ms (1340 TFLOP/s) and dw 0.94 ms
-// (1170; 0.90 without hits: both operands come through transposed reads, two for
-// each one of rows, and with a workgroup per tile nothing covers a tile's first
-// copies and epilogue).
+// times what the class weights share, c: the roundings then multiply w - c, and an
+// offset of all classes cancels as it should, for sum_v G is 0 (30 classes that share
+// 64 times their spread, bf16: dx was off by 0.4 of its size). Bound by the matrix
+// cores: with 8192 rows, a piece of 16384 classes and 4096 features, bf16, dx takes 0.82
+// ms (1340 TFLOP/s) and dw 0.94 ms (1170; 0.90 without hits: both operands come through
+// transposed reads, two for each one of rows, and with a workgroup per tile nothing
+// covers a tile's first copies and epilogue).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -107,30 +107,41 @@ struct LowExtra {
     }
 };
 
-// dx: acc += rest * shared for this part's share of the blocks of classes. A lane's column is
-// row n of dx; the four lanes of a column take every fourth block.
-template <typename C>
+// dx: acc += rest * c for this part's share of the blocks of classes, with c what the
+// class weights share but no more than the weight of the row's own target (between 0
+// and that): then |rest c| is within a rounding of the target's own |G w|, whatever the
+// other classes' weights, and no element's error bound grows. (Without it the mean of
+// the classes, or the least of those looked at, exceeds an element's bound where the few
+// classes that count in its row lie apart from the others.) A lane's column is row n of
+// dx; the four lanes of a column take every fourth block.
+template <typename T, typename C>
 __device__ __forceinline__ void add_rest(const ProductArgs &a, int part, int64_t m0, int64_t n0, int lane,
                                          floatx4_t (&acc)[C::FM][C::FN])
 {
+    constexpr int E = 16 / int(sizeof(T));
+    const int64_t m = m0 + (lane >> 4) * 4;
     // nothing shared (weights of either sign, the usual case): nothing to add
     bool any = false;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
         float c[4];
-        load_vec<4>(a.shared + m0 + i * 16 + (lane >> 4) * 4, c);
+        load_vec<4>(a.shared + m + i * 16, c);
         any |= c[0] != 0.f || c[1] != 0.f || c[2] != 0.f || c[3] != 0.f;
     }
     if (!__ballot(any)) return;
     const int begin = int(int64_t(a.blocks) * part / a.split), end = int(int64_t(a.blocks) * (part + 1) / a.split);
+    const int64_t row = n0 + (lane & 15);                // and 16 j on: below ldr, a multiple of 256
     float rest[C::FN];
+    int tgt[C::FN];
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) rest[j] = 0.f;
-    const float *p = a.rest + n0 + (lane & 15);          // rows below ldr, a multiple of 256
+    for (int j = 0; j < C::FN; ++j) {
+        tgt[j] = max(a.t32[row + 16 * j], 0);            // a masked row's rest is 0
+        rest[j] = 0.f;
+    }
 #pragma unroll 2
     for (int b = begin + (lane >> 4); b < end; b += 4)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) rest[j] += p[b * a.ldr + 16 * j];
+        for (int j = 0; j < C::FN; ++j) rest[j] += a.rest[b * a.ldr + row + 16 * j];
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
         rest[j] += __shfl_xor(rest[j], 16, 64);
@@ -139,11 +150,16 @@ __device__ __forceinline__ void add_rest(const ProductArgs &a, int part, int64_t
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
         float c[4];
-        load_vec<4>(a.shared + m0 + i * 16 + (lane >> 4) * 4, c);
+        load_vec<4>(a.shared + m + i * 16, c);
+        const int64_t at = min(m + i * 16, (a.M + E - 1) / E * E - 4);   // w's rows are whole granules
+        Raw<T, 4> w[C::FN];
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            w[j] = load_raw<T, 4>(reinterpret_cast<const T *>(static_cast<const char *>(a.w) + tgt[j] * a.ldw) + at);
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i][j][v] += rest[j] * c[v];
+            for (int v = 0; v < 4; ++v) acc[i][j][v] += rest[j] * __builtin_amdgcn_fmed3f(element(w[j], v), 0.f, c[v]);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
@@ -190,7 +206,7 @@ __device__ __forceinline__ void product_tiles(const ProductArgs &a, int tiles_m,
             NoExtra none;
             pipe.template run<STORES>(stored, acc, none);
         }
-        if constexpr (HALF && !DW) add_rest<C>(a, part, mt, nt, lane, acc);
+        if constexpr (HALF && !DW) add_rest<T, C>(a, part, mt, nt, lane, acc);
         if constexpr (!ONE) {
             stored = m0 + C::BM <= a.M && n0 + C::BN <= a.n;
             if (t + step < all) start(t + step);
