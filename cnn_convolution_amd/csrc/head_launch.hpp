@@ -11,8 +11,8 @@
 namespace im2win {
 
 // Workgroups of `threads` that one launch may have: a grid of more than 2^32 threads is
-// run modulo 2^32, without an error (one of 2^32 is refused). Kernels with more to do stride over the rest
-// or are launched in parts.
+// run modulo 2^32, without an error (one of 2^32 is refused). Kernels with more to do
+// stride over the rest or are launched in parts.
 constexpr int64_t max_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
 
 // Dropout over elements numbered in 64 bits (see im2win_head.h): element i is

@@ -90,9 +90,9 @@ __global__ __launch_bounds__(1024) void xent_scale_kernel(const float *grad, con
 
 // What the class weights share: per feature their mean where all have one sign, else 0,
 // over up to 64 classes spread over all (dx takes no more of it than the weight of a
-// row's own target). 256 features per workgroup,
-// every fourth class a wave; beside the row copy, for whose launch it costs 0.8 us
-// (64 rows, 1000 classes, 512 features, bf16: step 23.3 -> 24.8 us).
+// row's own target). 256 features per workgroup, every fourth class a wave; beside the
+// row copy, for whose launch it costs 0.8 us (64 rows, 1000 classes, 512 features, bf16:
+// step 23.3 -> 24.8 us).
 constexpr int kSharedRows = 64;
 template <typename T>
 __device__ __forceinline__ void shared_weights(const T *w, int64_t ldw, int64_t V, int64_t D, int64_t d0, float *shared,
