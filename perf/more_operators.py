@@ -282,11 +282,11 @@ def _prepare_ff(case, s, rnd):
     if own:
         import cnn_convolution_amd as conv
         s["y"] = torch.empty_like(s["x"])
-        n = conv.feed_forward_workspace_size(s["x"], s["wg"], s["wd"], saved=train, backward=train)
+        n = conv.feed_forward_workspace_size(s["x"], s["wg"], s["wu"], s["wd"], saved=train, dy=s.get("dy"))
         s["ws"] = torch.empty(max(n, 1), dtype=torch.uint8, device=DEV)
         s["saved"] = None
         if train:
-            n = conv.feed_forward_saved_size(s["x"], s["wg"], s["wd"])
+            n = conv.feed_forward_saved_size(s["x"], s["wg"])
             s["saved"] = torch.empty(n, dtype=torch.uint8, device=DEV)
             s["grads"] = [torch.empty_like(s[k]) for k in ("x", "wg", "wu", "wd")]
 
