@@ -13,7 +13,10 @@ include/im2win_conv2d.h).
 
 On the features a convolution leaves, ``head`` has layer norm over the
 channels, dropout, and the softmax cross entropy of a linear classifier, with
-their gradients (include/im2win_head.h); its functions are exported here too.
+their gradients (include/im2win_head.h). ``block`` has what goes between those and
+what trains them: a gated feed-forward block, the norms around its residual sum, and
+AdamW over many tensors (include/im2win_block.h). Their functions are exported here
+too.
 """
 from __future__ import annotations
 
@@ -22,6 +25,10 @@ from .head import (dropout, dropout_into, layer_norm, layer_norm_into, layer_nor
                    layer_norm_backward_into, layer_norm_workspace_size, linear_cross_entropy,
                    linear_cross_entropy_into, linear_cross_entropy_backward,
                    linear_cross_entropy_backward_into, linear_cross_entropy_workspace_size)
+from .block import (AdamWState, adamw, adamw_state, adamw_state_values, adamw_state_values_into,  # noqa: F401
+                    feed_forward, feed_forward_into, feed_forward_backward, feed_forward_backward_into,
+                    feed_forward_saved_size, feed_forward_workspace_size, residual_norm, residual_norm_into,
+                    residual_norm_backward, residual_norm_backward_into, residual_norm_workspace_size)
 from ._lib import (Conv2dError, Desc, Plan, ImplicitPlan, LAYOUT_CL, LAYOUT_FRAG, LAYOUT_ROW,  # noqa: F401
                    F16, F32, BF16, NCHW, NHWC, make_desc, workspace_size, plan, implicit_plan,
                    implicit_workspace_size, profile_enable, profile_read, status_string)
@@ -33,7 +40,11 @@ __all__ = ["conv2d", "conv2d_into", "conv2d_implicit", "conv2d_implicit_into", "
            "dropout", "dropout_into", "layer_norm", "layer_norm_into", "layer_norm_backward",
            "layer_norm_backward_into", "layer_norm_workspace_size", "linear_cross_entropy",
            "linear_cross_entropy_into", "linear_cross_entropy_backward",
-           "linear_cross_entropy_backward_into", "linear_cross_entropy_workspace_size"]
+           "linear_cross_entropy_backward_into", "linear_cross_entropy_workspace_size",
+           "AdamWState", "adamw", "adamw_state", "adamw_state_values", "adamw_state_values_into",
+           "feed_forward", "feed_forward_into", "feed_forward_backward", "feed_forward_backward_into",
+           "feed_forward_saved_size", "feed_forward_workspace_size", "residual_norm", "residual_norm_into",
+           "residual_norm_backward", "residual_norm_backward_into", "residual_norm_workspace_size"]
 
 
 def _dtype_code(t) -> int:

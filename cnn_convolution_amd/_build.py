@@ -25,6 +25,7 @@ SOURCES = [
     os.path.join(CSRC, "plan.cpp"),
     os.path.join(CSRC, "api.cpp"),
     os.path.join(CSRC, "head_api.cpp"),
+    os.path.join(CSRC, "block_api.cpp"),
     os.path.join(CSRC, "noalloc.hip"),
     os.path.join(CSRC, "kernels", "pack.hip"),
     os.path.join(CSRC, "kernels", "weight_stage.hip"),
@@ -42,6 +43,11 @@ SOURCES = [
     os.path.join(CSRC, "kernels", "linear_xent.hip"),
     os.path.join(CSRC, "kernels", "xent_logits.hip"),
     os.path.join(CSRC, "kernels", "xent_products.hip"),
+    os.path.join(CSRC, "kernels", "feed_forward.hip"),
+    os.path.join(CSRC, "kernels", "ff_tiles.hip"),
+    os.path.join(CSRC, "kernels", "ff_products.hip"),
+    os.path.join(CSRC, "kernels", "residual_norm.hip"),
+    os.path.join(CSRC, "kernels", "adamw.hip"),
 ]
 
 ARCH = "gfx950"

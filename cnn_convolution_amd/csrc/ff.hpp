@@ -1,0 +1,82 @@
+// The feed-forward block's plan and the launchers of its tiled products.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "block_launch.hpp"
+#include "tile_launch.hpp"
+
+namespace im2win {
+
+// a and u as the matrix cores leave them: fp32 blocks of 16 x 16, [rows_pad / 16][F / 16
+// up][a, u][lane][4], lane l holding f = 4(l/16) + v and row l%16. Written and read
+// by the same lanes, 1 KB at a time.
+struct FfSaved {
+    float *pre;
+    int64_t fblocks;
+    void *h;                 // [rows_pad][Fp], zeros past N and F
+};
+
+// h (and with `pre` a, u) of rows 0 .. rows_pad - 1
+struct FfGate {
+    const void *x, *wg, *wu;
+    int64_t ldx, ldg, ldu;   // bytes
+    int64_t N, F, Dp, rows_pad, Fp;
+    FfSaved to;              // pre: or null
+    int act;
+};
+hipError_t launch_ff_gate(const FfGate &a, int dtype, int tile, hipStream_t s);
+
+// da and du, each [rows_pad][Fp] with zeros past N and F, side by side in rows of 2 Fp
+struct FfBack {
+    const void *dy, *wd;
+    int64_t lddy, ldd;       // bytes
+    int64_t N, F, O, Op, rows_pad, Fp;
+    FfSaved from;
+    void *g;
+    const float *amax;       // [kAmaxParts]: of |dy|, or null (no scale)
+    int act;
+};
+hipError_t launch_ff_back(const FfBack &a, int dtype, int tile, hipStream_t s);
+constexpr int kAmaxParts = 256;
+
+// out[n][m] = sum over segments and k of a[seg] times b: the products that leave an
+// output. a: rows ([m][k], y) or columns ([k][m]); b: rows ([n][k], y and dx) or
+// columns ([k][n], the weight gradients).
+struct FfProduct {
+    const void *a[2];        // per segment of K
+    int64_t lda[2], ldb;     // bytes
+    const void *b;
+    int64_t b_step;          // bytes from b's part of a segment or output to the next one's
+    int64_t M, a_count;      // outputs, and what exists of a
+    int64_t n, b_count;      // rows of an output, and what exists of b
+    int64_t K, k_a, k_b;     // of a segment
+    int segs, outs;          // 1 or 2; outs 2: two outputs of n rows each
+    int split;
+    float *slab;             // [split][outs n][M] fp32, or null
+    void *out[2];
+    int64_t ldo;             // elements
+    const float *amax;       // the outputs are divided by the scale it gives, or null
+};
+hipError_t launch_ff_y(const FfProduct &p, int dtype, int tile, hipStream_t s);
+hipError_t launch_ff_dx(const FfProduct &p, int dtype, int tile, hipStream_t s);
+hipError_t launch_ff_dw(const FfProduct &p, int dtype, int tile, hipStream_t s);
+// dx, dw_down and dw_gate with dw_up in one launch, 64 x 64 tiles
+hipError_t launch_ff_all(const FfProduct &dx, const FfProduct &dwd, const FfProduct &dwgu, int dtype, hipStream_t s);
+// the slabs of up to three products added in order
+hipError_t launch_ff_join(const FfProduct *p, int count, int dtype, hipStream_t s);
+
+// few rows, nothing saved: h stays fp32
+struct FfRows {
+    const void *x, *wg, *wu, *wd;
+    int64_t ldx, ldg, ldu, ldd, ldy;   // elements
+    int64_t N, D, F, O;
+    float *h;                // [N][F]
+    void *y;
+    int act;
+};
+hipError_t launch_ff_rows(const FfRows &a, int dtype, hipStream_t s);
+
+}  // namespace im2win

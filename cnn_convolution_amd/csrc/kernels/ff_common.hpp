@@ -1,0 +1,59 @@
+// Shared by the feed-forward kernels: the activations, the scale of fp16 gradients.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../ff.hpp"
+#include "im2win_block.h"
+
+namespace im2win {
+
+// act(a) and its slope. expf, erff and tanhf are within a few ulp, and divisions are
+// whole ones: fp32 outputs keep their digits.
+__device__ __forceinline__ void activate(int act, float a, float &f, float &df)
+{
+    if (act == FF_SILU || act == FF_SIGMOID) {
+        const float s = 1.f / (1.f + expf(-a));
+        const bool silu = act == FF_SILU;
+        f = silu ? a * s : s;
+        df = silu ? s * (1.f + a * (1.f - s)) : s * (1.f - s);
+    } else if (act == FF_GELU) {
+        const float c = 0.5f * (1.f + erff(a * 0.70710678118654752f));
+        f = a * c;
+        df = c + a * (expf(-0.5f * a * a) * 0.39894228040143268f);
+    } else if (act == FF_GELU_TANH) {
+        const float k = 0.79788456080286536f, q = 0.044715f * a * a;
+        const float t = tanhf(k * a * (1.f + q));
+        f = 0.5f * a * (1.f + t);
+        df = 0.5f * (1.f + t) + 0.5f * a * (1.f - t * t) * k * (1.f + 3.f * q);
+    } else {
+        f = a < 0.f ? 0.f : a;               // NaN stays
+        df = a > 0.f ? 1.f : 0.f;
+    }
+}
+
+// S: the power of two with S * max |dy| in [1, 2) (1 where there is none), by every
+// wave for itself
+__device__ __forceinline__ float dy_scale(const float *amax)
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAmaxParts / 64; ++i) m = fmaxf(m, amax[(threadIdx.x & 63) + i * 64]);
+    for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
+    if (!(m > 0.f)) return 1.f;
+    int e = 0;
+    (void)frexpf(m, &e);                     // m = f 2^e, f in [1/2, 1)
+    return ldexpf(1.f, 1 - e);
+}
+
+template <typename F>
+hipError_t with_ff_type(int dtype, F f)
+{
+    if (dtype == 0) return f(float{});
+    if (dtype == 1) return f(_Float16{});
+    return f(__bf16{});
+}
+
+}  // namespace im2win

@@ -1,0 +1,262 @@
+// The feed-forward block's products with an epilogue of their own, the hidden
+// features along m:
+//   gate   a[n][f] = sum_d Wg[f][d] x[n][d] and u likewise in one tile: its rows
+//          alternate, 16 of Wg and the same 16 of Wu, so that a lane holds a and u of
+//          the same (n, f); h = act(a) u leaves once, with a and u in fp32 for the
+//          backward pass
+//   back   dh[n][f] = sum_o Wd[o][f] dy[n][o]; da = dh u act'(a), du = dh act(a)
+// a and u are kept rather than formed again: forming them costs a third more products
+// in the backward pass, keeping them 8 bytes per (n, f) written and read once; in
+// half precision bits they would cost the gradients theirs (half as much error again
+// as the outputs' own rounding).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "ff_common.hpp"
+#include "head_gemm.hpp"
+#include "head_vec.hpp"
+
+namespace im2win {
+namespace {
+
+// rows of two matrices, alternating 16 by 16: row r of the tile is row
+// 16 (r / 32) + r % 16 of matrix r / 16 % 2
+struct DualOperand {
+    const void *p[2];
+    int64_t ld[2];           // bytes
+    int64_t count;           // rows of each
+    int64_t k_end;
+};
+
+template <typename T, int TB, int WAVES>
+struct DualLoad {
+    static constexpr int E = 16 / int(sizeof(T)), KI = 128 / int(sizeof(T));
+    static constexpr int blocks = TB / 8, per_wave = blocks / WAVES;
+    static_assert(blocks % WAVES == 0 && WAVES % 4 == 0, "a wave's blocks are of one matrix");
+
+    const char *base;        // of this wave's matrix
+    uint32_t off[per_wave];
+
+    static __device__ __forceinline__ int block(int wave, int i) { return wave + WAVES * i; }
+
+    __device__ __forceinline__ void init(const DualOperand &op, int64_t first, int wave, int lane)
+    {
+        const int half = (wave >> 1) & 1;
+        const int64_t ld = half ? op.ld[1] : op.ld[0];
+        first = first < op.count ? first : op.count - 1;
+        const int n = int(op.count - first < TB / 2 ? op.count - first : TB / 2);
+        base = static_cast<const char *>(half ? op.p[1] : op.p[0]) + first * ld;
+#pragma unroll
+        for (int i = 0; i < per_wave; ++i) {
+            const int r = block(wave, i) * 8 + (lane >> 3), f = min((r >> 5) * 16 + (r & 15), n - 1);
+            off[i] = uint32_t(f) * uint32_t(ld) + (((lane & 7) ^ (lane >> 3)) << 4);
+        }
+    }
+    __device__ __forceinline__ void issue(int64_t s, int i, uint32_t lds, int wave) const
+    {
+        copy_to_lds_at(base + s * 128, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
+    }
+    // the last stage of a K that ends inside it: zeros past it
+    __device__ __forceinline__ void issue_tail(int64_t stage, int left, uint32_t lds, int wave, int lane) const
+    {
+        const char *b = base + stage * 128;
+#pragma unroll
+        for (int i = 0; i < per_wave; ++i) {
+            const bool ok = ((lane & 7) ^ (lane >> 3)) * E < left;
+            const char *src = ok ? b + off[i] : reinterpret_cast<const char *>(&zero_granule);
+            copy_to_lds(src, __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
+        }
+    }
+};
+
+// 4 consecutive values of each of NB blocks of 16 (m0 + 16 b + 4 (lane / 16) ..) of row
+// p, up to `end`: half precision pairs of blocks as 16-byte stores
+template <typename T, int NB>
+__device__ __forceinline__ void store_blocks(T *p, int64_t m0, int64_t end, int lane, const floatx4_t (&v)[NB])
+{
+    if constexpr (sizeof(T) == 2 && NB % 2 == 0) {
+        const int64_t m8 = m0 + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+            const uint4 q = pair_blocks<T>(v[b], v[b + 1]);
+            store_some_raw(p + m8 + b * 16, end - m8 - b * 16, __builtin_bit_cast(Raw<T, 8>, q));
+        }
+    } else {
+        const int64_t m4 = m0 + (lane >> 4) * 4;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float q[4] = {v[b][0], v[b][1], v[b][2], v[b][3]};
+            store_some<4>(p + m4 + b * 16, end - m4 - b * 16, q);
+        }
+    }
+}
+
+template <typename T, typename C, bool SAVE>
+__global__ __launch_bounds__(C::threads, C::per_simd) void ff_gate_kernel(const FfGate a, int tiles_m, int tiles_n)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    constexpr int NB = C::FM / 2;              // blocks of 16 hidden features of a wave
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    const int tiles = tiles_m * tiles_n, stages = int((a.Dp + 128 / int(sizeof(T)) - 1) / (128 / int(sizeof(T))));
+    const DualOperand A{{a.wg, a.wu}, {a.ldg, a.ldu}, a.F, a.Dp};
+    const GemmOperand B{a.x, a.ldx, a.N, a.Dp};
+    TilePipe<T, C, false, false, DualLoad<T, C::BM, C::waves>> pipe(smem);
+    int64_t f0 = 0, n0 = 0;
+    auto start = [&](int t) {
+        int tm, tn;
+        strip_tile(t, tiles_m, tiles_n, tm, tn);
+        f0 = int64_t(tm) * (C::BM / 2);
+        n0 = int64_t(tn) * C::BN;
+        pipe.start(A, B, f0, n0, 0, stages);
+    };
+    start(blockIdx.x);
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t ft = f0 + wm * (C::BM / C::WM / 2), nt = n0 + wn * (C::BN / C::WN);
+        floatx4_t acc[C::FM][C::FN];
+        NoExtra none;
+        pipe.template run<0>(false, acc, none);
+        if (t + int(gridDim.x) < tiles) start(t + gridDim.x);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            if (nt + 16 * j >= a.rows_pad) continue;
+            const int64_t row = nt + 16 * j + (lane & 15);
+            const bool in = row < a.N;
+            floatx4_t h[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int64_t f = ft + b * 16 + (lane >> 4) * 4;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    float g, dg;
+                    activate(a.act, acc[2 * b][j][v], g, dg);
+                    h[b][v] = in && f + v < a.F ? g * acc[2 * b + 1][j][v] : 0.f;
+                }
+                if (SAVE && ft + b * 16 < a.F) {
+                    floatx4_t *p = reinterpret_cast<floatx4_t *>(a.to.pre) +
+                                   ((nt / 16 + j) * a.to.fblocks + ft / 16 + b) * 128 + lane;
+                    p[0] = acc[2 * b][j];
+                    p[64] = acc[2 * b + 1][j];
+                }
+            }
+            store_blocks<T, NB>(static_cast<T *>(a.to.h) + row * a.Fp, ft, a.Fp, lane, h);
+        }
+    }
+}
+
+template <typename T, typename C>
+__global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const FfBack a, int tiles_m, int tiles_n)
+{
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    const int tiles = tiles_m * tiles_n, stages = int((a.O + 128 / int(sizeof(T)) - 1) / (128 / int(sizeof(T))));
+    const GemmOperand A{a.wd, a.ldd, a.Fp, a.O};
+    const GemmOperand B{a.dy, a.lddy, a.N, a.Op};
+    TilePipe<T, C, true, false> pipe(smem);
+    int64_t m0 = 0, n0 = 0;
+    auto start = [&](int t) {
+        int tm, tn;
+        strip_tile(t, tiles_m, tiles_n, tm, tn);
+        m0 = int64_t(tm) * C::BM;
+        n0 = int64_t(tn) * C::BN;
+        pipe.start(A, B, m0, n0, 0, stages);
+    };
+    start(blockIdx.x);
+    const float S = a.amax ? dy_scale(a.amax) : 1.f;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t ft = m0 + wm * (C::BM / C::WM), nt = n0 + wn * (C::BN / C::WN);
+        floatx4_t acc[C::FM][C::FN];
+        NoExtra none;
+        pipe.template run<0>(false, acc, none);
+        if (t + int(gridDim.x) < tiles) start(t + gridDim.x);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            if (nt + 16 * j >= a.rows_pad) continue;
+            const int64_t row = nt + 16 * j + (lane & 15);
+            const bool in = row < a.N;
+            floatx4_t du[C::FM];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                // blocks past the last hidden feature read that one's again
+                const int64_t fb = min(ft / 16 + i, a.from.fblocks - 1), f = ft + i * 16 + (lane >> 4) * 4;
+                const floatx4_t *p =
+                    reinterpret_cast<const floatx4_t *>(a.from.pre) + ((nt / 16 + j) * a.from.fblocks + fb) * 128 + lane;
+                const floatx4_t av = p[0], uv = p[64];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    float g, dg;
+                    activate(a.act, av[v], g, dg);
+                    const bool ok = in && f + v < a.F;
+                    const float dh = acc[i][j][v] * S;
+                    du[i][v] = ok ? dh * g : 0.f;
+                    acc[i][j][v] = ok ? dh * (uv[v] * dg) : 0.f;
+                }
+            }
+            floatx4_t da[C::FM];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) da[i] = acc[i][j];
+            T *g = static_cast<T *>(a.g) + row * 2 * a.Fp;
+            store_blocks<T, C::FM>(g, ft, a.Fp, lane, da);
+            store_blocks<T, C::FM>(g + a.Fp, ft, a.Fp, lane, du);
+        }
+    }
+}
+
+template <typename C, typename K, typename A>
+hipError_t launch_tiles(K kernel, const A &a, int64_t tm, int64_t tn, int64_t stages, std::atomic<uint64_t> &allowed,
+                        hipStream_t s)
+{
+    if (tm * tn > kMaxTiles) return hipErrorInvalidValue;
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid_of<C>(tm * tn, stages))), dim3(C::threads), C::lds_bytes, s, a,
+                       int(tm), int(tn));
+    return hipGetLastError();
+}
+
+template <typename T, typename C>
+hipError_t launch_gate(const FfGate &a, hipStream_t s)
+{
+    const int64_t tm = ceil_div(a.Fp, C::BM / 2), tn = ceil_div(a.rows_pad, C::BN);
+    const int64_t stages = ceil_div(a.Dp * int64_t(sizeof(T)), 128);
+    static std::atomic<uint64_t> allowed[2];
+    if (a.to.pre) return launch_tiles<C>(ff_gate_kernel<T, C, true>, a, tm, tn, stages, allowed[1], s);
+    return launch_tiles<C>(ff_gate_kernel<T, C, false>, a, tm, tn, stages, allowed[0], s);
+}
+
+template <typename T, typename C>
+hipError_t launch_back(const FfBack &a, hipStream_t s)
+{
+    const int64_t tm = ceil_div(a.Fp, C::BM), tn = ceil_div(a.rows_pad, C::BN);
+    static std::atomic<uint64_t> allowed;
+    return launch_tiles<C>(ff_back_kernel<T, C>, a, tm, tn, ceil_div(a.O * int64_t(sizeof(T)), 128), allowed, s);
+}
+
+}  // namespace
+
+hipError_t launch_ff_gate(const FfGate &a, int dtype, int tile, hipStream_t s)
+{
+    return with_ff_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        switch (tile) {
+        case kTile256: return launch_gate<T, C256>(a, s);
+        case kTile128: return launch_gate<T, C128>(a, s);
+        default: return launch_gate<T, C64>(a, s);
+        }
+    });
+}
+
+hipError_t launch_ff_back(const FfBack &a, int dtype, int tile, hipStream_t s)
+{
+    return with_ff_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        switch (tile) {
+        case kTile256: return launch_back<T, C256>(a, s);
+        case kTile128: return launch_back<T, C128>(a, s);
+        default: return launch_back<T, C64>(a, s);
+        }
+    });
+}
+
+}  // namespace im2win

@@ -1,5 +1,5 @@
-// Tiled matrix product of the linear cross entropy, out[n][m] = sum_k A[m][k]
-// B[n][k], on the matrix cores with fp32 accumulation.
+// Tiled matrix product of the linear cross entropy and the feed-forward block,
+// out[n][m] = sum_k A[m][k] B[n][k], on the matrix cores with fp32 accumulation.
 //
 // A K stage is 128 bytes of K (64 half-precision or 32 fp32 values). Both tiles
 // go from memory straight into LDS (global_load_lds_dwordx4, 1 KB per wave
@@ -104,6 +104,13 @@ __device__ __forceinline__ void copy_to_lds_at(const char *base, uint32_t off, u
                  : "memory", "m0");
 }
 
+struct GemmOperand {
+    const void *p;
+    int64_t ld;              // bytes between rows (rows) or K rows (columns), a multiple of 16
+    int64_t count;           // rows or columns that exist; columns: a multiple of 16 bytes' worth
+    int64_t k_end;           // K values that exist; columns repeat the last one past it
+};
+
 // one operand's tile: TB rows or columns, of which `count` exist in memory from
 // `base` on
 template <typename T, int TB, int WAVES, bool COLS>
@@ -132,9 +139,10 @@ struct TileLoad {
 
     static __device__ __forceinline__ int block(int wave, int i) { return (wave + WAVES * i) % blocks; }
 
-    __device__ __forceinline__ void init(const char *p, int64_t ld_bytes, int64_t first, int64_t count, int wave,
-                                         int lane)
+    __device__ __forceinline__ void init(const GemmOperand &op, int64_t first, int wave, int lane)
     {
+        const char *p = static_cast<const char *>(op.p);
+        const int64_t ld_bytes = op.ld, count = op.count;
         kstride = ld_bytes;
         if constexpr (!COLS) first = first < count ? first : count - 1;   // a tile of padding alone
         const int n = int(count - first < TB ? count - first : TB);       // at least 1
@@ -167,10 +175,10 @@ struct TileLoad {
         return min((lane % GR) ^ swz(k), n / E - 1);
     }
 
-    // copy i of this wave for the stage whose K starts at b
-    __device__ __forceinline__ void issue(const char *b, int i, uint32_t lds, int wave) const
+    // copy i of this wave for whole stage s
+    __device__ __forceinline__ void issue(int64_t s, int i, uint32_t lds, int wave) const
     {
-        copy_to_lds_at(b, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
+        copy_to_lds_at(base + s * step, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
     }
     // the last stage of a K that ends inside it (left < KI values): rows read
     // zeros past it, columns repeat the last K row (the other operand has zeros
@@ -254,13 +262,6 @@ __device__ __forceinline__ floatx4_t mfma_half(const uint4 &a, const uint4 &b, f
     }
 }
 
-struct GemmOperand {
-    const void *p;
-    int64_t ld;              // bytes between rows (rows) or K rows (columns), a multiple of 16
-    int64_t count;           // rows or columns that exist; columns: a multiple of 16 bytes' worth
-    int64_t k_end;           // K values that exist; columns repeat the last one past it
-};
-
 // No further products (see tile_product).
 struct NoExtra {
     template <typename R, typename A>
@@ -288,7 +289,8 @@ struct NoExtra {
 //   memory path 1024 cycles of a stage's 2048).
 // 256 x 256 tiles, bf16: 1.36 us per 64-wide stage, 1540 TFLOP/s (without the
 // copies 1700, without the LDS reads 1580: what is left is issue and power).
-template <typename T, typename C, bool ACOLS, bool BCOLS>
+// LoadA: what brings A's tile into LDS, one operand's unless said.
+template <typename T, typename C, bool ACOLS, bool BCOLS, typename LoadA = TileLoad<T, C::BM, C::waves, ACOLS>>
 struct TilePipe {
     static constexpr int KI = 128 / int(sizeof(T)), FM = C::FM, FN = C::FN, NST = C::NST;
     static constexpr int STEPS = 2 * FM;
@@ -301,7 +303,7 @@ struct TilePipe {
     const int lane, wave;
     const lds_ptr sm;        // the A buffers first, then the B buffers
     const uint32_t sbase;
-    TileLoad<T, C::BM, C::waves, ACOLS> la;
+    LoadA la;
     TileLoad<T, C::BN, C::waves, BCOLS> lb;
     FragRead<T, C::BM, ACOLS> ra;
     FragRead<T, C::BN, BCOLS> rb;
@@ -352,21 +354,22 @@ struct TilePipe {
     __device__ __forceinline__ void copy(int u, int s, int buf)      // copy u of whole stage s
     {
         if (u < UA)
-            la.issue(la.base + int64_t(s) * la.step, u, sbase + buf * C::a_bytes, wave);
+            la.issue(s, u, sbase + buf * C::a_bytes, wave);
         else
-            lb.issue(lb.base + int64_t(s) * lb.step, u - UA, sbase + NST * C::a_bytes + buf * C::b_bytes, wave);
+            lb.issue(s, u - UA, sbase + NST * C::a_bytes + buf * C::b_bytes, wave);
     }
 
     // The buffers are free (run() has ended or not begun).
-    __device__ __forceinline__ void start(const GemmOperand &A, const GemmOperand &B, int64_t m0, int64_t n0,
-                                          int first, int end)
+    template <typename OpA>
+    __device__ __forceinline__ void start(const OpA &A, const GemmOperand &B, int64_t m0, int64_t n0, int first,
+                                          int end)
     {
         s0 = first;
         s1 = end;
         a_end = A.k_end;
         b_end = B.k_end;
-        la.init(static_cast<const char *>(A.p), A.ld, m0, A.count, wave, lane);
-        lb.init(static_cast<const char *>(B.p), B.ld, n0, B.count, wave, lane);
+        la.init(A, m0, wave, lane);
+        lb.init(B, n0, wave, lane);
 #pragma unroll
         for (int s = 0; s < NST; ++s)
             if (s0 + s < s1) request(s0 + s, s);
@@ -374,16 +377,19 @@ struct TilePipe {
 
     // since: vector memory operations that each wave is known to have issued
     // since start() (no more than it has). extra.run(s, read, acc) may add products
-    // of stage s's A fragments, read(i, h) for block i of half h.
+    // of stage s's A fragments, read(i, h) for block i of half h. clear: acc starts at 0,
+    // else the products are added to it.
     template <int SINCE, typename Extra>
-    __device__ __forceinline__ void run(bool since, floatx4_t (&acc)[C::FM][C::FN], Extra &extra)
+    __device__ __forceinline__ void run(bool since, floatx4_t (&acc)[C::FM][C::FN], Extra &extra, bool clear = true)
     {
         const int whole = int(min(a_end, b_end) / KI);        // stages that both operands fill
         const int last = s1 - 1;
+        if (clear) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < FN; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        }
 
         floatx4_t total[PARTS ? FM : 1][PARTS ? FN : 1] = {};
         auto add_up = [&](bool clear) {

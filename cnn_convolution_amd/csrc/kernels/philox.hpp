@@ -20,9 +20,10 @@ __device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c)
     return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
 }
 
-__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t seed)
+// counter (block, high), 64 bits each
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t high, uint64_t seed)
 {
-    uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32), c2 = 0, c3 = 0;
+    uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32), c2 = uint32_t(high), c3 = uint32_t(high >> 32);
     uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
@@ -40,7 +41,7 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t seed)
 // bit j: element j of the block is kept
 __device__ __forceinline__ uint32_t keep_bits(uint64_t block, const DropSpec &d)
 {
-    const uint4 w = philox(d.offset + block, d.seed);
+    const uint4 w = philox(d.offset + block, 0, d.seed);
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
     uint32_t m = 0;
 #pragma unroll
@@ -54,7 +55,7 @@ __device__ __forceinline__ uint32_t keep_bits(uint64_t block, const DropSpec &d)
 // a whole block: f = kept ? f * scale : 0
 __device__ __forceinline__ void drop_block(uint64_t block, const DropSpec &d, float (&f)[8])
 {
-    const uint4 w = philox(d.offset + block, d.seed);
+    const uint4 w = philox(d.offset + block, 0, d.seed);
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

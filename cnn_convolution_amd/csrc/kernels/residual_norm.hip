@@ -1,0 +1,814 @@
+// The norm after a block, its gate, the residual sum and the norm before the next
+// block (im2win_block.h) over rows of channels: forward, backward and the reduction of
+// the parameters' gradients. All bound by HBM: forward reads b and r and writes out and
+// y once, backward reads dy, dout, b and out and writes dr and db once.
+//
+// A row of each tensor is held in registers by a group of LPR lanes, KCH chunks of 8
+// channels per lane, between the two norms as well; the next row's loads are issued
+// before the current row is worked on. A workgroup takes consecutive rows, so that the
+// gate stays in registers until its group ends.
+//
+// Backward needs, per gate's group and channel, S1 = sum t xhat(b) and S2 = sum t alone:
+//   dgate = bs (pw S1 + pb S2),  dpw = sum_groups bs gate S1,  dpb = sum_groups bs gate S2
+// (without the norm after the block S1 = sum t b and dgate = bs S1), and of the next
+// norm sum dy xhat(out) and sum dy: four sums per channel stay in registers over all of a
+// workgroup's rows. S1 and S2 leave at the end of each group that the workgroup sees,
+// the others at its end; a second launch adds them in a fixed order.
+// Rows wider than a group holds, or narrower than a vector, are read again for each
+// pass over them.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../block_launch.hpp"
+#include "norm_common.hpp"
+
+namespace im2win {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int threads_of(int lpr) { return lpr > 64 ? lpr : kThreads; }
+
+// Rows of block b of B: consecutive. Record (block, group of gates) is number
+// block + group: blocks share at most their end's group, so no two are the same.
+__host__ __device__ __forceinline__ int64_t first_row(int64_t N, int64_t B, int64_t b)
+{
+    const int64_t q = N / B, rem = N - q * B;
+    return q * b + (b < rem ? b : rem);
+}
+__device__ __forceinline__ int64_t block_of(int64_t N, int64_t B, int64_t row)
+{
+    const int64_t q = N / B, rem = N - q * B;              // B <= N: q >= 1
+    return row < rem * (q + 1) ? row / (q + 1) : rem + (row - rem * (q + 1)) / q;
+}
+
+// sum of (a, b) over the LPR lanes of a row; `slot` alternates between calls
+template <int LPR>
+__device__ __forceinline__ void row_sum2(float &a, float &b, float2 (*red)[threads_of(LPR) / 64], int &slot)
+{
+    a = lane_sum<(LPR < 64 ? LPR : 64)>(a);
+    b = lane_sum<(LPR < 64 ? LPR : 64)>(b);
+    if constexpr (LPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = float2{a, b};
+        __syncthreads();
+        a = 0.f;
+        b = 0.f;
+#pragma unroll
+        for (int w = 0; w < LPR / 64; ++w) {
+            a += red[slot][w].x;
+            b += red[slot][w].y;
+        }
+        slot ^= 1;
+    }
+}
+
+// channels of a row that wave w of its lanes holds
+template <int LPR, int KCH>
+__device__ __forceinline__ float count_of(int C, int w)
+{
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < KCH; ++i) n += max(0, min(C - (i * LPR + w * 64) * 8, (LPR < 64 ? LPR : 64) * 8));
+    return float(n);
+}
+
+// Mean (0 but for layer norms) and rstd of a row: each wave's own mean and squared
+// deviations around it, then the row's from those: sum (z - mean)^2 = sum_w [Q_w + n_w
+// (mean_w - mean)^2], as safe against cancellation as two passes, with one barrier.
+template <int LPR, int KCH>
+__device__ __forceinline__ float2 row_stats(const float (&v)[KCH][8], int l, int C, int layer, float eps,
+                                            float2 (*red)[threads_of(LPR) / 64], int &slot)
+{
+    constexpr int L = LPR < 64 ? LPR : 64, WAVES = LPR > 64 ? LPR / 64 : 1;
+    const float fc = float(C);
+    float mean = 0.f, sq = 0.f;
+    if (layer) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < KCH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += (i * LPR + l) * 8 + e < C ? v[i][e] : 0.f;
+        mean = lane_sum<L>(sum) / fmaxf(count_of<LPR, KCH>(C, l / 64), 1.f);
+    }
+#pragma unroll
+    for (int i = 0; i < KCH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = v[i][e] - mean;
+            sq += (i * LPR + l) * 8 + e < C ? d * d : 0.f;
+        }
+    sq = lane_sum<L>(sq);
+    if constexpr (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) red[slot][l / 64] = float2{mean, sq};
+        __syncthreads();
+        float total = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) total += red[slot][w].x * count_of<LPR, KCH>(C, w);
+        mean = total / fc;
+        sq = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float d = red[slot][w].x - mean;
+            sq += red[slot][w].y + count_of<LPR, KCH>(C, w) * d * d;
+        }
+        slot ^= 1;
+    }
+    return float2{mean, 1.f / sqrtf(sq / fc + eps)};
+}
+
+// channels c .. c + 7 of a parameter vector, `absent` where there is none
+__device__ __forceinline__ void param(const float *p, float absent, int c, int C, float (&f)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = absent;
+    if (p) load_some<8>(p + c, max(0, C - c), f);
+}
+
+template <bool EXACT, typename T>
+__device__ __forceinline__ void store_row(T *p, int left, const Raw<T, 8> &r)
+{
+    if constexpr (EXACT) {
+        if (left > 0) store_raw(p, r);
+    } else {
+        store_some_raw(p, max(left, 0), r);
+    }
+}
+
+template <typename TR, typename TB, int LPR, int KCH, bool EXACT>
+__global__ __launch_bounds__(threads_of(LPR)) void res_norm_fwd_kernel(const ResNormArgs a)
+{
+    constexpr int G = threads_of(LPR) / LPR;               // rows in flight per workgroup
+    __shared__ float2 red[2][threads_of(LPR) / 64];
+    const int l = threadIdx.x % LPR, C = a.C;
+    const TB *b = static_cast<const TB *>(a.b);
+    const TR *r = static_cast<const TR *>(a.r);
+    const int64_t end = first_row(a.N, gridDim.x, blockIdx.x + 1);
+    int64_t row = first_row(a.N, gridDim.x, blockIdx.x) + threadIdx.x / LPR;
+
+    Raw<TB, 8> qb[KCH];
+    Raw<TR, 8> qr[KCH];
+    auto load = [&](int64_t k) {
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            qb[i] = load_row<TB, 8, EXACT>(b + k * a.ldb, (i * LPR + l) * 8, C);
+            qr[i] = load_row<TR, 8, EXACT>(r + k * a.ldr, (i * LPR + l) * 8, C);
+        }
+    };
+    // past the last row that one is read again (no branch around a load)
+    load(min(row, a.N - 1));
+    float pw[KCH][8], pb[KCH][8], w[KCH][8], bias[KCH][8], gate[KCH][8];
+#pragma unroll
+    for (int i = 0; i < KCH; ++i) {
+        const int c = (i * LPR + l) * 8;
+        param(a.pw, 1.f, c, C, pw[i]);
+        param(a.pb, 0.f, c, C, pb[i]);
+        param(a.w, 1.f, c, C, w[i]);
+        param(a.bias, 0.f, c, C, bias[i]);
+    }
+    int64_t group = -1;
+    int slot = 0;
+    // a workgroup-wide row's barriers: every thread makes the same number of rounds
+    for (; row < end; row += G) {
+        const int64_t g = a.groups > 1 ? row / a.rows : 0;
+        if (g != group) {
+            group = g;
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) {
+                param(a.gate ? a.gate + g * C : nullptr, 1.f, (i * LPR + l) * 8, C, gate[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) gate[i][e] *= a.bs;
+            }
+        }
+        float v[KCH][8], o[KCH][8];
+#pragma unroll
+        for (int i = 0; i < KCH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[i][e] = element(qb[i], e);
+                o[i][e] = element(qr[i], e);
+            }
+        load(min(row + G, a.N - 1));
+        float2 st{0.f, 0.f};
+        if (a.post) {
+            st = row_stats<LPR, KCH>(v, l, C, a.layer, a.eps, red, slot);
+#pragma unroll
+            for (int i = 0; i < KCH; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = (v[i][e] - st.x) * st.y * pw[i][e] + pb[i][e];
+        }
+        Raw<TR, 8> out[KCH];
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[i][e] = a.rs * o[i][e] + gate[i][e] * v[i][e];
+            out[i] = to_raw<TR, 8>(o[i]);
+        }
+        const float2 so = row_stats<LPR, KCH>(o, l, C, a.layer, a.eps, red, slot);
+        Raw<TB, 8> y[KCH];
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[i][e] = (o[i][e] - so.x) * so.y * w[i][e] + bias[i][e];
+            y[i] = to_raw<TB, 8>(o[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            arrive(qb[i]);
+            arrive(qr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            const int c = (i * LPR + l) * 8;
+            store_row<EXACT>(static_cast<TR *>(a.out) + row * a.ldo + c, C - c, out[i]);
+            store_row<EXACT>(static_cast<TB *>(a.y) + row * a.ldy + c, C - c, y[i]);
+        }
+        if (l == 0 && a.stats) reinterpret_cast<float4 *>(a.stats)[row] = float4{st.x, st.y, so.x, so.y};
+    }
+}
+
+// any row: one workgroup per row, which reads it again for each pass
+template <typename TR, typename TB>
+__global__ __launch_bounds__(kThreads) void res_norm_fwd_wide_kernel(const ResNormArgs a)
+{
+    __shared__ float2 red[2][kThreads / 64];
+    const int C = a.C;
+    const float fc = float(C);
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+        const TB *b = static_cast<const TB *>(a.b) + row * a.ldb;
+        const TR *r = static_cast<const TR *>(a.r) + row * a.ldr;
+        const float *gate = a.gate ? a.gate + (a.groups > 1 ? row / a.rows : 0) * C : nullptr;
+        float v[8], zero = 0.f;
+        float2 st{0.f, 0.f}, so{0.f, 0.f};
+        if (a.post) {
+            if (a.layer) {
+                float sum = 0.f;
+                for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+                    load_some<8>(b + c, C - c, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum += v[e];
+                }
+                row_sum2<kThreads>(sum, zero, red, slot);
+                st.x = sum / fc;
+            }
+            float sq = 0.f;
+            for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+                load_some<8>(b + c, C - c, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sq += e < C - c ? (v[e] - st.x) * (v[e] - st.x) : 0.f;
+            }
+            row_sum2<kThreads>(sq, zero, red, slot);
+            st.y = 1.f / sqrtf(sq / fc + a.eps);
+        }
+        auto sum_at = [&](int c, float (&o)[8]) {
+            float p[8], q[8];
+            load_some<8>(b + c, C - c, v);
+            load_some<8>(r + c, C - c, o);
+            if (a.post) {
+                param(a.pw, 1.f, c, C, p);
+                param(a.pb, 0.f, c, C, q);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = (v[e] - st.x) * st.y * p[e] + q[e];
+            }
+            param(gate, 1.f, c, C, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = e < C - c ? a.rs * o[e] + p[e] * a.bs * v[e] : 0.f;
+        };
+        float o[8];
+        if (a.layer) {
+            float sum = 0.f;
+            for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+                sum_at(c, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += o[e];
+            }
+            row_sum2<kThreads>(sum, zero, red, slot);
+            so.x = sum / fc;
+        }
+        float sq = 0.f;
+        for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+            sum_at(c, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sq += e < C - c ? (o[e] - so.x) * (o[e] - so.x) : 0.f;
+        }
+        row_sum2<kThreads>(sq, zero, red, slot);
+        so.y = 1.f / sqrtf(sq / fc + a.eps);
+        for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+            float w[8], bias[8];
+            sum_at(c, o);
+            store_some<8>(static_cast<TR *>(a.out) + row * a.ldo + c, C - c, o);
+            param(a.w, 1.f, c, C, w);
+            param(a.bias, 0.f, c, C, bias);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = (o[e] - so.x) * so.y * w[e] + bias[e];
+            store_some<8>(static_cast<TB *>(a.y) + row * a.ldy + c, C - c, o);
+        }
+        if (threadIdx.x == 0 && a.stats)
+            reinterpret_cast<float4 *>(a.stats)[row] = float4{st.x, st.y, so.x, so.y};
+    }
+}
+
+// Workspace of the backward pass: the blocks' sums of the next norm [B][2][C], then
+// the records [B + groups][2][C], then (wide rows) each row's two means [N][2].
+struct Sums {
+    float *norm, *record;
+    float2 *means;
+};
+__host__ __device__ __forceinline__ Sums sums_of(const ResNormArgs &a, int64_t B)
+{
+    float *p = static_cast<float *>(a.ws);
+    const int64_t G = a.groups > 1 ? a.groups : 1;
+    return {p, p + B * 2 * a.C, reinterpret_cast<float2 *>(p + (2 * B + G) * 2 * a.C)};
+}
+
+template <typename TR, typename TB, int LPR, int KCH, bool EXACT>
+__global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const ResNormArgs a)
+{
+    constexpr int THREADS = threads_of(LPR), G = THREADS / LPR;
+    __shared__ float2 red[2][THREADS / 64];
+    __shared__ __align__(16) float part[LPR * KCH * 8];
+    const int l = threadIdx.x % LPR, q = threadIdx.x / LPR, C = a.C;
+    const float fc = float(C);
+    const TB *dy = static_cast<const TB *>(a.dy), *b = static_cast<const TB *>(a.b);
+    const TR *dout = static_cast<const TR *>(a.dout), *out = static_cast<const TR *>(a.out);
+    const float4 *stats = reinterpret_cast<const float4 *>(a.stats);
+    const int64_t begin = first_row(a.N, gridDim.x, blockIdx.x), end = first_row(a.N, gridDim.x, blockIdx.x + 1);
+    const Sums sums = sums_of(a, gridDim.x);
+    const bool records = a.ws && (a.post || a.gate), has_dout = a.dout != nullptr;
+
+    Raw<TB, 8> qy[KCH], qb[KCH], ny[KCH], nb[KCH];
+    Raw<TR, 8> qd[KCH], qo[KCH], nd[KCH], no[KCH];
+    float4 qs, ns;
+    auto load = [&](int64_t k, Raw<TB, 8> (&y)[KCH], Raw<TB, 8> (&x)[KCH], Raw<TR, 8> (&d)[KCH], Raw<TR, 8> (&o)[KCH],
+                    float4 &s) {
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            const int c = (i * LPR + l) * 8;
+            y[i] = load_row<TB, 8, EXACT>(dy + k * a.lddy, c, C);
+            x[i] = load_row<TB, 8, EXACT>(b + k * a.ldb, c, C);
+            o[i] = load_row<TR, 8, EXACT>(out + k * a.ldo, c, C);
+            // without a dout: out again, and cleared below
+            d[i] = load_row<TR, 8, EXACT>(has_dout ? dout + k * a.lddo : out + k * a.ldo, c, C);
+        }
+        s = stats[k];
+    };
+    float w[KCH][8], gq[KCH][8], s1[KCH][8], s2[KCH][8], s3[KCH][8], s4[KCH][8];
+#pragma unroll
+    for (int i = 0; i < KCH; ++i) {
+        param(a.w, 1.f, (i * LPR + l) * 8, C, w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s3[i][e] = s4[i][e] = 0.f;
+    }
+    // the workgroup's groups of lanes added in order into dst[C]
+    auto flush = [&](const float (&v)[KCH][8], float *dst) {
+        for (int k = 0; k < G; ++k) {
+            __syncthreads();
+            if (q == k)
+#pragma unroll
+                for (int i = 0; i < KCH; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float &t = part[(i * LPR + l) * 8 + e];
+                        t = (k ? t : 0.f) + v[i][e];
+                    }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < C; c += THREADS) dst[c] = part[c];
+    };
+    int slot = 0;
+    for (int64_t from = begin; from < end;) {
+        // the rows of one gate
+        const int64_t g = a.groups > 1 ? from / a.rows : 0;
+        const int64_t to = a.groups > 1 ? min(end, (g + 1) * a.rows) : end;
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            const int c = (i * LPR + l) * 8;
+            float p[8];
+            param(a.gate ? a.gate + g * C : nullptr, 1.f, c, C, gq[i]);
+            param(a.post ? a.pw : nullptr, 1.f, c, C, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                gq[i][e] *= a.bs * p[e];
+                s1[i][e] = s2[i][e] = 0.f;
+            }
+        }
+        load(min(from + q, a.N - 1), qy, qb, qd, qo, qs);
+        for (int64_t row = from + q; row < to; row += G) {
+            load(min(row + G, a.N - 1), ny, nb, nd, no, ns);
+            float t[KCH][8], h[KCH][8], u = 0.f, v = 0.f;
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) {
+                const int left = C - (i * LPR + l) * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = EXACT ? 0 < left : e < left;
+                    const float y = in ? element(qy[i], e) : 0.f;
+                    h[i][e] = in ? (element(qo[i], e) - qs.z) * qs.w : 0.f;
+                    s3[i][e] += y * h[i][e];
+                    s4[i][e] += y;
+                    t[i][e] = y * w[i][e];
+                    u += t[i][e];
+                    v += t[i][e] * h[i][e];
+                }
+            }
+            row_sum2<LPR>(u, v, red, slot);
+            u = a.layer ? u / fc : 0.f;
+            v /= fc;
+            Raw<TR, 8> dr[KCH];
+            Raw<TB, 8> db[KCH];
+            float m = 0.f, n = 0.f;
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) {
+                const int left = C - (i * LPR + l) * 8;
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = EXACT ? 0 < left : e < left;
+                    t[i][e] = (has_dout ? element(qd[i], e) : 0.f) + qs.w * (t[i][e] - u - h[i][e] * v);
+                    t[i][e] = in ? t[i][e] : 0.f;
+                    f[e] = a.rs * t[i][e];
+                    const float x = in ? element(qb[i], e) : 0.f;
+                    h[i][e] = a.post ? (in ? (x - qs.x) * qs.y : 0.f) : x;
+                    s1[i][e] += t[i][e] * h[i][e];
+                    s2[i][e] += t[i][e];
+                    t[i][e] *= gq[i][e];
+                    m += t[i][e];
+                    n += t[i][e] * h[i][e];
+                }
+                dr[i] = to_raw<TR, 8>(f);
+            }
+            if (a.post) {
+                row_sum2<LPR>(m, n, red, slot);
+                m = a.layer ? m / fc : 0.f;
+                n /= fc;
+#pragma unroll
+                for (int i = 0; i < KCH; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[i][e] = qs.y * (t[i][e] - m - h[i][e] * n);
+            }
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) db[i] = to_raw<TB, 8>(t[i]);
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) {
+                qy[i] = ny[i];
+                qb[i] = nb[i];
+                qd[i] = nd[i];
+                qo[i] = no[i];
+            }
+            qs = ns;
+#pragma unroll
+            for (int i = 0; i < KCH; ++i) {
+                const int c = (i * LPR + l) * 8;
+                store_row<EXACT>(static_cast<TR *>(a.dr) + row * a.lddr + c, C - c, dr[i]);
+                store_row<EXACT>(static_cast<TB *>(a.db) + row * a.lddb + c, C - c, db[i]);
+            }
+        }
+        if (records) {
+            float *rec = sums.record + (blockIdx.x + g) * 2 * C;
+            flush(s1, rec);
+            flush(s2, rec + C);
+        }
+        from = to;
+    }
+    if (!a.ws) return;
+    flush(s3, sums.norm + int64_t(blockIdx.x) * 2 * C);
+    flush(s4, sums.norm + (int64_t(blockIdx.x) * 2 + 1) * C);
+}
+
+// any row: one workgroup per row, three reads of it
+template <typename TR, typename TB>
+__global__ __launch_bounds__(kThreads) void res_norm_bwd_wide_kernel(const ResNormArgs a, float2 *means)
+{
+    __shared__ float2 red[2][kThreads / 64];
+    const int C = a.C;
+    const float fc = float(C);
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+        const TB *dy = static_cast<const TB *>(a.dy) + row * a.lddy, *b = static_cast<const TB *>(a.b) + row * a.ldb;
+        const TR *dout = a.dout ? static_cast<const TR *>(a.dout) + row * a.lddo : nullptr;
+        const TR *out = static_cast<const TR *>(a.out) + row * a.ldo;
+        const float *gate = a.gate ? a.gate + (a.groups > 1 ? row / a.rows : 0) * C : nullptr;
+        const float4 st = reinterpret_cast<const float4 *>(a.stats)[row];
+        float h[8], g[8], w[8], u = 0.f, v = 0.f;
+        auto next = [&](int c) {               // xhat(out) and dy * weight
+            load_some<8>(out + c, C - c, h);
+            load_some<8>(dy + c, C - c, g);
+            param(a.w, 1.f, c, C, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[e] = e < C - c ? (h[e] - st.z) * st.w : 0.f;
+                g[e] *= w[e];
+            }
+        };
+        for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+            next(c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                u += g[e];
+                v += g[e] * h[e];
+            }
+        }
+        row_sum2<kThreads>(u, v, red, slot);
+        u = a.layer ? u / fc : 0.f;
+        v /= fc;
+        if (means && threadIdx.x == 0) means[row] = float2{u, v};
+        float t[8], m = 0.f, n = 0.f;
+        auto through = [&](int c) {            // t, then xhat(b) (or b) in h
+            next(c);
+            float d[8] = {};
+            if (dout) load_some<8>(dout + c, C - c, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = e < C - c ? d[e] + st.w * (g[e] - u - h[e] * v) : 0.f;
+            load_some<8>(b + c, C - c, h);
+            if (a.post)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = e < C - c ? (h[e] - st.x) * st.y : 0.f;
+        };
+        auto gated = [&](int c) {
+            float p[8];
+            param(gate, 1.f, c, C, w);
+            param(a.post ? a.pw : nullptr, 1.f, c, C, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] *= w[e] * (a.bs * p[e]);
+        };
+        for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+            through(c);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = a.rs * t[e];
+            store_some<8>(static_cast<TR *>(a.dr) + row * a.lddr + c, C - c, f);
+            gated(c);
+            if (a.post) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    m += t[e];
+                    n += t[e] * h[e];
+                }
+            } else {
+                store_some<8>(static_cast<TB *>(a.db) + row * a.lddb + c, C - c, t);
+            }
+        }
+        if (!a.post) continue;
+        row_sum2<kThreads>(m, n, red, slot);
+        m = a.layer ? m / fc : 0.f;
+        n /= fc;
+        for (int c = threadIdx.x * 8; c < C; c += kThreads * 8) {
+            through(c);
+            gated(c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = st.y * (t[e] - m - h[e] * n);
+            store_some<8>(static_cast<TB *>(a.db) + row * a.lddb + c, C - c, t);
+        }
+    }
+}
+
+// the wide rows' sums: a workgroup takes 512 channels of one block's rows, a wave one
+// row at a time
+template <typename TR, typename TB>
+__global__ __launch_bounds__(kThreads) void res_norm_cols_kernel(const ResNormArgs a)
+{
+    __shared__ float part[4][512];
+    const int C = a.C, wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int64_t B = gridDim.y, begin = first_row(a.N, B, blockIdx.y), end = first_row(a.N, B, blockIdx.y + 1);
+    const int c0 = blockIdx.x * 512, c = c0 + l * 8, left = C - c;
+    const Sums sums = sums_of(a, B);
+    float w[8], s3[8] = {}, s4[8] = {};
+    param(a.w, 1.f, c, C, w);
+    auto flush = [&](const float (&v)[8], float *dst) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[wave][l * 8 + e] = v[e];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 512 && c0 + i < C; i += kThreads)
+            dst[c0 + i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+    };
+    for (int64_t from = begin; from < end;) {
+        const int64_t g = a.groups > 1 ? from / a.rows : 0;
+        const int64_t to = a.groups > 1 ? min(end, (g + 1) * a.rows) : end;
+        float s1[8] = {}, s2[8] = {};
+        if (left > 0)
+            for (int64_t row = from + wave; row < to; row += 4) {
+                const float4 st = reinterpret_cast<const float4 *>(a.stats)[row];
+                const float2 mean = sums.means[row];
+                float o[8], y[8], d[8] = {}, b[8];
+                load_some<8>(static_cast<const TR *>(a.out) + row * a.ldo + c, left, o);
+                load_some<8>(static_cast<const TB *>(a.dy) + row * a.lddy + c, left, y);
+                load_some<8>(static_cast<const TB *>(a.b) + row * a.ldb + c, left, b);
+                if (a.dout) load_some<8>(static_cast<const TR *>(a.dout) + row * a.lddo + c, left, d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float h = (o[e] - st.z) * st.w;
+                    const float t = d[e] + st.w * (y[e] * w[e] - mean.x - h * mean.y);
+                    s3[e] += y[e] * h;
+                    s4[e] += y[e];
+                    s1[e] += t * (a.post ? (b[e] - st.x) * st.y : b[e]);
+                    s2[e] += t;
+                }
+            }
+        if (a.post || a.gate) {
+            float *rec = sums.record + (blockIdx.y + g) * 2 * C;
+            flush(s1, rec);
+            flush(s2, rec + C);
+        }
+        from = to;
+    }
+    flush(s3, sums.norm + int64_t(blockIdx.y) * 2 * C);
+    flush(s4, sums.norm + (int64_t(blockIdx.y) * 2 + 1) * C);
+}
+
+// The parameters' gradients from the blocks' sums: a workgroup takes 64 channels of one
+// output pair (dweight, dbias), (dpw, dpb) or of one group's dgate, 16 threads a channel.
+__global__ __launch_bounds__(1024) void res_norm_join_kernel(const ResNormArgs a, int64_t B)
+{
+    __shared__ float2 part[16][64];
+    const int C = a.C, col = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const Sums sums = sums_of(a, B);
+    const int64_t G = a.groups > 1 ? a.groups : 1, tiles = (C + 63) / 64;
+    const int64_t jobs = a.dgate ? 2 + G : 2;
+    for (int64_t k = blockIdx.x; k < jobs * tiles; k += gridDim.x) {
+        const int64_t job = k / tiles;
+        const int c = int(k - job * tiles) * 64 + col;
+        float x = 0.f, y = 0.f;
+        if (c < C) {
+            if (job == 0 && (a.dw || a.dbias)) {
+#pragma unroll 4
+                for (int64_t b = q; b < B; b += 16) {
+                    x += sums.norm[b * 2 * C + c];
+                    y += sums.norm[(b * 2 + 1) * C + c];
+                }
+            } else if (job == 1 && (a.dpw || a.dpb)) {
+                for (int64_t b = q; b < B; b += 16) {
+                    const int64_t first = a.groups > 1 ? first_row(a.N, B, b) / a.rows : 0;
+                    const int64_t last = a.groups > 1 ? (first_row(a.N, B, b + 1) - 1) / a.rows : 0;
+                    for (int64_t g = first; g <= last; ++g) {
+                        const float s = a.gate ? a.bs * a.gate[g * C + c] : a.bs;
+                        x += s * sums.record[(b + g) * 2 * C + c];
+                        y += s * sums.record[((b + g) * 2 + 1) * C + c];
+                    }
+                }
+            } else if (job >= 2) {
+                const int64_t g = job - 2;
+                const int64_t first = a.groups > 1 ? block_of(a.N, B, g * a.rows) : 0;
+                const int64_t last = a.groups > 1 ? block_of(a.N, B, (g + 1) * a.rows - 1) : B - 1;
+#pragma unroll 4
+                for (int64_t b = first + q; b <= last; b += 16) {
+                    x += sums.record[(b + g) * 2 * C + c];
+                    y += sums.record[((b + g) * 2 + 1) * C + c];
+                }
+            }
+        }
+        part[q][col] = float2{x, y};
+        __syncthreads();
+        for (int m = 8; m > 0; m >>= 1) {
+            if (q < m) {
+                part[q][col].x += part[q + m][col].x;
+                part[q][col].y += part[q + m][col].y;
+            }
+            __syncthreads();
+        }
+        // the next job's part[0] is written by the threads that read this one's
+        if (q > 0 || c >= C) continue;
+        const float2 s = part[0][col];
+        if (job == 0) {
+            if (a.dw) a.dw[c] = s.x;
+            if (a.dbias) a.dbias[c] = s.y;
+        } else if (job == 1) {
+            if (a.dpw) a.dpw[c] = s.x;
+            if (a.dpb) a.dpb[c] = s.y;
+        } else {
+            const float pw = a.post && a.pw ? a.pw[c] : 1.f, pb = a.post && a.pb ? a.pb[c] : 0.f;
+            a.dgate[(job - 2) * C + c] = a.bs * (pw * s.x + pb * s.y);
+        }
+    }
+}
+
+// no rows: the sums are 0
+__global__ __launch_bounds__(kThreads) void res_norm_zero_kernel(const ResNormArgs a)
+{
+    const int64_t step = int64_t(gridDim.x) * kThreads;
+    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < a.groups * a.C || i < a.C; i += step) {
+        if (a.dgate && i < a.groups * a.C) a.dgate[i] = 0.f;
+        if (i >= a.C) continue;
+        for (float *p : {a.dpw, a.dpb, a.dw, a.dbias})
+            if (p) p[i] = 0.f;
+    }
+}
+
+// The group that holds a row of C channels: as few lanes as keep it to one chunk
+// each. lpr 0: no group holds it.
+struct Group {
+    int lpr, kch;
+};
+Group group_of(int64_t C)
+{
+    const int64_t ch = (C + 7) / 8;
+    if (C < 8) return {0, 0};
+    for (int l : {8, 16, 32, 64, 128, 256, 512})
+        if (ch <= l) return {l, 1};
+    if (ch <= 1024) return {512, 2};
+    return {0, 0};
+}
+
+template <typename F>
+hipError_t with_group(const Group &g, F f)
+{
+    using std::integral_constant;
+#define IM2WIN_GROUP(L, K) \
+    if (g.lpr == L && g.kch == K) return f(integral_constant<int, L>{}, integral_constant<int, K>{});
+    IM2WIN_GROUP(8, 1)
+    IM2WIN_GROUP(16, 1)
+    IM2WIN_GROUP(32, 1)
+    IM2WIN_GROUP(64, 1)
+    IM2WIN_GROUP(128, 1)
+    IM2WIN_GROUP(256, 1)
+    IM2WIN_GROUP(512, 1)
+    IM2WIN_GROUP(512, 2)
+#undef IM2WIN_GROUP
+    return hipErrorInvalidValue;
+}
+
+// workgroups: 16 waves to a CU forward, 8 backward, where each leaves sums
+int64_t blocks_of(int64_t N, const Group &g, int waves)
+{
+    const int64_t per = threads_of(g.lpr) / g.lpr;
+    return std::max<int64_t>(1, std::min((N + per - 1) / per, int64_t(256) * waves / (threads_of(g.lpr) / 64)));
+}
+constexpr int64_t kWideBlocks = 2048, kColBlocks = 32;
+
+int64_t bwd_blocks(int64_t N, int64_t C)
+{
+    const Group g = group_of(C);
+    return g.lpr ? blocks_of(N, g, 8) : std::max<int64_t>(1, std::min(N, kColBlocks));
+}
+
+}  // namespace
+
+int64_t res_norm_bwd_ws_bytes(int64_t N, int64_t C, int64_t groups)
+{
+    const int64_t B = bwd_blocks(N, C), G = std::max<int64_t>(groups, 1);
+    return ((2 * B + G) * 2 * C * 4 + (group_of(C).lpr ? 0 : N * 8) + 255) / 256 * 256;
+}
+
+hipError_t launch_res_norm_fwd(const ResNormArgs &a, hipStream_t s)
+{
+    const Group g = group_of(a.C);
+    return with_norm_types(a.dtype, a.branch_dtype, [&](auto tr, auto tb) {
+        using TR = typename decltype(tr)::type;
+        using TB = typename decltype(tb)::type;
+        if (!g.lpr) {
+            hipLaunchKernelGGL((res_norm_fwd_wide_kernel<TR, TB>), dim3(unsigned(std::min(a.N, kWideBlocks))),
+                               dim3(kThreads), 0, s, a);
+            return hipGetLastError();
+        }
+        return with_group(g, [&](auto lpr, auto kch) {
+            constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
+            const dim3 grid(unsigned(blocks_of(a.N, g, 16))), threads(threads_of(LPR));
+            if (a.C % 8 == 0)
+                hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
+            else
+                hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
+{
+    if (a.N == 0) {
+        const int64_t n = std::max<int64_t>(a.groups, 1) * a.C;
+        hipLaunchKernelGGL(res_norm_zero_kernel, dim3(unsigned(std::min<int64_t>((n + 255) / 256, 4096))),
+                           dim3(kThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    const Group g = group_of(a.C);
+    const int64_t B = bwd_blocks(a.N, a.C);
+    const hipError_t e = with_norm_types(a.dtype, a.branch_dtype, [&](auto tr, auto tb) {
+        using TR = typename decltype(tr)::type;
+        using TB = typename decltype(tb)::type;
+        if (!g.lpr) {
+            hipLaunchKernelGGL((res_norm_bwd_wide_kernel<TR, TB>), dim3(unsigned(std::min(a.N, kWideBlocks))),
+                               dim3(kThreads), 0, s, a, a.ws ? sums_of(a, B).means : nullptr);
+            const hipError_t e1 = hipGetLastError();
+            if (e1 != hipSuccess || !a.ws) return e1;
+            hipLaunchKernelGGL((res_norm_cols_kernel<TR, TB>), dim3(unsigned((a.C + 511) / 512), unsigned(B)),
+                               dim3(kThreads), 0, s, a);
+            return hipGetLastError();
+        }
+        return with_group(g, [&](auto lpr, auto kch) {
+            constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
+            const dim3 grid{unsigned(B)}, threads(threads_of(LPR));
+            if (a.C % 8 == 0)
+                hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
+            else
+                hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
+            return hipGetLastError();
+        });
+    });
+    if (e != hipSuccess || !a.ws) return e;
+    const int64_t jobs = (a.dgate ? 2 + std::max<int64_t>(a.groups, 1) : 2) * ((a.C + 63) / 64);
+    hipLaunchKernelGGL(res_norm_join_kernel, dim3(unsigned(std::min<int64_t>(jobs, 4096))), dim3(1024), 0, s, a, B);
+    return hipGetLastError();
+}
+
+}  // namespace im2win
