@@ -10,16 +10,17 @@
 
 namespace im2win {
 
-// a and u as the matrix cores leave them: fp32 blocks of 16 x 16, [rows_pad / 16][F / 16
-// up][a, u][lane][4], lane l holding f = 4(l/16) + v and row l%16. Written and read
-// by the same lanes, 1 KB at a time.
+// act(a) and u act'(a), the factors of dh in du and da, as the matrix cores leave them:
+// fp32 blocks of 16 x 16, [row / 16][f / 16][two][lane][4] for whole tiles of 256 rows
+// and features, lane l holding f = 4(l/16) + v and row l%16. Written (where rows and
+// features exist) and read by the same lanes, 1 KB at a time.
 struct FfSaved {
     float *pre;
     int64_t fblocks;
     void *h;                 // [rows_pad][Fp], zeros past N and F
 };
 
-// h (and with `pre` a, u) of rows 0 .. rows_pad - 1
+// h (and with `pre` the factors) of rows 0 .. rows_pad - 1
 struct FfGate {
     const void *x, *wg, *wu;
     int64_t ldx, ldg, ldu;   // bytes

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         float g, dg;
-        activate(a.act, acc[0][v], g, dg);
+        activate<sizeof(T) == 4>(a.act, acc[0][v], g, dg);
         h[v] = g * acc[1][v];
     }
     const int64_t m = f0 + (lane >> 4) * 4;
@@ -267,8 +267,9 @@ FfPlan plan_common(const FfSizes &z)
     p.Fp = round_up(z.F, e);
     p.Op = round_up(z.O, e);
     p.rows_pad = round_up(z.N, 128 / es);
-    p.fblocks = ceil_div(z.F, 16);
-    p.pre_bytes = p.rows_pad / 16 * p.fblocks * 2048;
+    // whole tiles: the back launch's reads need no bounds
+    p.fblocks = round_up(z.F, 256) / 16;
+    p.pre_bytes = round_up(z.N, 256) / 16 * p.fblocks * 2048;
     p.copy_x = z.D % e != 0 || z.ldx % e != 0;
     p.copy_g = z.D % e != 0 || z.ldg % e != 0;
     p.copy_u = z.D % e != 0 || z.ldu % e != 0;

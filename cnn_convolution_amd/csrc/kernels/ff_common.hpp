@@ -10,24 +10,36 @@
 
 namespace im2win {
 
-// act(a) and its slope. expf, erff and tanhf are within a few ulp, and divisions are
-// whole ones: fp32 outputs keep their digits.
+// 1 / (1 + exp(-a)): fp32 outputs keep their digits (expf and the division are within
+// an ulp or two); half precision takes the hardware's exp2 and reciprocal, a few fp32
+// ulp off, which is all that the epilogue of a 256 x 256 tile has time for
+template <bool EXACT>
+__device__ __forceinline__ float logistic(float a)
+{
+    if constexpr (EXACT) return 1.f / (1.f + expf(-a));
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
+}
+
+// act(a) and its slope. EXACT: for fp32 outputs.
+template <bool EXACT>
 __device__ __forceinline__ void activate(int act, float a, float &f, float &df)
 {
     if (act == FF_SILU || act == FF_SIGMOID) {
-        const float s = 1.f / (1.f + expf(-a));
+        const float s = logistic<EXACT>(a);
         const bool silu = act == FF_SILU;
         f = silu ? a * s : s;
         df = silu ? s * (1.f + a * (1.f - s)) : s * (1.f - s);
     } else if (act == FF_GELU) {
         const float c = 0.5f * (1.f + erff(a * 0.70710678118654752f));
+        const float q = -0.5f * a * a, e = EXACT ? expf(q) : __builtin_amdgcn_exp2f(q * 1.4426950408889634f);
         f = a * c;
-        df = c + a * (expf(-0.5f * a * a) * 0.39894228040143268f);
+        df = c + a * (e * 0.39894228040143268f);
     } else if (act == FF_GELU_TANH) {
-        const float k = 0.79788456080286536f, q = 0.044715f * a * a;
-        const float t = tanhf(k * a * (1.f + q));
-        f = 0.5f * a * (1.f + t);
-        df = 0.5f * (1.f + t) + 0.5f * a * (1.f - t * t) * k * (1.f + 3.f * q);
+        // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
+        const float k = 1.5957691216057308f, q = 0.044715f * a * a;
+        const float s = logistic<EXACT>(k * a * (1.f + q));
+        f = a * s;
+        df = s + a * s * (1.f - s) * k * (1.f + 3.f * q);
     } else {
         f = a < 0.f ? 0.f : a;               // NaN stays
         df = a > 0.f ? 1.f : 0.f;

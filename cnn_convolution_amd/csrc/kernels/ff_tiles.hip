@@ -71,24 +71,25 @@ struct DualLoad {
     }
 };
 
-// 4 consecutive values of each of NB blocks of 16 (m0 + 16 b + 4 (lane / 16) ..) of row
-// p, up to `end`: half precision pairs of blocks as 16-byte stores
+// 4 consecutive values of each of NB blocks of 16 (16 b + 4 (lane / 16) ..) at p, of
+// which `left` are in the row, whole vectors; half precision pairs of blocks as 16-byte
+// stores
 template <typename T, int NB>
-__device__ __forceinline__ void store_blocks(T *p, int64_t m0, int64_t end, int lane, const floatx4_t (&v)[NB])
+__device__ __forceinline__ void store_blocks(T *p, int left, int lane, const floatx4_t (&v)[NB])
 {
     if constexpr (sizeof(T) == 2 && NB % 2 == 0) {
-        const int64_t m8 = m0 + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+        const int m8 = ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
 #pragma unroll
         for (int b = 0; b < NB; b += 2) {
             const uint4 q = pair_blocks<T>(v[b], v[b + 1]);
-            store_some_raw(p + m8 + b * 16, end - m8 - b * 16, __builtin_bit_cast(Raw<T, 8>, q));
+            if (m8 + b * 16 < left) store_raw(p + m8 + b * 16, __builtin_bit_cast(Raw<T, 8>, q));
         }
     } else {
-        const int64_t m4 = m0 + (lane >> 4) * 4;
+        const int m4 = (lane >> 4) * 4;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const float q[4] = {v[b][0], v[b][1], v[b][2], v[b][3]};
-            store_some<4>(p + m4 + b * 16, end - m4 - b * 16, q);
+            if (m4 + b * 16 < left) store_vec<4>(p + m4 + b * 16, q);
         }
     }
 }
@@ -98,7 +99,8 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_gate_kernel(const 
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     constexpr int NB = C::FM / 2;              // blocks of 16 hidden features of a wave
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % C::WM, wn = wave / C::WM;
     const int tiles = tiles_m * tiles_n, stages = int((a.Dp + 128 / int(sizeof(T)) - 1) / (128 / int(sizeof(T))));
     const DualOperand A{{a.wg, a.wu}, {a.ldg, a.ldu}, a.F, a.Dp};
     const GemmOperand B{a.x, a.ldx, a.N, a.Dp};
@@ -118,29 +120,43 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_gate_kernel(const 
         NoExtra none;
         pipe.template run<0>(false, acc, none);
         if (t + int(gridDim.x) < tiles) start(t + gridDim.x);
+        // past the last row and feature h and the factors are zeros: the other passes
+        // multiply them
+        const bool edge = nt + C::BN / C::WN > a.N || ft + C::BM / C::WM / 2 > a.F;
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             if (nt + 16 * j >= a.rows_pad) continue;
             const int64_t row = nt + 16 * j + (lane & 15);
-            const bool in = row < a.N;
             floatx4_t h[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int64_t f = ft + b * 16 + (lane >> 4) * 4;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     float g, dg;
-                    activate(a.act, acc[2 * b][j][v], g, dg);
-                    h[b][v] = in && f + v < a.F ? g * acc[2 * b + 1][j][v] : 0.f;
+                    activate<sizeof(T) == 4>(a.act, acc[2 * b][j][v], g, dg);
+                    h[b][v] = g * acc[2 * b + 1][j][v];
+                    acc[2 * b][j][v] = g;
+                    acc[2 * b + 1][j][v] *= dg;
                 }
-                if (SAVE && ft + b * 16 < a.F) {
-                    floatx4_t *p = reinterpret_cast<floatx4_t *>(a.to.pre) +
-                                   ((nt / 16 + j) * a.to.fblocks + ft / 16 + b) * 128 + lane;
-                    p[0] = acc[2 * b][j];
-                    p[64] = acc[2 * b + 1][j];
-                }
+            if (edge) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (row >= a.N || b * 16 + (lane >> 4) * 4 + v >= a.F - ft)
+                            h[b][v] = acc[2 * b][j][v] = acc[2 * b + 1][j][v] = 0.f;
             }
-            store_blocks<T, NB>(static_cast<T *>(a.to.h) + row * a.Fp, ft, a.Fp, lane, h);
+            if constexpr (SAVE) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if (ft + b * 16 < a.F) {
+                        floatx4_t *p = reinterpret_cast<floatx4_t *>(a.to.pre) +
+                                       ((nt / 16 + j) * a.to.fblocks + ft / 16 + b) * 128 + lane;
+                        p[0] = acc[2 * b][j];
+                        p[64] = acc[2 * b + 1][j];
+                    }
+            }
+            store_blocks<T, NB>(static_cast<T *>(a.to.h) + row * a.Fp + ft, int(a.Fp - ft), lane, h);
         }
     }
 }
@@ -149,7 +165,8 @@ template <typename T, typename C>
 __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const FfBack a, int tiles_m, int tiles_n)
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % C::WM, wn = wave / C::WM;
     const int tiles = tiles_m * tiles_n, stages = int((a.O + 128 / int(sizeof(T)) - 1) / (128 / int(sizeof(T))));
     const GemmOperand A{a.wd, a.ldd, a.Fp, a.O};
     const GemmOperand B{a.dy, a.lddy, a.N, a.Op};
@@ -170,35 +187,40 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
         NoExtra none;
         pipe.template run<0>(false, acc, none);
         if (t + int(gridDim.x) < tiles) start(t + gridDim.x);
+        // The factors of H blocks at a time, AHEAD groups of them requested before they are
+        // used: one pair at a time, waited for, this epilogue took longer than its products
+        // (8192 rows, 4096 outputs, 16384 hidden features, bf16: 1606 us). Past the last
+        // row and feature the factors are zeros.
+        constexpr int H = 2, GROUPS = C::FM / H * C::FN, AHEAD = 2;
+        floatx4_t ring[AHEAD + 1][H][2];
+        const char *pre = reinterpret_cast<const char *>(a.from.pre) +
+                          ((nt / 16) * a.from.fblocks + ft / 16) * 2048;
+        auto request = [&](int q) {
+            const char *p = pre + (int64_t(q * H / C::FM) * a.from.fblocks + q * H % C::FM) * 2048;
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-            if (nt + 16 * j >= a.rows_pad) continue;
+            for (int i = 0; i < 2 * H; ++i)
+                ring[q % (AHEAD + 1)][i / 2][i % 2] = *reinterpret_cast<const floatx4_t *>(p + i * 1024 + lane * 16);
+        };
+#pragma unroll
+        for (int q = 0; q < AHEAD && q < GROUPS; ++q) request(q);
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q) {
+            const int j = q * H / C::FM, i0 = q * H % C::FM;
             const int64_t row = nt + 16 * j + (lane & 15);
-            const bool in = row < a.N;
-            floatx4_t du[C::FM];
+            if (q + AHEAD < GROUPS) request(q + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+            floatx4_t da[H], du[H];
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i) {
-                // blocks past the last hidden feature read that one's again
-                const int64_t fb = min(ft / 16 + i, a.from.fblocks - 1), f = ft + i * 16 + (lane >> 4) * 4;
-                const floatx4_t *p =
-                    reinterpret_cast<const floatx4_t *>(a.from.pre) + ((nt / 16 + j) * a.from.fblocks + fb) * 128 + lane;
-                const floatx4_t av = p[0], uv = p[64];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    float g, dg;
-                    activate(a.act, av[v], g, dg);
-                    const bool ok = in && f + v < a.F;
-                    const float dh = acc[i][j][v] * S;
-                    du[i][v] = ok ? dh * g : 0.f;
-                    acc[i][j][v] = ok ? dh * (uv[v] * dg) : 0.f;
-                }
+            for (int i = 0; i < H; ++i) {
+                const floatx4_t dh = acc[i0 + i][j] * S;
+                du[i] = dh * ring[q % (AHEAD + 1)][i][0];
+                da[i] = dh * ring[q % (AHEAD + 1)][i][1];
             }
-            floatx4_t da[C::FM];
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i) da[i] = acc[i][j];
-            T *g = static_cast<T *>(a.g) + row * 2 * a.Fp;
-            store_blocks<T, C::FM>(g, ft, a.Fp, lane, da);
-            store_blocks<T, C::FM>(g + a.Fp, ft, a.Fp, lane, du);
+            if (nt + 16 * j < a.rows_pad) {
+                T *g = static_cast<T *>(a.g) + row * 2 * a.Fp + ft + i0 * 16;
+                store_blocks<T, H>(g, int(a.Fp - ft) - i0 * 16, lane, da);
+                store_blocks<T, H>(g + a.Fp, int(a.Fp - ft) - i0 * 16, lane, du);
+            }
         }
     }
 }
