@@ -275,8 +275,8 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
         if (!t.param || !t.grad || !t.m || !t.v || (coded && (!t.m_scale || !t.v_scale)))
             return CONV2D_ERR_NULL_POINTER;
         if (!aligned(t.param, esize(t.param_dtype)) || !aligned(t.grad, esize(t.grad_dtype)) ||
-            (t.copy && !aligned(t.copy, esize(t.copy_dtype))) || !aligned(t.m, coded ? 8 : 4) ||
-            !aligned(t.v, coded ? 8 : 4) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+            (t.copy && !aligned(t.copy, esize(t.copy_dtype))) || !aligned(t.m, 4) || !aligned(t.v, 4) ||
+            !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
             return CONV2D_ERR_MISALIGNED;
     }
     AdamArgs a{};
@@ -286,6 +286,12 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
     a.beta1 = d->beta1;
     a.beta2 = d->beta2;
     a.step = d->step;
+    // 1 - beta^t without the cancellation of small steps (beta 0: 1)
+    const auto correction = [&](double beta) { return beta > 0.0 ? -std::expm1(double(d->step) * std::log(beta)) : 1.0; };
+    if (!step_ptr) {
+        a.rate = 1.0 / correction(d->beta1);
+        a.root = float(1.0 / std::sqrt(correction(d->beta2)));
+    }
     a.seed = d->seed;
     a.eps = float(d->eps);
     a.grad_scale = float(d->grad_scale);
@@ -299,6 +305,7 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
     // a launch has at most kAdamTensors tensors and kMost chunks; longer tensors are
     // taken in parts
     constexpr int64_t kMost = int64_t(1) << 22;
+    const int64_t chunk = adam_chunk(d->bits);
     for (int64_t i = 0; i < d->count; ++i) {
         const adamw_tensor_t &t = tensors[i];
         for (int64_t at = 0; at < t.n;) {
@@ -306,8 +313,8 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
                 const conv2d_status_t st = launch();
                 if (st != CONV2D_OK) return st;
             }
-            const int64_t n = std::min(t.n - at, (kMost - chunks) * kAdamChunk);
-            chunks += (n + kAdamChunk - 1) / kAdamChunk;
+            const int64_t n = std::min(t.n - at, (kMost - chunks) * chunk);
+            chunks += (n + chunk - 1) / chunk;
             const auto part = [&](const void *p, int64_t size) {
                 return p ? static_cast<char *>(const_cast<void *>(p)) + at * size : nullptr;
             };
@@ -329,6 +336,7 @@ conv2d_status_t adamw_values(int64_t n, const void *m, const void *v, const floa
     if (n < 0 || n > kMaxElems) return CONV2D_ERR_INVALID_DESC;
     if (n == 0) return CONV2D_OK;
     if (!m || !v || !m_scale || !v_scale || !m_values || !v_values) return CONV2D_ERR_NULL_POINTER;
+    if (!aligned(m, 4) || !aligned(v, 4)) return CONV2D_ERR_MISALIGNED;
     for (const float *p : {m_scale, v_scale, static_cast<const float *>(m_values), static_cast<const float *>(v_values)})
         if (!aligned(p, 4)) return CONV2D_ERR_MISALIGNED;
     return hip_status(launch_adamw_values(n, m, v, m_scale, v_scale, m_values, v_values, static_cast<hipStream_t>(stream)));

@@ -68,13 +68,15 @@ struct AdamArgs {
     const int64_t *step_ptr;
     const float *grad_scale_ptr, *lr_ptr;
     double beta1, beta2;
+    double rate;             // 1 / (1 - beta1^step), unless step_ptr gives the step
     int64_t step;
     uint64_t seed;
+    float root;              // 1 / sqrt(1 - beta2^step), likewise
     float eps, grad_scale;
     int count;
     AdamTensor t[kAdamTensors];
 };
-constexpr int64_t kAdamChunk = 2048;           // elements of a workgroup
+constexpr int64_t adam_chunk(int bits) { return bits == 8 ? 1024 : 2048; }   // elements of a workgroup
 hipError_t launch_adamw(const AdamArgs &a, int bits, hipStream_t s);
 hipError_t launch_adamw_values(int64_t n, const void *m, const void *v, const float *ms, const float *vs, float *mo,
                                float *vo, hipStream_t s);

@@ -2,17 +2,20 @@
 // the values of 8-bit states. Bound by HBM: every element of p, g, m and v is read and
 // of p, m and v written once.
 //
-// A launch takes up to kAdamTensors tensors by value, a workgroup one chunk of 2048
-// consecutive elements of one of them, a lane 8 consecutive ones: half a wave holds a
-// block of 256 of an 8-bit state, whose scale is a maximum over 32 lanes, so the states
-// need one pass and no LDS. The types of p, g and copy are a workgroup's affair (a
-// branch that all its lanes take alike).
+// A launch takes up to kAdamTensors tensors by value, a workgroup one chunk of
+// consecutive elements of one of them, a lane 8 (8 bits: 4) consecutive ones: a wave
+// holds a block of 256 of an 8-bit state, whose scale is a maximum over its lanes, so the
+// states need one pass and no LDS. (With 4 elements a lane 32-bit states take 1152 us for
+// 1100 over 200 million; with 8 a lane 8-bit ones 306 us for 218 over 40 million, for
+// want of waves.) The types of p and g are a workgroup's affair: it branches
+// once to the code for its tensor's, so that all loads go out together.
 //
-// 8-bit states are formed in fp64, where the level that an element gets, and so the
-// step, is the definition's to the last bit whatever the order of operations: a value in
-// units of its block's scale, x = |m| 127^2 / M or v 255^4 / V, lies between c^2 (c^4) and
-// (c + 1)^2 ((c + 1)^4), all whole numbers below 2^53; c comes from fp32 square roots
-// and is put right by comparing.
+// 8-bit states: m, v and the scales are formed in fp64, so that the level that an element
+// gets is the definition's whatever the order of operations. A value in units of its
+// block's scale, x = |m| 127^2 / M or v 255^4 / V, lies between c^2 and (c + 1)^2 (fourth
+// powers for v), and goes to the upper one if 65536 times its share of the interval
+// exceeds its number u. fp32 decides that (c from square roots) unless the two are within
+// fp32's error of each other, one element in some ten thousands, for which fp64 does.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -26,8 +29,8 @@ namespace im2win {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLane = 8;                       // elements of a lane
-static_assert(kThreads * kLane == kAdamChunk, "one round per chunk");
+template <int BITS>
+constexpr int kLaneOf = int(adam_chunk(BITS)) / kThreads;    // elements of a lane
 
 template <typename F>
 __device__ __forceinline__ void with_type(int t, F f)
@@ -40,19 +43,14 @@ __device__ __forceinline__ void with_type(int t, F f)
         f(__bf16{});
 }
 
-// the step's factors, the same for all elements of a tensor
-struct Factors {
-    float keep, rate, root, eps;               // p keep - rate m / (sqrt(v) root + eps)
-};
-
-// 1 - beta^t in fp64; beta 0: 1
+// 1 - beta^t in fp64
 __device__ __forceinline__ double correction(double beta, int64_t t)
 {
     return beta > 0.0 ? -expm1(double(t) * log(beta)) : 1.0;
 }
 
-// largest |value| of an aligned half wave as bits: NaN and infinity are above all
-__device__ __forceinline__ uint32_t half_wave_max(uint32_t v)
+// largest of a wave (of |values| as bits: NaN and infinity are above all)
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
     auto dpp = [](uint32_t x, auto ctrl) {
         return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), decltype(ctrl)::value, 0xF, 0xF, true));
@@ -63,13 +61,16 @@ __device__ __forceinline__ uint32_t half_wave_max(uint32_t v)
     v = max(v, dpp(v, integral_constant<int, 0x141>{}));
     v = max(v, dpp(v, integral_constant<int, 0x140>{}));
     const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return max(uint32_t(p[0]), uint32_t(p[1]));
+    v = max(uint32_t(p[0]), uint32_t(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max(uint32_t(q[0]), uint32_t(q[1]));
 }
 
 constexpr double kTopM = 16129.0, kTopV = 4228250625.0;    // 127^2, 255^4
+constexpr double kUnitM = 1.0 / kTopM, kUnitV = 1.0 / kTopV;
 
-// code of x in [0, 127^2] (with a hair above: the scale is rounded)
-__device__ __forceinline__ int level2(double x, uint32_t u)
+// code of x in [0, 127^2] (or a hair above: the scale is rounded)
+__device__ __forceinline__ int exact_level2(double x, uint32_t u)
 {
     int c = int(sqrtf(float(x)));
     c -= double(c * c) > x;
@@ -78,7 +79,7 @@ __device__ __forceinline__ int level2(double x, uint32_t u)
     return min(c + int(up), 127);
 }
 // code of x in [0, 255^4]
-__device__ __forceinline__ int level4(double x, uint32_t u)
+__device__ __forceinline__ int exact_level4(double x, uint32_t u)
 {
     const auto four = [](int c) {
         const uint32_t s = uint32_t(c * c);
@@ -92,11 +93,183 @@ __device__ __forceinline__ int level4(double x, uint32_t u)
     return min(c + int(up), 255);
 }
 
-__device__ __forceinline__ double value2(int k, double unit) { return double(k * abs(k)) * unit; }
-__device__ __forceinline__ double value4(int k, double unit)
+// The same in fp32, with whether it is sure. x is within 3 roundings and a reciprocal's
+// ulp (3e-7 of it) of the exact one, d and with it 65536 d within what `err` says; next to an end of the
+// interval, where the exact x may lie in the next one, u decides alike in both unless
+// it is within 16 of its own ends (err is less than 2 of its steps).
+__device__ __forceinline__ bool sure_at(float d, float width, float err, float lhs, float rhs, uint32_t u)
 {
-    const double s = double(k * k);
-    return s * s * unit;
+    const float e = err * (1.f / 65536);
+    return fabsf(lhs - rhs) > err && ((d >= e && width - d >= e) || u - 16u < 65504u);
+}
+__device__ __forceinline__ int level2(float x, uint32_t u, bool &sure)
+{
+    const int c = int(__builtin_amdgcn_sqrtf(x));
+    const float d = x - float(c * c), width = float(2 * c + 1);
+    const float lhs = d * 65536.f, rhs = float(u) * width;       // below 2^24
+    sure = sure_at(d, width, x * (3.6e-7f * 65536.f), lhs, rhs, u);
+    return min(c + int(lhs > rhs), 127);
+}
+__device__ __forceinline__ int level4(float x, uint32_t u, bool &sure)
+{
+    const uint32_t c = min(uint32_t(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(x))), 255u);
+    const uint32_t lo = c * c * (c * c), hi = (c + 1) * (c + 1) * ((c + 1) * (c + 1));   // 256^4 wraps to 0
+    const float d = x - float(lo), width = float(hi - lo);
+    const float lhs = d * 65536.f, rhs = float(u) * width;
+    sure = sure_at(d, width, x * (4.2e-7f * 65536.f) + rhs * 1.5e-7f, lhs, rhs, u);
+    return int(min(c + uint32_t(lhs > rhs), 255u));
+}
+
+__device__ __forceinline__ double value2(int k, double unit) { return double(k * abs(k)) * unit; }
+__device__ __forceinline__ double value4(uint32_t k, double unit) { return double(k * k * (k * k)) * unit; }
+
+// A lane's elements of a tensor, from its element i on; WHOLE: all of them exist, in all of the
+// workgroup's lanes
+template <int BITS, bool WHOLE, typename P, typename G>
+__device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTensor &t, int64_t i, int64_t step, float gs,
+                                               const float4 &f)
+{
+    constexpr int kLane = kLaneOf<BITS>;
+    const int64_t left = WHOLE ? kLane : max(t.n - i, int64_t(0));
+    float p[kLane], g[kLane], m[kLane], v[kLane];
+    Raw<P, kLane> rp;
+    Raw<G, kLane> rg;
+    if constexpr (WHOLE) {
+        rp = load_raw<P, kLane>(static_cast<const P *>(t.p) + i);
+        rg = load_raw<G, kLane>(static_cast<const G *>(t.g) + i);
+    } else {
+        load_some<kLane>(static_cast<const P *>(t.p) + i, left, p);
+        load_some<kLane>(static_cast<const G *>(t.g) + i, left, g);
+    }
+    const auto unpack = [&] {
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            if (WHOLE) {
+                p[e] = element(rp, e);
+                g[e] = element(rg, e);
+            }
+            g[e] *= gs;
+        }
+    };
+    if constexpr (BITS == 32) {
+        float *pm = static_cast<float *>(t.m) + i, *pv = static_cast<float *>(t.v) + i;
+        load_some<kLane>(pm, left, m);
+        load_some<kLane>(pv, left, v);
+        unpack();
+        const float b1 = float(a.beta1), b2 = float(a.beta2), r1 = float(1.0 - a.beta1), r2 = float(1.0 - a.beta2);
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            m[e] = b1 * m[e] + r1 * g[e];
+            v[e] = b2 * v[e] + r2 * (g[e] * g[e]);
+        }
+        store_some<kLane>(pm, left, m);
+        store_some<kLane>(pv, left, v);
+    } else {
+        // codes and scales; lanes past the tensor's end hold zeros, whole blocks past it
+        // have no scale
+        int8_t *pm = static_cast<int8_t *>(t.m) + i;
+        uint8_t *pv = static_cast<uint8_t *>(t.v) + i;
+        const bool any = WHOLE || i / 256 * 256 < t.n;
+        float sm = 0.f, sv = 0.f;
+        if (any) {
+            sm = t.ms[i / 256];
+            sv = t.vs[i / 256];
+        }
+        uint32_t cm = 0, cv = 0;
+        if (WHOLE || left >= kLane) {
+            cm = *reinterpret_cast<const uint32_t *>(pm);
+            cv = *reinterpret_cast<const uint32_t *>(pv);
+        } else {
+            for (int e = 0; e < left; ++e) {
+                cm |= uint32_t(uint8_t(pm[e])) << (8 * e);
+                cv |= uint32_t(pv[e]) << (8 * e);
+            }
+        }
+        // the numbers while the loads are on their way
+        const uint4 word = philox(uint64_t(t.first + i) / 4, uint64_t(step), a.seed);
+        const uint32_t w[kLane] = {word.x, word.y, word.z, word.w};
+        unpack();
+        const double um = a.beta1 * (double(sm) * kUnitM), uv = a.beta2 * (double(sv) * kUnitV);
+        const double r1 = 1.0 - a.beta1, r2 = 1.0 - a.beta2;
+        double md[kLane], vd[kLane];
+        uint32_t tm = 0, tv = 0;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            const bool in = WHOLE || e < left;
+            const double gd = double(g[e]);
+            md[e] = value2(int(int8_t(cm >> (8 * e))), um) + r1 * gd;
+            vd[e] = value4(uint8_t(cv >> (8 * e)), uv) + r2 * (gd * gd);
+            if (!in) md[e] = vd[e] = 0.0;
+            m[e] = float(md[e]);
+            v[e] = float(vd[e]);
+            tm = max(tm, __float_as_uint(m[e]) & 0x7fffffffu);
+            tv = max(tv, __float_as_uint(v[e]) & 0x7fffffffu);
+        }
+        tm = wave_max(tm);
+        tv = wave_max(tv);
+        constexpr uint32_t INF = 0x7f800000u;
+        const bool bad = tm >= INF || tv >= INF;
+        sm = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(tm);
+        sv = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(tv);
+        const float fm = sm > 0.f ? float(kTopM) * __builtin_amdgcn_rcpf(sm) : 0.f;
+        const float fv = sv > 0.f ? float(kTopV) * __builtin_amdgcn_rcpf(sv) : 0.f;
+        // a scale so small that its reciprocal leaves fp32 (or the scale its normal
+        // numbers) is fp64's affair
+        const bool tiny = (sm > 0.f && !(sm > 1e-30f)) || (sv > 0.f && !(sv > 1e-26f));
+        int km[kLane], kv[kLane];
+        uint32_t unsure = 0;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            bool sure_m, sure_v;
+            km[e] = level2(fabsf(m[e]) * fm, w[e] & 0xffffu, sure_m);
+            kv[e] = level4(v[e] * fv, w[e] >> 16, sure_v);
+            unsure |= uint32_t(tiny || !(sure_m && sure_v)) << e;
+        }
+        if (unsure) {
+            const double xm = sm > 0.f ? kTopM / double(sm) : 0.0, xv = sv > 0.f ? kTopV / double(sv) : 0.0;
+#pragma unroll
+            for (int e = 0; e < kLane; ++e)
+                if (unsure >> e & 1) {
+                    km[e] = exact_level2(fabs(md[e]) * xm, w[e] & 0xffffu);
+                    kv[e] = exact_level4(vd[e] * xv, w[e] >> 16);
+                }
+        }
+        cm = cv = 0;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            const int q = bad ? 0 : m[e] < 0.f ? -km[e] : km[e];
+            const int r = bad || !(vd[e] > 0.0) ? 0 : max(kv[e], 1);
+            cm |= uint32_t(uint8_t(q)) << (8 * e);
+            cv |= uint32_t(uint8_t(r)) << (8 * e);
+        }
+        if (WHOLE || left >= kLane) {
+            *reinterpret_cast<uint32_t *>(pm) = cm;
+            *reinterpret_cast<uint32_t *>(pv) = cv;
+        } else {
+            for (int e = 0; e < left; ++e) {
+                pm[e] = int8_t(cm >> (8 * e));
+                pv[e] = uint8_t(cv >> (8 * e));
+            }
+        }
+        if (any && (threadIdx.x & 63) == 0) {
+            t.ms[i / 256] = sm;
+            t.vs[i / 256] = sv;
+        }
+    }
+    // With 8 bits the arithmetic is what a step waits for: the hardware's square root and
+    // reciprocal, an ulp off each (150 cycles of a SIMD less per element than whole ones)
+    // unless so small an eps lets a denormal v count, which that root takes for 0.
+    if (BITS == 8 && f.w > 1e-12f) {
+#pragma unroll
+        for (int e = 0; e < kLane; ++e)
+            p[e] = p[e] * f.x - f.y * m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e]) * f.z + f.w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) p[e] = p[e] * f.x - f.y * m[e] / (sqrtf(v[e]) * f.z + f.w);
+    }
+    store_some<kLane>(static_cast<P *>(t.p) + i, left, p);
+    if (t.copy)
+        with_type(t.ct, [&](auto z) { store_some<kLane>(static_cast<decltype(z) *>(t.copy) + i, left, p); });
 }
 
 template <int BITS>
@@ -106,128 +279,62 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a)
     int k = 0;
     while (int(blockIdx.x) >= a.t[k].end) ++k;
     const AdamTensor &t = a.t[k];
-    const int64_t chunk = int64_t(blockIdx.x) - (k ? a.t[k - 1].end : 0);
-    const int64_t i = chunk * kAdamChunk + threadIdx.x * kLane, left = t.n - i;
-
-    __shared__ Factors shared;
-    const int64_t step = a.step_ptr ? *a.step_ptr : a.step;
-    if (threadIdx.x == 0) {
-        const float lr = t.lr * (a.lr_ptr ? *a.lr_ptr : 1.f);
-        const double c1 = correction(a.beta1, step), c2 = correction(a.beta2, step);
-        shared = Factors{float(1.0 - double(lr) * double(t.decay)), float(double(lr) / c1), float(1.0 / sqrt(c2)), a.eps};
+    const int64_t first = (int64_t(blockIdx.x) - (k ? a.t[k - 1].end : 0)) * adam_chunk(BITS);
+    int64_t step = a.step;
+    double rate = a.rate;
+    float root = a.root;
+    if (a.step_ptr) {
+        // by one lane: 1 - beta^t takes as long as the rest of the step
+        __shared__ double factor[2];
+        step = *a.step_ptr;
+        if (threadIdx.x == 0) {
+            factor[0] = 1.0 / correction(a.beta1, step);
+            factor[1] = 1.0 / sqrt(correction(a.beta2, step));
+        }
+        __syncthreads();
+        rate = factor[0];
+        root = float(factor[1]);
     }
-    const float gs = a.grad_scale * (a.grad_scale_ptr ? *a.grad_scale_ptr : 1.f);
-
-    float p[kLane], g[kLane], m[kLane], v[kLane];
-    with_type(t.pt, [&](auto z) { load_some<kLane>(static_cast<const decltype(z) *>(t.p) + i, max(left, int64_t(0)), p); });
-    with_type(t.gt, [&](auto z) { load_some<kLane>(static_cast<const decltype(z) *>(t.g) + i, max(left, int64_t(0)), g); });
-#pragma unroll
-    for (int e = 0; e < kLane; ++e) g[e] *= gs;
-
-    if constexpr (BITS == 32) {
-        float *pm = static_cast<float *>(t.m) + i, *pv = static_cast<float *>(t.v) + i;
-        load_some<kLane>(pm, max(left, int64_t(0)), m);
-        load_some<kLane>(pv, max(left, int64_t(0)), v);
-        const float b1 = float(a.beta1), b2 = float(a.beta2), r1 = float(1.0 - a.beta1), r2 = float(1.0 - a.beta2);
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            m[e] = b1 * m[e] + r1 * g[e];
-            v[e] = b2 * v[e] + r2 * (g[e] * g[e]);
-        }
-        store_some<kLane>(pm, max(left, int64_t(0)), m);
-        store_some<kLane>(pv, max(left, int64_t(0)), v);
-    } else {
-        // codes and scales; lanes past the tensor's end hold zeros, whole blocks past it
-        // have no scale
-        int8_t *pm = static_cast<int8_t *>(t.m) + i;
-        uint8_t *pv = static_cast<uint8_t *>(t.v) + i;
-        const bool any = i / 256 * 256 < t.n;
-        double um = 0.0, uv = 0.0;
-        if (any) {
-            um = double(t.ms[i / 256]) / kTopM;
-            uv = double(t.vs[i / 256]) / kTopV;
-        }
-        double md[kLane], vd[kLane];
-        uint64_t cm = 0, cv = 0;
-        if (left >= kLane) {
-            cm = *reinterpret_cast<const uint64_t *>(pm);
-            cv = *reinterpret_cast<const uint64_t *>(pv);
-        } else {
-            for (int e = 0; e < left; ++e) {
-                cm |= uint64_t(uint8_t(pm[e])) << (8 * e);
-                cv |= uint64_t(pv[e]) << (8 * e);
-            }
-        }
-        uint32_t tm = 0, tv = 0;
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            const double gd = double(g[e]);
-            md[e] = a.beta1 * value2(int(int8_t(cm >> (8 * e))), um) + (1.0 - a.beta1) * gd;
-            vd[e] = a.beta2 * value4(int(uint8_t(cv >> (8 * e))), uv) + (1.0 - a.beta2) * (gd * gd);
-            if (e >= left) md[e] = vd[e] = 0.0;
-            m[e] = float(md[e]);
-            v[e] = float(vd[e]);
-            tm = max(tm, __float_as_uint(m[e]) & 0x7fffffffu);
-            tv = max(tv, __float_as_uint(v[e]) & 0x7fffffffu);
-        }
-        tm = half_wave_max(tm);
-        tv = half_wave_max(tv);
-        constexpr uint32_t INF = 0x7f800000u;
-        const bool bad = tm >= INF || tv >= INF;
-        const float sm = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(tm);
-        const float sv = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(tv);
-        const double xm = sm > 0.f ? kTopM / double(sm) : 0.0, xv = sv > 0.f ? kTopV / double(sv) : 0.0;
-        const uint64_t block = uint64_t(t.first + i) / 4;
-        const uint4 w0 = philox(block, uint64_t(step), a.seed), w1 = philox(block + 1, uint64_t(step), a.seed);
-        const uint32_t w[kLane] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        cm = cv = 0;
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            int km = bad ? 0 : level2(fabs(md[e]) * xm, w[e] & 0xffffu);
-            int kv = bad ? 0 : level4(vd[e] * xv, w[e] >> 16);
-            km = md[e] < 0.0 ? -km : km;
-            kv = vd[e] > 0.0 && !bad ? max(kv, 1) : 0;
-            cm |= uint64_t(uint8_t(km)) << (8 * e);
-            cv |= uint64_t(uint8_t(kv)) << (8 * e);
-        }
-        if (left >= kLane) {
-            *reinterpret_cast<uint64_t *>(pm) = cm;
-            *reinterpret_cast<uint64_t *>(pv) = cv;
-        } else {
-            for (int e = 0; e < left; ++e) {
-                pm[e] = int8_t(cm >> (8 * e));
-                pv[e] = uint8_t(cv >> (8 * e));
-            }
-        }
-        if (any && (threadIdx.x & 31) == 0) {
-            t.ms[i / 256] = sm;
-            t.vs[i / 256] = sv;
-        }
-    }
-    __syncthreads();
-    const Factors f = shared;
-#pragma unroll
-    for (int e = 0; e < kLane; ++e) p[e] = p[e] * f.keep - f.rate * m[e] / (sqrtf(v[e]) * f.root + f.eps);
-    with_type(t.pt, [&](auto z) { store_some<kLane>(static_cast<decltype(z) *>(t.p) + i, max(left, int64_t(0)), p); });
-    if (t.copy)
-        with_type(t.ct, [&](auto z) { store_some<kLane>(static_cast<decltype(z) *>(t.copy) + i, max(left, int64_t(0)), p); });
+    const float lr = t.lr * (a.lr_ptr ? *a.lr_ptr : 1.f), gs = a.grad_scale * (a.grad_scale_ptr ? *a.grad_scale_ptr : 1.f);
+    // p keep - rate m / (sqrt(v) root + eps)
+    const float4 f{float(1.0 - double(lr) * double(t.decay)), float(double(lr) * rate), root, a.eps};
+    const int64_t i = first + threadIdx.x * kLaneOf<BITS>;
+    with_type(t.pt, [&](auto p) {
+        with_type(t.gt, [&](auto g) {
+            if (first + adam_chunk(BITS) <= t.n)
+                adamw_elements<BITS, true, decltype(p), decltype(g)>(a, t, i, step, gs, f);
+            else
+                adamw_elements<BITS, false, decltype(p), decltype(g)>(a, t, i, step, gs, f);
+        });
+    });
 }
 
+// 4 elements a lane: a wave's loads and stores are consecutive
 __global__ __launch_bounds__(kThreads) void adamw_values_kernel(int64_t n, const int8_t *m, const uint8_t *v,
                                                                 const float *ms, const float *vs, float *mo, float *vo)
 {
-    const int64_t step = int64_t(gridDim.x) * kThreads * kLane;
-    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * kLane; i < n; i += step) {
+    const int64_t step = int64_t(gridDim.x) * kThreads * 4;
+    for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n; i += step) {
         const int64_t left = n - i;
         const double um = double(ms[i / 256]) / kTopM, uv = double(vs[i / 256]) / kTopV;
-        float a[kLane], b[kLane];
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            a[e] = e < left ? float(value2(m[i + e], um)) : 0.f;
-            b[e] = e < left ? float(value4(v[i + e], uv)) : 0.f;
+        uint32_t cm = 0, cv = 0;
+        if (left >= 4) {
+            cm = *reinterpret_cast<const uint32_t *>(m + i);
+            cv = *reinterpret_cast<const uint32_t *>(v + i);
+        } else {
+            for (int e = 0; e < left; ++e) {
+                cm |= uint32_t(uint8_t(m[i + e])) << (8 * e);
+                cv |= uint32_t(v[i + e]) << (8 * e);
+            }
         }
-        store_some<kLane>(mo + i, left, a);
-        store_some<kLane>(vo + i, left, b);
+        float a[4], b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            a[e] = float(value2(int(int8_t(cm >> (8 * e))), um));
+            b[e] = float(value4(uint8_t(cv >> (8 * e)), uv));
+        }
+        store_some<4>(mo + i, left, a);
+        store_some<4>(vo + i, left, b);
     }
 }
 
@@ -246,7 +353,7 @@ hipError_t launch_adamw(const AdamArgs &a, int bits, hipStream_t s)
 hipError_t launch_adamw_values(int64_t n, const void *m, const void *v, const float *ms, const float *vs, float *mo,
                                float *vo, hipStream_t s)
 {
-    const int64_t groups = std::min<int64_t>((n + kAdamChunk - 1) / kAdamChunk, 8192);
+    const int64_t groups = std::min<int64_t>((n + kThreads * 4 - 1) / (kThreads * 4), int64_t(1) << 20);
     hipLaunchKernelGGL(adamw_values_kernel, dim3(unsigned(groups)), dim3(kThreads), 0, s, n,
                        static_cast<const int8_t *>(m), static_cast<const uint8_t *>(v), ms, vs, mo, vo);
     return hipGetLastError();

@@ -31,16 +31,18 @@ constexpr int kThreads = 256;
 constexpr int threads_of(int lpr) { return lpr > 64 ? lpr : kThreads; }
 
 // Rows of block b of B: consecutive. Record (block, group of gates) is number
-// block + group: blocks share at most their end's group, so no two are the same.
+// block + group: blocks share at most their end's group, so no two are the same. Where a
+// block ends with a group, the number after its last record is no one's: that block
+// writes zeros there, so that records 0 .. B + groups - 2 are all written.
 __host__ __device__ __forceinline__ int64_t first_row(int64_t N, int64_t B, int64_t b)
 {
     const int64_t q = N / B, rem = N - q * B;
     return q * b + (b < rem ? b : rem);
 }
-__device__ __forceinline__ int64_t block_of(int64_t N, int64_t B, int64_t row)
+__device__ __forceinline__ int block_of(uint32_t N, uint32_t B, uint32_t row)
 {
-    const int64_t q = N / B, rem = N - q * B;              // B <= N: q >= 1
-    return row < rem * (q + 1) ? row / (q + 1) : rem + (row - rem * (q + 1)) / q;
+    const uint32_t q = N / B, rem = N - q * B;             // B <= N: q >= 1
+    return int(row < rem * (q + 1) ? row / (q + 1) : rem + (row - rem * (q + 1)) / q);
 }
 
 // sum of (a, b) over the LPR lanes of a row; `slot` alternates between calls
@@ -310,16 +312,26 @@ __global__ __launch_bounds__(kThreads) void res_norm_fwd_wide_kernel(const ResNo
 }
 
 // Workspace of the backward pass: the blocks' sums of the next norm [B][2][C], then
-// the records [B + groups][2][C], then (wide rows) each row's two means [N][2].
+// the records [B + groups][2][C] and their groups, then (wide rows) each row's two
+// means [N][2].
 struct Sums {
     float *norm, *record;
+    int *group;
     float2 *means;
 };
 __host__ __device__ __forceinline__ Sums sums_of(const ResNormArgs &a, int64_t B)
 {
     float *p = static_cast<float *>(a.ws);
     const int64_t G = a.groups > 1 ? a.groups : 1;
-    return {p, p + B * 2 * a.C, reinterpret_cast<float2 *>(p + (2 * B + G) * 2 * a.C)};
+    float *end = p + (2 * B + G) * 2 * a.C;
+    return {p, p + B * 2 * a.C, reinterpret_cast<int *>(end), reinterpret_cast<float2 *>(end + (B + G + 1) / 2 * 2)};
+}
+
+template <int THREADS>
+__device__ __forceinline__ void skip_record(const Sums &sums, int64_t k, int C)
+{
+    for (int c = threadIdx.x; c < 2 * C; c += THREADS) sums.record[k * 2 * C + c] = 0.f;
+    if (threadIdx.x == 0) sums.group[k] = 0;
 }
 
 template <typename TR, typename TB, int LPR, int KCH, bool EXACT>
@@ -468,6 +480,8 @@ __global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const Res
             float *rec = sums.record + (blockIdx.x + g) * 2 * C;
             flush(s1, rec);
             flush(s2, rec + C);
+            if (threadIdx.x == 0) sums.group[blockIdx.x + g] = int(g);
+            if (to == end && a.groups > 1 && end % a.rows == 0 && end < a.N) skip_record<THREADS>(sums, blockIdx.x + g + 1, C);
         }
         from = to;
     }
@@ -610,6 +624,9 @@ __global__ __launch_bounds__(kThreads) void res_norm_cols_kernel(const ResNormAr
             float *rec = sums.record + (blockIdx.y + g) * 2 * C;
             flush(s1, rec);
             flush(s2, rec + C);
+            // every workgroup of the block's rows writes the same
+            if (threadIdx.x == 0) sums.group[blockIdx.y + g] = int(g);
+            if (to == end && a.groups > 1 && end % a.rows == 0 && end < a.N) skip_record<kThreads>(sums, blockIdx.y + g + 1, C);
         }
         from = to;
     }
@@ -638,19 +655,19 @@ __global__ __launch_bounds__(1024) void res_norm_join_kernel(const ResNormArgs a
                     y += sums.norm[(b * 2 + 1) * C + c];
                 }
             } else if (job == 1 && (a.dpw || a.dpb)) {
-                for (int64_t b = q; b < B; b += 16) {
-                    const int64_t first = a.groups > 1 ? first_row(a.N, B, b) / a.rows : 0;
-                    const int64_t last = a.groups > 1 ? (first_row(a.N, B, b + 1) - 1) / a.rows : 0;
-                    for (int64_t g = first; g <= last; ++g) {
-                        const float s = a.gate ? a.bs * a.gate[g * C + c] : a.bs;
-                        x += s * sums.record[(b + g) * 2 * C + c];
-                        y += s * sums.record[((b + g) * 2 + 1) * C + c];
-                    }
+#pragma unroll 4
+                for (int64_t r = q; r < B + G - 1; r += 16) {
+                    const float s = a.gate ? a.bs * a.gate[int64_t(sums.group[r]) * C + c] : a.bs;
+                    x += s * sums.record[r * 2 * C + c];
+                    y += s * sums.record[(r * 2 + 1) * C + c];
                 }
             } else if (job >= 2) {
                 const int64_t g = job - 2;
-                const int64_t first = a.groups > 1 ? block_of(a.N, B, g * a.rows) : 0;
-                const int64_t last = a.groups > 1 ? block_of(a.N, B, (g + 1) * a.rows - 1) : B - 1;
+                int first = 0, last = int(B) - 1;
+                if (a.groups > 1) {
+                    first = block_of(uint32_t(a.N), uint32_t(B), uint32_t(g * a.rows));
+                    last = block_of(uint32_t(a.N), uint32_t(B), uint32_t((g + 1) * a.rows - 1));
+                }
 #pragma unroll 4
                 for (int64_t b = first + q; b <= last; b += 16) {
                     x += sums.record[(b + g) * 2 * C + c];
@@ -747,7 +764,7 @@ int64_t bwd_blocks(int64_t N, int64_t C)
 int64_t res_norm_bwd_ws_bytes(int64_t N, int64_t C, int64_t groups)
 {
     const int64_t B = bwd_blocks(N, C), G = std::max<int64_t>(groups, 1);
-    return ((2 * B + G) * 2 * C * 4 + (group_of(C).lpr ? 0 : N * 8) + 255) / 256 * 256;
+    return ((2 * B + G) * 2 * C * 4 + (B + G + 1) / 2 * 8 + (group_of(C).lpr ? 0 : N * 8) + 255) / 256 * 256;
 }
 
 hipError_t launch_res_norm_fwd(const ResNormArgs &a, hipStream_t s)
