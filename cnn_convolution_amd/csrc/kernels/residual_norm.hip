@@ -634,59 +634,82 @@ __global__ __launch_bounds__(kThreads) void res_norm_cols_kernel(const ResNormAr
     flush(s4, sums.norm + (int64_t(blockIdx.y) * 2 + 1) * C);
 }
 
-// The parameters' gradients from the blocks' sums: a workgroup takes 64 channels of one
-// output pair (dweight, dbias), (dpw, dpb) or of one group's dgate, 16 threads a channel.
+// Channels of a workgroup of the join, with 1024 threads: many threads a channel where
+// there are few channels (4096 channels, 256 blocks: 15 us with 16, 9 with 64; 1001: 8
+// with 16).
+__host__ __device__ __forceinline__ int join_channels(int C) { return C >= 2048 ? 64 : 16; }
+// Whether dgate's groups have few records each: 4 threads a channel then.
+__host__ __device__ __forceinline__ bool short_groups(int64_t B, int64_t G) { return (B + G) / G <= 32; }
+
+// The parameters' gradients from the blocks' sums: a workgroup takes 16 or 64
+// channels of (dweight, dbias), of (dpw, dpb) or of one group's dgate, or 256 elements of
+// the dgate of short groups.
 __global__ __launch_bounds__(1024) void res_norm_join_kernel(const ResNormArgs a, int64_t B)
 {
-    __shared__ float2 part[16][64];
-    const int C = a.C, col = threadIdx.x & 63, q = threadIdx.x >> 6;
+    __shared__ float2 part[1024];
+    const int C = a.C, t = threadIdx.x;
     const Sums sums = sums_of(a, B);
-    const int64_t G = a.groups > 1 ? a.groups : 1, tiles = (C + 63) / 64;
-    const int64_t jobs = a.dgate ? 2 + G : 2;
-    for (int64_t k = blockIdx.x; k < jobs * tiles; k += gridDim.x) {
-        const int64_t job = k / tiles;
-        const int c = int(k - job * tiles) * 64 + col;
+    const int W = join_channels(C);
+    const int64_t G = a.groups > 1 ? a.groups : 1, tiles = (C + W - 1) / W;
+    const bool few = a.dgate && short_groups(B, G);
+    const int64_t trees = (a.dgate && !few ? 2 + G : 2) * tiles, all = trees + (few ? (G * C + 255) / 256 : 0);
+    const auto records = [&](int64_t g, int &first, int &last) {
+        first = 0;
+        last = int(B) - 1;
+        if (a.groups > 1) {
+            first = block_of(uint32_t(a.N), uint32_t(B), uint32_t(g * a.rows));
+            last = block_of(uint32_t(a.N), uint32_t(B), uint32_t((g + 1) * a.rows - 1));
+        }
+    };
+    for (int64_t k = blockIdx.x; k < all; k += gridDim.x) {
+        // the channel, its job (0, 1, or 2 + group) and this thread's share of it
+        const int64_t job = k < trees ? k / tiles : 2, e = (k - trees) * 256 + (t & 255);
+        int64_t g = job - 2;
+        int c = int(k - job * tiles) * W + t % W, q = t / W, Q = 1024 / W;
+        if (k >= trees) {
+            g = e / C;
+            c = g < G ? int(e - g * C) : C;
+            q = t >> 8;
+            Q = 4;
+        }
         float x = 0.f, y = 0.f;
         if (c < C) {
             if (job == 0 && (a.dw || a.dbias)) {
 #pragma unroll 4
-                for (int64_t b = q; b < B; b += 16) {
+                for (int64_t b = q; b < B; b += Q) {
                     x += sums.norm[b * 2 * C + c];
                     y += sums.norm[(b * 2 + 1) * C + c];
                 }
             } else if (job == 1 && (a.dpw || a.dpb)) {
 #pragma unroll 4
-                for (int64_t r = q; r < B + G - 1; r += 16) {
+                for (int64_t r = q; r < B + G - 1; r += Q) {
                     const float s = a.gate ? a.bs * a.gate[int64_t(sums.group[r]) * C + c] : a.bs;
                     x += s * sums.record[r * 2 * C + c];
                     y += s * sums.record[(r * 2 + 1) * C + c];
                 }
             } else if (job >= 2) {
-                const int64_t g = job - 2;
-                int first = 0, last = int(B) - 1;
-                if (a.groups > 1) {
-                    first = block_of(uint32_t(a.N), uint32_t(B), uint32_t(g * a.rows));
-                    last = block_of(uint32_t(a.N), uint32_t(B), uint32_t((g + 1) * a.rows - 1));
-                }
+                int first, last;
+                records(g, first, last);
 #pragma unroll 4
-                for (int64_t b = first + q; b <= last; b += 16) {
+                for (int64_t b = first + q; b <= last; b += Q) {
                     x += sums.record[(b + g) * 2 * C + c];
                     y += sums.record[((b + g) * 2 + 1) * C + c];
                 }
             }
         }
-        part[q][col] = float2{x, y};
+        part[t] = float2{x, y};
         __syncthreads();
-        for (int m = 8; m > 0; m >>= 1) {
+        const int width = 1024 / Q;            // threads of one share
+        for (int m = Q / 2; m > 0; m >>= 1) {
             if (q < m) {
-                part[q][col].x += part[q + m][col].x;
-                part[q][col].y += part[q + m][col].y;
+                part[t].x += part[t + m * width].x;
+                part[t].y += part[t + m * width].y;
             }
             __syncthreads();
         }
-        // the next job's part[0] is written by the threads that read this one's
+        // the next job's part[t] is written by the threads that read this one's
         if (q > 0 || c >= C) continue;
-        const float2 s = part[0][col];
+        const float2 s = part[t];
         if (job == 0) {
             if (a.dw) a.dw[c] = s.x;
             if (a.dbias) a.dbias[c] = s.y;
@@ -694,8 +717,8 @@ __global__ __launch_bounds__(1024) void res_norm_join_kernel(const ResNormArgs a
             if (a.dpw) a.dpw[c] = s.x;
             if (a.dpb) a.dpb[c] = s.y;
         } else {
-            const float pw = a.post && a.pw ? a.pw[c] : 1.f, pb = a.post && a.pb ? a.pb[c] : 0.f;
-            a.dgate[(job - 2) * C + c] = a.bs * (pw * s.x + pb * s.y);
+            const float pw = a.pw ? a.pw[c] : 1.f, pb = a.pb ? a.pb[c] : 0.f;
+            a.dgate[g * C + c] = a.bs * (a.post ? pw * s.x + pb * s.y : s.x);
         }
     }
 }
@@ -712,22 +735,30 @@ __global__ __launch_bounds__(kThreads) void res_norm_zero_kernel(const ResNormAr
     }
 }
 
-// The group that holds a row of C channels: as few lanes as keep it to one chunk
-// each. lpr 0: no group holds it.
+// The group that holds a row of C channels: as few lanes as keep it to one chunk each,
+// then two chunks a lane: fewer waves meet at a row's barriers, and backward one wave to a
+// row needs none. us of 256 (lanes, chunks) measured with 8 workgroups' worth of waves and
+// more: 32768 rows of 4096, bf16, forward (256, 2) 214, (512, 1) 221 .. 284, (128, 4) 215;
+// backward 329, 325 and -; 19941 rows of 1001, fp32 with fp16, backward (64, 2) 103, (128, 1)
+// 133, forward 59.5 and 56.5; 65536 rows of 2048, bf16, backward (256, 1) 337, (128, 2) 358.
+// lpr 0: no group holds it.
 struct Group {
     int lpr, kch;
 };
-Group group_of(int64_t C)
+Group group_of(int64_t C, bool backward)
 {
     const int64_t ch = (C + 7) / 8;
     if (C < 8) return {0, 0};
-    for (int l : {8, 16, 32, 64, 128, 256, 512})
+    for (int l : {8, 16, 32, 64})
         if (ch <= l) return {l, 1};
+    if (ch <= 128) return backward ? Group{64, 2} : Group{128, 1};
+    if (ch <= 256) return {256, 1};
+    if (ch <= 512) return {256, 2};
     if (ch <= 1024) return {512, 2};
     return {0, 0};
 }
 
-template <typename F>
+template <bool BACKWARD, typename F>
 hipError_t with_group(const Group &g, F f)
 {
     using std::integral_constant;
@@ -737,26 +768,35 @@ hipError_t with_group(const Group &g, F f)
     IM2WIN_GROUP(16, 1)
     IM2WIN_GROUP(32, 1)
     IM2WIN_GROUP(64, 1)
-    IM2WIN_GROUP(128, 1)
+    if constexpr (BACKWARD) {
+        IM2WIN_GROUP(64, 2)
+    } else {
+        IM2WIN_GROUP(128, 1)
+    }
     IM2WIN_GROUP(256, 1)
-    IM2WIN_GROUP(512, 1)
+    IM2WIN_GROUP(256, 2)
     IM2WIN_GROUP(512, 2)
 #undef IM2WIN_GROUP
     return hipErrorInvalidValue;
 }
 
-// workgroups: 16 waves to a CU forward, 8 backward, where each leaves sums
-int64_t blocks_of(int64_t N, const Group &g, int waves)
+// Workgroups: forward 16 waves to a CU (one chunk of 256 lanes: 32, two chunks: 8; 65536
+// rows of 2048, bf16: 231 and 226 us with 16 and 32; 32768 of 4096: 214, 222 and 234 with 8,
+// 12 and 16); backward one workgroup to a CU, since each leaves sums (200000 rows of 512,
+// bf16: 265 us with one or two; 4096 channels 329 and 344).
+int64_t blocks_of(int64_t N, const Group &g, bool backward)
 {
-    const int64_t per = threads_of(g.lpr) / g.lpr;
-    return std::max<int64_t>(1, std::min((N + per - 1) / per, int64_t(256) * waves / (threads_of(g.lpr) / 64)));
+    const int64_t threads = threads_of(g.lpr), per = threads / g.lpr;
+    const int64_t waves = g.kch > 1 ? 8 : g.lpr == 256 ? 32 : 16;
+    const int64_t most = backward ? 256 : 256 * waves / (threads / 64);
+    return std::max<int64_t>(1, std::min((N + per - 1) / per, most));
 }
 constexpr int64_t kWideBlocks = 2048, kColBlocks = 32;
 
 int64_t bwd_blocks(int64_t N, int64_t C)
 {
-    const Group g = group_of(C);
-    return g.lpr ? blocks_of(N, g, 8) : std::max<int64_t>(1, std::min(N, kColBlocks));
+    const Group g = group_of(C, true);
+    return g.lpr ? blocks_of(N, g, true) : std::max<int64_t>(1, std::min(N, kColBlocks));
 }
 
 }  // namespace
@@ -764,12 +804,12 @@ int64_t bwd_blocks(int64_t N, int64_t C)
 int64_t res_norm_bwd_ws_bytes(int64_t N, int64_t C, int64_t groups)
 {
     const int64_t B = bwd_blocks(N, C), G = std::max<int64_t>(groups, 1);
-    return ((2 * B + G) * 2 * C * 4 + (B + G + 1) / 2 * 8 + (group_of(C).lpr ? 0 : N * 8) + 255) / 256 * 256;
+    return ((2 * B + G) * 2 * C * 4 + (B + G + 1) / 2 * 8 + (group_of(C, true).lpr ? 0 : N * 8) + 255) / 256 * 256;
 }
 
 hipError_t launch_res_norm_fwd(const ResNormArgs &a, hipStream_t s)
 {
-    const Group g = group_of(a.C);
+    const Group g = group_of(a.C, false);
     return with_norm_types(a.dtype, a.branch_dtype, [&](auto tr, auto tb) {
         using TR = typename decltype(tr)::type;
         using TB = typename decltype(tb)::type;
@@ -778,9 +818,9 @@ hipError_t launch_res_norm_fwd(const ResNormArgs &a, hipStream_t s)
                                dim3(kThreads), 0, s, a);
             return hipGetLastError();
         }
-        return with_group(g, [&](auto lpr, auto kch) {
+        return with_group<false>(g, [&](auto lpr, auto kch) {
             constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
-            const dim3 grid(unsigned(blocks_of(a.N, g, 16))), threads(threads_of(LPR));
+            const dim3 grid(unsigned(blocks_of(a.N, g, false))), threads(threads_of(LPR));
             if (a.C % 8 == 0)
                 hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
             else
@@ -798,7 +838,7 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
                            dim3(kThreads), 0, s, a);
         return hipGetLastError();
     }
-    const Group g = group_of(a.C);
+    const Group g = group_of(a.C, true);
     const int64_t B = bwd_blocks(a.N, a.C);
     const hipError_t e = with_norm_types(a.dtype, a.branch_dtype, [&](auto tr, auto tb) {
         using TR = typename decltype(tr)::type;
@@ -812,7 +852,7 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
                                dim3(kThreads), 0, s, a);
             return hipGetLastError();
         }
-        return with_group(g, [&](auto lpr, auto kch) {
+        return with_group<true>(g, [&](auto lpr, auto kch) {
             constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
             const dim3 grid{unsigned(B)}, threads(threads_of(LPR));
             if (a.C % 8 == 0)
@@ -823,8 +863,11 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
         });
     });
     if (e != hipSuccess || !a.ws) return e;
-    const int64_t jobs = (a.dgate ? 2 + std::max<int64_t>(a.groups, 1) : 2) * ((a.C + 63) / 64);
-    hipLaunchKernelGGL(res_norm_join_kernel, dim3(unsigned(std::min<int64_t>(jobs, 4096))), dim3(1024), 0, s, a, B);
+    const int W = join_channels(a.C);
+    const int64_t G = std::max<int64_t>(a.groups, 1), tiles = (a.C + W - 1) / W;
+    const int64_t gates = !a.dgate ? 0 : short_groups(B, G) ? (G * a.C + 255) / 256 : G * tiles;
+    hipLaunchKernelGGL(res_norm_join_kernel, dim3(unsigned(std::min<int64_t>(2 * tiles + gates, 8192))), dim3(1024), 0, s,
+                       a, B);
     return hipGetLastError();
 }
 
