@@ -69,15 +69,15 @@ hipError_t launch_ff_all(const FfProduct &dx, const FfProduct &dwd, const FfProd
 // the slabs of up to three products added in order
 hipError_t launch_ff_join(const FfProduct *p, int count, int dtype, hipStream_t s);
 
-// few rows, nothing saved: h stays fp32
+// few rows: h in two parts (half precision), h itself and `lo` [N][Fp]; with a `pre` the
+// factors, and h with its zero rows
 struct FfRows {
     const void *x, *wg, *wu, *wd;
     int64_t ldx, ldg, ldu, ldd, ldy;   // elements
-    int64_t N, D, F, O;
-    float *h;                // [N][F]
-    void *y;
+    int64_t N, D, F, O, Fp;
+    FfSaved to;
+    void *lo, *y;
     int act;
 };
-hipError_t launch_ff_rows(const FfRows &a, int dtype, hipStream_t s);
 
 }  // namespace im2win

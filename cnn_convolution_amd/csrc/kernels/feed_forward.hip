@@ -79,152 +79,238 @@ __global__ __launch_bounds__(256) void ff_zero_kernel(T *p, int64_t n)
 
 // ---- few rows ------------------------------------------------------------------------
 //
-// At most 16 rows: the weights are read once and that read is all that counts. A
-// workgroup takes 16 rows of a weight matrix (of Wg and of Wu for h), its waves split
-// K; the weights go from memory straight to the lanes that multiply them (16 rows x 64
-// bytes a load, the matrix cores' own layout, so no LDS and no barrier until the waves'
-// sums are joined), x or h come from the caches. Rows past N repeat the last one and
-// are not stored.
+// At most FF_ROWS rows, NB blocks of 16: the weights are read once and that read is all
+// that counts. A workgroup takes 16 rows of a weight matrix (of Wg and of Wu for h), its
+// waves split K; the weights go from memory straight to the lanes that multiply them (16
+// rows x 64 bytes a load, the matrix cores' own layout, so no LDS and no barrier until the
+// waves' sums are joined, no padded copies of odd rows), x or h come from the caches.
+// Rows past N repeat the last one. In half precision h is kept in two parts, rounded and
+// what that took: its rounding would be as large in y as y's own.
+// 1 row, 4096 inputs and outputs, 8192 hidden features, bf16: h 23.5 us (5.7 TB/s), y
+// 14.4 (4.7).
 
-// K values at `k` of a row of K: whole vectors in the steps below `whole`, else up to
-// the row's end and zeros past it
-template <typename T>
-__device__ __forceinline__ uint4 row_frag(const T *row, int64_t k, int64_t K, bool whole)
-{
-    constexpr int E = 16 / int(sizeof(T));
-    if (whole) {
-        const Raw<T, E> r = load_raw<T, E>(row + k);
-        return uint4{r.d[0], r.d[1], r.d[2], r.d[3]};
+// A row of K values. ODD: half-precision rows that start at any element are read as the
+// dwords that hold them and shifted into place, for 16-byte loads that start between
+// dwords take twice the time (16 rows, 1001 inputs, 2000 hidden features, fp16: h 10.1 us,
+// 1002 inputs 5.4). No dword is touched that holds nothing of the vector.
+template <typename T, bool ODD>
+struct Row {
+    static constexpr int E = 16 / int(sizeof(T));
+    const T *row;
+    uint32_t shift;          // bits
+
+    __device__ __forceinline__ void init(const T *p)
+    {
+        row = p;
+        shift = ODD ? uint32_t(reinterpret_cast<uintptr_t>(p) & 2) * 8 : 0;
     }
-    uint32_t d[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (k + e < K) {
-            if constexpr (sizeof(T) == 4)
-                d[e] = __float_as_uint(row[k + e]);
-            else
-                d[e / 2] |= uint32_t(__builtin_bit_cast(uint16_t, row[k + e])) << (e & 1) * 16;
+    // E values from `k` on, all in the row
+    __device__ __forceinline__ uint4 vec(int64_t k) const
+    {
+        if constexpr (!ODD) {
+            const Raw<T, E> r = load_raw<T, E>(row + k);
+            return uint4{r.d[0], r.d[1], r.d[2], r.d[3]};
+        } else {
+            typedef uint32_t vec4 __attribute__((ext_vector_type(4), aligned(4)));
+            const char *p = reinterpret_cast<const char *>(row + k) - shift / 8;
+            const vec4 d = *reinterpret_cast<const vec4 *>(p);
+            const uint32_t e = *reinterpret_cast<const uint32_t *>(p + (shift ? 16 : 12));
+            return uint4{__builtin_amdgcn_alignbit(d[1], d[0], shift), __builtin_amdgcn_alignbit(d[2], d[1], shift),
+                         __builtin_amdgcn_alignbit(d[3], d[2], shift), __builtin_amdgcn_alignbit(e, d[3], shift)};
         }
-    return uint4{d[0], d[1], d[2], d[3]};
-}
+    }
+    // up to the row's end and zeros past it, without a branch (element by element, each
+    // a wait behind a branch, the step that K ends in took longer than all others)
+    __device__ __forceinline__ uint4 end(int64_t k, int64_t K) const
+    {
+        if (K >= E) {
+            const Raw<T, E> r = load_row<T, E, false>(row, k, K);
+            return uint4{r.d[0], r.d[1], r.d[2], r.d[3]};
+        }
+        uint32_t d[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (k + e < K) {
+                if constexpr (sizeof(T) == 4)
+                    d[e] = __float_as_uint(row[k + e]);
+                else
+                    d[e / 2] |= uint32_t(__builtin_bit_cast(uint16_t, row[k + e])) << (e & 1) * 16;
+            }
+        return uint4{d[0], d[1], d[2], d[3]};
+    }
+};
 
 template <typename T>
 constexpr int kFragK = 64 / int(sizeof(T));    // K of a fragment pair: 16 bytes a lane
 
-// the waves' sums in order, left with the first wave
-template <int WAVES, int NB>
-__device__ __forceinline__ void join_parts(floatx4_t (&acc)[NB], floatx4_t *part)
+// The waves' sums of M sets of NB blocks, added in order: wave w < NB is left with block
+// w of each set.
+template <int WAVES, int M, int NB>
+__device__ __forceinline__ void join_parts(const floatx4_t (&acc)[M][NB], floatx4_t (&out)[M], floatx4_t *part)
 {
+    static_assert(NB <= WAVES, "a wave per block");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (wave > 0)
 #pragma unroll
-        for (int i = 0; i < NB; ++i) part[((wave - 1) * NB + i) * 64 + lane] = acc[i];
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) part[((wave * M + m) * NB + b) * 64 + lane] = acc[m][b];
     __syncthreads();
-    if (wave > 0) return;
-    for (int w = 1; w < WAVES; ++w)
+    if (wave >= NB) return;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) acc[i] += part[((w - 1) * NB + i) * 64 + lane];
+    for (int m = 0; m < M; ++m) {
+        out[m] = part[(m * NB + wave) * 64 + lane];
+        for (int w = 1; w < WAVES; ++w) out[m] += part[((w * M + m) * NB + wave) * 64 + lane];
+    }
 }
 
-template <typename T, int WAVES>
+template <typename T, int WAVES, int NB, bool SAVE, bool ODD>
 __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a)
 {
     constexpr int KF = kFragK<T>, U = 4;       // fragments in flight per matrix
-    __shared__ floatx4_t part[(WAVES - 1) * 2 * 64];
+    __shared__ floatx4_t part[WAVES * 2 * NB * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t f0 = int64_t(blockIdx.x) * 16, f = min(f0 + (lane & 15), a.F - 1);
-    const int64_t n = min(int64_t(lane & 15), a.N - 1);
-    const T *wg = static_cast<const T *>(a.wg) + f * a.ldg, *wu = static_cast<const T *>(a.wu) + f * a.ldu;
-    const T *x = static_cast<const T *>(a.x) + n * a.ldx;
+    Row<T, ODD> wg, wu, x[NB];
+    wg.init(static_cast<const T *>(a.wg) + f * a.ldg);
+    wu.init(static_cast<const T *>(a.wu) + f * a.ldu);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        x[b].init(static_cast<const T *>(a.x) + min(int64_t((blockIdx.y * NB + b) * 16 + (lane & 15)), a.N - 1) * a.ldx);
     const int q = (lane >> 4) * (16 / int(sizeof(T)));
     const int64_t steps = (a.D + KF - 1) / KF, whole = a.D / KF;
     int64_t s = steps * wave / WAVES;
     const int64_t end = steps * (wave + 1) / WAVES;
-    floatx4_t acc[2] = {};
-    for (; s + U <= min(end, whole); s += U) {
-        uint4 g[U], u[U], b[U];
+    floatx4_t acc[2][NB] = {};
+    // the loads of U steps at a time; in the last batch past the wave's last step that
+    // one again, unused
+    const int64_t last = min(end, whole) - 1;
+    auto batch = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        uint4 g[U], u[U], xf[NB][U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            g[i] = row_frag(wg, (s + i) * KF + q, a.D, true);
-            u[i] = row_frag(wu, (s + i) * KF + q, a.D, true);
-            b[i] = row_frag(x, (s + i) * KF + q, a.D, true);
+            const int64_t k = (FULL ? s + i : min(s + i, last)) * KF + q;
+            g[i] = wg.vec(k);
+            u[i] = wu.vec(k);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) xf[b][i] = x[b].vec(k);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            acc[0] = mfma_half<T>(g[i], b[i], acc[0]);
-            acc[1] = mfma_half<T>(u[i], b[i], acc[1]);
+            if (!FULL && s + i > last) break;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                acc[0][b] = mfma_half<T>(g[i], xf[b][i], acc[0][b]);
+                acc[1][b] = mfma_half<T>(u[i], xf[b][i], acc[1][b]);
+            }
+        }
+    };
+    for (; s + U - 1 <= last; s += U) batch(std::true_type{});
+    if (s <= last) batch(std::false_type{});
+    if (end > whole) {                         // the step that K ends in
+        const uint4 g = wg.end(whole * KF + q, a.D), u = wu.end(whole * KF + q, a.D);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint4 xf = x[b].end(whole * KF + q, a.D);
+            acc[0][b] = mfma_half<T>(g, xf, acc[0][b]);
+            acc[1][b] = mfma_half<T>(u, xf, acc[1][b]);
         }
     }
-    for (; s < end; ++s) {
-        const uint4 b = row_frag(x, s * KF + q, a.D, s < whole);
-        acc[0] = mfma_half<T>(row_frag(wg, s * KF + q, a.D, s < whole), b, acc[0]);
-        acc[1] = mfma_half<T>(row_frag(wu, s * KF + q, a.D, s < whole), b, acc[1]);
-    }
-    join_parts<WAVES, 2>(acc, part);
-    if (wave > 0 || (lane & 15) >= a.N) return;
+    floatx4_t sum[2];
+    join_parts<WAVES, 2, NB>(acc, sum, part);
+    if (wave >= NB) return;
+    const int rb = blockIdx.y * NB + wave;     // block of rows
+    const int64_t row = rb * 16 + (lane & 15), m = f0 + (lane >> 4) * 4;
     float h[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
+        const bool in = row < a.N && m + v < a.F;
         float g, dg;
-        activate<sizeof(T) == 4>(a.act, acc[0][v], g, dg);
-        h[v] = g * acc[1][v];
+        activate<sizeof(T) == 4>(a.act, sum[0][v], g, dg);
+        h[v] = in ? g * sum[1][v] : 0.f;
+        sum[0][v] = in ? g : 0.f;
+        sum[1][v] = in ? sum[1][v] * dg : 0.f;
     }
-    const int64_t m = f0 + (lane >> 4) * 4;
-    store_some<4>(a.h + (lane & 15) * a.F + m, a.F - m, h);
+    if constexpr (SAVE) {
+        floatx4_t *p = reinterpret_cast<floatx4_t *>(a.to.pre) + (rb * a.to.fblocks + blockIdx.x) * 128 + lane;
+        p[0] = sum[0];
+        p[64] = sum[1];
+    }
+    if (m >= a.Fp || (!SAVE && row >= a.N)) return;
+    const Raw<T, 4> hi = to_raw<T, 4>(h);
+    store_raw(static_cast<T *>(a.to.h) + row * a.Fp + m, hi);
+    if (sizeof(T) == 4 || row >= a.N) return;
+    float rest[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) rest[v] = h[v] - element(hi, v);
+    store_vec<4>(static_cast<T *>(a.lo) + row * a.Fp + m, rest);
 }
 
-// y from the fp32 h: half precision as the sum of a rounded h and what that took
-template <typename T, int WAVES>
+template <typename T, int WAVES, int NB, bool ODD>
 __global__ __launch_bounds__(WAVES * 64) void ff_rows_down_kernel(const FfRows a)
 {
-    constexpr int KF = kFragK<T>, E = 16 / int(sizeof(T)), U = 4;
-    __shared__ floatx4_t part[(WAVES - 1) * 64];
+    constexpr int KF = kFragK<T>, U = 4;
+    constexpr bool HALF = sizeof(T) == 2;
+    __shared__ floatx4_t part[WAVES * NB * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t o0 = int64_t(blockIdx.x) * 16, o = min(o0 + (lane & 15), a.O - 1);
-    const int64_t n = min(int64_t(lane & 15), a.N - 1);
-    const T *w = static_cast<const T *>(a.wd) + o * a.ldd;
-    const float *h = a.h + n * a.F;
-    const int q = (lane >> 4) * E;
+    Row<T, ODD> w;
+    w.init(static_cast<const T *>(a.wd) + o * a.ldd);
+    const int q = (lane >> 4) * (16 / int(sizeof(T)));
+    Row<T, false> hi[NB], lo[NB];              // whole vectors up to Fp, zeros past F
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t at = min(int64_t((blockIdx.y * NB + b) * 16 + (lane & 15)), a.N - 1) * a.Fp;
+        hi[b].init(static_cast<const T *>(a.to.h) + at);
+        lo[b].init(static_cast<const T *>(a.lo) + at);
+    }
     const int64_t steps = (a.F + KF - 1) / KF, whole = a.F / KF;
     int64_t s = steps * wave / WAVES;
     const int64_t end = steps * (wave + 1) / WAVES;
-    floatx4_t acc[1] = {};
-    auto multiply = [&](const uint4 &wf, const float (&f)[E]) {
-        if constexpr (sizeof(T) == 4) {
-            acc[0] = mfma_half<T>(wf, uint4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                            __float_as_uint(f[3])}, acc[0]);
-        } else {
-            const Raw<T, 8> hi = to_raw<T, 8>(f);
-            float rest[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) rest[e] = f[e] - element(hi, e);
-            const Raw<T, 8> lo = to_raw<T, 8>(rest);
-            acc[0] = mfma_half<T>(wf, uint4{hi.d[0], hi.d[1], hi.d[2], hi.d[3]}, acc[0]);
-            acc[0] = mfma_half<T>(wf, uint4{lo.d[0], lo.d[1], lo.d[2], lo.d[3]}, acc[0]);
-        }
-    };
-    for (; s + U <= min(end, whole); s += U) {
-        uint4 wf[U];
-        float f[U][E];
+    floatx4_t acc[1][NB] = {};
+    const int64_t last = min(end, whole) - 1;
+    auto batch = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        uint4 wf[U], hf[NB][U], lf[NB][U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            wf[i] = row_frag(w, (s + i) * KF + q, a.F, true);
-            load_vec<E>(h + (s + i) * KF + q, f[i]);
+            const int64_t k = (FULL ? s + i : min(s + i, last)) * KF + q;
+            wf[i] = w.vec(k);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                hf[b][i] = hi[b].vec(k);
+                if (HALF) lf[b][i] = lo[b].vec(k);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) multiply(wf[i], f[i]);
+        for (int i = 0; i < U; ++i) {
+            if (!FULL && s + i > last) break;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                acc[0][b] = mfma_half<T>(wf[i], hf[b][i], acc[0][b]);
+                if (HALF) acc[0][b] = mfma_half<T>(wf[i], lf[b][i], acc[0][b]);
+            }
+        }
+    };
+    for (; s + U - 1 <= last; s += U) batch(std::true_type{});
+    if (s <= last) batch(std::false_type{});
+    if (end > whole) {
+        const uint4 wf = w.end(whole * KF + q, a.F);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            acc[0][b] = mfma_half<T>(wf, hi[b].end(whole * KF + q, a.Fp), acc[0][b]);
+            if (HALF) acc[0][b] = mfma_half<T>(wf, lo[b].end(whole * KF + q, a.Fp), acc[0][b]);
+        }
     }
-    for (; s < end; ++s) {
-        float f[E];
-        load_some<E>(h + s * KF + q, max(int64_t(0), a.F - s * KF - q), f);
-        multiply(row_frag(w, s * KF + q, a.F, s < whole), f);
-    }
-    join_parts<WAVES, 1>(acc, part);
-    if (wave > 0 || (lane & 15) >= a.N) return;
-    const int64_t m = o0 + (lane >> 4) * 4;
-    const float y[4] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
-    store_some<4>(static_cast<T *>(a.y) + (lane & 15) * a.ldy + m, a.O - m, y);
+    floatx4_t sum[1];
+    join_parts<WAVES, 1, NB>(acc, sum, part);
+    const int64_t row = (blockIdx.y * NB + wave) * 16 + (lane & 15), m = o0 + (lane >> 4) * 4;
+    if (wave >= NB || row >= a.N) return;
+    const float y[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+    store_some<4>(static_cast<T *>(a.y) + row * a.ldy + m, a.O - m, y);
 }
+
+constexpr int64_t kRowsGroups = 512;
 
 // ---- plan ------------------------------------------------------------------------------
 
@@ -233,7 +319,7 @@ struct FfPlan {
     int64_t Dp, Fp, Op, rows_pad, fblocks;
     bool copy_x, copy_g, copy_u, copy_d, copy_y;   // rows not made of 16-byte granules
     int gate_tile, y_tile, y_split, back_tile, dx_tile, dx_split, dd_tile, dd_split, dg_tile, dg_split;
-    int64_t off_x, off_g, off_u, off_d, off_dy, off_h, off_slab_x, off_slab_d, off_slab_g, off_grad, off_amax, bytes;
+    int64_t off_x, off_g, off_u, off_d, off_dy, off_h, off_lo, off_slab_x, off_slab_d, off_slab_g, off_grad, off_amax, bytes;
     int64_t pre_bytes;       // of saved, before h
 };
 
@@ -244,13 +330,16 @@ int64_t take(FfPlan &p, int64_t bytes)
     return at;
 }
 
-// tile of a product that is not split
-int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes)
+// tile of a product that is not split (back: of dh, else of the gate)
+int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, bool back)
 {
     double best = 1e30;
     int tile = 0;
-    for (int t = 0; t < 3; ++t) {
-        const double us = product_us(kShapes[t], M, N, stages, 1, dtype, out_bytes);
+    for (int t = 0; t < 5; ++t) {
+        if (t == kTile32K && (!back || dtype)) continue;
+        if (t == kTile64x32 && N > 64) continue;       // (W would be read three times and more)
+        const int64_t own = t == kTile32K ? ceil_div(stages, 4) : stages;
+        const double us = product_us(kShapes[t], M, N, own, 1, dtype, out_bytes);
         if (us < best * 0.98) {
             best = us;
             tile = t;
@@ -293,14 +382,15 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     FfPlan p = plan_common(z);
     if (z.N == 0) return p;
     const int64_t es = elem(z.dtype), ki = 128 / es;
-    p.few = z.N <= FF_ROWS && !saved;
+    p.few = z.N <= 16 || (z.N <= FF_ROWS && (!z.dtype || p.copy_g || p.copy_u || p.copy_d));
     if (p.few) {
-        p.off_h = take(p, z.N * z.F * 4);
+        if (!saved) p.off_h = take(p, z.N * p.Fp * es);
+        if (z.dtype) p.off_lo = take(p, z.N * p.Fp * es);
         return p;
     }
     plan_copies(p, z);
     if (!saved) p.off_h = take(p, p.rows_pad * p.Fp * es);
-    p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(saved ? 4 + es / 2 : es / 2));
+    p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(saved ? 4 + es / 2 : es / 2), false);
     pick_product(z.O, z.N, ceil_div(p.Fp, ki), z.dtype, 0, &p.y_tile, &p.y_split);
     if (p.y_split > 1) p.off_slab_x = take(p, p.y_split * z.N * z.O * 4);
     return p;
@@ -315,7 +405,7 @@ FfPlan plan_bwd(const FfSizes &z)
     if (p.copy_y) p.off_dy = take(p, z.N * p.Op * es);
     p.off_grad = take(p, p.rows_pad * 2 * p.Fp * es);
     p.off_amax = take(p, kAmaxParts * 4);
-    p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es));
+    p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), true);
     pick_product(z.D, z.N, 2 * ceil_div(z.F, ki), z.dtype, 0, &p.dx_tile, &p.dx_split);
     pick_product(z.F, z.O, ceil_div(z.N, ki), z.dtype, 0, &p.dd_tile, &p.dd_split);
     pick_product(z.D, 2 * z.F, ceil_div(z.N, ki), z.dtype, 0, &p.dg_tile, &p.dg_split);
@@ -376,16 +466,45 @@ FfSaved saved_of(const FfPlan &p, const void *saved, void *h)
     return FfSaved{reinterpret_cast<float *>(c), p.fblocks, c ? c + p.pre_bytes : h};
 }
 
-// the waves of a workgroup that split K: a wave should have some steps of its own
-template <typename T>
-hipError_t launch_rows(const FfRows &a, hipStream_t s)
+// nb blocks of rows: NB at a time by a workgroup, the others by further workgroups
+template <typename T, int NB, bool ODD>
+hipError_t launch_rows(const FfRows &a, int64_t nb, hipStream_t s)
 {
-    const dim3 gate(unsigned(ceil_div(a.F, 16))), down(unsigned(ceil_div(a.O, 16)));
-    hipLaunchKernelGGL((ff_rows_gate_kernel<T, 4>), gate, dim3(256), 0, s, a);
+    constexpr int DOWN = NB == 1 ? 16 : 8;
+    const dim3 gate(unsigned(ceil_div(a.F, 16)), unsigned(ceil_div(nb, NB)));
+    const dim3 down(unsigned(ceil_div(a.O, 16)), gate.y);
+    if (a.to.pre)
+        hipLaunchKernelGGL((ff_rows_gate_kernel<T, 4, NB, true, ODD>), gate, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((ff_rows_gate_kernel<T, 4, NB, false, ODD>), gate, dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ff_rows_down_kernel<T, 16>), down, dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((ff_rows_down_kernel<T, DOWN, NB, ODD>), down, dim3(DOWN * 64), 0, s, a);
     return hipGetLastError();
+}
+
+// rows: with `saved` h's zero rows up to rows_pad are written too. Weights that few
+// workgroups read are read again for each block of rows, by workgroups of its own (64
+// rows, 512 inputs, 1024 hidden features, fp32: h 6.8 us, 11.8 with 64 rows a workgroup;
+// 2048 inputs, 4096 hidden features 79 and 74 us in all).
+hipError_t launch_rows(const FfRows &a, int dtype, int64_t rows, hipStream_t s)
+{
+    const int64_t nb = ceil_div(rows, 16);
+    return with_ff_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        const auto blocks = [&](auto odd) {
+            constexpr bool ODD = decltype(odd)::value;
+            if (nb == 1 || ceil_div(a.F, 16) * nb <= kRowsGroups) return launch_rows<T, 1, ODD>(a, nb, s);
+            if (nb == 2) return launch_rows<T, 2, ODD>(a, nb, s);
+            return launch_rows<T, 4, ODD>(a, nb, s);
+        };
+        if constexpr (sizeof(T) == 2) {
+            bool odd = (a.ldx | a.ldg | a.ldu | a.ldd) & 1;
+            for (const void *p : {a.x, a.wg, a.wu, a.wd}) odd = odd || reinterpret_cast<uintptr_t>(p) % 4 != 0;
+            if (odd) return blocks(std::true_type{});
+        }
+        return blocks(std::false_type{});
+    });
 }
 
 }  // namespace
@@ -399,11 +518,6 @@ int64_t ff_saved_bytes(const FfSizes &z)
 int64_t ff_fwd_ws_bytes(const FfSizes &z, bool saved) { return plan_fwd(z, saved).bytes; }
 int64_t ff_bwd_ws_bytes(const FfSizes &z) { return plan_bwd(z).bytes; }
 
-hipError_t launch_ff_rows(const FfRows &a, int dtype, hipStream_t s)
-{
-    return with_ff_type(dtype, [&](auto t) { return launch_rows<decltype(t)>(a, s); });
-}
-
 hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s)
 {
     const FfSizes &z = a.z;
@@ -411,13 +525,14 @@ hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s)
     const FfPlan p = plan_fwd(z, a.saved != nullptr);
     char *ws = static_cast<char *>(a.ws);
     const int64_t es = elem(z.dtype);
+    const FfSaved to = saved_of(p, a.saved, ws + p.off_h);
     if (p.few)
-        return launch_ff_rows(FfRows{a.x, a.wg, a.wu, a.wd, z.ldx, z.ldg, z.ldu, z.ldd, z.ldy, z.N, z.D, z.F, z.O,
-                                     reinterpret_cast<float *>(ws + p.off_h), a.y, z.act}, z.dtype, s);
+        return launch_rows(FfRows{a.x, a.wg, a.wu, a.wd, z.ldx, z.ldg, z.ldu, z.ldd, z.ldy, z.N, z.D, z.F, z.O, p.Fp, to,
+                                  ws + p.off_lo, a.y, z.act},
+                           z.dtype, a.saved ? p.rows_pad : z.N, s);
     FfRead r{};
     hipError_t e = launch_pads(p, a, false, &r, s);
     if (e != hipSuccess) return e;
-    const FfSaved to = saved_of(p, a.saved, ws + p.off_h);
     const FfGate g{r.x, r.wg, r.wu, r.ldx, r.ldg, r.ldu, z.N, z.F, p.Dp, p.rows_pad, p.Fp, to, z.act};
     if ((e = launch_ff_gate(g, z.dtype, p.gate_tile, s)) != hipSuccess) return e;
     FfProduct y{};

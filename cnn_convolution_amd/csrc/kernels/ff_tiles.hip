@@ -164,9 +164,10 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_gate_kernel(const 
 template <typename T, typename C>
 __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const FfBack a, int tiles_m, int tiles_n)
 {
+    using E = typename EpiOf<C>::type;         // how the waves hold a tile's sums
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % C::WM, wn = wave / C::WM;
+    const int wm = wave % E::WM, wn = wave / E::WM;
     const int tiles = tiles_m * tiles_n, stages = int((a.O + 128 / int(sizeof(T)) - 1) / (128 / int(sizeof(T))));
     const GemmOperand A{a.wd, a.ldd, a.Fp, a.O};
     const GemmOperand B{a.dy, a.lddy, a.N, a.Op};
@@ -177,26 +178,35 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
         strip_tile(t, tiles_m, tiles_n, tm, tn);
         m0 = int64_t(tm) * C::BM;
         n0 = int64_t(tn) * C::BN;
-        pipe.start(A, B, m0, n0, 0, stages);
+        if constexpr (kSplitWaves<C>)
+            pipe.start(A, B, m0, n0, stages * wave / C::groups, stages * (wave + 1) / C::groups);
+        else
+            pipe.start(A, B, m0, n0, 0, stages);
     };
     start(blockIdx.x);
     const float S = a.amax ? dy_scale(a.amax) : 1.f;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t ft = m0 + wm * (C::BM / C::WM), nt = n0 + wn * (C::BN / C::WN);
-        floatx4_t acc[C::FM][C::FN];
+        const int64_t ft = m0 + wm * (E::BM / E::WM), nt = n0 + wn * (E::BN / E::WN);
+        floatx4_t acc[E::FM][E::FN];
         NoExtra none;
-        pipe.template run<0>(false, acc, none);
+        if constexpr (kSplitWaves<C>) {
+            floatx4_t part[C::FM][C::FN];
+            pipe.template run<0>(false, part, none);
+            join_waves<C>(smem, part, acc);
+        } else {
+            pipe.template run<0>(false, acc, none);
+        }
         if (t + int(gridDim.x) < tiles) start(t + gridDim.x);
         // The factors of H blocks at a time, AHEAD groups of them requested before they are
         // used: one pair at a time, waited for, this epilogue took longer than its products
         // (8192 rows, 4096 outputs, 16384 hidden features, bf16: 1606 us). Past the last
         // row and feature the factors are zeros.
-        constexpr int H = 2, GROUPS = C::FM / H * C::FN, AHEAD = 2;
+        constexpr int H = E::FM < 2 ? 1 : 2, GROUPS = E::FM / H * E::FN, AHEAD = 2;
         floatx4_t ring[AHEAD + 1][H][2];
         const char *pre = reinterpret_cast<const char *>(a.from.pre) +
                           ((nt / 16) * a.from.fblocks + ft / 16) * 2048;
         auto request = [&](int q) {
-            const char *p = pre + (int64_t(q * H / C::FM) * a.from.fblocks + q * H % C::FM) * 2048;
+            const char *p = pre + (int64_t(q * H / E::FM) * a.from.fblocks + q * H % E::FM) * 2048;
 #pragma unroll
             for (int i = 0; i < 2 * H; ++i)
                 ring[q % (AHEAD + 1)][i / 2][i % 2] = *reinterpret_cast<const floatx4_t *>(p + i * 1024 + lane * 16);
@@ -205,7 +215,7 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
         for (int q = 0; q < AHEAD && q < GROUPS; ++q) request(q);
 #pragma unroll
         for (int q = 0; q < GROUPS; ++q) {
-            const int j = q * H / C::FM, i0 = q * H % C::FM;
+            const int j = q * H / E::FM, i0 = q * H % E::FM;
             const int64_t row = nt + 16 * j + (lane & 15);
             if (q + AHEAD < GROUPS) request(q + AHEAD);
             __builtin_amdgcn_sched_barrier(0);
@@ -264,6 +274,7 @@ hipError_t launch_ff_gate(const FfGate &a, int dtype, int tile, hipStream_t s)
         switch (tile) {
         case kTile256: return launch_gate<T, C256>(a, s);
         case kTile128: return launch_gate<T, C128>(a, s);
+        case kTile64x32: return launch_gate<T, C64x32>(a, s);
         default: return launch_gate<T, C64>(a, s);
         }
     });
@@ -276,6 +287,12 @@ hipError_t launch_ff_back(const FfBack &a, int dtype, int tile, hipStream_t s)
         switch (tile) {
         case kTile256: return launch_back<T, C256>(a, s);
         case kTile128: return launch_back<T, C128>(a, s);
+        case kTile64x32: return launch_back<T, C64x32>(a, s);
+        case kTile32K:
+            // (a tile of 32 columns in half precision has too few granules for the
+            // transposed reads)
+            if constexpr (sizeof(T) == 4) return launch_back<T, C32K>(a, s);
+            return hipErrorInvalidValue;
         default: return launch_back<T, C64>(a, s);
         }
     });

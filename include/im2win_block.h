@@ -43,11 +43,11 @@ extern "C" {
  * All products are accumulated in fp32, a, u and dh are fp32 throughout; h, da and
  * du are rounded to the type of x where the matrix cores read them (fp16: h has to
  * stay in that type's range; da and du are held times a power of two that brings
- * the largest finite |dy| into [1, 2)). With at most FF_ROWS rows and nothing
- * saved h stays fp32. The outputs are rounded once. Limits: N <= 2^22; D, F, O
+ * the largest finite |dy| into [1, 2)); with at most FF_ROWS rows y is formed from
+ * an h of twice those digits. The outputs are rounded once. Limits: N <= 2^22; D, F, O
  * and the row strides <= 2^20. N = 0 gives zero weight gradients. */
 enum { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2, FF_RELU = 3, FF_SIGMOID = 4 };
-enum { FF_ROWS = 16 };
+enum { FF_ROWS = 64 };
 
 typedef struct {
     int64_t N, D, F, O;
@@ -63,8 +63,8 @@ typedef struct {
  * to start on a 16-byte boundary; other rows may start anywhere and, for more than
  * FF_ROWS rows or a backward pass, are copied into the workspace first.
  *
- * saved: what feed_forward_bwd needs of the forward pass (a and u in fp32, h),
- * feed_forward_saved_size() bytes, 256-byte aligned; NULL when no backward pass
+ * saved: what feed_forward_bwd needs of the forward pass (act(a) and u act'(a) in fp32,
+ * h), feed_forward_saved_size() bytes, 256-byte aligned; NULL when no backward pass
  * follows (feed_forward_fwd_workspace_size has to be asked with the same choice).
  * Sizes are 0 if d is invalid, or when nothing is needed. */
 size_t feed_forward_saved_size(const feed_forward_desc_t *d);
