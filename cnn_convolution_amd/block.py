@@ -39,11 +39,13 @@ def _enqueue(dev, name, *args) -> None:
             _block.call(name, *args, head._raw_stream(dev))
 
 
-def _on(t, name, dev, dtype, shape):
+def _stride(t, name, dev, dtype, shape):
+    """The row stride of a tensor of this device, type and shape (0: contiguous)."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a device tensor on the same device as the others")
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    return 0 if t.is_contiguous() else _rows(t, name)[2]
 
 
 # ---- gated feed-forward block ----------------------------------------------------
@@ -51,24 +53,21 @@ def _on(t, name, dev, dtype, shape):
 def _ff_desc(x, w_gate, w_up, w_down, y, activation):
     """(descriptor, device); y: y or dy, or None where its strides do not count."""
     dev = _device(x, "x")
-    code = _code(x.dtype)
+    dtype = x.dtype
     N, D, ldx = _rows(x, "x")
-    if w_gate.dim() != 2 or w_down.dim() != 2 or w_gate.shape[1] != D or w_down.shape[1] != w_gate.shape[0]:
+    shape_g, shape_d = w_gate.shape, w_down.shape
+    if len(shape_g) != 2 or len(shape_d) != 2 or shape_g[1] != D or shape_d[1] != shape_g[0]:
         raise ValueError("x must be [..., D], w_gate and w_up [F][D], w_down [O][F]")
-    F, O = w_gate.shape[0], w_down.shape[0]
-    _on(w_gate, "w_gate", dev, x.dtype, (F, D))
-    _on(w_up, "w_up", dev, x.dtype, (F, D))
-    _on(w_down, "w_down", dev, x.dtype, (O, F))
-    ldy = 0
-    if y is not None:
-        _on(y, "y and dy", dev, x.dtype, x.shape[:-1] + (O,))
-        ldy = _rows(y, "y and dy")[2]
+    F, O = shape_g[0], shape_d[0]
     try:
         act = _block.ACTIVATIONS[activation]
     except KeyError:
         raise ValueError(f"unknown activation {activation!r}") from None
-    return FeedForwardDesc(N, D, F, O, ldx, _rows(w_gate, "w_gate")[2], _rows(w_up, "w_up")[2],
-                           _rows(w_down, "w_down")[2], ldy, code, act, 0, 0), dev
+    return FeedForwardDesc(N, D, F, O, ldx, _stride(w_gate, "w_gate", dev, dtype, shape_g) or D,
+                           _stride(w_up, "w_up", dev, dtype, shape_g) or D,
+                           _stride(w_down, "w_down", dev, dtype, shape_d) or F,
+                           0 if y is None else _stride(y, "y and dy", dev, dtype, x.shape[:-1] + (O,)) or O,
+                           _code(dtype), act, 0, 0), dev
 
 
 def _ff_inputs(d, x, w_gate, w_up, w_down):
@@ -168,8 +167,7 @@ def _rn_desc(branch, gate, kind, post, eps, residual_scale, branch_scale, residu
 
 def _row_tensor(t, name, shape, dtype, dev):
     """(pointer, row stride)"""
-    _on(t, name, dev, dtype, shape)
-    return t.data_ptr(), _rows(t, name)[2]
+    return t.data_ptr(), _stride(t, name, dev, dtype, shape)
 
 
 def _no_post(post, **vectors):
@@ -280,6 +278,15 @@ def residual_norm_backward(dy, dout, branch, out, stats, *, gate=None, post_weig
 
 # ---- AdamW over many tensors ---------------------------------------------------------
 
+# adamw's table of tensors is filled column by column: words of 8 bytes of an AdamWTensor
+# (a call with 150 tensors spends its time here: 250 us field by field, 140 so)
+_TABLE_WORDS = ctypes.sizeof(AdamWTensor) // 8
+
+
+def _data_ptr(t):
+    return t.data_ptr()
+
+
 class AdamWState:
     """The states of ``adamw`` for a list of tensors, in one buffer each: tensor i's
     elements are at first[i] .. first[i] + sizes[i], every tensor starting at a multiple
@@ -303,6 +310,22 @@ class AdamWState:
         if bits == 8:
             self.exp_avg_scale = torch.zeros(n // _block.BLOCK, device=device)
             self.exp_avg_sq_scale = torch.zeros(n // _block.BLOCK, device=device)
+        self._numel, self._table = n, (None, None)
+
+    def _entries(self, m, v, ms, vs):
+        """The table of tensors with what the state's buffers at these addresses give."""
+        if self._table[0] != (m, v, ms, vs):
+            table = bytearray(len(self.sizes) * _TABLE_WORDS * 8)
+            whole, es = memoryview(table).cast("q"), 1 if self.bits == 8 else 4
+            whole[3::_TABLE_WORDS] = array("q", [m + at * es for at in self.first])
+            whole[4::_TABLE_WORDS] = array("q", [v + at * es for at in self.first])
+            if ms is not None:
+                whole[5::_TABLE_WORDS] = array("q", [ms + at // _block.BLOCK * 4 for at in self.first])
+                whole[6::_TABLE_WORDS] = array("q", [vs + at // _block.BLOCK * 4 for at in self.first])
+                whole[8::_TABLE_WORDS] = array("q", self.first)
+            whole[7::_TABLE_WORDS] = array("q", self.sizes)
+            self._table = (m, v, ms, vs), bytes(table)
+        return bytearray(self._table[1])
 
 
 def adamw_state(params, bits: int = 32) -> AdamWState:
@@ -319,8 +342,8 @@ def adamw_state(params, bits: int = 32) -> AdamWState:
 
 def _state_pointers(state, dev):
     """Pointers of the state's buffers, checked: m, v, and with 8 bits the scales."""
-    n = state.first[-1] + -(-state.sizes[-1] // _block.BLOCK) * _block.BLOCK
     import torch
+    n = state._numel
     types = (torch.int8, torch.uint8) if state.bits == 8 else (torch.float32, torch.float32)
     m, v = (_vector(t, name, n, dev, dtype) for t, name, dtype in (
         (state.exp_avg, "exp_avg", types[0]), (state.exp_avg_sq, "exp_avg_sq", types[1])))
@@ -331,24 +354,16 @@ def _state_pointers(state, dev):
         _vector(state.exp_avg_sq_scale, "exp_avg_sq_scale", k, dev)
 
 
-# the table of tensors is filled column by column: words of 8 bytes of an AdamWTensor
-# (a call with 150 tensors spends its time here: 250 us field by field, 110 so)
-_TABLE_WORDS = ctypes.sizeof(AdamWTensor) // 8
-
-
-def _data_ptr(t):
-    return t.data_ptr()
-
-
 def _checked(tensors, name, sizes, dev):
     """The type codes of contiguous tensors of these sizes on device dev."""
-    codes = []
-    for i, (t, n) in enumerate(zip(tensors, sizes)):
+    known, codes = head._codes, []
+    for t, n in zip(tensors, sizes):
         if t.get_device() != dev:
-            raise ValueError(f"{name}[{i}] must be on the device of params[0]")
+            raise ValueError(f"{name}[{len(codes)}] must be on the device of params[0]")
         if t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be a contiguous tensor of {n} elements, as its state is")
-        codes.append(_code(t.dtype))
+            raise ValueError(f"{name}[{len(codes)}] must be a contiguous tensor of {n} elements, as its state is")
+        code = known.get(t.dtype)
+        codes.append(_code(t.dtype) if code is None else code)
     return codes
 
 
@@ -378,18 +393,13 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
     if count == 0 or len(grads) != count or len(state.sizes) != count:
         raise ValueError("params, grads and state must be of the same, non-zero number of tensors")
     dev = _device(params[0], "params[0]")
-    m, v, ms, vs = _state_pointers(state, dev)
-    words = _TABLE_WORDS
-    table = bytearray(count * words * 8)
+    _code(params[0].dtype)                   # (what the checks below need of torch)
+    words, types = _TABLE_WORDS, _checked(params, "params", state.sizes, dev)
+    table = state._entries(*_state_pointers(state, dev))
     whole, real = memoryview(table).cast("q"), memoryview(table).cast("d")
-
-    def column(k, values):
-        whole[k::words] = array("q", values)
-
-    types = _checked(params, "params", state.sizes, dev), _checked(grads, "grads", state.sizes, dev)
-    column(0, map(_data_ptr, params))
-    column(1, map(_data_ptr, grads))
-    column(9, [p | g << 32 for p, g in zip(*types)])
+    whole[0::words] = array("q", map(_data_ptr, params))
+    whole[1::words] = array("q", map(_data_ptr, grads))
+    whole[9::words] = array("q", [p | g << 32 for p, g in zip(types, _checked(grads, "grads", state.sizes, dev))])
     if copies is not None:
         copies = list(copies)
         if len(copies) != count:
@@ -398,14 +408,6 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
         codes = _checked([copies[i] for i in some], "copies", [state.sizes[i] for i in some], dev)
         for i, code in zip(some, codes):
             whole[i * words + 2], whole[i * words + 10] = copies[i].data_ptr(), code
-    es = 1 if state.bits == 8 else 4
-    column(3, [m + at * es for at in state.first])
-    column(4, [v + at * es for at in state.first])
-    if ms is not None:
-        column(5, [ms + at // _block.BLOCK * 4 for at in state.first])
-        column(6, [vs + at // _block.BLOCK * 4 for at in state.first])
-        column(8, state.first)
-    column(7, state.sizes)
     real[11::words] = array("d", _each(lr, "lr", count))
     real[12::words] = array("d", _each(weight_decay, "weight_decay", count))
     step_ptr = scale_ptr = None
