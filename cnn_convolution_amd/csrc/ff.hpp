@@ -64,8 +64,9 @@ struct FfProduct {
 hipError_t launch_ff_y(const FfProduct &p, int dtype, int tile, hipStream_t s);
 hipError_t launch_ff_dx(const FfProduct &p, int dtype, int tile, hipStream_t s);
 hipError_t launch_ff_dw(const FfProduct &p, int dtype, int tile, hipStream_t s);
-// dx, dw_down and dw_gate with dw_up in one launch, 64 x 64 tiles
-hipError_t launch_ff_all(const FfProduct &dx, const FfProduct &dwd, const FfProduct &dwgu, int dtype, hipStream_t s);
+// dx, dw_down and dw_gate with dw_up in one launch, tiles of 128 or 64
+hipError_t launch_ff_all(const FfProduct &dx, const FfProduct &dwd, const FfProduct &dwgu, int dtype, int tile,
+                         hipStream_t s);
 // the slabs of up to three products added in order
 hipError_t launch_ff_join(const FfProduct *p, int count, int dtype, hipStream_t s);
 

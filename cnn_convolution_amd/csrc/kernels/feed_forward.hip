@@ -319,6 +319,7 @@ struct FfPlan {
     int64_t Dp, Fp, Op, rows_pad, fblocks;
     bool copy_x, copy_g, copy_u, copy_d, copy_y;   // rows not made of 16-byte granules
     int gate_tile, y_tile, y_split, back_tile, dx_tile, dx_split, dd_tile, dd_split, dg_tile, dg_split;
+    int all_tile;            // of dx, dWd, dWg and dWu in one launch, or -1
     int64_t off_x, off_g, off_u, off_d, off_dy, off_h, off_lo, off_slab_x, off_slab_d, off_slab_g, off_grad, off_amax, bytes;
     int64_t pre_bytes;       // of saved, before h
 };
@@ -346,6 +347,54 @@ int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, bo
         }
     }
     return tile;
+}
+
+struct Product {
+    int64_t M, N, stages;
+};
+
+// of a split product's slabs: written, read once more at about 3 TB/s by a launch of
+// their own
+double slab_us(const Product &q, int split) { return 5.0 + double(split) * double(q.M) * double(q.N) * 4 / 3e6; }
+
+// tile and split of a product by itself, and its microseconds
+double pick(const Product &q, int dtype, int *tile, int *split)
+{
+    double best = 1e30;
+    for (int t = 0; t < 3; ++t)
+        for (int sp : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (sp > 1 && (q.stages / sp < 4 || int64_t(sp) * q.M * q.N * 4 > kSlabBytes)) break;
+            const double us = product_us(kShapes[t], q.M, q.N, q.stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
+                              (sp > 1 ? slab_us(q, sp) : 0.0);
+            if (us < best * 0.98) {
+                best = us;
+                *tile = t;
+                *split = sp;
+            }
+        }
+    return best;
+}
+
+// microseconds of three products in one launch of tiles t: what the chip's slots have to
+// do, but at least the longest workgroup; a product's K is split where its workgroups
+// would be longer than that share
+double together_us(int t, const Product (&q)[3], int dtype, int (&split)[3])
+{
+    const TileShape &c = kShapes[t];
+    const double stage = (dtype == 0 ? c.f32 : c.half)[c.per_cu - 1], slots = double(kCus * c.per_cu);
+    const double fixed = c.fixed + double(c.m * c.n) * 7.0 / 65536;
+    double work = 0.0, longest = 0.0, slabs = 0.0;
+    for (const Product &p : q)
+        work += double(ceil_div(p.M, c.m) * ceil_div(p.N, c.n)) * (stage * double(p.stages) + fixed) / slots;
+    for (int k = 0; k < 3; ++k) {
+        split[k] = 1;
+        while (split[k] < 32 && stage * double(q[k].stages) / split[k] > 1.2 * work + 3.0 &&
+               q[k].stages / (2 * split[k]) >= 4 && int64_t(2 * split[k]) * q[k].M * q[k].N * 4 <= kSlabBytes)
+            split[k] *= 2;
+        if (split[k] > 1) slabs += slab_us(q[k], split[k]) - 5.0;
+        longest = std::max(longest, stage * double(ceil_div(q[k].stages, split[k])) + fixed);
+    }
+    return std::max(work, longest) + 0.25 * longest + (slabs > 0.0 ? slabs + 5.0 : 0.0);
 }
 
 FfPlan plan_common(const FfSizes &z)
@@ -391,7 +440,7 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     plan_copies(p, z);
     if (!saved) p.off_h = take(p, p.rows_pad * p.Fp * es);
     p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(saved ? 4 + es / 2 : es / 2), false);
-    pick_product(z.O, z.N, ceil_div(p.Fp, ki), z.dtype, 0, &p.y_tile, &p.y_split);
+    pick(Product{z.O, z.N, ceil_div(p.Fp, ki)}, z.dtype, &p.y_tile, &p.y_split);
     if (p.y_split > 1) p.off_slab_x = take(p, p.y_split * z.N * z.O * 4);
     return p;
 }
@@ -406,9 +455,22 @@ FfPlan plan_bwd(const FfSizes &z)
     p.off_grad = take(p, p.rows_pad * 2 * p.Fp * es);
     p.off_amax = take(p, kAmaxParts * 4);
     p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), true);
-    pick_product(z.D, z.N, 2 * ceil_div(z.F, ki), z.dtype, 0, &p.dx_tile, &p.dx_split);
-    pick_product(z.F, z.O, ceil_div(z.N, ki), z.dtype, 0, &p.dd_tile, &p.dd_split);
-    pick_product(z.D, 2 * z.F, ceil_div(z.N, ki), z.dtype, 0, &p.dg_tile, &p.dg_split);
+    const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki)}, dd{z.F, z.O, ceil_div(z.N, ki)}, dg{z.D, 2 * z.F, dd.stages};
+    double apart = 0.0;
+    apart += pick(dx, z.dtype, &p.dx_tile, &p.dx_split);
+    apart += pick(dd, z.dtype, &p.dd_tile, &p.dd_split);
+    apart += pick(dg, z.dtype, &p.dg_tile, &p.dg_split);
+    p.all_tile = -1;
+    for (int t : {kTile128, kTile64}) {
+        int split[3];
+        const double us = together_us(t, {dx, dd, dg}, z.dtype, split);
+        if (us > apart * 0.95) continue;
+        apart = us;
+        p.all_tile = t;
+        p.dx_split = split[0];
+        p.dd_split = split[1];
+        p.dg_split = split[2];
+    }
     if (p.dx_split > 1) p.off_slab_x = take(p, p.dx_split * z.N * z.D * 4);
     if (p.dd_split > 1) p.off_slab_d = take(p, p.dd_split * z.O * z.F * 4);
     if (p.dg_split > 1) p.off_slab_g = take(p, p.dg_split * 2 * z.F * z.D * 4);
@@ -628,8 +690,8 @@ hipError_t launch_ff_bwd(const FfArgs &a, hipStream_t s)
     dd.out[0] = a.dwd;
     dd.ldo = z.F;
 
-    if (p.dx_tile == kTile64 && p.dd_tile == kTile64 && p.dg_tile == kTile64) {
-        if ((e = launch_ff_all(dx, dd, dg, z.dtype, s)) != hipSuccess) return e;
+    if (p.all_tile >= 0) {
+        if ((e = launch_ff_all(dx, dd, dg, z.dtype, p.all_tile, s)) != hipSuccess) return e;
     } else {
         if ((e = launch_ff_dx(dx, z.dtype, p.dx_tile, s)) != hipSuccess) return e;
         if ((e = launch_ff_dw(dd, z.dtype, p.dd_tile, s)) != hipSuccess) return e;
