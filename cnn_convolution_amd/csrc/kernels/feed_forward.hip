@@ -332,7 +332,7 @@ int64_t take(FfPlan &p, int64_t bytes)
 }
 
 // tile of a product that is not split (back: of dh, else of the gate)
-int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, bool back)
+int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, int saved_bytes, bool back)
 {
     double best = 1e30;
     int tile = 0;
@@ -340,7 +340,10 @@ int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, bo
         if (t == kTile32K && (!back || dtype)) continue;
         if (t == kTile64x32 && N > 64) continue;       // (W would be read three times and more)
         const int64_t own = t == kTile32K ? ceil_div(stages, 4) : stages;
-        const double us = product_us(kShapes[t], M, N, own, 1, dtype, out_bytes);
+        // what is saved goes out at the chip's rate, hidden by nothing: all workgroups
+        // store at once (4097 x 1032 x 3001, fp16, tiles of 256 95 us, of 128 114)
+        const double us = product_us(kShapes[t], M, N, own, 1, dtype, out_bytes) +
+                          double(M) * double(N) * saved_bytes / 5e6;
         if (us < best * 0.98) {
             best = us;
             tile = t;
@@ -439,7 +442,7 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     }
     plan_copies(p, z);
     if (!saved) p.off_h = take(p, p.rows_pad * p.Fp * es);
-    p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(saved ? 4 + es / 2 : es / 2), false);
+    p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(es / 2), saved ? 4 : 0, false);
     pick(Product{z.O, z.N, ceil_div(p.Fp, ki)}, z.dtype, &p.y_tile, &p.y_split);
     if (p.y_split > 1) p.off_slab_x = take(p, p.y_split * z.N * z.O * 4);
     return p;
@@ -454,7 +457,7 @@ FfPlan plan_bwd(const FfSizes &z)
     if (p.copy_y) p.off_dy = take(p, z.N * p.Op * es);
     p.off_grad = take(p, p.rows_pad * 2 * p.Fp * es);
     p.off_amax = take(p, kAmaxParts * 4);
-    p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), true);
+    p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), 0, true);
     const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki)}, dd{z.F, z.O, ceil_div(z.N, ki)}, dg{z.D, 2 * z.F, dd.stages};
     double apart = 0.0;
     apart += pick(dx, z.dtype, &p.dx_tile, &p.dx_split);
