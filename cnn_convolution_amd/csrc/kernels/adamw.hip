@@ -11,7 +11,7 @@
 // once to the code for its tensor's, so that all loads go out together.
 //
 // 8-bit states: m, v and the scales are formed in fp64, so that the level that an element
-// gets is the definition's whatever the order of operations. A value in units of its
+// gets is the definition's but for fp64's own roundings. A value in units of its
 // block's scale, x = |m| 127^2 / M or v 255^4 / V, lies between c^2 and (c + 1)^2 (fourth
 // powers for v), and goes to the upper one if 65536 times its share of the interval
 // exceeds its number u. fp32 decides that (c from square roots) unless the two are within
