@@ -93,53 +93,62 @@ __device__ __forceinline__ int exact_level4(double x, uint32_t u)
     return min(c + int(up), 255);
 }
 
-// The same in fp32, with whether it is sure. x is within 3 roundings and a reciprocal's
-// ulp (3e-7 of it) of the exact one, d and with it 65536 d within what `err` says; next to an end of the
-// interval, where the exact x may lie in the next one, u decides alike in both unless
-// it is within 16 of its own ends (err is less than 2 of its steps).
-__device__ __forceinline__ bool sure_at(float d, float width, float err, float lhs, float rhs, uint32_t u)
+// The same in fp32: the level, and in `least` the least of what decides it less the error
+// of that (of 65536 times the value's share of its interval, `width` wide, against u).
+// x is within 3 roundings and a reciprocal's ulp (3e-7 of it) of the exact one, so the
+// error is less than 2 of u's steps. Next to an end of the interval, where the exact x may
+// lie in the next one, both decide alike unless u is within 2 of its own ends; those are
+// left to fp64 too (one wave in thirty has some).
+__device__ __forceinline__ float level2(float x, float u, float &least)
 {
-    const float e = err * (1.f / 65536);
-    return fabsf(lhs - rhs) > err && ((d >= e && width - d >= e) || u - 16u < 65504u);
+    const float c = floorf(__builtin_amdgcn_sqrtf(x));
+    const float d = __builtin_fmaf(-c, c, x), width = __builtin_fmaf(2.f, c, 1.f);
+    const float over = d * 65536.f - u * width;                  // the product is exact
+    least = fminf(least, fabsf(over) - x * (3.6e-7f * 65536.f));
+    return fminf(c + (over > 0.f ? 1.f : 0.f), 127.f);
 }
-__device__ __forceinline__ int level2(float x, uint32_t u, bool &sure)
+__device__ __forceinline__ float level4(float x, float u, float &least)
 {
-    const int c = int(__builtin_amdgcn_sqrtf(x));
-    const float d = x - float(c * c), width = float(2 * c + 1);
-    const float lhs = d * 65536.f, rhs = float(u) * width;       // below 2^24
-    sure = sure_at(d, width, x * (3.6e-7f * 65536.f), lhs, rhs, u);
-    return min(c + int(lhs > rhs), 127);
-}
-__device__ __forceinline__ int level4(float x, uint32_t u, bool &sure)
-{
-    const uint32_t c = min(uint32_t(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(x))), 255u);
-    const uint32_t lo = c * c * (c * c), hi = (c + 1) * (c + 1) * ((c + 1) * (c + 1));   // 256^4 wraps to 0
-    const float d = x - float(lo), width = float(hi - lo);
-    const float lhs = d * 65536.f, rhs = float(u) * width;
-    sure = sure_at(d, width, x * (4.2e-7f * 65536.f) + rhs * 1.5e-7f, lhs, rhs, u);
-    return int(min(c + uint32_t(lhs > rhs), 255u));
+    const float c = fminf(floorf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(x))), 255.f), s = c * c;
+    const float d = __builtin_fmaf(-s, s, x);
+    const float width = __builtin_fmaf(c, __builtin_fmaf(c, __builtin_fmaf(c, 4.f, 6.f), 4.f), 1.f);
+    const float rhs = u * width, over = d * 65536.f - rhs;
+    least = fminf(least, fabsf(over) - (x * (4.2e-7f * 65536.f) + rhs * 3e-7f));
+    return fminf(c + (over > 0.f ? 1.f : 0.f), 255.f);
 }
 
-__device__ __forceinline__ double value2(int k, double unit) { return double(k * abs(k)) * unit; }
-__device__ __forceinline__ double value4(uint32_t k, double unit) { return double(k * k * (k * k)) * unit; }
+__device__ __forceinline__ double value2(int k, double unit)
+{
+    const float f = float(k);
+    return double(f * fabsf(f)) * unit;        // the square is exact
+}
+__device__ __forceinline__ double value4(uint32_t k, double unit)
+{
+    const float f = float(k);
+    const double s = double(f * f);
+    return s * s * unit;
+}
 
-// A lane's elements of a tensor, from its element i on; WHOLE: all of them exist, in all of the
-// workgroup's lanes
+// A lane's elements of the chunk that begins at element `first` of a tensor; WHOLE: all of
+// them exist, in all of the workgroup's lanes
 template <int BITS, bool WHOLE, typename P, typename G>
-__device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTensor &t, int64_t i, int64_t step, float gs,
-                                               const float4 &f)
+__device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTensor &t, int64_t first, int64_t step,
+                                               float gs, const float4 &f)
 {
     constexpr int kLane = kLaneOf<BITS>;
-    const int64_t left = WHOLE ? kLane : max(t.n - i, int64_t(0));
+    const uint32_t i = threadIdx.x * kLane;
+    P *const pp = static_cast<P *>(t.p) + first;
+    const G *const pg = static_cast<const G *>(t.g) + first;
+    const int left = WHOLE ? kLane : int(max(min(t.n - first, adam_chunk(BITS)) - int64_t(i), int64_t(0)));
     float p[kLane], g[kLane], m[kLane], v[kLane];
     Raw<P, kLane> rp;
     Raw<G, kLane> rg;
     if constexpr (WHOLE) {
-        rp = load_raw<P, kLane>(static_cast<const P *>(t.p) + i);
-        rg = load_raw<G, kLane>(static_cast<const G *>(t.g) + i);
+        rp = load_raw<P, kLane>(pp + i);
+        rg = load_raw<G, kLane>(pg + i);
     } else {
-        load_some<kLane>(static_cast<const P *>(t.p) + i, left, p);
-        load_some<kLane>(static_cast<const G *>(t.g) + i, left, g);
+        load_some<kLane>(pp + i, left, p);
+        load_some<kLane>(pg + i, left, g);
     }
     const auto unpack = [&] {
 #pragma unroll
@@ -152,9 +161,9 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
         }
     };
     if constexpr (BITS == 32) {
-        float *pm = static_cast<float *>(t.m) + i, *pv = static_cast<float *>(t.v) + i;
-        load_some<kLane>(pm, left, m);
-        load_some<kLane>(pv, left, v);
+        float *pm = static_cast<float *>(t.m) + first, *pv = static_cast<float *>(t.v) + first;
+        load_some<kLane>(pm + i, left, m);
+        load_some<kLane>(pv + i, left, v);
         unpack();
         const float b1 = float(a.beta1), b2 = float(a.beta2), r1 = float(1.0 - a.beta1), r2 = float(1.0 - a.beta2);
 #pragma unroll
@@ -162,31 +171,32 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
             m[e] = b1 * m[e] + r1 * g[e];
             v[e] = b2 * v[e] + r2 * (g[e] * g[e]);
         }
-        store_some<kLane>(pm, left, m);
-        store_some<kLane>(pv, left, v);
+        store_some<kLane>(pm + i, left, m);
+        store_some<kLane>(pv + i, left, v);
     } else {
         // codes and scales; lanes past the tensor's end hold zeros, whole blocks past it
         // have no scale
-        int8_t *pm = static_cast<int8_t *>(t.m) + i;
-        uint8_t *pv = static_cast<uint8_t *>(t.v) + i;
-        const bool any = WHOLE || i / 256 * 256 < t.n;
+        int8_t *pm = static_cast<int8_t *>(t.m) + first;
+        uint8_t *pv = static_cast<uint8_t *>(t.v) + first;
+        const bool any = WHOLE || first + i / 256 * 256 < t.n;
+        float *const ps = t.ms + first / 256, *const pz = t.vs + first / 256;
         float sm = 0.f, sv = 0.f;
         if (any) {
-            sm = t.ms[i / 256];
-            sv = t.vs[i / 256];
+            sm = ps[i / 256];
+            sv = pz[i / 256];
         }
         uint32_t cm = 0, cv = 0;
         if (WHOLE || left >= kLane) {
-            cm = *reinterpret_cast<const uint32_t *>(pm);
-            cv = *reinterpret_cast<const uint32_t *>(pv);
+            cm = *reinterpret_cast<const uint32_t *>(pm + i);
+            cv = *reinterpret_cast<const uint32_t *>(pv + i);
         } else {
             for (int e = 0; e < left; ++e) {
-                cm |= uint32_t(uint8_t(pm[e])) << (8 * e);
-                cv |= uint32_t(pv[e]) << (8 * e);
+                cm |= uint32_t(uint8_t(pm[i + e])) << (8 * e);
+                cv |= uint32_t(pv[i + e]) << (8 * e);
             }
         }
         // the numbers while the loads are on their way
-        const uint4 word = philox(uint64_t(t.first + i) / 4, uint64_t(step), a.seed);
+        const uint4 word = philox(uint64_t(t.first + first) / 4 + threadIdx.x, uint64_t(step), a.seed);
         const uint32_t w[kLane] = {word.x, word.y, word.z, word.w};
         unpack();
         const double um = a.beta1 * (double(sm) * kUnitM), uv = a.beta2 * (double(sv) * kUnitV);
@@ -203,57 +213,58 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
             m[e] = float(md[e]);
             v[e] = float(vd[e]);
             tm = max(tm, __float_as_uint(m[e]) & 0x7fffffffu);
-            tv = max(tv, __float_as_uint(v[e]) & 0x7fffffffu);
+            tv = max(tv, __float_as_uint(v[e]));       // never negative
         }
         tm = wave_max(tm);
         tv = wave_max(tv);
         constexpr uint32_t INF = 0x7f800000u;
-        const bool bad = tm >= INF || tv >= INF;
-        sm = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(tm);
-        sv = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(tv);
-        const float fm = sm > 0.f ? float(kTopM) * __builtin_amdgcn_rcpf(sm) : 0.f;
-        const float fv = sv > 0.f ? float(kTopV) * __builtin_amdgcn_rcpf(sv) : 0.f;
-        // a scale so small that its reciprocal leaves fp32 (or the scale its normal
-        // numbers) is fp64's affair
-        const bool tiny = (sm > 0.f && !(sm > 1e-30f)) || (sv > 0.f && !(sv > 1e-26f));
-        int km[kLane], kv[kLane];
-        uint32_t unsure = 0;
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            bool sure_m, sure_v;
-            km[e] = level2(fabsf(m[e]) * fm, w[e] & 0xffffu, sure_m);
-            kv[e] = level4(v[e] * fv, w[e] >> 16, sure_v);
-            unsure |= uint32_t(tiny || !(sure_m && sure_v)) << e;
-        }
-        if (unsure) {
-            const double xm = sm > 0.f ? kTopM / double(sm) : 0.0, xv = sv > 0.f ? kTopV / double(sv) : 0.0;
-#pragma unroll
-            for (int e = 0; e < kLane; ++e)
-                if (unsure >> e & 1) {
-                    km[e] = exact_level2(fabs(md[e]) * xm, w[e] & 0xffffu);
-                    kv[e] = exact_level4(vd[e] * xv, w[e] >> 16);
-                }
-        }
         cm = cv = 0;
+        if (tm >= INF || tv >= INF) {
+            sm = sv = __uint_as_float(0x7fc00000u);
+        } else {
+            sm = __uint_as_float(tm);
+            sv = __uint_as_float(tv);
+            const float fm = sm > 0.f ? float(kTopM) * __builtin_amdgcn_rcpf(sm) : 0.f;
+            const float fv = sv > 0.f ? float(kTopV) * __builtin_amdgcn_rcpf(sv) : 0.f;
+            float km[kLane], kv[kLane], least = 1.f;
+            uint32_t lowest = 65535, highest = 0;
 #pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            const int q = bad ? 0 : m[e] < 0.f ? -km[e] : km[e];
-            const int r = bad || !(vd[e] > 0.0) ? 0 : max(kv[e], 1);
-            cm |= uint32_t(uint8_t(q)) << (8 * e);
-            cv |= uint32_t(uint8_t(r)) << (8 * e);
+            for (int e = 0; e < kLane; ++e) {
+                const uint32_t um16 = w[e] & 0xffffu, uv16 = w[e] >> 16;
+                km[e] = level2(fabsf(m[e]) * fm, float(um16), least);
+                kv[e] = level4(v[e] * fv, float(uv16), least);
+                lowest = min(lowest, min(um16, uv16));
+                highest = max(highest, max(um16, uv16));
+            }
+            // (a scale so small that its reciprocal leaves fp32, or the scale its normal
+            // numbers, is fp64's affair)
+            const bool tiny = (sm > 0.f && !(sm > 1e-30f)) || (sv > 0.f && !(sv > 1e-26f));
+            if (!(least > 0.f) || lowest < 2 || highest > 65533 || tiny) {
+                const double xm = sm > 0.f ? kTopM / double(sm) : 0.0, xv = sv > 0.f ? kTopV / double(sv) : 0.0;
+#pragma unroll
+                for (int e = 0; e < kLane; ++e) {
+                    km[e] = float(exact_level2(fabs(md[e]) * xm, w[e] & 0xffffu));
+                    kv[e] = float(exact_level4(vd[e] * xv, w[e] >> 16));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) {
+                cm |= (uint32_t(int(copysignf(km[e], m[e]))) & 0xffu) << (8 * e);
+                cv |= uint32_t(vd[e] > 0.0 ? fmaxf(kv[e], 1.f) : 0.f) << (8 * e);
+            }
         }
         if (WHOLE || left >= kLane) {
-            *reinterpret_cast<uint32_t *>(pm) = cm;
-            *reinterpret_cast<uint32_t *>(pv) = cv;
+            *reinterpret_cast<uint32_t *>(pm + i) = cm;
+            *reinterpret_cast<uint32_t *>(pv + i) = cv;
         } else {
             for (int e = 0; e < left; ++e) {
-                pm[e] = int8_t(cm >> (8 * e));
-                pv[e] = uint8_t(cv >> (8 * e));
+                pm[i + e] = int8_t(cm >> (8 * e));
+                pv[i + e] = uint8_t(cv >> (8 * e));
             }
         }
         if (any && (threadIdx.x & 63) == 0) {
-            t.ms[i / 256] = sm;
-            t.vs[i / 256] = sv;
+            ps[i / 256] = sm;
+            pz[i / 256] = sv;
         }
     }
     // With 8 bits the arithmetic is what a step waits for: the hardware's square root and
@@ -267,9 +278,9 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
 #pragma unroll
         for (int e = 0; e < kLane; ++e) p[e] = p[e] * f.x - f.y * m[e] / (sqrtf(v[e]) * f.z + f.w);
     }
-    store_some<kLane>(static_cast<P *>(t.p) + i, left, p);
+    store_some<kLane>(pp + i, left, p);
     if (t.copy)
-        with_type(t.ct, [&](auto z) { store_some<kLane>(static_cast<decltype(z) *>(t.copy) + i, left, p); });
+        with_type(t.ct, [&](auto z) { store_some<kLane>(static_cast<decltype(z) *>(t.copy) + first + i, left, p); });
 }
 
 template <int BITS>
@@ -298,13 +309,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a)
     const float lr = t.lr * (a.lr_ptr ? *a.lr_ptr : 1.f), gs = a.grad_scale * (a.grad_scale_ptr ? *a.grad_scale_ptr : 1.f);
     // p keep - rate m / (sqrt(v) root + eps)
     const float4 f{float(1.0 - double(lr) * double(t.decay)), float(double(lr) * rate), root, a.eps};
-    const int64_t i = first + threadIdx.x * kLaneOf<BITS>;
     with_type(t.pt, [&](auto p) {
         with_type(t.gt, [&](auto g) {
             if (first + adam_chunk(BITS) <= t.n)
-                adamw_elements<BITS, true, decltype(p), decltype(g)>(a, t, i, step, gs, f);
+                adamw_elements<BITS, true, decltype(p), decltype(g)>(a, t, first, step, gs, f);
             else
-                adamw_elements<BITS, false, decltype(p), decltype(g)>(a, t, i, step, gs, f);
+                adamw_elements<BITS, false, decltype(p), decltype(g)>(a, t, first, step, gs, f);
         });
     });
 }

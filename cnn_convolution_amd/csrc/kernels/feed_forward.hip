@@ -181,6 +181,15 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
     int64_t s = steps * wave / WAVES;
     const int64_t end = steps * (wave + 1) / WAVES;
     floatx4_t acc[2][NB] = {};
+    // the step that K ends in, by the wave that has it: its loads go out first
+    uint4 tg{}, tu{}, tx[NB] = {};
+    const bool tail = end > whole;
+    if (tail) {
+        tg = wg.end(whole * KF + q, a.D);
+        tu = wu.end(whole * KF + q, a.D);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) tx[b] = x[b].end(whole * KF + q, a.D);
+    }
     // the loads of U steps at a time; in the last batch past the wave's last step that
     // one again, unused
     const int64_t last = min(end, whole) - 1;
@@ -207,15 +216,12 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
     };
     for (; s + U - 1 <= last; s += U) batch(std::true_type{});
     if (s <= last) batch(std::false_type{});
-    if (end > whole) {                         // the step that K ends in
-        const uint4 g = wg.end(whole * KF + q, a.D), u = wu.end(whole * KF + q, a.D);
+    if (tail)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint4 xf = x[b].end(whole * KF + q, a.D);
-            acc[0][b] = mfma_half<T>(g, xf, acc[0][b]);
-            acc[1][b] = mfma_half<T>(u, xf, acc[1][b]);
+            acc[0][b] = mfma_half<T>(tg, tx[b], acc[0][b]);
+            acc[1][b] = mfma_half<T>(tu, tx[b], acc[1][b]);
         }
-    }
     floatx4_t sum[2];
     join_parts<WAVES, 2, NB>(acc, sum, part);
     if (wave >= NB) return;
@@ -268,6 +274,16 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_down_kernel(const FfRows a
     int64_t s = steps * wave / WAVES;
     const int64_t end = steps * (wave + 1) / WAVES;
     floatx4_t acc[1][NB] = {};
+    uint4 tw{}, th[NB] = {}, tl[NB] = {};
+    const bool tail = end > whole;
+    if (tail) {
+        tw = w.end(whole * KF + q, a.F);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            th[b] = hi[b].end(whole * KF + q, a.Fp);
+            if (HALF) tl[b] = lo[b].end(whole * KF + q, a.Fp);
+        }
+    }
     const int64_t last = min(end, whole) - 1;
     auto batch = [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
@@ -294,14 +310,12 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_down_kernel(const FfRows a
     };
     for (; s + U - 1 <= last; s += U) batch(std::true_type{});
     if (s <= last) batch(std::false_type{});
-    if (end > whole) {
-        const uint4 wf = w.end(whole * KF + q, a.F);
+    if (tail)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            acc[0][b] = mfma_half<T>(wf, hi[b].end(whole * KF + q, a.Fp), acc[0][b]);
-            if (HALF) acc[0][b] = mfma_half<T>(wf, lo[b].end(whole * KF + q, a.Fp), acc[0][b]);
+            acc[0][b] = mfma_half<T>(tw, th[b], acc[0][b]);
+            if (HALF) acc[0][b] = mfma_half<T>(tw, tl[b], acc[0][b]);
         }
-    }
     floatx4_t sum[1];
     join_parts<WAVES, 1, NB>(acc, sum, part);
     const int64_t row = (blockIdx.y * NB + wave) * 16 + (lane & 15), m = o0 + (lane >> 4) * 4;
@@ -535,13 +549,13 @@ FfSaved saved_of(const FfPlan &p, const void *saved, void *h)
 template <typename T, int NB, bool ODD>
 hipError_t launch_rows(const FfRows &a, int64_t nb, hipStream_t s)
 {
-    constexpr int DOWN = NB == 1 ? 16 : 8;
+    constexpr int GATE = NB == 1 ? 8 : 4, DOWN = NB == 1 ? 16 : 8;
     const dim3 gate(unsigned(ceil_div(a.F, 16)), unsigned(ceil_div(nb, NB)));
     const dim3 down(unsigned(ceil_div(a.O, 16)), gate.y);
     if (a.to.pre)
-        hipLaunchKernelGGL((ff_rows_gate_kernel<T, 4, NB, true, ODD>), gate, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((ff_rows_gate_kernel<T, GATE, NB, true, ODD>), gate, dim3(GATE * 64), 0, s, a);
     else
-        hipLaunchKernelGGL((ff_rows_gate_kernel<T, 4, NB, false, ODD>), gate, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((ff_rows_gate_kernel<T, GATE, NB, false, ODD>), gate, dim3(GATE * 64), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((ff_rows_down_kernel<T, DOWN, NB, ODD>), down, dim3(DOWN * 64), 0, s, a);
