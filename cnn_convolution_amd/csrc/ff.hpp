@@ -79,6 +79,7 @@ struct FfRows {
     FfSaved to;
     void *lo, *y;
     int act;
+    int blocks;              // of 16 rows to write
 };
 
 }  // namespace im2win

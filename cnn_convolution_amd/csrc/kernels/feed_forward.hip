@@ -224,8 +224,11 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
         }
     floatx4_t sum[2];
     join_parts<WAVES, 2, NB>(acc, sum, part);
-    if (wave >= NB) return;
-    const int rb = blockIdx.y * NB + wave;     // block of rows
+    // waves past the blocks of rows that there are leave the zeros of those that there are not
+    if (wave >= NB && (!SAVE || blockIdx.y > 0)) return;
+    const int rb = (wave < NB ? blockIdx.y : gridDim.y - 1) * NB + wave;     // block of rows
+    if (rb >= a.blocks) return;
+    if (wave >= NB) sum[0] = sum[1] = floatx4_t{};
     const int64_t row = rb * 16 + (lane & 15), m = f0 + (lane >> 4) * 4;
     float h[4];
 #pragma unroll
@@ -352,7 +355,9 @@ int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, in
     int tile = 0;
     for (int t = 0; t < 5; ++t) {
         if (t == kTile32K && (!back || dtype)) continue;
-        if (t == kTile64x32 && N > 64) continue;       // (W would be read three times and more)
+        // W would be read three times and more; Wd's columns take twice the time in tiles
+        // of 32 rows (24 rows, 2048 outputs, 8192 hidden features, bf16: 13 us, 21)
+        if (t == kTile64x32 && (back || N > 64)) continue;
         const int64_t own = t == kTile32K ? ceil_div(stages, 4) : stages;
         // what is saved goes out at the chip's rate, hidden by nothing: all workgroups
         // store at once (4097 x 1032 x 3001, fp16, tiles of 256 95 us, of 128 114)
@@ -368,11 +373,14 @@ int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, in
 
 struct Product {
     int64_t M, N, stages;
+    int64_t outs;            // N: rows of each
+
+    int64_t rows(const TileShape &t) const { return outs > 1 ? outs * round_up(N, t.n) : N; }
 };
 
 // of a split product's slabs: written, read once more at about 3 TB/s by a launch of
 // their own
-double slab_us(const Product &q, int split) { return 5.0 + double(split) * double(q.M) * double(q.N) * 4 / 3e6; }
+double slab_us(const Product &q, int split) { return 5.0 + double(split) * double(q.M) * double(q.N * q.outs) * 4 / 3e6; }
 
 // tile and split of a product by itself, and its microseconds
 double pick(const Product &q, int dtype, int *tile, int *split)
@@ -380,8 +388,8 @@ double pick(const Product &q, int dtype, int *tile, int *split)
     double best = 1e30;
     for (int t = 0; t < 3; ++t)
         for (int sp : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-            if (sp > 1 && (q.stages / sp < 4 || int64_t(sp) * q.M * q.N * 4 > kSlabBytes)) break;
-            const double us = product_us(kShapes[t], q.M, q.N, q.stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
+            if (sp > 1 && (q.stages / sp < 4 || int64_t(sp) * q.M * q.N * q.outs * 4 > kSlabBytes)) break;
+            const double us = product_us(kShapes[t], q.M, q.rows(kShapes[t]), q.stages, sp, dtype, sp > 1 ? 4 : int(elem(dtype))) +
                               (sp > 1 ? slab_us(q, sp) : 0.0);
             if (us < best * 0.98) {
                 best = us;
@@ -402,11 +410,11 @@ double together_us(int t, const Product (&q)[3], int dtype, int (&split)[3])
     const double fixed = c.fixed + double(c.m * c.n) * 7.0 / 65536;
     double work = 0.0, longest = 0.0, slabs = 0.0;
     for (const Product &p : q)
-        work += double(ceil_div(p.M, c.m) * ceil_div(p.N, c.n)) * (stage * double(p.stages) + fixed) / slots;
+        work += double(ceil_div(p.M, c.m) * ceil_div(p.rows(c), c.n)) * (stage * double(p.stages) + fixed) / slots;
     for (int k = 0; k < 3; ++k) {
         split[k] = 1;
         while (split[k] < 32 && stage * double(q[k].stages) / split[k] > 1.2 * work + 3.0 &&
-               q[k].stages / (2 * split[k]) >= 4 && int64_t(2 * split[k]) * q[k].M * q[k].N * 4 <= kSlabBytes)
+               q[k].stages / (2 * split[k]) >= 4 && int64_t(2 * split[k]) * q[k].M * q[k].N * q[k].outs * 4 <= kSlabBytes)
             split[k] *= 2;
         if (split[k] > 1) slabs += slab_us(q[k], split[k]) - 5.0;
         longest = std::max(longest, stage * double(ceil_div(q[k].stages, split[k])) + fixed);
@@ -457,7 +465,7 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     plan_copies(p, z);
     if (!saved) p.off_h = take(p, p.rows_pad * p.Fp * es);
     p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(es / 2), saved ? 4 : 0, false);
-    pick(Product{z.O, z.N, ceil_div(p.Fp, ki)}, z.dtype, &p.y_tile, &p.y_split);
+    pick(Product{z.O, z.N, ceil_div(p.Fp, ki), 1}, z.dtype, &p.y_tile, &p.y_split);
     if (p.y_split > 1) p.off_slab_x = take(p, p.y_split * z.N * z.O * 4);
     return p;
 }
@@ -472,7 +480,7 @@ FfPlan plan_bwd(const FfSizes &z)
     p.off_grad = take(p, p.rows_pad * 2 * p.Fp * es);
     p.off_amax = take(p, kAmaxParts * 4);
     p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), 0, true);
-    const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki)}, dd{z.F, z.O, ceil_div(z.N, ki)}, dg{z.D, 2 * z.F, dd.stages};
+    const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki), 1}, dd{z.F, z.O, ceil_div(z.N, ki), 1}, dg{z.D, z.F, dd.stages, 2};
     double apart = 0.0;
     apart += pick(dx, z.dtype, &p.dx_tile, &p.dx_split);
     apart += pick(dd, z.dtype, &p.dd_tile, &p.dd_split);
@@ -562,13 +570,13 @@ hipError_t launch_rows(const FfRows &a, int64_t nb, hipStream_t s)
     return hipGetLastError();
 }
 
-// rows: with `saved` h's zero rows up to rows_pad are written too. Weights that few
+// Weights that few
 // workgroups read are read again for each block of rows, by workgroups of its own (64
 // rows, 512 inputs, 1024 hidden features, fp32: h 6.8 us, 11.8 with 64 rows a workgroup;
 // 2048 inputs, 4096 hidden features 79 and 74 us in all).
-hipError_t launch_rows(const FfRows &a, int dtype, int64_t rows, hipStream_t s)
+hipError_t launch_rows(const FfRows &a, int dtype, hipStream_t s)
 {
-    const int64_t nb = ceil_div(rows, 16);
+    const int64_t nb = ceil_div(a.N, 16);
     return with_ff_type(dtype, [&](auto t) {
         using T = decltype(t);
         const auto blocks = [&](auto odd) {
@@ -607,8 +615,8 @@ hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s)
     const FfSaved to = saved_of(p, a.saved, ws + p.off_h);
     if (p.few)
         return launch_rows(FfRows{a.x, a.wg, a.wu, a.wd, z.ldx, z.ldg, z.ldu, z.ldd, z.ldy, z.N, z.D, z.F, z.O, p.Fp, to,
-                                  ws + p.off_lo, a.y, z.act},
-                           z.dtype, a.saved ? p.rows_pad : z.N, s);
+                                  ws + p.off_lo, a.y, z.act, int(ceil_div(a.saved ? p.rows_pad : z.N, 16))},
+                           z.dtype, s);
     FfRead r{};
     hipError_t e = launch_pads(p, a, false, &r, s);
     if (e != hipSuccess) return e;

@@ -287,7 +287,6 @@ hipError_t launch_ff_back(const FfBack &a, int dtype, int tile, hipStream_t s)
         switch (tile) {
         case kTile256: return launch_back<T, C256>(a, s);
         case kTile128: return launch_back<T, C128>(a, s);
-        case kTile64x32: return launch_back<T, C64x32>(a, s);
         case kTile32K:
             // (a tile of 32 columns in half precision has too few granules for the
             // transposed reads)
