@@ -80,6 +80,9 @@ struct FfRows {
     void *lo, *y;
     int act;
     int blocks;              // of 16 rows to write
+    float *slab;             // y's sums over parts of K, where it is split
+    int *count;              // [counts] of parts that are there, cleared by the gate's launch
+    int counts;
 };
 
 }  // namespace im2win

@@ -168,6 +168,8 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
 {
     constexpr int KF = kFragK<T>, U = 4;       // fragments in flight per matrix
     __shared__ floatx4_t part[WAVES * 2 * NB * 64];
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < a.counts; i += WAVES * 64) a.count[i] = 0;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t f0 = int64_t(blockIdx.x) * 16, f = min(f0 + (lane & 15), a.F - 1);
     Row<T, ODD> wg, wu, x[NB];
@@ -274,8 +276,9 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_down_kernel(const FfRows a
         lo[b].init(static_cast<const T *>(a.lo) + at);
     }
     const int64_t steps = (a.F + KF - 1) / KF, whole = a.F / KF;
-    int64_t s = steps * wave / WAVES;
-    const int64_t end = steps * (wave + 1) / WAVES;
+    const int turn = blockIdx.z * WAVES + wave, turns = gridDim.z * WAVES;
+    int64_t s = steps * turn / turns;
+    const int64_t end = steps * (turn + 1) / turns;
     floatx4_t acc[1][NB] = {};
     uint4 tw{}, th[NB] = {}, tl[NB] = {};
     const bool tail = end > whole;
@@ -321,18 +324,55 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_down_kernel(const FfRows a
         }
     floatx4_t sum[1];
     join_parts<WAVES, 1, NB>(acc, sum, part);
+    if (gridDim.z > 1) {
+        // the workgroup that comes last adds all parts, in their order. Parts pass the L2
+        // caches (stores and loads of the device's scope, the count taken once the stores
+        // are done): a fence that writes a whole L2 back takes 100 us and more here
+        __shared__ int last_one;
+        const int64_t tile = blockIdx.y * int64_t(gridDim.x) + blockIdx.x, tiles = int64_t(gridDim.x) * gridDim.y;
+        float *slab = a.slab + (tile * NB + wave) * 256 + lane;
+        const int64_t part_step = tiles * NB * 256;
+        if (wave < NB) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                __hip_atomic_store(slab + blockIdx.z * part_step + v * 64, sum[0][v], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last_one = __hip_atomic_fetch_add(a.count + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                       int(gridDim.z) - 1;
+        __syncthreads();
+        if (!last_one || wave >= NB) return;
+        sum[0] = floatx4_t{};
+        for (unsigned p = 0; p < gridDim.z; ++p)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                sum[0][v] += __hip_atomic_load(slab + p * part_step + v * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     const int64_t row = (blockIdx.y * NB + wave) * 16 + (lane & 15), m = o0 + (lane >> 4) * 4;
     if (wave >= NB || row >= a.N) return;
     const float y[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
     store_some<4>(static_cast<T *>(a.y) + row * a.ldy + m, a.O - m, y);
 }
 
+// workgroups up to which each block of rows has workgroups of its own, which read the same
+// weights again (64 rows, fp32, 512 inputs, 1024 hidden features, 256 of them: h 6.8 us,
+// 11.8 with 64 rows a workgroup; 2048 inputs, 4096 hidden features, 1024: 79 us in all, 74)
 constexpr int64_t kRowsGroups = 512;
+// parts of y's K: as many as leave at most a workgroup per CU, for with few outputs each
+// workgroup reads all of h and few CUs do (bf16, 16 rows, 1024 outputs, 4096 hidden features:
+// 8 us, 13 in one part; fp32, 64 rows, 2048 outputs, 8192: 45 us, 78). Two workgroups a CU
+// are slower (bf16, 1 row, 4096 outputs, 8192: 21 us, 14 in one part).
+constexpr int64_t kPartGroups = 256, kMaxParts = 16;
 
 // ---- plan ------------------------------------------------------------------------------
 
 struct FfPlan {
     bool few;                // the kernels for few rows
+    int row_blocks, parts, tiles;   // blocks of rows a workgroup, parts of y's K, workgroups of a part if there are some
+    int64_t off_count;
     int64_t Dp, Fp, Op, rows_pad, fblocks;
     bool copy_x, copy_g, copy_u, copy_d, copy_y;   // rows not made of 16-byte granules
     int gate_tile, y_tile, y_split, back_tile, dx_tile, dx_split, dd_tile, dd_split, dg_tile, dg_split;
@@ -460,6 +500,18 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     if (p.few) {
         if (!saved) p.off_h = take(p, z.N * p.Fp * es);
         if (z.dtype) p.off_lo = take(p, z.N * p.Fp * es);
+        const int64_t nb = ceil_div(z.N, 16);
+        p.row_blocks = nb == 1 || ceil_div(z.F, 16) * nb <= kRowsGroups ? 1 : nb == 2 ? 2 : 4;
+        const int waves = p.row_blocks == 1 ? 16 : 8;
+        const int64_t tiles = ceil_div(z.O, 16) * ceil_div(nb, p.row_blocks), steps = ceil_div(p.Fp * es, 64);
+        p.parts = 1;
+        while (p.parts < kMaxParts && tiles * p.parts * 2 <= kPartGroups && steps / (p.parts * 2) >= 2 * waves)
+            p.parts *= 2;
+        if (p.parts > 1) {
+            p.off_slab_x = take(p, tiles * p.row_blocks * p.parts * 1024);
+            p.off_count = take(p, tiles * 4);
+            p.tiles = int(tiles);
+        }
         return p;
     }
     plan_copies(p, z);
@@ -555,11 +607,11 @@ FfSaved saved_of(const FfPlan &p, const void *saved, void *h)
 
 // nb blocks of rows: NB at a time by a workgroup, the others by further workgroups
 template <typename T, int NB, bool ODD>
-hipError_t launch_rows(const FfRows &a, int64_t nb, hipStream_t s)
+hipError_t launch_rows(const FfRows &a, int64_t nb, int parts, hipStream_t s)
 {
     constexpr int GATE = NB == 1 ? 8 : 4, DOWN = NB == 1 ? 16 : 8;
     const dim3 gate(unsigned(ceil_div(a.F, 16)), unsigned(ceil_div(nb, NB)));
-    const dim3 down(unsigned(ceil_div(a.O, 16)), gate.y);
+    const dim3 down(unsigned(ceil_div(a.O, 16)), gate.y, unsigned(parts));
     if (a.to.pre)
         hipLaunchKernelGGL((ff_rows_gate_kernel<T, GATE, NB, true, ODD>), gate, dim3(GATE * 64), 0, s, a);
     else
@@ -570,20 +622,16 @@ hipError_t launch_rows(const FfRows &a, int64_t nb, hipStream_t s)
     return hipGetLastError();
 }
 
-// Weights that few
-// workgroups read are read again for each block of rows, by workgroups of its own (64
-// rows, 512 inputs, 1024 hidden features, fp32: h 6.8 us, 11.8 with 64 rows a workgroup;
-// 2048 inputs, 4096 hidden features 79 and 74 us in all).
-hipError_t launch_rows(const FfRows &a, int dtype, hipStream_t s)
+hipError_t launch_rows(const FfRows &a, int dtype, int row_blocks, int parts, hipStream_t s)
 {
     const int64_t nb = ceil_div(a.N, 16);
     return with_ff_type(dtype, [&](auto t) {
         using T = decltype(t);
         const auto blocks = [&](auto odd) {
             constexpr bool ODD = decltype(odd)::value;
-            if (nb == 1 || ceil_div(a.F, 16) * nb <= kRowsGroups) return launch_rows<T, 1, ODD>(a, nb, s);
-            if (nb == 2) return launch_rows<T, 2, ODD>(a, nb, s);
-            return launch_rows<T, 4, ODD>(a, nb, s);
+            if (row_blocks == 1) return launch_rows<T, 1, ODD>(a, nb, parts, s);
+            if (row_blocks == 2) return launch_rows<T, 2, ODD>(a, nb, parts, s);
+            return launch_rows<T, 4, ODD>(a, nb, parts, s);
         };
         if constexpr (sizeof(T) == 2) {
             bool odd = (a.ldx | a.ldg | a.ldu | a.ldd) & 1;
@@ -615,8 +663,10 @@ hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s)
     const FfSaved to = saved_of(p, a.saved, ws + p.off_h);
     if (p.few)
         return launch_rows(FfRows{a.x, a.wg, a.wu, a.wd, z.ldx, z.ldg, z.ldu, z.ldd, z.ldy, z.N, z.D, z.F, z.O, p.Fp, to,
-                                  ws + p.off_lo, a.y, z.act, int(ceil_div(a.saved ? p.rows_pad : z.N, 16))},
-                           z.dtype, s);
+                                  ws + p.off_lo, a.y, z.act, int(ceil_div(a.saved ? p.rows_pad : z.N, 16)),
+                                  p.parts > 1 ? reinterpret_cast<float *>(ws + p.off_slab_x) : nullptr,
+                                  p.parts > 1 ? reinterpret_cast<int *>(ws + p.off_count) : nullptr, p.tiles},
+                           z.dtype, p.row_blocks, p.parts, s);
     FfRead r{};
     hipError_t e = launch_pads(p, a, false, &r, s);
     if (e != hipSuccess) return e;

@@ -213,6 +213,34 @@ def test_feed_forward_reads_nothing_it_has_not_written(N, D, F, dt):
     assert all(torch.equal(a, b) for a, b in zip(*outs))
 
 
+@pytest.mark.parametrize("N,D,F,O,dt", [
+    (1, 40, 16384, 24, "bf16"), (5, 24, 2500, 40, "f16"), (16, 512, 4096, 1024, "bf16"), (33, 72, 1600, 72, "f32"),
+    (48, 33, 3001, 201, "f16"), (64, 520, 8200, 300, "f32"), (24, 2048, 8192, 640, "f32"), (40, 129, 9001, 100, "f16")])
+def test_feed_forward_few_rows_and_outputs(N, D, F, O, dt):
+    """y's sum over the hidden features split over workgroups: its bound; the same bits from
+    every run, replayed ones among them, whatever the workspace holds."""
+    x, wg, wu, wd, dy = case = _ff_case(N, D, F, O, dt, seed=N + F)
+    _check_ff(case, "silu", dt)
+    n = conv.feed_forward_workspace_size(x, wg, wu, wd)
+    ws = torch.full((n + 256,), 255, dtype=torch.uint8, device=DEV)
+    y, want = torch.empty_like(dy), conv.feed_forward(x, wg, wu, wd, save=False)[0]
+    for fill in (255, 0, 1):
+        ws.fill_(fill)
+        for _ in range(4):
+            y.fill_(NAN)
+            conv.feed_forward_into(x, wg, wu, wd, y, None, ws)
+            assert torch.equal(y, want)
+        assert bool((ws[n:] == fill).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        conv.feed_forward_into(x, wg, wu, wd, y, None, ws)
+    for _ in range(3):
+        y.fill_(NAN)
+        ws.fill_(255)
+        graph.replay()
+        assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "sigmoid"])
 def test_feed_forward_gradients_against_differences(act):
     x, wg, wu, wd, dy = _ff_case(30, 48, 80, 40, "f32", seed=9)
