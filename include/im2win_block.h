@@ -16,8 +16,9 @@
  * Pointers, streams, workspaces, statuses and element types are as in
  * im2win_head.h: device pointers of the current device, everything enqueued on
  * `stream`, nothing allocated, kept or synchronised, every argument checked before
- * anything is enqueued, no atomics (the same call gives the same bits), calls may
- * be captured into a graph. Inputs and outputs must not overlap unless said.
+ * anything is enqueued, no sum whose order changes (the same call gives the same
+ * bits), calls may be captured into a graph. Inputs and outputs must not overlap
+ * unless said.
  */
 #ifndef IM2WIN_BLOCK_H
 #define IM2WIN_BLOCK_H
@@ -43,7 +44,7 @@ extern "C" {
  * All products are accumulated in fp32, a, u and dh are fp32 throughout; h, da and
  * du are rounded to the type of x where the matrix cores read them (fp16: h has to
  * stay in that type's range; da and du are held times a power of two that brings
- * the largest finite |dy| into [1, 2)); with at most FF_ROWS rows y is formed from
+ * the largest finite |dy| into [1/16, 1/8)); with at most FF_ROWS rows y is formed from
  * an h of twice those digits. The outputs are rounded once. Limits: N <= 2^22; D, F, O
  * and the row strides <= 2^20. N = 0 gives zero weight gradients. */
 enum { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2, FF_RELU = 3, FF_SIGMOID = 4 };
@@ -178,7 +179,8 @@ typedef struct {
 } adamw_desc_t;
 
 /* tensors: host array of d->count entries, read before the call returns. The
- * gradients, codes and scales of different tensors must not overlap. Device
+ * parameters, copies, states and scales of different tensors must not overlap
+ * (gradients may: they are read). Device
  * scalars for steps that are captured and replayed, or NULL: step_ptr (int64, t),
  * grad_scale_ptr (fp32, multiplies grad_scale), lr_ptr (fp32, multiplies every lr). */
 conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors, const int64_t *step_ptr,

@@ -66,8 +66,8 @@ def _ff_bounds(x, wg, wu, wd, dy, act, dt, few):
     ty = ehy @ Dn.t() + 2 * (2 * F + 2) * U * (h.abs() @ Dn.t()) + last * y.abs() + SUB[dt]
     dh = dy.double() @ wd.double()
     edh = 2 * (O + 1) * U * (DY @ Dn)
-    # fp16: held times S with S max|dy| in [1, 2), so half a subnormal step over S
-    sub = SUB["f16"] * 2 * DY.max().item() if dt == "f16" else 0.0
+    # fp16: held times S with S max|dy| >= 1/16, so half a subnormal step over S
+    sub = SUB["f16"] * 16 * DY.max().item() if dt == "f16" else 0.0
     eda = edh * (u * df).abs() + dh.abs() * e2 + 2 * U * da.abs()
     edu = edh * f.abs() + dh.abs() * e1 + 2 * U * du.abs()
     eda, edu = eda + uo * (da.abs() + eda) + sub, edu + uo * (du.abs() + edu) + sub
@@ -153,6 +153,17 @@ def test_feed_forward_gradients_of_any_size(dt, scale):
     """fp16's da and du are scaled into range: gradients far from 1 keep their digits up to
     the outputs' own storage."""
     _check_ff(_ff_case(80, 96, 136, 64, dt, seed=5, scale=scale), "silu", dt, what=f"dy * {scale}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [9, 90])
+def test_feed_forward_gradients_far_above_dy(N, dt):
+    """da 10^5 times max |dy| (large Wu and Wd, a small gate) is finite in fp16 too."""
+    x, wg, wu, wd, dy = _ff_case(N, 96, 136, 64, dt, seed=6, scale=1e-3)
+    case = x, wg * 2.0 ** -4, wu * 512, wd * 256, dy
+    da = ref.feed_forward_grad(dy, *case[:4], "silu")[4]
+    assert da.abs().max().item() > 65504 * dy.abs().max().item()
+    _check_ff(case, "silu", dt)
 
 
 def test_feed_forward_no_rows():
