@@ -538,10 +538,14 @@ FfPlan plan_bwd(const FfSizes &z)
     apart += pick(dd, z.dtype, &p.dd_tile, &p.dd_split);
     apart += pick(dg, z.dtype, &p.dg_tile, &p.dg_split);
     p.all_tile = -1;
+    const Product all[3] = {dx, dd, dg};
     for (int t : {kTile128, kTile64}) {
         int split[3];
-        const double us = together_us(t, {dx, dd, dg}, z.dtype, split);
-        if (us > apart * 0.95) continue;
+        const double us = together_us(t, all, z.dtype, split);
+        int64_t groups = 0;
+        for (int k = 0; k < 3; ++k)
+            groups += ceil_div(all[k].M, kShapes[t].m) * ceil_div(all[k].rows(kShapes[t]), kShapes[t].n) * split[k];
+        if (us > apart * 0.95 || groups > max_groups(256)) continue;
         apart = us;
         p.all_tile = t;
         p.dx_split = split[0];
