@@ -358,6 +358,8 @@ def _checked(tensors, name, sizes, dev):
     """The type codes of contiguous tensors of these sizes on device dev."""
     known, codes = head._codes, []
     for t, n in zip(tensors, sizes):
+        if t is None:
+            raise ValueError(f"{name}[{len(codes)}] is None: leave its tensor out, with a state of its own")
         if t.get_device() != dev:
             raise ValueError(f"{name}[{len(codes)}] must be on the device of params[0]")
         if t.numel() != n or not t.is_contiguous():
@@ -365,6 +367,17 @@ def _checked(tensors, name, sizes, dev):
         code = known.get(t.dtype)
         codes.append(_code(t.dtype) if code is None else code)
     return codes
+
+
+def _no_twice(pointers, name, numbers, sizes):
+    """Refuses a tensor that is in the list twice (two workgroups would update it at once)."""
+    if len(set(pointers)) == len(pointers):
+        return
+    seen = set()
+    for i, p in zip(numbers, pointers):
+        if sizes[i] and p in seen:
+            raise ValueError(f"{name}[{i}] is in the list twice")
+        seen.add(p)
 
 
 def _each(value, name, count):
@@ -397,9 +410,10 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
     words, types = _TABLE_WORDS, _checked(params, "params", state.sizes, dev)
     table = state._entries(*_state_pointers(state, dev))
     whole, real = memoryview(table).cast("q"), memoryview(table).cast("d")
-    whole[0::words] = array("q", map(_data_ptr, params))
-    whole[1::words] = array("q", map(_data_ptr, grads))
+    whole[0::words] = pointers = array("q", map(_data_ptr, params))
+    _no_twice(pointers, "params", range(count), state.sizes)
     whole[9::words] = array("q", [p | g << 32 for p, g in zip(types, _checked(grads, "grads", state.sizes, dev))])
+    whole[1::words] = array("q", map(_data_ptr, grads))
     if copies is not None:
         copies = list(copies)
         if len(copies) != count:
@@ -408,6 +422,7 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
         codes = _checked([copies[i] for i in some], "copies", [state.sizes[i] for i in some], dev)
         for i, code in zip(some, codes):
             whole[i * words + 2], whole[i * words + 10] = copies[i].data_ptr(), code
+        _no_twice([whole[i * words + 2] for i in some], "copies", some, state.sizes)
     real[11::words] = array("d", _each(lr, "lr", count))
     real[12::words] = array("d", _each(weight_decay, "weight_decay", count))
     step_ptr = scale_ptr = None

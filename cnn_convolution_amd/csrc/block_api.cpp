@@ -18,6 +18,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;    // of one tensor: byte offset
 
 bool type_ok(int32_t t) { return t == CONV2D_F32 || t == CONV2D_F16 || t == CONV2D_BF16; }
 int64_t esize(int32_t t) { return t == CONV2D_F32 ? 4 : 2; }
+// (a number that fp32 does not hold is an infinity in the kernels)
+bool finite32(double v) { return std::isfinite(float(v)); }
 bool aligned(const void *p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % uintptr_t(a) == 0; }
 
 conv2d_status_t hip_status(hipError_t e) { return e == hipSuccess ? CONV2D_OK : CONV2D_ERR_HIP; }
@@ -70,8 +72,8 @@ conv2d_status_t check_res_norm(const residual_norm_desc_t *d, ResNormArgs *a)
         return CONV2D_ERR_INVALID_DESC;
     if (d->N > 0 && d->groups > d->N) return CONV2D_ERR_INVALID_DESC;
     for (double v : {d->residual_scale, d->branch_scale})
-        if (!std::isfinite(v)) return CONV2D_ERR_INVALID_DESC;
-    if (!(d->eps >= 0.0) || !std::isfinite(d->eps)) return CONV2D_ERR_INVALID_DESC;
+        if (!finite32(v)) return CONV2D_ERR_INVALID_DESC;
+    if (!(d->eps >= 0.0) || !finite32(d->eps)) return CONV2D_ERR_INVALID_DESC;
     *a = ResNormArgs{};
     const auto stride = [&](int64_t ld) { return ld ? ld : d->C; };
     a->ldb = stride(d->ldb);
@@ -258,7 +260,7 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
     if (d->reserved != 0 || d->count < 0) return CONV2D_ERR_INVALID_DESC;
     if (d->bits != 32 && d->bits != 8) return CONV2D_ERR_UNSUPPORTED;
     if (!(d->beta1 >= 0.0 && d->beta1 < 1.0) || !(d->beta2 >= 0.0 && d->beta2 < 1.0)) return CONV2D_ERR_INVALID_DESC;
-    if (!(d->eps >= 0.0) || !std::isfinite(d->eps) || !std::isfinite(d->grad_scale)) return CONV2D_ERR_INVALID_DESC;
+    if (!(d->eps >= 0.0) || !finite32(d->eps) || !finite32(d->grad_scale)) return CONV2D_ERR_INVALID_DESC;
     if (step_ptr ? d->step != 0 : d->step < 1) return CONV2D_ERR_INVALID_DESC;
     if (!aligned(step_ptr, 8) || !aligned(grad_scale_ptr, 4) || !aligned(lr_ptr, 4)) return CONV2D_ERR_MISALIGNED;
     if (d->count > 0 && !tensors) return CONV2D_ERR_NULL_POINTER;
@@ -268,7 +270,7 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
         if (t.reserved != 0 || t.n < 0 || t.n > kMaxElems) return CONV2D_ERR_INVALID_DESC;
         if (!type_ok(t.param_dtype) || !type_ok(t.grad_dtype) || (t.copy && !type_ok(t.copy_dtype)))
             return CONV2D_ERR_UNSUPPORTED;
-        if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay)) return CONV2D_ERR_INVALID_DESC;
+        if (!finite32(t.lr) || !finite32(t.weight_decay)) return CONV2D_ERR_INVALID_DESC;
         if (coded ? t.first < 0 || t.first % 256 != 0 : t.first != 0) return CONV2D_ERR_INVALID_DESC;
         if (!coded && (t.m_scale || t.v_scale)) return CONV2D_ERR_INVALID_DESC;
         if (t.n == 0) continue;

@@ -172,6 +172,7 @@ RN = dict(N=6, C=16, groups=3, ldb=0, ldr=0, ldo=0, ldy=0, lddr=0, lddb=0, lddo=
     (dict(groups=12), 1), (dict(ldb=15), 1), (dict(ldr=15), 1), (dict(ldo=15), 1), (dict(ldy=15), 1), (dict(lddr=15), 1),
     (dict(lddb=15), 1), (dict(lddo=15), 1), (dict(lddy=15), 1), (dict(N=1 << 30, groups=1, ldb=1 << 20), 1),
     (dict(post=2), 1), (dict(eps=-1.0), 1), (dict(eps=NAN), 1), (dict(residual_scale=INF), 1), (dict(branch_scale=NAN), 1),
+    (dict(residual_scale=1e39), 1), (dict(branch_scale=-1e39), 1), (dict(eps=1e39), 1),
     (dict(dtype=5), 4), (dict(branch_dtype=7), 4), (dict(dtype=1), 4), (dict(dtype=2, branch_dtype=0), 4), (dict(kind=2), 4),
 ])
 def test_residual_norm_refuses(bad, want):
@@ -220,7 +221,7 @@ def _adam(desc=(), tensor=(), pointers=(None, None, None)):
 @pytest.mark.parametrize("bad,want", [
     (dict(count=-1), 1), (dict(reserved=1), 1), (dict(beta1=1.0), 1), (dict(beta1=-0.1), 1), (dict(beta2=1.0), 1),
     (dict(beta2=NAN), 1), (dict(eps=-1.0), 1), (dict(eps=INF), 1), (dict(grad_scale=NAN), 1), (dict(step=0), 1),
-    (dict(step=-3), 1), (dict(bits=16), 4), (dict(bits=0), 4),
+    (dict(step=-3), 1), (dict(eps=1e39), 1), (dict(grad_scale=-1e39), 1), (dict(bits=16), 4), (dict(bits=0), 4),
 ])
 def test_adamw_refuses(bad, want):
     assert _adam(bad) == want
@@ -228,7 +229,7 @@ def test_adamw_refuses(bad, want):
 
 @pytest.mark.parametrize("bad,want", [
     (dict(n=-1), 1), (dict(n=1 << 41), 1), (dict(reserved=1), 1), (dict(lr=NAN), 1), (dict(weight_decay=INF), 1),
-    (dict(first=-256), 1), (dict(first=100), 1), (dict(param_dtype=3), 4), (dict(grad_dtype=-1), 4), (dict(copy_dtype=9), 4),
+    (dict(first=-256), 1), (dict(first=100), 1), (dict(lr=1e39), 1), (dict(weight_decay=-1e39), 1), (dict(param_dtype=3), 4), (dict(grad_dtype=-1), 4), (dict(copy_dtype=9), 4),
     (dict(param=None), 2), (dict(grad=None), 2), (dict(m=None), 2), (dict(v=None), 2), (dict(m_scale=None), 2),
     (dict(v_scale=None), 2), (dict(param=P + 2), 3), (dict(grad=P + 1), 3), (dict(copy=P + 1), 3), (dict(m=P + 2), 3),
     (dict(v=P + 2), 3), (dict(m_scale=P + 2), 3), (dict(v_scale=P + 1), 3),
@@ -366,9 +367,22 @@ def test_the_optimizers_table(monkeypatch):
                 else:
                     assert (e.first, e.m_scale, e.v_scale) == (0, None, None)
     for bad, what in ((dict(params=p[:2]), "number"), (dict(copies=c[:2]), "copies"), (dict(step=0), "from 1 on"),
-                      (dict(lr=[1.0, 2.0]), "lr"), (dict(grads=[g[0], g[1], DeviceTensor(2)]), r"grads\[2\]")):
+                      (dict(lr=[1.0, 2.0]), "lr"), (dict(grads=[g[0], g[1], DeviceTensor(2)]), r"grads\[2\]"),
+                      (dict(grads=[g[0], None, g[2]]), r"grads\[1\] is None")):
         with pytest.raises(ValueError, match=what):
             conv.adamw(**{**dict(params=p, grads=g, state=state, step=9, lr=1.0), **bad})
+    # one tensor twice would be updated by two workgroups at once; empty ones share an address
+    state, twice = conv.AdamWState([6, 4, 0, 6, 0], 32, "cpu"), DeviceTensor(6)
+    for name in ("exp_avg", "exp_avg_sq"):
+        setattr(state, name, DeviceTensor(*getattr(state, name).shape))
+    p = [twice, DeviceTensor(4), DeviceTensor(0), DeviceTensor(6), DeviceTensor(0)]
+    g = [DeviceTensor(n) for n in state.sizes]
+    p[2].data_ptr = p[4].data_ptr = lambda: 0
+    conv.adamw(p, g, state, 1, 1.0)
+    with pytest.raises(ValueError, match=r"params\[3\] is in the list twice"):
+        conv.adamw(p[:3] + [twice] + p[4:], g, state, 1, 1.0)
+    with pytest.raises(ValueError, match=r"copies\[3\] is in the list twice"):
+        conv.adamw(p, g, state, 1, 1.0, copies=[g[0], None, None, g[0], None])
 
 
 def test_rows_of_blocks_have_records_of_their_own():
