@@ -271,7 +271,8 @@ conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors,
         if (!type_ok(t.param_dtype) || !type_ok(t.grad_dtype) || (t.copy && !type_ok(t.copy_dtype)))
             return CONV2D_ERR_UNSUPPORTED;
         if (!finite32(t.lr) || !finite32(t.weight_decay)) return CONV2D_ERR_INVALID_DESC;
-        if (coded ? t.first < 0 || t.first % 256 != 0 : t.first != 0) return CONV2D_ERR_INVALID_DESC;
+        if (coded ? t.first < 0 || t.first > int64_t(1) << 62 || t.first % 256 != 0 : t.first != 0)
+            return CONV2D_ERR_INVALID_DESC;
         if (!coded && (t.m_scale || t.v_scale)) return CONV2D_ERR_INVALID_DESC;
         if (t.n == 0) continue;
         if (!t.param || !t.grad || !t.m || !t.v || (coded && (!t.m_scale || !t.v_scale)))

@@ -229,7 +229,7 @@ def test_adamw_refuses(bad, want):
 
 @pytest.mark.parametrize("bad,want", [
     (dict(n=-1), 1), (dict(n=1 << 41), 1), (dict(reserved=1), 1), (dict(lr=NAN), 1), (dict(weight_decay=INF), 1),
-    (dict(first=-256), 1), (dict(first=100), 1), (dict(lr=1e39), 1), (dict(weight_decay=-1e39), 1), (dict(param_dtype=3), 4), (dict(grad_dtype=-1), 4), (dict(copy_dtype=9), 4),
+    (dict(first=-256), 1), (dict(first=100), 1), (dict(first=1 << 62 | 256), 1), (dict(lr=1e39), 1), (dict(weight_decay=-1e39), 1), (dict(param_dtype=3), 4), (dict(grad_dtype=-1), 4), (dict(copy_dtype=9), 4),
     (dict(param=None), 2), (dict(grad=None), 2), (dict(m=None), 2), (dict(v=None), 2), (dict(m_scale=None), 2),
     (dict(v_scale=None), 2), (dict(param=P + 2), 3), (dict(grad=P + 1), 3), (dict(copy=P + 1), 3), (dict(m=P + 2), 3),
     (dict(v=P + 2), 3), (dict(m_scale=P + 2), 3), (dict(v_scale=P + 1), 3),

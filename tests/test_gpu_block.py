@@ -651,6 +651,77 @@ def test_adamw_device_scalars():
                 assert torch.equal(x, y)
 
 
+# ---- more than 2^32 elements ------------------------------------------------------------------
+
+def _half(seed, dt, *shape, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    t = torch.empty(shape, dtype=TYPES[dt], device=DEV)
+    for part in t.split(1 << 16):
+        part.copy_(torch.randn(part.shape, generator=g, device=DEV) * scale)
+    return t
+
+
+def test_residual_norm_beyond_32_bits():
+    """Rows before, across and past 2^31 and 2^32 elements are what they are by themselves."""
+    N, C = (1 << 20) + 3, 4100
+    b, r, dy, dout = (_half(k, "bf16", N, C) for k in range(4))
+    w = torch.linspace(0.5, 2.0, C, device=DEV)
+    out, y, st = conv.residual_norm(b, r, weight=w, post_weight=w)
+    dr, db, grads = conv.residual_norm_backward(dy, dout, b, out, st, weight=w, post_weight=w)
+    for at in (0, (1 << 31) // C - 5, (1 << 32) // C - 9, N - 12):
+        part = slice(at, at + 12)
+        b1, r1, dy1, do1 = (t[part].clone() for t in (b, r, dy, dout))
+        o1, y1, s1 = conv.residual_norm(b1, r1, weight=w, post_weight=w)
+        dr1, db1, _ = conv.residual_norm_backward(dy1, do1, b1, o1, s1, weight=w, post_weight=w)
+        for name, t, t1 in (("out", out, o1), ("y", y, y1), ("stats", st, s1), ("dr", dr, dr1), ("db", db, db1)):
+            assert torch.equal(t[part], t1), (name, at)
+    want, size = (torch.zeros(C, dtype=torch.float64, device=DEV) for _ in range(2))
+    for part in dy.split(1 << 16):
+        want += part.double().sum(0)
+        size += part.double().abs().sum(0)
+    # 4097 rows a workgroup one after another, 256 workgroups in a tree
+    _close(grads["bias"], want, 4200 * U * size, "dbias")
+    del b, r, dy, dout, out, y, st, dr, db, part, b1, r1, dy1, do1
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("N,D,F,O,dt", [(3, 4104, 1 << 20, 40, "bf16"), (40, 4103, (1 << 20) - 1, 24, "f16"),
+                                        (130, 40, 1 << 20, 4104, "bf16")])
+def test_feed_forward_beyond_32_bits(N, D, F, O, dt):
+    """Weights and their gradients of more than 2^32 elements: features at both ends and in
+    the middle against the formulas, the others' share of y and dx by zeros in Wd."""
+    x, wg, wu = _half(1, dt, N, D), _half(2, dt, F, D, scale=D ** -0.5), _half(3, dt, F, D, scale=D ** -0.5)
+    dy, wd = _half(4, dt, N, O), torch.zeros(O, F, dtype=TYPES[dt], device=DEV)
+    some = torch.tensor([0, 1, 17, F // 2 - 1, F // 2 + 3, F - 18, F - 2, F - 1], device=DEV)
+    wd[:, some] = _half(5, dt, O, len(some))
+    y, saved = conv.feed_forward(x, wg, wu, wd)
+    got = (y,) + conv.feed_forward_backward(dy, x, wg, wu, wd, saved)
+    tol, want = _ff_bounds(x, wg[some], wu[some], wd[:, some].contiguous(), dy, "silu", dt, N <= 16)
+    # (the bounds' sums are over the features that count: the zeros add none)
+    for g, w, t, name in zip((got[0], got[1], got[2][some], got[3][some], got[4][:, some]), want, tol,
+                             ("y", "dx", "dw_gate", "dw_up", "dw_down")):
+        _close(g, w, t, name)
+    rest = torch.tensor([2, F // 3, F - 3], device=DEV)
+    assert not bool(got[2][rest].any()) and not bool(got[3][rest].any())
+    del x, wg, wu, wd, dy, y, saved, got, g
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_beyond_32_bits(bits):
+    n, last = (1 << 32) + 300, 300
+    p = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device=DEV)
+    g[-last:] = -0.25
+    state = conv.adamw_state([p], bits)
+    # (every step is lr whatever the gradient's size)
+    conv.adamw([p], [g], state, 1, 0.5)
+    conv.adamw([p], [g], state, 2, 0.25)
+    assert bool((p[:-last] == 0.25).all()) and bool((p[-last:] == 1.75).all())
+    del p, g, state
+    torch.cuda.empty_cache()
+
+
 # ---- refusals ---------------------------------------------------------------------------------
 
 def test_python_refusals():
