@@ -17,7 +17,8 @@ namespace im2win {
 struct FfSaved {
     float *pre;
     int64_t fblocks;
-    void *h;                 // [rows_pad][Fp], zeros past N and F
+    void *h;                 // [rows_pad] rows of Fp, zeros past N and F
+    int64_t ldh;             // elements between them: whole cache lines
 };
 
 // h (and with `pre` the factors) of rows 0 .. rows_pad - 1
@@ -30,7 +31,8 @@ struct FfGate {
 };
 hipError_t launch_ff_gate(const FfGate &a, int dtype, int tile, hipStream_t s);
 
-// da and du, each [rows_pad][Fp] with zeros past N and F, side by side in rows of 2 Fp
+// da and du, each [rows_pad] rows of Fp with zeros past N and F, side by side in rows of
+// 2 from.ldh
 struct FfBack {
     const void *dy, *wd;
     int64_t lddy, ldd;       // bytes
@@ -70,7 +72,7 @@ hipError_t launch_ff_all(const FfProduct &dx, const FfProduct &dwd, const FfProd
 // the slabs of up to three products added in order
 hipError_t launch_ff_join(const FfProduct *p, int count, int dtype, hipStream_t s);
 
-// few rows: h in two parts (half precision), h itself and `lo` [N][Fp]; with a `pre` the
+// few rows: h in two parts (half precision), h itself and `lo` [N][ldh]; with a `pre` the
 // factors, and h with its zero rows
 struct FfRows {
     const void *x, *wg, *wu, *wd;

@@ -22,7 +22,8 @@ namespace {
 struct PadJob {
     const void *src;
     void *dst;
-    int64_t ld, rows, D, Dp; // elements; dst [rows][Dp]
+    int64_t ld, rows, D, Dp; // elements; dst: rows of Dp, ldd apart
+    int64_t ldd;
     int64_t end;             // workgroups up to and with this job's
 };
 struct PadArgs {
@@ -66,7 +67,7 @@ __global__ __launch_bounds__(256) void ff_pad_kernel(const PadArgs a)
     for (int64_t c = lane * E; c < j.Dp; c += 64 * E) {
         float f[E];
         load_some<E>(static_cast<const T *>(j.src) + row * j.ld + c, std::min<int64_t>(E, j.D - c), f);
-        store_vec<E>(static_cast<T *>(j.dst) + row * j.Dp + c, f);
+        store_vec<E>(static_cast<T *>(j.dst) + row * j.ldd + c, f);
     }
 }
 
@@ -249,12 +250,12 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
     }
     if (m >= a.Fp || (!SAVE && row >= a.N)) return;
     const Raw<T, 4> hi = to_raw<T, 4>(h);
-    store_raw(static_cast<T *>(a.to.h) + row * a.Fp + m, hi);
+    store_raw(static_cast<T *>(a.to.h) + row * a.to.ldh + m, hi);
     if (sizeof(T) == 4 || row >= a.N) return;
     float rest[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) rest[v] = h[v] - element(hi, v);
-    store_vec<4>(static_cast<T *>(a.lo) + row * a.Fp + m, rest);
+    store_vec<4>(static_cast<T *>(a.lo) + row * a.to.ldh + m, rest);
 }
 
 template <typename T, int WAVES, int NB, bool ODD>
@@ -271,7 +272,7 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_down_kernel(const FfRows a
     Row<T, false> hi[NB], lo[NB];              // whole vectors up to Fp, zeros past F
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const int64_t at = min(int64_t((blockIdx.y * NB + b) * 16 + (lane & 15)), a.N - 1) * a.Fp;
+        const int64_t at = min(int64_t((blockIdx.y * NB + b) * 16 + (lane & 15)), a.N - 1) * a.to.ldh;
         hi[b].init(static_cast<const T *>(a.to.h) + at);
         lo[b].init(static_cast<const T *>(a.lo) + at);
     }
@@ -374,6 +375,7 @@ struct FfPlan {
     int row_blocks, parts, tiles;   // blocks of rows a workgroup, parts of y's K, workgroups of a part if there are some
     int64_t off_count;
     int64_t Dp, Fp, Op, rows_pad, fblocks;
+    int64_t ldd, ldf, ldo;   // strides of rows of D, F and O in the workspace
     bool copy_x, copy_g, copy_u, copy_d, copy_y;   // rows not made of 16-byte granules
     int gate_tile, y_tile, y_split, back_tile, dx_tile, dx_split, dd_tile, dd_split, dg_tile, dg_split;
     int all_tile;            // of dx, dWd, dWg and dWu in one launch, or -1
@@ -469,6 +471,11 @@ FfPlan plan_common(const FfSizes &z)
     p.Dp = round_up(z.D, e);
     p.Fp = round_up(z.F, e);
     p.Op = round_up(z.O, e);
+    // whole cache lines: a stage's 128 bytes of a row are one (4097 rows, 1032 inputs, 3000
+    // hidden features, fp16, rows of Fp: y 56 us; 8 features more fill their lines: 49)
+    p.ldd = round_up(z.D, 128 / es);
+    p.ldf = round_up(z.F, 128 / es);
+    p.ldo = round_up(z.O, 128 / es);
     p.rows_pad = round_up(z.N, 128 / es);
     // whole tiles: the back launch's reads need no bounds
     p.fblocks = round_up(z.F, 256) / 16;
@@ -485,10 +492,10 @@ FfPlan plan_common(const FfSizes &z)
 void plan_copies(FfPlan &p, const FfSizes &z)
 {
     const int64_t es = elem(z.dtype);
-    if (p.copy_x) p.off_x = take(p, z.N * p.Dp * es);
-    if (p.copy_g) p.off_g = take(p, z.F * p.Dp * es);
-    if (p.copy_u) p.off_u = take(p, z.F * p.Dp * es);
-    if (p.copy_d) p.off_d = take(p, z.O * p.Fp * es);
+    if (p.copy_x) p.off_x = take(p, z.N * p.ldd * es);
+    if (p.copy_g) p.off_g = take(p, z.F * p.ldd * es);
+    if (p.copy_u) p.off_u = take(p, z.F * p.ldd * es);
+    if (p.copy_d) p.off_d = take(p, z.O * p.ldf * es);
 }
 
 FfPlan plan_fwd(const FfSizes &z, bool saved)
@@ -498,8 +505,8 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     const int64_t es = elem(z.dtype), ki = 128 / es;
     p.few = z.N <= 16 || (z.N <= FF_ROWS && (!z.dtype || p.copy_g || p.copy_u || p.copy_d));
     if (p.few) {
-        if (!saved) p.off_h = take(p, z.N * p.Fp * es);
-        if (z.dtype) p.off_lo = take(p, z.N * p.Fp * es);
+        if (!saved) p.off_h = take(p, z.N * p.ldf * es);
+        if (z.dtype) p.off_lo = take(p, z.N * p.ldf * es);
         const int64_t nb = ceil_div(z.N, 16);
         p.row_blocks = nb == 1 || ceil_div(z.F, 16) * nb <= kRowsGroups ? 1 : nb == 2 ? 2 : 4;
         const int waves = p.row_blocks == 1 ? 16 : 8;
@@ -515,7 +522,7 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
         return p;
     }
     plan_copies(p, z);
-    if (!saved) p.off_h = take(p, p.rows_pad * p.Fp * es);
+    if (!saved) p.off_h = take(p, p.rows_pad * p.ldf * es);
     p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(es / 2), saved ? 4 : 0, false);
     pick(Product{z.O, z.N, ceil_div(p.Fp, ki), 1}, z.dtype, &p.y_tile, &p.y_split);
     if (p.y_split > 1) p.off_slab_x = take(p, p.y_split * z.N * z.O * 4);
@@ -528,8 +535,8 @@ FfPlan plan_bwd(const FfSizes &z)
     if (z.N == 0) return p;
     const int64_t es = elem(z.dtype), ki = 128 / es;
     plan_copies(p, z);
-    if (p.copy_y) p.off_dy = take(p, z.N * p.Op * es);
-    p.off_grad = take(p, p.rows_pad * 2 * p.Fp * es);
+    if (p.copy_y) p.off_dy = take(p, z.N * p.ldo * es);
+    p.off_grad = take(p, p.rows_pad * 2 * p.ldf * es);
     p.off_amax = take(p, kAmaxParts * 4);
     p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), 0, true);
     const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki), 1}, dd{z.F, z.O, ceil_div(z.N, ki), 1}, dg{z.D, z.F, dd.stages, 2};
@@ -571,22 +578,22 @@ hipError_t launch_pads(const FfPlan &p, const FfArgs &a, bool backward, FfRead *
     char *ws = static_cast<char *>(a.ws);
     PadArgs pad{};
     int64_t groups = 0;
-    auto add = [&](bool copy, const void *src, int64_t ld, int64_t rows, int64_t D, int64_t Dp, int64_t off,
-                   const void *&to, int64_t &to_ld) {
+    auto add = [&](bool copy, const void *src, int64_t ld, int64_t rows, int64_t D, int64_t Dp, int64_t ldd,
+                   int64_t off, const void *&to, int64_t &to_ld) {
         to = src;
         to_ld = ld * es;
         if (!copy) return;
         to = ws + off;
-        to_ld = Dp * es;
+        to_ld = ldd * es;
         groups += ceil_div(rows, 4);
-        pad.job[pad.count++] = PadJob{src, ws + off, ld, rows, D, Dp, groups};
+        pad.job[pad.count++] = PadJob{src, ws + off, ld, rows, D, Dp, ldd, groups};
     };
-    add(p.copy_x, a.x, z.ldx, z.N, z.D, p.Dp, p.off_x, r->x, r->ldx);
-    add(p.copy_g, a.wg, z.ldg, z.F, z.D, p.Dp, p.off_g, r->wg, r->ldg);
-    add(p.copy_u, a.wu, z.ldu, z.F, z.D, p.Dp, p.off_u, r->wu, r->ldu);
-    add(p.copy_d, a.wd, z.ldd, z.O, z.F, p.Fp, p.off_d, r->wd, r->ldd);
+    add(p.copy_x, a.x, z.ldx, z.N, z.D, p.Dp, p.ldd, p.off_x, r->x, r->ldx);
+    add(p.copy_g, a.wg, z.ldg, z.F, z.D, p.Dp, p.ldd, p.off_g, r->wg, r->ldg);
+    add(p.copy_u, a.wu, z.ldu, z.F, z.D, p.Dp, p.ldd, p.off_u, r->wu, r->ldu);
+    add(p.copy_d, a.wd, z.ldd, z.O, z.F, p.Fp, p.ldf, p.off_d, r->wd, r->ldd);
     if (backward) {
-        add(p.copy_y, a.dy, z.ldy, z.N, z.O, p.Op, p.off_dy, r->dy, r->lddy);
+        add(p.copy_y, a.dy, z.ldy, z.N, z.O, p.Op, p.ldo, p.off_dy, r->dy, r->lddy);
         if (z.dtype == 1) {
             pad.dy = a.dy;
             pad.lddy = z.ldy;
@@ -606,7 +613,7 @@ hipError_t launch_pads(const FfPlan &p, const FfArgs &a, bool backward, FfRead *
 FfSaved saved_of(const FfPlan &p, const void *saved, void *h)
 {
     char *c = static_cast<char *>(const_cast<void *>(saved));
-    return FfSaved{reinterpret_cast<float *>(c), p.fblocks, c ? c + p.pre_bytes : h};
+    return FfSaved{reinterpret_cast<float *>(c), p.fblocks, c ? c + p.pre_bytes : h, p.ldf};
 }
 
 // nb blocks of rows: NB at a time by a workgroup, the others by further workgroups
@@ -651,7 +658,7 @@ hipError_t launch_rows(const FfRows &a, int dtype, int row_blocks, int parts, hi
 int64_t ff_saved_bytes(const FfSizes &z)
 {
     const FfPlan p = plan_common(z);
-    return p.pre_bytes + p.rows_pad * p.Fp * elem(z.dtype);
+    return p.pre_bytes + p.rows_pad * p.ldf * elem(z.dtype);
 }
 
 int64_t ff_fwd_ws_bytes(const FfSizes &z, bool saved) { return plan_fwd(z, saved).bytes; }
@@ -680,7 +687,7 @@ hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s)
     y.a[0] = r.wd;
     y.lda[0] = r.ldd;
     y.b = to.h;
-    y.ldb = p.Fp * es;
+    y.ldb = p.ldf * es;
     y.M = y.a_count = z.O;
     y.n = y.b_count = z.N;
     y.K = y.k_a = y.k_b = p.Fp;
@@ -725,8 +732,8 @@ hipError_t launch_ff_bwd(const FfArgs &a, hipStream_t s)
     dx.lda[0] = r.ldg;
     dx.lda[1] = r.ldu;
     dx.b = dg.b = ws + p.off_grad;
-    dx.b_step = dg.b_step = p.Fp * es;
-    dx.ldb = dg.ldb = 2 * p.Fp * es;
+    dx.b_step = dg.b_step = p.ldf * es;
+    dx.ldb = dg.ldb = 2 * p.ldf * es;
     dx.M = dg.M = z.D;
     dx.a_count = dg.a_count = p.Dp;
     dx.n = dx.b_count = z.N;
@@ -754,7 +761,7 @@ hipError_t launch_ff_bwd(const FfArgs &a, hipStream_t s)
     dg.out[1] = a.dwu;
 
     dd.a[0] = from.h;
-    dd.lda[0] = p.Fp * es;
+    dd.lda[0] = p.ldf * es;
     dd.b = r.dy;
     dd.ldb = r.lddy;
     dd.M = z.F;

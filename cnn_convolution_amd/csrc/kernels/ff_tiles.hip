@@ -156,7 +156,7 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_gate_kernel(const 
                         p[64] = acc[2 * b + 1][j];
                     }
             }
-            store_blocks<T, NB>(static_cast<T *>(a.to.h) + row * a.Fp + ft, int(a.Fp - ft), lane, h);
+            store_blocks<T, NB>(static_cast<T *>(a.to.h) + row * a.to.ldh + ft, int(a.Fp - ft), lane, h);
         }
     }
 }
@@ -227,9 +227,9 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
                 da[i] = dh * ring[q % (AHEAD + 1)][i][1];
             }
             if (nt + 16 * j < a.rows_pad) {
-                T *g = static_cast<T *>(a.g) + row * 2 * a.Fp + ft + i0 * 16;
+                T *g = static_cast<T *>(a.g) + row * 2 * a.from.ldh + ft + i0 * 16;
                 store_blocks<T, H>(g, int(a.Fp - ft) - i0 * 16, lane, da);
-                store_blocks<T, H>(g + a.Fp, int(a.Fp - ft) - i0 * 16, lane, du);
+                store_blocks<T, H>(g + a.from.ldh, int(a.Fp - ft) - i0 * 16, lane, du);
             }
         }
     }
