@@ -401,8 +401,9 @@ int pick_tile(int64_t M, int64_t N, int64_t stages, int dtype, int out_bytes, in
         // of 32 rows (24 rows, 2048 outputs, 8192 hidden features, bf16: 13 us, 21)
         if (t == kTile64x32 && (back || N > 64)) continue;
         const int64_t own = t == kTile32K ? ceil_div(stages, 4) : stages;
-        // what is saved goes out at the chip's rate, hidden by nothing: all workgroups
-        // store at once (4097 x 1032 x 3001, fp16, tiles of 256 95 us, of 128 114)
+        // what is saved or read back goes at the chip's rate, hidden by nothing: all
+        // workgroups are in their epilogues at once (4097 x 1032 x 3001, fp16, gate with
+        // tiles of 256 95 us, of 128 114; 8192 x 2048 x 8192, bf16, back 363 and 397)
         const double us = product_us(kShapes[t], M, N, own, 1, dtype, out_bytes) +
                           double(M) * double(N) * saved_bytes / 5e6;
         if (us < best * 0.98) {
@@ -538,7 +539,7 @@ FfPlan plan_bwd(const FfSizes &z)
     if (p.copy_y) p.off_dy = take(p, z.N * p.ldo * es);
     p.off_grad = take(p, p.rows_pad * 2 * p.ldf * es);
     p.off_amax = take(p, kAmaxParts * 4);
-    p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, int(8 + 2 * es), 0, true);
+    p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, 0, int(8 + 2 * es), true);
     const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki), 1}, dd{z.F, z.O, ceil_div(z.N, ki), 1}, dg{z.D, z.F, dd.stages, 2};
     double apart = 0.0;
     apart += pick(dx, z.dtype, &p.dx_tile, &p.dx_split);
