@@ -3,7 +3,7 @@
 //
 // Forward: the gate launch (ff_tiles.hip) forms both projections, the activation and
 // the product and leaves h; a plain product (ff_products.hip) leaves y. Backward: the
-// back launch leaves da and du from dy, Wd and the saved a and u; then dx, dWd and
+// back launch leaves da and du from dy, Wd and the saved factors; then dx, dWd and
 // dWg with dWu.
 #include <hip/hip_runtime.h>
 
@@ -87,13 +87,15 @@ __global__ __launch_bounds__(256) void ff_zero_kernel(T *p, int64_t n)
 // waves' sums are joined, no padded copies of odd rows), x or h come from the caches.
 // Rows past N repeat the last one. In half precision h is kept in two parts, rounded and
 // what that took: its rounding would be as large in y as y's own.
-// 1 row, 4096 inputs and outputs, 8192 hidden features, bf16: h 23.5 us (5.7 TB/s), y
-// 14.4 (4.7).
+// 1 row, 4096 inputs and outputs, 8192 hidden features, bf16: h 23.3 us (5.8 TB/s), y
+// 15.5 (4.3). 37 rows, 1001, 2003, fp16: h 11.9 us, y 8.3, the latency of a few loads one
+// after the other. Above 16 rows tiles are faster where they can read in place (2048, 8192,
+// bf16: 24 rows 28 us, 16 rows here 33), but their y has 1.4 times the error.
 
 // A row of K values. ODD: half-precision rows that start at any element are read as the
 // dwords that hold them and shifted into place, for 16-byte loads that start between
 // dwords take twice the time (16 rows, 1001 inputs, 2000 hidden features, fp16: h 10.1 us,
-// 1002 inputs 5.4). No dword is touched that holds nothing of the vector.
+// 8.3 so, 1002 inputs 6.5). No dword is touched that holds nothing of the vector.
 template <typename T, bool ODD>
 struct Row {
     static constexpr int E = 16 / int(sizeof(T));

@@ -6,6 +6,8 @@
 //   dWg[f][d], dWu[f][d] = sum_n x[n][d] da[n][f], .. du     both in columns, the two
 //              outputs as one launch's tiles
 // K may be split over workgroups into fp32 slabs that another kernel adds in order.
+// Bound by the matrix cores: 8192 rows, 4096 inputs and outputs, 16384 hidden features,
+// bf16: y 903 us (1217 TFLOP/s), dx 1562 (1408), dWd 835 (1317), dWg and dWu 1730 (1271).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -124,7 +126,7 @@ struct FfTiles {
 
 // The products of a backward pass in one launch, a workgroup per tile, the longest first:
 // none fills the chip by itself (or its last round does not), and all need only da, du
-// and h. 4097 x 1032 x 3001, fp16: 242 us one after the other.
+// and h. 4097 x 1032 x 3001, fp16: 173 us, 242 one after the other.
 template <typename T, typename C>
 __global__ __launch_bounds__(C::threads, C::per_simd) void ff_all_kernel(const FfProduct dx, const FfProduct dwd,
                                                                          const FfProduct dwgu, FfTiles tx, FfTiles td,
