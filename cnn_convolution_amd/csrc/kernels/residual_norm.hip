@@ -14,8 +14,7 @@
 // norm sum dy xhat(out) and sum dy: four sums per channel stay in registers over all of a
 // workgroup's rows. S1 and S2 leave at the end of each group that the workgroup sees,
 // the others at its end; a second launch adds them in a fixed order.
-// Rows wider than a group holds, or narrower than a vector, are read again for each
-// pass over them.
+// Rows wider than a group holds are read again for each pass over them.
 // 32768 rows of 4096, bf16: forward 212 us (5.1 TB/s), backward 317 and 10 for the second
 // launch (4.9). 19941 rows of 1001, fp32 with fp16, a gate for every 289: 82 and 9 (4.0).
 #include <hip/hip_runtime.h>
@@ -129,6 +128,23 @@ __device__ __forceinline__ void param(const float *p, float absent, int c, int C
     if (p) load_some<8>(p + c, max(0, C - c), f);
 }
 
+// channels c .. c + 7 of a row of C, zeros past its end (EXACT: anything), without a branch.
+// A lane that holds a whole row (C < 8) reads its elements one by one.
+template <int LPR, bool EXACT, typename T>
+__device__ __forceinline__ Raw<T, 8> load_chunk(const T *row, int c, int C)
+{
+    if constexpr (LPR == 1) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = float(row[min(e, C - 1)]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) f[e] = e < C ? f[e] : 0.f;
+        return to_raw<T, 8>(f);
+    } else {
+        return load_row<T, 8, EXACT>(row, c, C);
+    }
+}
+
 template <bool EXACT, typename T>
 __device__ __forceinline__ void store_row(T *p, int left, const Raw<T, 8> &r)
 {
@@ -155,8 +171,8 @@ __global__ __launch_bounds__(threads_of(LPR)) void res_norm_fwd_kernel(const Res
     auto load = [&](int64_t k) {
 #pragma unroll
         for (int i = 0; i < KCH; ++i) {
-            qb[i] = load_row<TB, 8, EXACT>(b + k * a.ldb, (i * LPR + l) * 8, C);
-            qr[i] = load_row<TR, 8, EXACT>(r + k * a.ldr, (i * LPR + l) * 8, C);
+            qb[i] = load_chunk<LPR, EXACT>(b + k * a.ldb, (i * LPR + l) * 8, C);
+            qr[i] = load_chunk<LPR, EXACT>(r + k * a.ldr, (i * LPR + l) * 8, C);
         }
     };
     // past the last row that one is read again (no branch around a load)
@@ -341,7 +357,7 @@ __global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const Res
 {
     constexpr int THREADS = threads_of(LPR), G = THREADS / LPR;
     __shared__ float2 red[2][THREADS / 64];
-    __shared__ __align__(16) float part[LPR * KCH * 8];
+    __shared__ __align__(16) float part[LPR == 1 ? THREADS / 8 : LPR * KCH * 8];
     const int l = threadIdx.x % LPR, q = threadIdx.x / LPR, C = a.C;
     const float fc = float(C);
     const TB *dy = static_cast<const TB *>(a.dy), *b = static_cast<const TB *>(a.b);
@@ -359,11 +375,11 @@ __global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const Res
 #pragma unroll
         for (int i = 0; i < KCH; ++i) {
             const int c = (i * LPR + l) * 8;
-            y[i] = load_row<TB, 8, EXACT>(dy + k * a.lddy, c, C);
-            x[i] = load_row<TB, 8, EXACT>(b + k * a.ldb, c, C);
-            o[i] = load_row<TR, 8, EXACT>(out + k * a.ldo, c, C);
+            y[i] = load_chunk<LPR, EXACT>(dy + k * a.lddy, c, C);
+            x[i] = load_chunk<LPR, EXACT>(b + k * a.ldb, c, C);
+            o[i] = load_chunk<LPR, EXACT>(out + k * a.ldo, c, C);
             // without a dout: out again, and cleared below
-            d[i] = load_row<TR, 8, EXACT>(has_dout ? dout + k * a.lddo : out + k * a.ldo, c, C);
+            d[i] = load_chunk<LPR, EXACT>(has_dout ? dout + k * a.lddo : out + k * a.ldo, c, C);
         }
         s = stats[k];
     };
@@ -376,6 +392,18 @@ __global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const Res
     }
     // the workgroup's groups of lanes added in order into dst[C]
     auto flush = [&](const float (&v)[KCH][8], float *dst) {
+        if constexpr (LPR == 1) {              // a lane's row: first over the waves
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float t = lane_sum<64>(v[0][e]);
+                if ((threadIdx.x & 63) == 0) part[(threadIdx.x >> 6) * 8 + e] = t;
+            }
+            __syncthreads();
+            if (int(threadIdx.x) < C)
+                dst[threadIdx.x] = (part[threadIdx.x] + part[8 + threadIdx.x]) + (part[16 + threadIdx.x] + part[24 + threadIdx.x]);
+            return;
+        }
         for (int k = 0; k < G; ++k) {
             __syncthreads();
             if (q == k)
@@ -750,7 +778,7 @@ struct Group {
 Group group_of(int64_t C, bool backward)
 {
     const int64_t ch = (C + 7) / 8;
-    if (C < 8) return {0, 0};
+    if (C < 8) return {1, 1};
     for (int l : {8, 16, 32, 64})
         if (ch <= l) return {l, 1};
     if (ch <= 128) return backward ? Group{64, 2} : Group{128, 1};
@@ -766,6 +794,7 @@ hipError_t with_group(const Group &g, F f)
     using std::integral_constant;
 #define IM2WIN_GROUP(L, K) \
     if (g.lpr == L && g.kch == K) return f(integral_constant<int, L>{}, integral_constant<int, K>{});
+    IM2WIN_GROUP(1, 1)
     IM2WIN_GROUP(8, 1)
     IM2WIN_GROUP(16, 1)
     IM2WIN_GROUP(32, 1)
@@ -823,10 +852,12 @@ hipError_t launch_res_norm_fwd(const ResNormArgs &a, hipStream_t s)
         return with_group<false>(g, [&](auto lpr, auto kch) {
             constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
             const dim3 grid(unsigned(blocks_of(a.N, g, false))), threads(threads_of(LPR));
-            if (a.C % 8 == 0)
-                hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
-            else
-                hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
+            if constexpr (LPR > 1)
+                if (a.C % 8 == 0) {
+                    hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
+                    return hipGetLastError();
+                }
+            hipLaunchKernelGGL((res_norm_fwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
             return hipGetLastError();
         });
     });
@@ -857,10 +888,12 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
         return with_group<true>(g, [&](auto lpr, auto kch) {
             constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
             const dim3 grid{unsigned(B)}, threads(threads_of(LPR));
-            if (a.C % 8 == 0)
-                hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
-            else
-                hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
+            if constexpr (LPR > 1)
+                if (a.C % 8 == 0) {
+                    hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
+                    return hipGetLastError();
+                }
+            hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
             return hipGetLastError();
         });
     });

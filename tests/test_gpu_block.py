@@ -382,6 +382,15 @@ def test_residual_norm(N, C, G, kind, post, rt, bt):
     _check_rn(_rn_case(N, C, G, rt, bt, post, seed=N + C), rt, bt, kind, post)
 
 
+@pytest.mark.parametrize("rt,bt", [("f32", "f32"), ("f32", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("N,C,G", [(70000, 4, 1), (1001, 7, 91), (4096, 2, 4096), (2500, 3, 50), (600, 1, 2), (513, 6, 0),
+                                   (130000, 5, 13)])
+def test_residual_norm_of_short_rows(N, C, G, rt, bt):
+    """Rows of fewer channels than a vector has: a lane to each."""
+    # (one channel's deviation from its mean is 0 or what is lost of it: RMS norms for it)
+    _check_rn(_rn_case(N, C, G, rt, bt, True, seed=C), rt, bt, "rms" if C == 1 else "layer", True)
+
+
 @pytest.mark.parametrize("rt,bt", [("f32", "bf16"), ("f16", "f16")])
 @pytest.mark.parametrize("N,C,G", [(5000, 64, 50), (20000, 256, 1), (4096, 1000, 4096), (3000, 520, 1000), (777, 24, 777),
                                    (2310, 96, 7), (1024, 3000, 3), (600, 9000, 60)])
