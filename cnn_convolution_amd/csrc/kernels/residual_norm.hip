@@ -352,7 +352,9 @@ __device__ __forceinline__ void skip_record(const Sums &sums, int64_t k, int C)
     if (threadIdx.x == 0) sums.group[k] = 0;
 }
 
-template <typename TR, typename TB, int LPR, int KCH, bool EXACT>
+// OWN: short groups of rows with a gate each. A row's lanes take whole groups, so that
+// dgate leaves from their registers and dpw and dpb stay there like the next norm's sums.
+template <typename TR, typename TB, int LPR, int KCH, bool EXACT, bool OWN>
 __global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const ResNormArgs a)
 {
     constexpr int THREADS = threads_of(LPR), G = THREADS / LPR;
@@ -419,101 +421,152 @@ __global__ __launch_bounds__(threads_of(LPR)) void res_norm_bwd_kernel(const Res
         for (int c = threadIdx.x; c < C; c += THREADS) dst[c] = part[c];
     };
     int slot = 0;
-    for (int64_t from = begin; from < end;) {
-        // the rows of one gate
-        const int64_t g = a.groups > 1 ? from / a.rows : 0;
-        const int64_t to = a.groups > 1 ? min(end, (g + 1) * a.rows) : end;
+    // the row that is in q*; `valid`: it is one of this lane's
+    const auto work = [&](int64_t row, bool valid) {
+        float t[KCH][8], h[KCH][8], u = 0.f, v = 0.f;
 #pragma unroll
         for (int i = 0; i < KCH; ++i) {
-            const int c = (i * LPR + l) * 8;
-            float p[8];
-            param(a.gate ? a.gate + g * C : nullptr, 1.f, c, C, gq[i]);
-            param(a.post ? a.pw : nullptr, 1.f, c, C, p);
+            const int left = valid ? C - (i * LPR + l) * 8 : 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                gq[i][e] *= a.bs * p[e];
+                const bool in = EXACT ? 0 < left : e < left;
+                const float y = in ? element(qy[i], e) : 0.f;
+                h[i][e] = in ? (element(qo[i], e) - qs.z) * qs.w : 0.f;
+                s3[i][e] += y * h[i][e];
+                s4[i][e] += y;
+                t[i][e] = y * w[i][e];
+                u += t[i][e];
+                v += t[i][e] * h[i][e];
+            }
+        }
+        row_sum2<LPR>(u, v, red, slot);
+        u = a.layer ? u / fc : 0.f;
+        v /= fc;
+        Raw<TR, 8> dr[KCH];
+        Raw<TB, 8> db[KCH];
+        float m = 0.f, n = 0.f;
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            const int left = valid ? C - (i * LPR + l) * 8 : 0;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool in = EXACT ? 0 < left : e < left;
+                t[i][e] = (has_dout ? element(qd[i], e) : 0.f) + qs.w * (t[i][e] - u - h[i][e] * v);
+                t[i][e] = in ? t[i][e] : 0.f;
+                f[e] = a.rs * t[i][e];
+                const float x = in ? element(qb[i], e) : 0.f;
+                h[i][e] = a.post ? (in ? (x - qs.x) * qs.y : 0.f) : x;
+                s1[i][e] += t[i][e] * h[i][e];
+                s2[i][e] += t[i][e];
+                t[i][e] *= gq[i][e];
+                m += t[i][e];
+                n += t[i][e] * h[i][e];
+            }
+            dr[i] = to_raw<TR, 8>(f);
+        }
+        if (a.post) {
+            row_sum2<LPR>(m, n, red, slot);
+            m = a.layer ? m / fc : 0.f;
+            n /= fc;
+#pragma unroll
+            for (int i = 0; i < KCH; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[i][e] = qs.y * (t[i][e] - m - h[i][e] * n);
+        }
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) db[i] = to_raw<TB, 8>(t[i]);
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            qy[i] = ny[i];
+            qb[i] = nb[i];
+            qd[i] = nd[i];
+            qo[i] = no[i];
+        }
+        qs = ns;
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            const int c = (i * LPR + l) * 8, left = valid ? C - c : 0;
+            store_row<EXACT>(static_cast<TR *>(a.dr) + row * a.lddr + c, left, dr[i]);
+            store_row<EXACT>(static_cast<TB *>(a.db) + row * a.lddb + c, left, db[i]);
+        }
+    };
+    // gq = gate post_weight branch_scale, and the group's sums cleared
+    const auto start = [&](const float (&gate)[KCH][8]) {
+#pragma unroll
+        for (int i = 0; i < KCH; ++i) {
+            float p[8];
+            param(a.post ? a.pw : nullptr, 1.f, (i * LPR + l) * 8, C, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                gq[i][e] = gate[i][e] * (a.bs * p[e]);
                 s1[i][e] = s2[i][e] = 0.f;
             }
         }
-        load(min(from + q, a.N - 1), qy, qb, qd, qo, qs);
-        for (int64_t row = from + q; row < to; row += G) {
-            load(min(row + G, a.N - 1), ny, nb, nd, no, ns);
-            float t[KCH][8], h[KCH][8], u = 0.f, v = 0.f;
+    };
+    const auto gate_of = [&](int64_t g, float (&gate)[KCH][8]) {
 #pragma unroll
-            for (int i = 0; i < KCH; ++i) {
-                const int left = C - (i * LPR + l) * 8;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool in = EXACT ? 0 < left : e < left;
-                    const float y = in ? element(qy[i], e) : 0.f;
-                    h[i][e] = in ? (element(qo[i], e) - qs.z) * qs.w : 0.f;
-                    s3[i][e] += y * h[i][e];
-                    s4[i][e] += y;
-                    t[i][e] = y * w[i][e];
-                    u += t[i][e];
-                    v += t[i][e] * h[i][e];
-                }
+        for (int i = 0; i < KCH; ++i) param(a.gate ? a.gate + g * C : nullptr, 1.f, (i * LPR + l) * 8, C, gate[i]);
+    };
+    if constexpr (OWN) {
+        const int64_t units = int64_t(gridDim.x) * G, unit = int64_t(blockIdx.x) * G + q;
+        int64_t g = first_row(a.groups, units, unit);
+        const int64_t last = first_row(a.groups, units, unit + 1), rounds = (a.groups + units - 1) / units;
+        float gate[KCH][8], next[KCH][8], p1[KCH][8] = {}, p2[KCH][8] = {};
+        load(min(g * a.rows, a.N - 1), qy, qb, qd, qo, qs);
+        gate_of(min(g, a.groups - 1), gate);
+        // every lane makes the same number of rounds
+        for (int64_t round = 0; round < rounds; ++round, ++g) {
+            const bool valid = g < last;
+            start(gate);
+            for (int64_t r = 0; r < a.rows; ++r) {
+                const int64_t row = g * a.rows + r;
+                load(min(row + 1, a.N - 1), ny, nb, nd, no, ns);
+                if (r + 1 == a.rows) gate_of(min(g + 1, a.groups - 1), next);
+                work(row, valid);
             }
-            row_sum2<LPR>(u, v, red, slot);
-            u = a.layer ? u / fc : 0.f;
-            v /= fc;
-            Raw<TR, 8> dr[KCH];
-            Raw<TB, 8> db[KCH];
-            float m = 0.f, n = 0.f;
-#pragma unroll
-            for (int i = 0; i < KCH; ++i) {
-                const int left = C - (i * LPR + l) * 8;
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool in = EXACT ? 0 < left : e < left;
-                    t[i][e] = (has_dout ? element(qd[i], e) : 0.f) + qs.w * (t[i][e] - u - h[i][e] * v);
-                    t[i][e] = in ? t[i][e] : 0.f;
-                    f[e] = a.rs * t[i][e];
-                    const float x = in ? element(qb[i], e) : 0.f;
-                    h[i][e] = a.post ? (in ? (x - qs.x) * qs.y : 0.f) : x;
-                    s1[i][e] += t[i][e] * h[i][e];
-                    s2[i][e] += t[i][e];
-                    t[i][e] *= gq[i][e];
-                    m += t[i][e];
-                    n += t[i][e] * h[i][e];
-                }
-                dr[i] = to_raw<TR, 8>(f);
-            }
-            if (a.post) {
-                row_sum2<LPR>(m, n, red, slot);
-                m = a.layer ? m / fc : 0.f;
-                n /= fc;
-#pragma unroll
-                for (int i = 0; i < KCH; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) t[i][e] = qs.y * (t[i][e] - m - h[i][e] * n);
-            }
-#pragma unroll
-            for (int i = 0; i < KCH; ++i) db[i] = to_raw<TB, 8>(t[i]);
-#pragma unroll
-            for (int i = 0; i < KCH; ++i) {
-                qy[i] = ny[i];
-                qb[i] = nb[i];
-                qd[i] = nd[i];
-                qo[i] = no[i];
-            }
-            qs = ns;
 #pragma unroll
             for (int i = 0; i < KCH; ++i) {
                 const int c = (i * LPR + l) * 8;
-                store_row<EXACT>(static_cast<TR *>(a.dr) + row * a.lddr + c, C - c, dr[i]);
-                store_row<EXACT>(static_cast<TB *>(a.db) + row * a.lddb + c, C - c, db[i]);
+                float pw[8], pb[8], d[8];
+                param(a.post ? a.pw : nullptr, 1.f, c, C, pw);
+                param(a.post ? a.pb : nullptr, 0.f, c, C, pb);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p1[i][e] += gate[i][e] * s1[i][e];
+                    p2[i][e] += gate[i][e] * s2[i][e];
+                    d[e] = a.bs * (pw[e] * s1[i][e] + pb[e] * s2[i][e]);
+                    gate[i][e] = next[i][e];
+                }
+                if (a.dgate && valid) store_some<8>(a.dgate + g * C + c, max(C - c, 0), d);
             }
         }
-        if (records) {
-            float *rec = sums.record + (blockIdx.x + g) * 2 * C;
-            flush(s1, rec);
-            flush(s2, rec + C);
-            if (threadIdx.x == 0) sums.group[blockIdx.x + g] = int(g);
-            if (to == end && a.groups > 1 && end % a.rows == 0 && end < a.N) skip_record<THREADS>(sums, blockIdx.x + g + 1, C);
+        if (records) {                         // (branch_scale is the second launch's)
+            flush(p1, sums.record + int64_t(blockIdx.x) * 2 * C);
+            flush(p2, sums.record + (int64_t(blockIdx.x) * 2 + 1) * C);
         }
-        from = to;
+    } else {
+        for (int64_t from = begin; from < end;) {
+            // the rows of one gate
+            const int64_t g = a.groups > 1 ? from / a.rows : 0;
+            const int64_t to = a.groups > 1 ? min(end, (g + 1) * a.rows) : end;
+            float gate[KCH][8];
+            gate_of(g, gate);
+            start(gate);
+            load(min(from + q, a.N - 1), qy, qb, qd, qo, qs);
+            for (int64_t row = from + q; row < to; row += G) {
+                load(min(row + G, a.N - 1), ny, nb, nd, no, ns);
+                work(row, true);
+            }
+            if (records) {
+                float *rec = sums.record + (blockIdx.x + g) * 2 * C;
+                flush(s1, rec);
+                flush(s2, rec + C);
+                if (threadIdx.x == 0) sums.group[blockIdx.x + g] = int(g);
+                if (to == end && a.groups > 1 && end % a.rows == 0 && end < a.N) skip_record<THREADS>(sums, blockIdx.x + g + 1, C);
+            }
+            from = to;
+        }
     }
     if (!a.ws) return;
     flush(s3, sums.norm + int64_t(blockIdx.x) * 2 * C);
@@ -830,6 +883,18 @@ int64_t bwd_blocks(int64_t N, int64_t C)
     return g.lpr ? blocks_of(N, g, true) : std::max<int64_t>(1, std::min(N, kColBlocks));
 }
 
+// Whether each row's lanes take whole groups of rows with a gate: where a workgroup would
+// leave sums every few rows, and groups enough to keep half of all lanes at work, or so short
+// that few rows wait for each other. us of a workgroup's rows group by group, and so:
+// 65536 rows of 64, bf16, 65536 groups 2796 and 39, 4096 groups (half of the lanes) 196 and
+// 38; 16384 of 1024, 512 groups (half) 78 and 69; 3000 of 512, fp32, 375 groups of 8 (a
+// third) 31 and 24; 19941 of 1001, 69 groups (one lane in 15) 93 and 591.
+bool own_groups(const ResNormArgs &a, const Group &g)
+{
+    if (!g.lpr || a.groups <= 1) return false;
+    return a.rows <= 8 || 2 * a.groups >= 256 * (threads_of(g.lpr) / g.lpr);
+}
+
 }  // namespace
 
 int64_t res_norm_bwd_ws_bytes(int64_t N, int64_t C, int64_t groups)
@@ -873,6 +938,7 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
     }
     const Group g = group_of(a.C, true);
     const int64_t B = bwd_blocks(a.N, a.C);
+    const bool own = own_groups(a, g);
     const hipError_t e = with_norm_types(a.dtype, a.branch_dtype, [&](auto tr, auto tb) {
         using TR = typename decltype(tr)::type;
         using TB = typename decltype(tb)::type;
@@ -887,22 +953,34 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
         }
         return with_group<true>(g, [&](auto lpr, auto kch) {
             constexpr int LPR = decltype(lpr)::value, KCH = decltype(kch)::value;
-            const dim3 grid{unsigned(B)}, threads(threads_of(LPR));
+            const dim3 threads(threads_of(LPR));
+            const auto launch = [&](auto exact) {
+                constexpr bool EXACT = decltype(exact)::value;
+                if (own)
+                    hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, EXACT, true>), dim3(unsigned(B)), threads, 0, s,
+                                       a);
+                else
+                    hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, EXACT, false>), dim3(unsigned(B)), threads, 0,
+                                       s, a);
+                return hipGetLastError();
+            };
             if constexpr (LPR > 1)
-                if (a.C % 8 == 0) {
-                    hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, true>), grid, threads, 0, s, a);
-                    return hipGetLastError();
-                }
-            hipLaunchKernelGGL((res_norm_bwd_kernel<TR, TB, LPR, KCH, false>), grid, threads, 0, s, a);
-            return hipGetLastError();
+                if (a.C % 8 == 0) return launch(std::true_type{});
+            return launch(std::false_type{});
         });
     });
     if (e != hipSuccess || !a.ws) return e;
+    ResNormArgs j = a;
+    if (own) {                                 // dgate is there, dpw and dpb one sum per workgroup
+        j.gate = nullptr;
+        j.dgate = nullptr;
+        j.groups = 0;
+    }
     const int W = join_channels(a.C);
-    const int64_t G = std::max<int64_t>(a.groups, 1), tiles = (a.C + W - 1) / W;
-    const int64_t gates = !a.dgate ? 0 : short_groups(B, G) ? (G * a.C + 255) / 256 : G * tiles;
+    const int64_t G = std::max<int64_t>(j.groups, 1), tiles = (a.C + W - 1) / W;
+    const int64_t gates = !j.dgate ? 0 : short_groups(B, G) ? (G * a.C + 255) / 256 : G * tiles;
     hipLaunchKernelGGL(res_norm_join_kernel, dim3(unsigned(std::min<int64_t>(2 * tiles + gates, 8192))), dim3(1024), 0, s,
-                       a, B);
+                       j, B);
     return hipGetLastError();
 }
 

@@ -393,7 +393,8 @@ def test_residual_norm_of_short_rows(N, C, G, rt, bt):
 
 @pytest.mark.parametrize("rt,bt", [("f32", "bf16"), ("f16", "f16")])
 @pytest.mark.parametrize("N,C,G", [(5000, 64, 50), (20000, 256, 1), (4096, 1000, 4096), (3000, 520, 1000), (777, 24, 777),
-                                   (2310, 96, 7), (1024, 3000, 3), (600, 9000, 60)])
+                                   (2310, 96, 7), (1024, 3000, 3), (600, 9000, 60), (40960, 64, 4096), (1300, 6000, 325),
+                                   (9000, 1001, 600), (60000, 3, 6000)])
 def test_residual_norm_of_many_rows_and_gates(N, C, G, rt, bt):
     if N % max(G, 1):
         N = N // G * G
@@ -415,9 +416,9 @@ def test_residual_norm_without_parameters_or_gradients(C):
 
 
 @pytest.mark.parametrize("some", ["gate", "post_weight", "post_bias", "weight", "bias"])
-@pytest.mark.parametrize("C", [100, 9001])
-def test_residual_norm_single_gradients(some, C):
-    c = _rn_case(30, C, 5, "f32", "f32", True)
+@pytest.mark.parametrize("N,C", [(30, 100), (330, 100), (30, 9001), (500, 5)])
+def test_residual_norm_single_gradients(some, N, C):
+    c = _rn_case(N, C, 5, "f32", "f32", True)
     kw = dict(gate=c["gate"], post_weight=c["pw"], post_bias=c["pb"], weight=c["w"])
     out, _, st = conv.residual_norm(c["b"], c["r"], bias=c["bias"], **kw)
     dr, db, want = conv.residual_norm_backward(c["dy"], c["dout"], c["b"], out, st, **kw)
