@@ -34,7 +34,7 @@ class BlockHead:
             return torch.randn(*shape, generator=gen, device=device) * shape[-1] ** -0.5
         vec = lambda value: torch.full((channels,), value, device=device)      # noqa: E731
         self.dtype, self.blocks = dtype, blocks
-        # norms and gates first, then the products' weights; 8 vectors and matrices a block
+        # norms and gates first, then the products' weights; 4 vectors and 3 matrices a block
         self.vectors = [vec(1.0), vec(0.0)] + [v for _ in range(blocks) for v in (vec(0.5), vec(1.0), vec(1.0), vec(0.0))]
         self.weights = [w for _ in range(blocks)
                         for w in (rnd(hidden, channels), rnd(hidden, channels), rnd(channels, hidden))] + [rnd(classes, channels)]

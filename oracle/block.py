@@ -1,6 +1,6 @@
 """Plain 64-bit forms of the block operators (feed-forward block, norms around a
 residual sum, AdamW with 32- and 8-bit states), written from their definitions in
-elementary torch operations on whatever device the inputs are on. Checker only: it
+elementary torch operations on whatever device the inputs are on. For tests only: it
 shares no code with the HIP library."""
 from __future__ import annotations
 
