@@ -99,9 +99,11 @@ __device__ __forceinline__ int exact_level4(double x, uint32_t u)
 // The same in fp32: the level, and in `least` the least of what decides it less the error
 // of that (of 65536 times the value's share of its interval, `width` wide, against u).
 // x is within 3 roundings and a reciprocal's ulp (3e-7 of it) of the exact one, so the
-// error is less than 2 of u's steps. Next to an end of the interval, where the exact x may
-// lie in the next one, both decide alike unless u is within 2 of its own ends; those are
-// left to fp64 too (one wave in thirty has some).
+// error is less than 2 of u's steps. Next to an end of the interval the exact x may lie in
+// the next one, or c be that one's for the square roots' ulps (of x: 2.4e-7 for m, 7.2e-7
+// for v's two): up to 1.02e-6 x / width <= 6.5e-5 of the interval, 4.3 steps, and both
+// decide alike unless u is within 5 of its own ends; within 6 is left to fp64 (one wave in
+// eleven has some).
 __device__ __forceinline__ float level2(float x, float u, float &least)
 {
     const float c = floorf(__builtin_amdgcn_sqrtf(x));
@@ -242,7 +244,7 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
             // (a scale so small that its reciprocal leaves fp32, or the scale its normal
             // numbers, is fp64's affair)
             const bool tiny = (sm > 0.f && !(sm > 1e-30f)) || (sv > 0.f && !(sv > 1e-26f));
-            if (!(least > 0.f) || lowest < 2 || highest > 65533 || tiny) {
+            if (!(least > 0.f) || lowest < 6 || highest > 65529 || tiny) {
                 const double xm = sm > 0.f ? kTopM / double(sm) : 0.0, xv = sv > 0.f ? kTopV / double(sv) : 0.0;
 #pragma unroll
                 for (int e = 0; e < kLane; ++e) {
