@@ -10,7 +10,7 @@
 // The types of p and g are a workgroup's affair: it branches once to the code for its
 // tensor's, so that all loads go out together.
 // 200 million elements, fp32 states, bf16 gradients and copies: 1091 us (5.1 TB/s). 40
-// million in 150 tensors, 8-bit states: 198 us (3.2 TB/s), for the VALU has 440
+// million in 150 tensors, 8-bit states: 205 us (3.1 TB/s), for the VALU has 440
 // instructions to a wave's 256 elements, those of fp64 and the square roots the longest.
 //
 // 8-bit states: m, v and the scales are formed in fp64, so that the level that an element
