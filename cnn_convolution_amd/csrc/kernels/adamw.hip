@@ -241,10 +241,13 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
                 lowest = min(lowest, min(um16, uv16));
                 highest = max(highest, max(um16, uv16));
             }
-            // (a scale so small that its reciprocal leaves fp32, or the scale its normal
-            // numbers, is fp64's affair)
-            const bool tiny = (sm > 0.f && !(sm > 1e-30f)) || (sv > 0.f && !(sv > 1e-26f));
-            if (!(least > 0.f) || lowest < 6 || highest > 65529 || tiny) {
+            // A scale so small that its reciprocal leaves fp32, or the scale its normal
+            // numbers, is fp64's affair; so is one whose reciprocal is no normal number (above
+            // 2^126), for the hardware's is 0 then.
+            const auto apart = [](float scale, float least_scale) {
+                return scale > 0.f && !(scale > least_scale && scale < 8e37f);
+            };
+            if (!(least > 0.f) || lowest < 6 || highest > 65529 || apart(sm, 1e-30f) || apart(sv, 1e-26f)) {
                 const double xm = sm > 0.f ? kTopM / double(sm) : 0.0, xv = sv > 0.f ? kTopV / double(sv) : 0.0;
 #pragma unroll
                 for (int e = 0; e < kLane; ++e) {
