@@ -406,7 +406,6 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
     if count == 0 or len(grads) != count or len(state.sizes) != count:
         raise ValueError("params, grads and state must be of the same, non-zero number of tensors")
     dev = _device(params[0], "params[0]")
-    _code(params[0].dtype)                   # (what the checks below need of torch)
     words, types = _TABLE_WORDS, _checked(params, "params", state.sizes, dev)
     table = state._entries(*_state_pointers(state, dev))
     whole, real = memoryview(table).cast("q"), memoryview(table).cast("d")

@@ -48,9 +48,11 @@ def _code(dtype) -> int:
 
 
 def _device(t, name) -> int:
-    """The device index of a device tensor."""
+    """The device index of a device tensor; every entry point begins here."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    if _codes is None:
+        _torch_names()
     return t.get_device()
 
 

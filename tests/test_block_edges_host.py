@@ -1,0 +1,36 @@
+"""Block operators without a GPU: a process's first call, limits that are refused before
+anything is enqueued, workspace sizes."""
+import os
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+FIRST = """
+import os, sys
+import torch
+from cnn_convolution_amd import _block, _head
+import test_block_host, test_head_binding_host
+torch._C._cuda_getDevice = lambda: 1
+torch._C._cuda_getCurrentRawStream = lambda index: 7
+seen = []
+_block.call = _head.call = lambda name, *args: seen.append((name, args[-1]))
+for calls in (test_block_host._calls(), test_head_binding_host._calls()):
+    for name, f in calls.items():
+        pid = os.fork()
+        if pid == 0:
+            try:
+                f()
+                os._exit(0 if seen == [(name, 7)] else 2)
+            except Exception as e:
+                print(name, repr(e), flush=True)
+                os._exit(1)
+        print(name, os.waitstatus_to_exitcode(os.waitpid(pid, 0)[1]), flush=True)
+"""
+
+
+def test_every_entry_point_may_be_a_process_first_call():
+    """What the entry points need of torch is looked up by whichever is called first."""
+    out = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, cwd=ROOT,
+                         env={**os.environ, "PYTHONPATH": f"{ROOT}:{ROOT}/tests"}, check=True).stdout
+    assert len(out.splitlines()) == 11 and all(line.endswith(" 0") for line in out.splitlines()), out
