@@ -278,14 +278,22 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
     // With 8 bits the arithmetic is what a step waits for: the hardware's square root and
     // reciprocal, an ulp off each (150 cycles of a SIMD less per element than whole ones)
     // unless so small an eps lets a denormal v count, which that root takes for 0.
+    float step_of[kLane];
     if (BITS == 8 && f.w > 1e-12f) {
 #pragma unroll
         for (int e = 0; e < kLane; ++e)
-            p[e] = p[e] * f.x - f.y * m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e]) * f.z + f.w);
+            step_of[e] = f.y * m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e]) * f.z + f.w);
     } else {
 #pragma unroll
-        for (int e = 0; e < kLane; ++e) p[e] = p[e] * f.x - f.y * m[e] / (sqrtf(v[e]) * f.z + f.w);
+        for (int e = 0; e < kLane; ++e) step_of[e] = f.y * m[e] / (sqrtf(v[e]) * f.z + f.w);
     }
+    // (p times 1 - lr weight_decay would take that factor's rounding, 2^-25, for the decay's
+    // own: 1.3 % of one of 10^-6, the same way at every step. An infinite p stays so: its decay
+    // is the largest finite number's.)
+    constexpr float kMost = 3.402823466e38f;
+#pragma unroll
+    for (int e = 0; e < kLane; ++e)
+        p[e] -= __builtin_fmaf(f.x, __builtin_amdgcn_fmed3f(p[e], -kMost, kMost), step_of[e]);
     store_some<kLane>(pp + i, left, p);
     if (t.copy)
         with_type(t.ct, [&](auto z) { store_some<kLane>(static_cast<decltype(z) *>(t.copy) + first + i, left, p); });
@@ -315,8 +323,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs a)
         root = float(factor[1]);
     }
     const float lr = t.lr * (a.lr_ptr ? *a.lr_ptr : 1.f), gs = a.grad_scale * (a.grad_scale_ptr ? *a.grad_scale_ptr : 1.f);
-    // p keep - rate m / (sqrt(v) root + eps)
-    const float4 f{float(1.0 - double(lr) * double(t.decay)), float(double(lr) * rate), root, a.eps};
+    // p - (decay p + rate m / (sqrt(v) root + eps))
+    const float4 f{float(double(lr) * double(t.decay)), float(double(lr) * rate), root, a.eps};
     with_type(t.pt, [&](auto p) {
         with_type(t.gt, [&](auto g) {
             if (first + adam_chunk(BITS) <= t.n)

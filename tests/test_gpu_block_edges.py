@@ -7,9 +7,10 @@ import cnn_convolution_amd as conv
 from cnn_convolution_amd import _lib
 from oracle import block as ref
 from test_gpu_block import _scales
-from test_gpu_head import DEV
+from test_gpu_head import DEV, U, _close
 
 pytestmark = pytest.mark.gpu
+INF = float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -48,3 +49,31 @@ def test_adamw_8_bit_scales_above_2_126():
     conv.adamw([p], [torch.zeros(n, device=DEV)], state, 2, 0.0, seed=6)
     assert bool((state.exp_avg_scale[:3] > 2.0 ** 126).all())
     _codes_follow(state, 0.9 * m0, 0.999 * v0, 2, 6)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("steps", [17.5, 3.5, 1000.5])
+def test_adamw_decay_keeps_its_digits(bits, steps):
+    """lr * weight_decay of a few and a half of fp32's steps below 1: p (1 - lr weight_decay) is
+    rounded once, and the rates and their product to fp32."""
+    p = 0.1 * torch.randn(100000, generator=torch.Generator().manual_seed(2))
+    q = p.to(DEV)
+    lr, decay = 1e-3, steps * 2.0 ** -24 / 1e-3
+    conv.adamw([q], [torch.zeros_like(q)], conv.adamw_state([q], bits), 1, lr, weight_decay=decay)
+    want = p.double() * (1 - lr * decay)
+    _close(q, want, 1.001 * U * want.abs() + 5 * U * lr * decay * p.double().abs() + 2.0 ** -149, "p")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+def test_adamw_infinite_parameters_stay(bits, decay):
+    """p (1 - lr weight_decay) - step of an infinite p, and the others as they are without it."""
+    gen = torch.Generator().manual_seed(1)
+    p, g = torch.randn(300, generator=gen).to(DEV), torch.randn(300, generator=gen).to(DEV)
+    q = p.clone()
+    q[7], q[261] = INF, -INF
+    for t in (p, q):
+        conv.adamw([t], [g], conv.adamw_state([t], bits), 1, 1e-2, weight_decay=decay)
+    assert q[7] == INF and q[261] == -INF
+    p[7], p[261] = INF, -INF
+    assert torch.equal(p, q)
