@@ -276,10 +276,11 @@ __device__ __forceinline__ void adamw_elements(const AdamArgs &a, const AdamTens
         }
     }
     // With 8 bits the arithmetic is what a step waits for: the hardware's square root and
-    // reciprocal, an ulp off each (150 cycles of a SIMD less per element than whole ones)
-    // unless so small an eps lets a denormal v count, which that root takes for 0.
+    // reciprocal, an ulp off each (150 cycles of a SIMD less per element than whole ones),
+    // unless a denormal v counts, which that root takes for 0: its term is at most 2^-63 root,
+    // and more than eps 2^-24 of the denominator where eps is below 1.8e-12 root.
     float step_of[kLane];
-    if (BITS == 8 && f.w > 1e-12f) {
+    if (BITS == 8 && f.w > 2e-12f * f.z) {
 #pragma unroll
         for (int e = 0; e < kLane; ++e)
             step_of[e] = f.y * m[e] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[e]) * f.z + f.w);

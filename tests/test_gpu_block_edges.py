@@ -77,3 +77,15 @@ def test_adamw_infinite_parameters_stay(bits, decay):
     assert q[7] == INF and q[261] == -INF
     p[7], p[261] = INF, -INF
     assert torch.equal(p, q)
+
+
+def test_adamw_8_bit_denominators_of_denormal_v():
+    """A beta2 next to 1 brings a v that is no normal fp32 number up to eps."""
+    beta2, eps = 1 - 1e-12, 3e-12
+    g = torch.full((300,), 1e-13)
+    p = torch.zeros(300, device=DEV)
+    conv.adamw([p], [g.to(DEV)], conv.adamw_state([p], 8), 1, 1e-3, beta2=beta2, eps=eps)
+    want, m, v = ref.adamw(torch.zeros(300), g, torch.zeros(300), torch.zeros(300), 1, 1e-3, 0.9, beta2, eps, 0.0)
+    assert 0 < v.max().item() < 2.0 ** -126
+    # v is off by half a subnormal step, 2^-150 of 10^-38 or 2^-23 of it
+    _close(p, want, 32 * U * want.abs(), "p")
