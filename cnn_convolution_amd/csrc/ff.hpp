@@ -32,15 +32,20 @@ struct FfGate {
 hipError_t launch_ff_gate(const FfGate &a, int dtype, int tile, hipStream_t s);
 
 // da and du, each [rows_pad] rows of Fp with zeros past N and F, side by side in rows of
-// 2 from.ldh
+// 2 from.ldh; fp16: times their row's scale, and x the other way for the weights' gradients
 struct FfBack {
     const void *dy, *wd;
     int64_t lddy, ldd;       // bytes
     int64_t N, F, O, Op, rows_pad, Fp;
     FfSaved from;
     void *g;
-    const float *amax;       // [kAmaxParts]: of |dy|, or null (no scale)
     int act;
+    // fp16 (see ff_common.hpp):
+    const float *amax;       // [2][kAmaxParts]: of |dy|, of |x|
+    const float *scale;      // [N]: of the rows of da and du
+    const void *x;           // its rows as the caller has them
+    int64_t ldx, D, Dp, ldt; // elements
+    void *to_x;              // [N] rows of Dp, ldt apart: x times what its row's scale leaves
 };
 hipError_t launch_ff_back(const FfBack &a, int dtype, int tile, hipStream_t s);
 constexpr int kAmaxParts = 256;
@@ -61,7 +66,8 @@ struct FfProduct {
     float *slab;             // [split][outs n][M] fp32, or null
     void *out[2];
     int64_t ldo;             // elements
-    const float *amax;       // the outputs are divided by the scale it gives, or null
+    const float *amax;       // the outputs are divided by the scales it gives, or null
+    const float *scale;      // or each row by its own (one output), or null
 };
 hipError_t launch_ff_y(const FfProduct &p, int dtype, int tile, hipStream_t s);
 hipError_t launch_ff_dx(const FfProduct &p, int dtype, int tile, hipStream_t s);

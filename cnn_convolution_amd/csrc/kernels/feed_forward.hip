@@ -17,7 +17,7 @@
 namespace im2win {
 namespace {
 
-// ---- rows padded to whole granules, the largest |dy| -------------------------------
+// ---- rows padded to whole granules, the rows' largest |dy| --------------------------
 
 struct PadJob {
     const void *src;
@@ -29,9 +29,11 @@ struct PadJob {
 struct PadArgs {
     PadJob job[5];
     int count;
-    const void *dy;          // of which the largest finite |value| is wanted, or null
-    int64_t lddy, N, O;
-    float *amax;             // [kAmaxParts]: of every kAmaxParts-th row
+    const void *dy;          // of which the largest finite |values| are wanted, or null
+    const void *x;           // and its, of rows whose dy is not 0
+    int64_t lddy, ldx, N, O, D;
+    float *amax;             // [2][kAmaxParts]: of a workgroup's rows, of dy and of x
+    float *scale;            // [N]: S of each row
 };
 
 template <typename T>
@@ -42,21 +44,52 @@ __global__ __launch_bounds__(256) void ff_pad_kernel(const PadArgs a)
     const int64_t copies = a.count ? a.job[a.count - 1].end : 0;
     int64_t b = blockIdx.x;
     if (b >= copies) {
-        __shared__ float red[4];
+        // a row to a wave, or where there are few to a workgroup
+        __shared__ float red[3][4];
+        const bool few = a.N <= kAmaxParts;
+        const int lanes = few ? 256 : 64, at = few ? int(threadIdx.x) : lane;
         b -= copies;
-        float m = 0.f;
-        for (int64_t r = b; r < a.N; r += kAmaxParts)
-            for (int64_t c = threadIdx.x * E; c < a.O; c += 256 * E) {
+        float most = 0.f, most_x = 0.f, own = 0.f;
+        bool some = false;
+        // the largest finite |value| of a row that these lanes read, and whether it has any but 0
+        const auto row_max = [&](const void *p, int64_t ld, int64_t r, int64_t n, bool &any) {
+            float m = 0.f;
+            for (int64_t c = at * E; c < n; c += lanes * E) {
                 float f[E];
-                load_some<E>(static_cast<const T *>(a.dy) + r * a.lddy + c, a.O - c, f);
+                load_some<E>(static_cast<const T *>(p) + r * ld + c, n - c, f);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
+                for (int e = 0; e < E; ++e) {
                     if (fabsf(f[e]) < __builtin_inff()) m = fmaxf(m, fabsf(f[e]));
+                    any = any || f[e] != 0.f;
+                }
             }
-        for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
-        if (lane == 0) red[wave] = m;
+            for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
+            any = __any(any);
+            return m;
+        };
+        for (int64_t r = few ? b : b * 4 + wave; r < a.N; r += few ? kAmaxParts : 4 * kAmaxParts) {
+            bool any = false, any_x = false;
+            own = row_max(a.dy, a.lddy, r, a.O, any);
+            const float x = row_max(a.x, a.ldx, r, a.D, any_x);
+            some = any;
+            most = fmaxf(most, own);
+            if (any || few) most_x = fmaxf(most_x, x);
+            if (!few && lane == 0) a.scale[r] = any ? scale_of(own) : kZeroRow;
+        }
+        if (lane == 0) {
+            red[0][wave] = most;
+            red[1][wave] = most_x;
+            red[2][wave] = some ? 1.f : 0.f;
+        }
         __syncthreads();
-        if (threadIdx.x == 0) a.amax[b] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        if (threadIdx.x == 0) {
+            const auto of = [&](const float (&v)[4]) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
+            const float m = of(red[0]);
+            const bool zeros = few && of(red[2]) == 0.f;      // the workgroup's one row, or none
+            a.amax[b] = m;
+            a.amax[kAmaxParts + b] = zeros ? 0.f : of(red[1]);
+            if (few && b < a.N) a.scale[b] = zeros ? kZeroRow : scale_of(m);
+        }
         return;
     }
     int k = 0;
@@ -381,7 +414,7 @@ struct FfPlan {
     bool copy_x, copy_g, copy_u, copy_d, copy_y;   // rows not made of 16-byte granules
     int gate_tile, y_tile, y_split, back_tile, dx_tile, dx_split, dd_tile, dd_split, dg_tile, dg_split;
     int all_tile;            // of dx, dWd, dWg and dWu in one launch, or -1
-    int64_t off_x, off_g, off_u, off_d, off_dy, off_h, off_lo, off_slab_x, off_slab_d, off_slab_g, off_grad, off_amax, bytes;
+    int64_t off_x, off_g, off_u, off_d, off_dy, off_h, off_lo, off_slab_x, off_slab_d, off_slab_g, off_grad, off_amax, off_scale, bytes;
     int64_t pre_bytes;       // of saved, before h
 };
 
@@ -537,10 +570,15 @@ FfPlan plan_bwd(const FfSizes &z)
     FfPlan p = plan_common(z);
     if (z.N == 0) return p;
     const int64_t es = elem(z.dtype), ki = 128 / es;
+    if (z.dtype == 1) p.copy_x = false;        // x is written anew
     plan_copies(p, z);
     if (p.copy_y) p.off_dy = take(p, z.N * p.ldo * es);
     p.off_grad = take(p, p.rows_pad * 2 * p.ldf * es);
-    p.off_amax = take(p, kAmaxParts * 4);
+    if (z.dtype == 1) {
+        p.off_x = take(p, z.N * p.ldd * es);
+        p.off_amax = take(p, 2 * kAmaxParts * 4);
+        p.off_scale = take(p, z.N * 4);
+    }
     p.back_tile = pick_tile(p.Fp, z.N, ceil_div(z.O, ki), z.dtype, 0, int(8 + 2 * es), true);
     const Product dx{z.D, z.N, 2 * ceil_div(z.F, ki), 1}, dd{z.F, z.O, ceil_div(z.N, ki), 1}, dg{z.D, z.F, dd.stages, 2};
     double apart = 0.0;
@@ -599,10 +637,14 @@ hipError_t launch_pads(const FfPlan &p, const FfArgs &a, bool backward, FfRead *
         add(p.copy_y, a.dy, z.ldy, z.N, z.O, p.Op, p.ldo, p.off_dy, r->dy, r->lddy);
         if (z.dtype == 1) {
             pad.dy = a.dy;
+            pad.x = a.x;
             pad.lddy = z.ldy;
+            pad.ldx = z.ldx;
+            pad.D = z.D;
             pad.N = z.N;
             pad.O = z.O;
             pad.amax = reinterpret_cast<float *>(ws + p.off_amax);
+            pad.scale = reinterpret_cast<float *>(ws + p.off_scale);
             groups += kAmaxParts;
         }
     }
@@ -724,9 +766,12 @@ hipError_t launch_ff_bwd(const FfArgs &a, hipStream_t s)
     FfRead r{};
     hipError_t e = launch_pads(p, a, true, &r, s);
     if (e != hipSuccess) return e;
-    const float *amax = z.dtype == 1 ? reinterpret_cast<const float *>(ws + p.off_amax) : nullptr;
+    const bool scaled = z.dtype == 1;
+    const float *amax = scaled ? reinterpret_cast<const float *>(ws + p.off_amax) : nullptr;
+    const float *scale = scaled ? reinterpret_cast<const float *>(ws + p.off_scale) : nullptr;
     const FfSaved from = saved_of(p, a.saved, nullptr);
-    const FfBack back{r.dy, r.wd, r.lddy, r.ldd, z.N, z.F, z.O, p.Op, p.rows_pad, p.Fp, from, ws + p.off_grad, amax, z.act};
+    const FfBack back{r.dy, r.wd, r.lddy, r.ldd, z.N, z.F, z.O, p.Op, p.rows_pad, p.Fp, from, ws + p.off_grad, z.act,
+                      amax, scale, a.x, z.ldx, z.D, p.Dp, p.ldd, scaled ? ws + p.off_x : nullptr};
     if ((e = launch_ff_back(back, z.dtype, p.back_tile, s)) != hipSuccess) return e;
 
     FfProduct dx{}, dd{}, dg{};
@@ -748,10 +793,11 @@ hipError_t launch_ff_bwd(const FfArgs &a, hipStream_t s)
     dx.slab = p.dx_split > 1 ? reinterpret_cast<float *>(ws + p.off_slab_x) : nullptr;
     dx.out[0] = a.dx;
     dx.ldo = dg.ldo = z.D;
-    dx.amax = dg.amax = amax;
+    dx.scale = scale;
+    dg.amax = amax;
 
-    dg.a[0] = r.x;
-    dg.lda[0] = r.ldx;
+    dg.a[0] = scaled ? ws + p.off_x : r.x;
+    dg.lda[0] = scaled ? p.ldd * es : r.ldx;
     dg.n = z.F;
     dg.b_count = p.Fp;
     dg.K = dg.k_a = z.N;

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "ff_common.hpp"
 #include "head_gemm.hpp"
@@ -26,14 +27,14 @@ __device__ __forceinline__ void product_tiles(const FfProduct &a, int tiles_m, i
                                               char *smem)
 {
     constexpr int KI = 128 / int(sizeof(T));
-    constexpr bool HALF = sizeof(T) == 2;
+    constexpr bool HALF = sizeof(T) == 2, SCALED = std::is_same<T, _Float16>::value;
     constexpr int STORES = HALF ? C::FM * C::FN / 2 : C::FM * C::FN;    // of a wave and whole tile, at least
     // tiles_n: of all outputs
     const int tiles = tiles_m * tiles_n, all = tiles * a.split, per_out = tiles_n / a.outs;
     const int nk = int((a.K + KI - 1) / KI);               // stages of a segment
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % C::WM, wn = wave / C::WM;
     const int mw = wm * (C::BM / C::WM), nw = wn * (C::BN / C::WN);
-    const float inv = a.amax ? 1.f / dy_scale(a.amax) : 1.f;
+    const float inv = a.amax ? 1.f / (dy_scale(a.amax) * x_scale(a.amax)) : 1.f;
     TilePipe<T, C, ACOLS, BCOLS> pipe(smem);
     int part = 0, o = 0;
     int64_t m0 = 0, n0 = 0;
@@ -92,8 +93,11 @@ __device__ __forceinline__ void product_tiles(const FfProduct &a, int tiles_m, i
                 continue;
             }
             T *p = static_cast<T *>(co ? a.out[1] : a.out[0]) + row * a.ldo;
+            float by = inv;
+            if constexpr (SCALED)
+                if (a.scale) by = 1.f / a.scale[row];
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i) acc[i][j] *= inv;
+            for (int i = 0; i < C::FM; ++i) acc[i][j] *= by;
             if constexpr (HALF) {
                 const int64_t m8 = mt + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
 #pragma unroll
@@ -193,7 +197,7 @@ __global__ __launch_bounds__(256) void ff_join_kernel(const FfJoin j)
     __shared__ float4 sum[Q > 1 ? 256 : 1];
     constexpr int CH = 256 / Q;
     const int64_t step = int64_t(gridDim.x) * CH, total = j.end[j.count - 1];
-    const float inv = j.amax ? 1.f / dy_scale(j.amax) : 1.f;
+    const float inv = j.amax ? 1.f / (dy_scale(j.amax) * x_scale(j.amax)) : 1.f;
     const int t = threadIdx.x % CH, q = threadIdx.x / CH;
     for (int64_t i0 = int64_t(blockIdx.x) * CH; i0 < total; i0 += step) {
         const int64_t i = min(i0 + t, total - 1);
@@ -232,9 +236,10 @@ __global__ __launch_bounds__(256) void ff_join_kernel(const FfJoin j)
             }
         }
         if (i0 + t >= total) continue;
-        if (a.amax) {
+        if (a.amax || a.scale) {
+            const float by = a.scale ? 1.f / a.scale[r] : inv;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) f[v] *= inv;
+            for (int v = 0; v < 4; ++v) f[v] *= by;
         }
         const int o = int(r / a.n);
         store_some<4>(static_cast<T *>(o ? a.out[1] : a.out[0]) + (r - o * a.n) * a.ldo + m, left, f);

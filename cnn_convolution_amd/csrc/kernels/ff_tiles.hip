@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "ff_common.hpp"
 #include "head_gemm.hpp"
@@ -166,9 +167,39 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_gate_kernel(const 
     }
 }
 
-template <typename T, typename C>
-__global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const FfBack a, int tiles_m, int tiles_n)
+// x as the weights' gradients of fp16 read it (ff_common.hpp), a row to a wave
+template <typename T>
+__device__ __forceinline__ void scale_x(const FfBack &a, int block, int blocks, int waves)
 {
+    constexpr int E = 16 / int(sizeof(T));
+    const int lane = threadIdx.x & 63;
+    const float least = dy_scale(a.amax), to = x_scale(a.amax);
+    for (int64_t row = int64_t(block) * waves + (threadIdx.x >> 6); row < a.N; row += int64_t(blocks) * waves) {
+        const float by = to * fminf(least / a.scale[row], 1.f);
+        const T *src = static_cast<const T *>(a.x) + row * a.ldx;
+        T *dst = static_cast<T *>(a.to_x) + row * a.ldt;
+#pragma unroll 4
+        for (int64_t c = lane * E; c < a.Dp; c += 64 * E) {
+            float f[E];
+            load_some<E>(src + c, a.D - c, f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] *= by;
+            store_vec<E>(dst + c, f);
+        }
+    }
+}
+
+// `groups` workgroups for the tiles; fp16: the others for x, where the tiles leave time
+template <typename T, typename C>
+__global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const FfBack a, int tiles_m, int tiles_n,
+                                                                          int groups)
+{
+    constexpr bool SCALED = std::is_same<T, _Float16>::value;
+    if constexpr (SCALED)
+        if (int(blockIdx.x) >= groups) {
+            scale_x<T>(a, int(blockIdx.x) - groups, int(gridDim.x) - groups, C::threads / 64);
+            return;
+        }
     using E = typename EpiOf<C>::type;         // how the waves hold a tile's sums
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -189,8 +220,7 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
             pipe.start(A, B, m0, n0, 0, stages);
     };
     start(blockIdx.x);
-    const float S = a.amax ? dy_scale(a.amax) : 1.f;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (int t = blockIdx.x; t < tiles; t += groups) {
         const int64_t ft = m0 + wm * (E::BM / E::WM), nt = n0 + wn * (E::BN / E::WN);
         floatx4_t acc[E::FM][E::FN];
         NoExtra none;
@@ -201,7 +231,7 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
         } else {
             pipe.template run<0>(false, acc, none);
         }
-        if (t + int(gridDim.x) < tiles) start(t + gridDim.x);
+        if (t + groups < tiles) start(t + groups);
         // The factors of H blocks at a time, AHEAD groups of them requested before they are
         // used: one pair at a time, waited for, this epilogue took longer than its products
         // (8192 rows, 4096 outputs, 16384 hidden features, bf16: 1606 us). Past the last
@@ -216,6 +246,10 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
             for (int i = 0; i < 2 * H; ++i)
                 ring[q % (AHEAD + 1)][i / 2][i % 2] = *reinterpret_cast<const floatx4_t *>(p + i * 1024 + lane * 16);
         };
+        float rows[SCALED ? E::FN : 1];        // the rows' own scales
+        if constexpr (SCALED)
+#pragma unroll
+            for (int j = 0; j < E::FN; ++j) rows[j] = a.scale[min(nt + 16 * j + (lane & 15), a.N - 1)];
 #pragma unroll
         for (int q = 0; q < AHEAD && q < GROUPS; ++q) request(q);
 #pragma unroll
@@ -227,15 +261,19 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
             floatx4_t da[H], du[H];
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                const floatx4_t dh = acc[i0 + i][j] * S;
-                du[i] = dh * ring[q % (AHEAD + 1)][i][0];
-                da[i] = dh * ring[q % (AHEAD + 1)][i][1];
+                du[i] = acc[i0 + i][j] * ring[q % (AHEAD + 1)][i][0];
+                da[i] = acc[i0 + i][j] * ring[q % (AHEAD + 1)][i][1];
             }
-            if (nt + 16 * j < a.rows_pad) {
-                T *g = static_cast<T *>(a.g) + row * 2 * a.from.ldh + ft + i0 * 16;
-                store_blocks<T, H>(g, int(a.Fp - ft) - i0 * 16, lane, da);
-                store_blocks<T, H>(g + a.from.ldh, int(a.Fp - ft) - i0 * 16, lane, du);
-            }
+            if (nt + 16 * j >= a.rows_pad) continue;
+            if constexpr (SCALED)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    da[i] *= rows[j];
+                    du[i] *= rows[j];
+                }
+            T *g = static_cast<T *>(a.g) + row * 2 * a.from.ldh + ft + i0 * 16;
+            store_blocks<T, H>(g, int(a.Fp - ft) - i0 * 16, lane, da);
+            store_blocks<T, H>(g + a.from.ldh, int(a.Fp - ft) - i0 * 16, lane, du);
         }
     }
 }
@@ -266,8 +304,16 @@ template <typename T, typename C>
 hipError_t launch_back(const FfBack &a, hipStream_t s)
 {
     const int64_t tm = ceil_div(a.Fp, C::BM), tn = ceil_div(a.rows_pad, C::BN);
+    if (tm * tn > kMaxTiles) return hipErrorInvalidValue;
     static std::atomic<uint64_t> allowed;
-    return launch_tiles<C>(ff_back_kernel<T, C>, a, tm, tn, ceil_div(a.O * int64_t(sizeof(T)), 128), allowed, s);
+    const auto kernel = ff_back_kernel<T, C>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
+    if (e != hipSuccess) return e;
+    const int64_t groups = grid_of<C>(tm * tn, ceil_div(a.O * int64_t(sizeof(T)), 128));
+    const int64_t more = std::is_same<T, _Float16>::value ? std::min<int64_t>(ceil_div(a.N, C::threads / 64), 1024) : 0;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(groups + more)), dim3(C::threads), C::lds_bytes, s, a, int(tm), int(tn),
+                       int(groups));
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -43,8 +43,9 @@ extern "C" {
  *
  * All products are accumulated in fp32, a, u and dh are fp32 throughout; h, da and
  * du are rounded to the type of x where the matrix cores read them (fp16: h has to
- * stay in that type's range; da and du are held times a power of two that brings
- * the largest finite |dy| into [1/16, 1/8)); with at most FF_ROWS rows y is formed from
+ * stay in that type's range; da and du are held times a power of two for each row, which
+ * brings its largest finite |dy| into [1/16, 1/8), and x for the weights' gradients over
+ * it); with at most FF_ROWS rows y is formed from
  * an h of twice those digits. The outputs are rounded once. Limits: N <= 2^22; D, F, O
  * and the row strides <= 2^20. N = 0 gives zero weight gradients. */
 enum { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2, FF_RELU = 3, FF_SIGMOID = 4 };

@@ -6,8 +6,8 @@ import torch
 import cnn_convolution_amd as conv
 from cnn_convolution_amd import _lib
 from oracle import block as ref
-from test_gpu_block import _scales
-from test_gpu_head import DEV, U, _close
+from test_gpu_block import _ff_bounds, _ff_case, _scales
+from test_gpu_head import DEV, SUB, U, _close, _say
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -89,3 +89,63 @@ def test_adamw_8_bit_denominators_of_denormal_v():
     assert 0 < v.max().item() < 2.0 ** -126
     # v is off by half a subnormal step, 2^-150 of 10^-38 or 2^-23 of it
     _close(p, want, 32 * U * want.abs(), "p")
+
+
+# ---- feed-forward block ----------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,D,F,O", [(3, 96, 136, 64), (40, 33, 70, 45), (300, 96, 136, 64), (700, 256, 1000, 200)])
+def test_feed_forward_rows_of_dy_far_apart(N, D, F, O, dt):
+    """dx of each row within its own bound where the rows' gradients spread over 2^20, and
+    the same bits whatever another row's gradient is."""
+    x, wg, wu, wd, dy = _ff_case(N, D, F, O, dt, seed=N)
+    k = (torch.arange(N, device=DEV) * 7 % 21) - 10
+    dy = (dy.float() * 2.0 ** k[:, None]).to(dy.dtype)
+    _say(f"feed-forward rows apart N={N} {dt}")
+    _, saved = conv.feed_forward(x, wg, wu, wd)
+    got = conv.feed_forward_backward(dy, x, wg, wu, wd, saved)
+    some = sorted({0, 1, 2, N // 2, N - 1} | set(range(0, N, max(1, N // 12))))
+    for n in some:
+        r = slice(n, n + 1)
+        tol, want = _ff_bounds(x[r], wg, wu, wd, dy[r], "silu", dt, False)
+        _close(got[0][r], want[1], tol[1], f"dx of row {n}")
+    tol, want = _ff_bounds(x, wg, wu, wd, dy, "silu", dt, False)
+    for g, w, t, name in zip(got[1:], want[2:], tol[2:], ("dw_gate", "dw_up", "dw_down")):
+        _close(g, w, t, name)
+    other = dy.clone()
+    other[1] *= 16
+    rest = torch.arange(N, device=DEV) != 1
+    assert torch.equal(conv.feed_forward_backward(other, x, wg, wu, wd, saved)[0][rest], got[0][rest])
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -10, 1.0, 2.0 ** 6])
+@pytest.mark.parametrize("N", [30, 300])
+def test_feed_forward_weights_gradients_beside_a_large_row(N, scale, dt):
+    """Inputs that are 0 in the row with the largest dy: their weights' gradients are those of
+    the other rows, 2^12 smaller, within those rows' own bounds; a row of zeros in dy adds
+    nothing whatever finite values its x holds."""
+    x, wg, wu, wd, dy = _ff_case(N, 96, 136, 64, dt, seed=N)
+    # x of that scale, and a and u as they were
+    x, wg, wu = (x.float() * scale).to(x.dtype), (wg.float() / scale).to(wg.dtype), (wu.float() / scale).to(wu.dtype)
+    dy = (dy.float() * 2.0 ** -8).to(dy.dtype)
+    dy[3] *= 4096.0
+    x[3, :48] = 0
+    dy[5] = 0
+    _, saved = conv.feed_forward(x, wg, wu, wd)
+    got = conv.feed_forward_backward(dy, x, wg, wu, wd, saved)
+    rest = torch.arange(N, device=DEV) != 3
+    tol, want = _ff_bounds(x[rest], wg, wu, wd, dy[rest], "silu", dt, False)
+    da, du = ref.feed_forward_grad(dy[rest], x[rest], wg, wu, wd, "silu")[4:]
+    for k, grad in ((2, da), (3, du)):
+        # fp16's x times M / S: half a subnormal step of it, |dy| up to 2^14 of the row's here
+        more = (grad.abs().sum(0) * SUB["f16"] * 2.0 ** 14 * x.abs().max().item() / 64)[:, None] if dt == "f16" else 0.0
+        _close(got[k - 1][:, :48], want[k][:, :48], tol[k][:, :48] + more, ("dw_gate", "dw_up")[k - 2])
+    tol, want = _ff_bounds(x, wg, wu, wd, dy, "silu", dt, False)
+    for g, w, t, name in zip(got, want[1:], tol[1:], ("dx", "dw_gate", "dw_up", "dw_down")):
+        _close(g, w, t, name)
+    big = x.clone()
+    big[5, ::2] = 6e4 if dt == "f16" else 3e6
+    _, other = conv.feed_forward(x, wg, wu, wd)
+    for a, b in zip(conv.feed_forward_backward(dy, big, wg, wu, wd, other)[:3], got[:3]):
+        assert torch.equal(a, b)
