@@ -289,7 +289,8 @@ __global__ __launch_bounds__(WAVES * 64) void ff_rows_gate_kernel(const FfRows a
     if (sizeof(T) == 4 || row >= a.N) return;
     float rest[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) rest[v] = h[v] - element(hi, v);
+    for (int v = 0; v < 4; ++v)              // (an infinite h has no second part)
+        rest[v] = fabsf(element(hi, v)) < __builtin_inff() ? h[v] - element(hi, v) : 0.f;
     store_vec<4>(static_cast<T *>(a.lo) + row * a.to.ldh + m, rest);
 }
 

@@ -42,8 +42,8 @@ extern "C" {
  * (its slope at 0 is 0), FF_SIGMOID 1 / (1 + exp(-a)).
  *
  * All products are accumulated in fp32, a, u and dh are fp32 throughout; h, da and
- * du are rounded to the type of x where the matrix cores read them (fp16: h has to
- * stay in that type's range; da and du are held times a power of two for each row, which
+ * du are rounded to the type of x where the matrix cores read them (fp16: an h beyond
+ * that type's range is infinite; da and du are held times a power of two for each row, which
  * brings its largest finite |dy| into [1/16, 1/8), and x for the weights' gradients over
  * it); with at most FF_ROWS rows y is formed from
  * an h of twice those digits. The outputs are rounded once. Limits: N <= 2^22; D, F, O

@@ -149,3 +149,17 @@ def test_feed_forward_weights_gradients_beside_a_large_row(N, scale, dt):
     _, other = conv.feed_forward(x, wg, wu, wd)
     for a, b in zip(conv.feed_forward_backward(dy, big, wg, wu, wd, other)[:3], got[:3]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N", [1, 16, 40, 70])
+@pytest.mark.parametrize("F", [9, 16])
+def test_feed_forward_h_beyond_fp16_is_infinite(N, F):
+    """An h that the type does not hold is infinite, and so are the sums it goes into."""
+    x = torch.ones(N, 8, dtype=torch.float16, device=DEV)
+    wg, wu = (torch.full((F, 8), 0.25, dtype=torch.float16, device=DEV) for _ in range(2))
+    wg[2], wu[2] = 40.0, 40.0                         # h = 320^2 = 102400
+    wd = torch.tensor([[0.5], [-0.5]], device=DEV).expand(2, F).contiguous().half()
+    y = conv.feed_forward(x, wg, wu, wd, "relu", save=False)[0]
+    assert bool((y[:, 0] == INF).all()) and bool((y[:, 1] == -INF).all())
+    y, saved = conv.feed_forward(x, wg, wu, wd, "relu")
+    assert bool((y[:, 0] == INF).all()) and bool((y[:, 1] == -INF).all())
