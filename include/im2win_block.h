@@ -45,9 +45,10 @@ extern "C" {
  * du are rounded to the type of x where the matrix cores read them (fp16: an h beyond
  * that type's range is infinite; da and du are held times a power of two for each row, which
  * brings its largest finite |dy| into [1/16, 1/8), and x for the weights' gradients over
- * it); with at most FF_ROWS rows y is formed from
- * an h of twice those digits. The outputs are rounded once. Limits: N <= 2^22; D, F, O
- * and the row strides <= 2^20. N = 0 gives zero weight gradients. */
+ * it). y of few rows is formed from an h of twice those digits: of at most 16 rows, and of
+ * at most FF_ROWS where Wg's, Wu's or Wd's rows or row strides are no multiples of 16 bytes.
+ * The outputs are rounded once. Limits: N <= 2^22; D, F, O and the row strides <= 2^20.
+ * N = 0 gives zero weight gradients. */
 enum { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2, FF_RELU = 3, FF_SIGMOID = 4 };
 enum { FF_ROWS = 64 };
 
@@ -62,8 +63,9 @@ typedef struct {
 } feed_forward_desc_t;
 
 /* Rows and row strides that are multiples of 16 bytes are read in place and have
- * to start on a 16-byte boundary; other rows may start anywhere and, for more than
- * FF_ROWS rows or a backward pass, are copied into the workspace first.
+ * to start on a 16-byte boundary; other rows may start anywhere and are copied into the
+ * workspace first, but for a forward pass of at most 16 rows, or of at most FF_ROWS in fp32
+ * or where the weights' rows are such ones.
  *
  * saved: what feed_forward_bwd needs of the forward pass (act(a) and u act'(a) in fp32,
  * h), feed_forward_saved_size() bytes, 256-byte aligned; NULL when no backward pass

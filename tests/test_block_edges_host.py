@@ -4,6 +4,8 @@ import os
 import subprocess
 import sys
 
+from cnn_convolution_amd import _block, _lib
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 FIRST = """
@@ -34,3 +36,17 @@ def test_every_entry_point_may_be_a_process_first_call():
     out = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, cwd=ROOT,
                          env={**os.environ, "PYTHONPATH": f"{ROOT}:{ROOT}/tests"}, check=True).stdout
     assert len(out.splitlines()) == 11 and all(line.endswith(" 0") for line in out.splitlines()), out
+
+
+def test_forward_workspaces_hold_the_copies_that_the_header_names():
+    """x of 17 to 64 rows that are no whole granules is copied beside weights whose rows are,
+    not beside others, in half precision; never in fp32."""
+    def size(N, D, ldx, ldg, dtype):
+        d = _block.FeedForwardDesc(N, D, 512, 64, ldx, ldg, 0, 0, 0, dtype, 0, 0, 0)
+        return _block.size("feed_forward_fwd_workspace_size", d, 1)
+    for dtype in (_lib.F16, _lib.BF16):
+        assert size(40, 64, 68, 0, dtype) - size(40, 64, 0, 0, dtype) == 40 * 64 * 2
+        assert size(40, 64, 68, 68, dtype) == size(40, 64, 0, 68, dtype)
+        assert size(16, 64, 68, 0, dtype) == size(16, 64, 0, 0, dtype)
+        assert size(65, 64, 68, 68, dtype) - size(65, 64, 0, 68, dtype) == 33 * 256           # 65 * 128 bytes in whole 256
+    assert size(64, 64, 65, 0, _lib.F32) == size(64, 64, 0, 0, _lib.F32)

@@ -163,3 +163,16 @@ def test_feed_forward_h_beyond_fp16_is_infinite(N, F):
     assert bool((y[:, 0] == INF).all()) and bool((y[:, 1] == -INF).all())
     y, saved = conv.feed_forward(x, wg, wu, wd, "relu")
     assert bool((y[:, 0] == INF).all()) and bool((y[:, 1] == -INF).all())
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("N,D,F,pad", [(16, 64, 512, 0), (17, 63, 512, 0), (64, 64, 515, 0), (40, 500, 1031, 0), (33, 64, 512, 4),
+                                       (17, 64, 512, 0), (64, 64, 512, 0), (33, 64, 512, 8), (65, 63, 511, 0)])
+def test_feed_forward_rows_with_h_in_two_parts(N, D, F, pad, dt):
+    """y of at most 16 rows, and of up to 64 where the weights' rows are no whole granules, is
+    within the bound of an h that is not rounded."""
+    x, wg, wu, wd, dy = _ff_case(N, D, F, 64, dt, seed=F)
+    wu = torch.cat([wu, wu.new_zeros(F, pad)], 1)[:, :D]
+    two = N <= 16 or (N <= 64 and (D % 8 != 0 or F % 8 != 0 or pad % 8 != 0))
+    tol, want = _ff_bounds(x, wg, wu, wd, dy, "silu", dt, two)
+    _close(conv.feed_forward(x, wg, wu, wd, save=False)[0], want[0], tol[0], "y")
