@@ -1,5 +1,7 @@
 """Edges of the block kernels: values at the ends of the types' ranges, rows far apart in
 size, saturated activations (the bounds' notation is test_gpu_block.py's)."""
+import math
+
 import pytest
 import torch
 
@@ -7,7 +9,7 @@ import cnn_convolution_amd as conv
 from cnn_convolution_amd import _lib
 from oracle import block as ref
 from test_gpu_block import _ff_bounds, _ff_case, _scales
-from test_gpu_head import DEV, SUB, U, _close, _say
+from test_gpu_head import DEV, SUB, TYPES, U, UO, _close, _say
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -176,3 +178,45 @@ def test_feed_forward_rows_with_h_in_two_parts(N, D, F, pad, dt):
     two = N <= 16 or (N <= 64 and (D % 8 != 0 or F % 8 != 0 or pad % 8 != 0))
     tol, want = _ff_bounds(x, wg, wu, wd, dy, "silu", dt, two)
     _close(conv.feed_forward(x, wg, wu, wd, save=False)[0], want[0], tol[0], "y")
+
+
+def _activations(act, dt, a):
+    """(act(a), act'(a)) as the block forms them: one input that is 1, Wg = a, Wu = 1, Wd = 1, a
+    row of its own for each feature's output."""
+    n = a.numel()
+    one = torch.ones(1, 1, dtype=TYPES[dt], device=DEV)
+    wg, wu = a.to(DEV).to(TYPES[dt]).reshape(n, 1), one.expand(n, 1).contiguous()
+    wd, dy = torch.eye(n, device=DEV).to(TYPES[dt]), one.expand(1, n).contiguous()
+    y, saved = conv.feed_forward(one, wg, wu, wd, act)
+    return y[0], conv.feed_forward_backward(dy, one, wg, wu, wd, saved, act)[1][:, 0]
+
+
+def _exact_activations(act, a):
+    a = a.double()
+    if act == "gelu":
+        return 0.5 * a * torch.erfc(-a / math.sqrt(2)), \
+            0.5 * torch.erfc(-a / math.sqrt(2)) + a * torch.exp(-a * a / 2) / math.sqrt(2 * math.pi)
+    if act == "gelu_tanh":
+        k = 2 * math.sqrt(2 / math.pi)
+        s, q = 1 / (1 + torch.exp(-k * a * (1 + 0.044715 * a * a))), 1 / (1 + torch.exp(k * a * (1 + 0.044715 * a * a)))
+        return a * s, s + a * s * q * k * (1 + 3 * 0.044715 * a * a)
+    s, q = 1 / (1 + torch.exp(-a)), 1 / (1 + torch.exp(a))
+    return (s, s * q) if act == "sigmoid" else (a * s, s * (1 + a * q))
+
+
+@pytest.mark.parametrize("act,end,dt", [("gelu", 9.0, "f16"), ("gelu", 9.0, "bf16")])
+def test_feed_forward_saturated_activations(act, end, dt):
+    """act(a) far from 0 on either side, and sigmoid's slope, keep their own digits."""
+    a = torch.linspace(-end, end, 513).to(TYPES[dt]).float()
+    f, df = _exact_activations(act, a)
+    y, da = _activations(act, dt, a)
+    A = a.double().abs()
+    # exp of z = a, a^2 / 2 or twice tanh's argument, within 6 |z| u for the roundings of its argument
+    # (8 for the tanh's) and a few u; erfc within 16 ulp, or in half precision 2^-20 of itself
+    z = {"gelu": A * A / 2, "gelu_tanh": 1.5958 * A * (1 + 0.04472 * A * A) * 8 / 6}.get(act, A)
+    rel = (6 * z + 48) * U + (2.0 ** -20 if act == "gelu" and dt != "f32" else 0.0)
+    # half precision: h in two parts, y rounded
+    _close(y, f, rel * f.abs() + 1.01 * UO[dt] * f.abs() + 2 * SUB[dt], "act")
+    # the slope's terms, rounded twice in half precision (da held times 1/16 in fp16)
+    terms = {"gelu": f.abs() / A.clamp(min=1e-30) + A * torch.exp(-A * A / 2) * 0.4, "sigmoid": df}.get(act, f.abs() + 1)
+    _close(da, df, rel * terms + 2.02 * UO[dt] * df.abs() + 17 * SUB[dt], "slope")
