@@ -31,7 +31,7 @@ __device__ __forceinline__ void activate(int act, float a, float &f, float &df)
         df = silu ? s * (1.f + a * (1.f - s)) : s * (1.f - s);
     } else if (act == FF_GELU) {
         if constexpr (EXACT) {
-            const float c = 0.5f * (1.f + erff(a * 0.70710678118654752f));
+            const float c = 0.5f * erfcf(a * -0.70710678118654752f);   // (1 + erf has no digits left below -5)
             f = a * c;
             df = c + a * (expf(-0.5f * a * a) * 0.39894228040143268f);
         } else {
