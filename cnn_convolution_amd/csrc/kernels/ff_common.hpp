@@ -24,11 +24,17 @@ __device__ __forceinline__ float logistic(float a)
 template <bool EXACT>
 __device__ __forceinline__ void activate(int act, float a, float &f, float &df)
 {
-    if (act == FF_SILU || act == FF_SIGMOID) {
+    if (act == FF_SILU) {
         const float s = logistic<EXACT>(a);
-        const bool silu = act == FF_SILU;
-        f = silu ? a * s : s;
-        df = silu ? s * (1.f + a * (1.f - s)) : s * (1.f - s);
+        f = a * s;
+        df = s * (1.f + a * (1.f - s));
+    } else if (act == FF_SIGMOID) {
+        // the smaller of f and 1 - f from the exponential: 1 - f by itself has no digits
+        // left where f is next to 1
+        const float x = fabsf(a), e = EXACT ? expf(-x) : __builtin_amdgcn_exp2f(x * -1.4426950408889634f);
+        const float r = EXACT ? 1.f / (1.f + e) : __builtin_amdgcn_rcpf(1.f + e);
+        f = a < 0.f ? e * r : r;
+        df = e * r * r;
     } else if (act == FF_GELU) {
         if constexpr (EXACT) {
             const float c = 0.5f * erfcf(a * -0.70710678118654752f);   // (1 + erf has no digits left below -5)

@@ -204,7 +204,9 @@ def _exact_activations(act, a):
     return (s, s * q) if act == "sigmoid" else (a * s, s * (1 + a * q))
 
 
-@pytest.mark.parametrize("act,end,dt", [("gelu", 9.0, "f32"), ("gelu", 9.0, "f16"), ("gelu", 9.0, "bf16")])
+@pytest.mark.parametrize("act,end,dt", [
+    (act, end, dt) for act, end in (("gelu", 9.0), ("sigmoid", 16.0), ("silu", 16.0), ("gelu_tanh", 6.0))
+    for dt in ("f32", "f16", "bf16")])
 def test_feed_forward_saturated_activations(act, end, dt):
     """act(a) far from 0 on either side, and sigmoid's slope, keep their own digits."""
     a = torch.linspace(-end, end, 513).to(TYPES[dt]).float()
