@@ -55,8 +55,9 @@ __device__ __forceinline__ void activate(int act, float a, float &f, float &df)
             df = c + a * (e * 0.39894228040143268f);
         }
     } else if (act == FF_GELU_TANH) {
-        // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
-        const float k = 1.5957691216057308f, q = 0.044715f * a * a;
+        // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)); beyond 100 it is 0 or 1 whatever a^2 is,
+        // which must not be infinite beside the 0 in the slope
+        const float k = 1.5957691216057308f, q = 0.044715f * fminf(a * a, 1e4f);
         const float s = logistic<EXACT>(k * a * (1.f + q));
         f = a * s;
         df = s + a * s * (1.f - s) * k * (1.f + 3.f * q);

@@ -222,3 +222,16 @@ def test_feed_forward_saturated_activations(act, end, dt):
     # the slope's terms, rounded twice in half precision (da held times 1/16 in fp16)
     terms = {"gelu": f.abs() / A.clamp(min=1e-30) + A * torch.exp(-A * A / 2) * 0.4, "sigmoid": df}.get(act, f.abs() + 1)
     _close(da, df, rel * terms + 2.02 * UO[dt] * df.abs() + 17 * SUB[dt], "slope")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
+def test_feed_forward_activations_of_huge_values(act, dt):
+    """Finite a whose powers are no fp32 numbers: act is a or 1 on one side and 0 on the other,
+    its slope 1 or 0."""
+    a = torch.tensor([1e13, 1e20, 2e30, 1e38, -1e13, -1e20, -2e30, -1e38]).to(TYPES[dt]).float()
+    y, da = _activations(act, dt, a)
+    up = torch.ones(4) if act == "sigmoid" else a[:4]
+    assert torch.equal(y.float().cpu(), torch.cat([up, torch.zeros(4)]))
+    slope = torch.zeros(4) if act == "sigmoid" else torch.ones(4)
+    assert torch.equal(da.float().cpu(), torch.cat([slope, torch.zeros(4)]))
