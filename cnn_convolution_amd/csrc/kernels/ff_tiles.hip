@@ -265,6 +265,13 @@ __global__ __launch_bounds__(C::threads, C::per_simd) void ff_back_kernel(const 
                 da[i] = acc[i0 + i][j] * ring[q % (AHEAD + 1)][i][1];
             }
             if (nt + 16 * j >= a.rows_pad) continue;
+            // past the last row and feature zeros, also beside an infinite dy
+            if (nt + 16 * j + 16 > a.N || ft + (i0 + H) * 16 > a.F)
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (row >= a.N || ft + (i0 + i) * 16 + (lane >> 4) * 4 + v >= a.F) da[i][v] = du[i][v] = 0.f;
             if constexpr (SCALED)
 #pragma unroll
                 for (int i = 0; i < H; ++i) {

@@ -108,7 +108,7 @@ struct GemmOperand {
     const void *p;
     int64_t ld;              // bytes between rows (rows) or K rows (columns), a multiple of 16
     int64_t count;           // rows or columns that exist; columns: a multiple of 16 bytes' worth
-    int64_t k_end;           // K values that exist; columns repeat the last one past it
+    int64_t k_end;           // K values that exist, zeros past them
 };
 
 // one operand's tile: TB rows or columns, of which `count` exist in memory from
@@ -125,7 +125,6 @@ struct TileLoad {
     const char *base;        // of this tile at K = 0
     int64_t step;            // bytes per stage
     uint32_t off[per_wave];  // per lane, of each block
-    int64_t kstride;         // columns: bytes per K row
 
     // columns: slot of granule g in K row k is g ^ swz(k). 16 columns are 2
     // (half precision) or 4 granules, kept together; the K rows that one read
@@ -143,7 +142,6 @@ struct TileLoad {
     {
         const char *p = static_cast<const char *>(op.p);
         const int64_t ld_bytes = op.ld, count = op.count;
-        kstride = ld_bytes;
         if constexpr (!COLS) first = first < count ? first : count - 1;   // a tile of padding alone
         const int n = int(count - first < TB ? count - first : TB);       // at least 1
         if constexpr (!COLS) {
@@ -180,22 +178,16 @@ struct TileLoad {
     {
         copy_to_lds_at(base + s * step, off[i], __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
     }
-    // the last stage of a K that ends inside it (left < KI values): rows read
-    // zeros past it, columns repeat the last K row (the other operand has zeros
-    // there)
+    // the last stage of a K that ends inside it (left < KI values): zeros past it, for both
+    // operands (beside the other's zeros a repeated infinite value would leave NaN)
     __device__ __forceinline__ void issue_tail(int64_t stage, int left, uint32_t lds, int wave, int lane) const
     {
         const char *b = base + stage * step;
 #pragma unroll
         for (int i = 0; i < per_wave; ++i) {
-            const char *src;                 // left >= KI: the stage is whole
-            if constexpr (!COLS) {
-                const bool ok = ((lane & 7) ^ (lane >> 3)) * E < left;
-                src = ok ? b + off[i] : reinterpret_cast<const char *>(&zero_granule);
-            } else {
-                const int k = krow(wave, lane, i);
-                src = b + off[i] - int64_t(max(0, k - (left - 1))) * kstride;
-            }
+            // left >= KI: the stage is whole
+            const int k = COLS ? krow(wave, lane, i) : ((lane & 7) ^ (lane >> 3)) * E;
+            const char *src = k < left ? b + off[i] : reinterpret_cast<const char *>(&zero_granule);
             copy_to_lds(src, __builtin_amdgcn_readfirstlane(lds + block(wave, i) * 1024));
         }
     }

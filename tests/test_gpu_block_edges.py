@@ -235,3 +235,20 @@ def test_feed_forward_activations_of_huge_values(act, dt):
     assert torch.equal(y.float().cpu(), torch.cat([up, torch.zeros(4)]))
     slope = torch.zeros(4) if act == "sigmoid" else torch.ones(4)
     assert torch.equal(da.float().cpu(), torch.cat([slope, torch.zeros(4)]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [3, 70, 129, 700])
+def test_feed_forward_infinite_gradient_in_the_last_row(N, dt):
+    """Sums with one infinite term are infinite, not NaN, where the rows end inside a stage."""
+    x, wg, wu, wd, dy = _ff_case(N, 40, 136, 72, dt, seed=N)
+    _, saved = conv.feed_forward(x, wg, wu, wd)
+    dx0 = conv.feed_forward_backward(dy, x, wg, wu, wd, saved)[0]
+    dy[-1, 5] = INF
+    dx, dwg, dwu, dwd = conv.feed_forward_backward(dy, x, wg, wu, wd, saved)
+    want = ref.feed_forward_grad(dy.cpu(), *(t.cpu() for t in (x, wg, wu, wd)), "silu")
+    for got, w, name in ((dwg, want[1], "dw_gate"), (dwu, want[2], "dw_up"), (dwd, want[3], "dw_down")):
+        got = got.double().cpu()
+        inf = torch.isinf(w)
+        assert torch.equal(torch.isnan(got), torch.isnan(w)) and torch.equal(got[inf], w[inf]), name
+    assert torch.equal(dx[:-1], dx0[:-1])
