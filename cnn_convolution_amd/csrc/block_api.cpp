@@ -113,13 +113,13 @@ size_t feed_forward_saved_size(const feed_forward_desc_t *d)
 size_t feed_forward_fwd_workspace_size(const feed_forward_desc_t *d, int32_t with_saved)
 {
     FfSizes z;
-    return check_ff(d, &z) == CONV2D_OK ? size_t(ff_fwd_ws_bytes(z, with_saved != 0)) : 0;
+    return check_ff(d, &z) == CONV2D_OK ? size_t(std::max<int64_t>(ff_fwd_ws_bytes(z, with_saved != 0), 0)) : 0;
 }
 
 size_t feed_forward_bwd_workspace_size(const feed_forward_desc_t *d)
 {
     FfSizes z;
-    return check_ff(d, &z) == CONV2D_OK ? size_t(ff_bwd_ws_bytes(z)) : 0;
+    return check_ff(d, &z) == CONV2D_OK ? size_t(std::max<int64_t>(ff_bwd_ws_bytes(z), 0)) : 0;
 }
 
 conv2d_status_t feed_forward_fwd(const feed_forward_desc_t *d, const void *x, const void *w_gate, const void *w_up,
@@ -130,7 +130,9 @@ conv2d_status_t feed_forward_fwd(const feed_forward_desc_t *d, const void *x, co
     if (st != CONV2D_OK) return st;
     if (d->N == 0) return CONV2D_OK;
     if (!x || !w_gate || !w_up || !w_down || !y) return CONV2D_ERR_NULL_POINTER;
-    if (!ws && ff_fwd_ws_bytes(a.z, saved != nullptr)) return CONV2D_ERR_WORKSPACE;
+    const int64_t need = ff_fwd_ws_bytes(a.z, saved != nullptr);
+    if (need < 0) return CONV2D_ERR_INVALID_DESC;
+    if (!ws && need) return CONV2D_ERR_WORKSPACE;
     if (!ff_inputs_aligned(a.z, x, w_gate, w_up, w_down) || !aligned(y, esize(d->dtype)) || !aligned(saved, 256) ||
         !aligned(ws, 256))
         return CONV2D_ERR_MISALIGNED;
@@ -153,7 +155,9 @@ conv2d_status_t feed_forward_bwd(const feed_forward_desc_t *d, const void *dy, c
     if (st != CONV2D_OK) return st;
     if (!dw_gate || !dw_up || !dw_down) return CONV2D_ERR_NULL_POINTER;
     if (d->N > 0 && (!dy || !x || !w_gate || !w_up || !w_down || !saved || !dx)) return CONV2D_ERR_NULL_POINTER;
-    if (!ws && ff_bwd_ws_bytes(a.z)) return CONV2D_ERR_WORKSPACE;
+    const int64_t need = ff_bwd_ws_bytes(a.z);
+    if (need < 0) return CONV2D_ERR_INVALID_DESC;
+    if (!ws && need) return CONV2D_ERR_WORKSPACE;
     if (d->N > 0 && (!ff_inputs_aligned(a.z, x, w_gate, w_up, w_down) || !rows_aligned(dy, d->O, a.z.ldy, d->dtype)))
         return CONV2D_ERR_MISALIGNED;
     for (const void *p : {static_cast<const void *>(dx), static_cast<const void *>(dw_gate),

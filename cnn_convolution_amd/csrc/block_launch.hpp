@@ -24,6 +24,7 @@ struct FfArgs {
     void *dx, *dwg, *dwu, *dwd;
 };
 int64_t ff_saved_bytes(const FfSizes &z);
+// of workspace; -1: a launch would have more tiles than one can
 int64_t ff_fwd_ws_bytes(const FfSizes &z, bool saved);
 int64_t ff_bwd_ws_bytes(const FfSizes &z);
 hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s);

@@ -408,6 +408,7 @@ constexpr int64_t kPartGroups = 256, kMaxParts = 16;
 
 struct FfPlan {
     bool few;                // the kernels for few rows
+    bool fits;               // no launch has more tiles than one can
     int row_blocks, parts, tiles;   // blocks of rows a workgroup, parts of y's K, workgroups of a part if there are some
     int64_t off_count;
     int64_t Dp, Fp, Op, rows_pad, fblocks;
@@ -479,6 +480,14 @@ double pick(const Product &q, int dtype, int *tile, int *split)
     return best;
 }
 
+// whether a launch takes the product's tiles; one: with a workgroup for each
+bool fits(const Product &q, int dtype, int tile, int split, bool columns)
+{
+    const TileShape &t = kShapes[tile];
+    const bool one = columns && dtype && tile == kTile256;
+    return ceil_div(q.M, t.m) * ceil_div(q.N, t.n) * q.outs * split <= (one ? max_groups(C256::threads) : kMaxTiles);
+}
+
 // microseconds of three products in one launch of tiles t: what the chip's slots have to
 // do, but at least the longest workgroup; a product's K is split where its workgroups
 // would be longer than that share
@@ -504,6 +513,7 @@ double together_us(int t, const Product (&q)[3], int dtype, int (&split)[3])
 FfPlan plan_common(const FfSizes &z)
 {
     FfPlan p{};
+    p.fits = true;
     const int64_t es = elem(z.dtype), e = 16 / es;
     p.Dp = round_up(z.D, e);
     p.Fp = round_up(z.F, e);
@@ -561,7 +571,9 @@ FfPlan plan_fwd(const FfSizes &z, bool saved)
     plan_copies(p, z);
     if (!saved) p.off_h = take(p, p.rows_pad * p.ldf * es);
     p.gate_tile = pick_tile(2 * p.Fp, z.N, ceil_div(p.Dp, ki), z.dtype, int(es / 2), saved ? 4 : 0, false);
-    pick(Product{z.O, z.N, ceil_div(p.Fp, ki), 1}, z.dtype, &p.y_tile, &p.y_split);
+    const Product gate{2 * p.Fp, p.rows_pad, 0, 1}, y{z.O, z.N, ceil_div(p.Fp, ki), 1};
+    pick(y, z.dtype, &p.y_tile, &p.y_split);
+    p.fits = fits(gate, z.dtype, p.gate_tile, 1, false) && fits(y, z.dtype, p.y_tile, p.y_split, false);
     if (p.y_split > 1) p.off_slab_x = take(p, p.y_split * z.N * z.O * 4);
     return p;
 }
@@ -586,6 +598,9 @@ FfPlan plan_bwd(const FfSizes &z)
     apart += pick(dx, z.dtype, &p.dx_tile, &p.dx_split);
     apart += pick(dd, z.dtype, &p.dd_tile, &p.dd_split);
     apart += pick(dg, z.dtype, &p.dg_tile, &p.dg_split);
+    p.fits = fits(Product{p.Fp, p.rows_pad, 0, 1}, z.dtype, p.back_tile, 1, false) &&
+             fits(dx, z.dtype, p.dx_tile, p.dx_split, false) && fits(dd, z.dtype, p.dd_tile, p.dd_split, true) &&
+             fits(dg, z.dtype, p.dg_tile, p.dg_split, true);
     p.all_tile = -1;
     const Product all[3] = {dx, dd, dg};
     for (int t : {kTile128, kTile64}) {
@@ -707,8 +722,16 @@ int64_t ff_saved_bytes(const FfSizes &z)
     return p.pre_bytes + p.rows_pad * p.ldf * elem(z.dtype);
 }
 
-int64_t ff_fwd_ws_bytes(const FfSizes &z, bool saved) { return plan_fwd(z, saved).bytes; }
-int64_t ff_bwd_ws_bytes(const FfSizes &z) { return plan_bwd(z).bytes; }
+int64_t ff_fwd_ws_bytes(const FfSizes &z, bool saved)
+{
+    const FfPlan p = plan_fwd(z, saved);
+    return p.fits ? p.bytes : -1;
+}
+int64_t ff_bwd_ws_bytes(const FfSizes &z)
+{
+    const FfPlan p = plan_bwd(z);
+    return p.fits ? p.bytes : -1;
+}
 
 hipError_t launch_ff_fwd(const FfArgs &a, hipStream_t s)
 {

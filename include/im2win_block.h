@@ -47,8 +47,9 @@ extern "C" {
  * brings its largest finite |dy| into [1/16, 1/8), and x for the weights' gradients over
  * it). y of few rows is formed from an h of twice those digits: of at most 16 rows, and of
  * at most FF_ROWS where Wg's, Wu's or Wd's rows or row strides are no multiples of 16 bytes.
- * The outputs are rounded once. Limits: N <= 2^22; D, F, O and the row strides <= 2^20.
- * N = 0 gives zero weight gradients. */
+ * The outputs are rounded once. Limits: N <= 2^22; D, F, O and the row strides <= 2^20; sizes
+ * whose tiles are more than one launch takes (weights' gradients of a terabyte and more)
+ * are refused as an invalid descriptor. N = 0 gives zero weight gradients. */
 enum { FF_SILU = 0, FF_GELU = 1, FF_GELU_TANH = 2, FF_RELU = 3, FF_SIGMOID = 4 };
 enum { FF_ROWS = 64 };
 

@@ -1,5 +1,6 @@
 """Block operators without a GPU: a process's first call, limits that are refused before
 anything is enqueued, workspace sizes."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -50,3 +51,16 @@ def test_forward_workspaces_hold_the_copies_that_the_header_names():
         assert size(16, 64, 68, 0, dtype) == size(16, 64, 0, 0, dtype)
         assert size(65, 64, 68, 68, dtype) - size(65, 64, 0, 68, dtype) == 33 * 256           # 65 * 128 bytes in whole 256
     assert size(64, 64, 65, 0, _lib.F32) == size(64, 64, 0, 0, _lib.F32)
+
+
+def test_launches_that_cannot_be_are_refused_before_anything_is_enqueued():
+    """Weights' gradients of more tiles than one launch takes: an invalid descriptor, with no
+    workspace size, whatever the pointers are; smaller ones are none of that."""
+    for dtype in (_lib.F16, _lib.BF16):
+        for D, F, O in ((1 << 20, 1 << 18, 64), (64, 1 << 20, 1 << 20), (1 << 20, 1 << 20, 1 << 20)):
+            d = _block.FeedForwardDesc(8192, D, F, O, 0, 0, 0, 0, 0, dtype, 0, 0, 0)
+            assert _block.size("feed_forward_bwd_workspace_size", d) == 0
+            assert _block.lib().feed_forward_bwd(ctypes.byref(d), *[4096] * 11, None) == 1
+    for dtype in (_lib.F32, _lib.F16, _lib.BF16):
+        d = _block.FeedForwardDesc(8192, 1 << 18, 1 << 18, 1 << 18, 0, 0, 0, 0, 0, dtype, 0, 0, 0)
+        assert _block.size("feed_forward_bwd_workspace_size", d) > 0
