@@ -123,7 +123,8 @@ def feed_forward(x, w_gate, w_up, w_down, activation: str = "silu", *, save: boo
 def feed_forward_backward_into(dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, dw_up, dw_down, ws,
                                activation: str = "silu") -> None:
     """Enqueue the gradients of feed_forward for the gradient dy of its y, with what it
-    saved for the same x, weights and activation. dy is read as x is."""
+    saved for the same x and weights (its activation and slopes among it: ``activation`` is
+    checked and has no other effect). dy is read as x is."""
     d, dev = _ff_desc(x, w_gate, w_up, w_down, dy, activation)
     need = _block.size("feed_forward_bwd_workspace_size", d)
     _enqueue(dev, "feed_forward_bwd", d, _row_start(dy, "dy", d.O, d.ldy), *_ff_inputs(d, x, w_gate, w_up, w_down),
@@ -134,7 +135,8 @@ def feed_forward_backward_into(dy, x, w_gate, w_up, w_down, saved, dx, dw_gate, 
 
 
 def feed_forward_backward(dy, x, w_gate, w_up, w_down, saved, activation: str = "silu"):
-    """(dx, dw_gate, dw_up, dw_down) of feed_forward for the gradient dy of its y."""
+    """(dx, dw_gate, dw_up, dw_down) of feed_forward for the gradient dy of its y, with
+    the activation of the forward pass that ``saved`` is from."""
     import torch
     _device(x, "x")
     out = [torch.empty(t.shape, dtype=x.dtype, device=x.device) for t in (x, w_gate, w_up, w_down)]

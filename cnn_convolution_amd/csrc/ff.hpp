@@ -39,7 +39,6 @@ struct FfBack {
     int64_t N, F, O, Op, rows_pad, Fp;
     FfSaved from;
     void *g;
-    int act;
     // fp16 (see ff_common.hpp):
     const float *amax;       // [2][kAmaxParts]: of |dy|, of |x|
     const float *scale;      // [N]: of the rows of da and du

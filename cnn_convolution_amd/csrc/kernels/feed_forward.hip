@@ -794,7 +794,7 @@ hipError_t launch_ff_bwd(const FfArgs &a, hipStream_t s)
     const float *amax = scaled ? reinterpret_cast<const float *>(ws + p.off_amax) : nullptr;
     const float *scale = scaled ? reinterpret_cast<const float *>(ws + p.off_scale) : nullptr;
     const FfSaved from = saved_of(p, a.saved, nullptr);
-    const FfBack back{r.dy, r.wd, r.lddy, r.ldd, z.N, z.F, z.O, p.Op, p.rows_pad, p.Fp, from, ws + p.off_grad, z.act,
+    const FfBack back{r.dy, r.wd, r.lddy, r.ldd, z.N, z.F, z.O, p.Op, p.rows_pad, p.Fp, from, ws + p.off_grad,
                       amax, scale, a.x, z.ldx, z.D, p.Dp, p.ldd, scaled ? ws + p.off_x : nullptr};
     if ((e = launch_ff_back(back, z.dtype, p.back_tile, s)) != hipSuccess) return e;
 

@@ -80,7 +80,8 @@ conv2d_status_t feed_forward_fwd(const feed_forward_desc_t *d, const void *x, co
                                  const void *w_down, void *y, void *saved, void *ws, void *stream);
 
 /* dx [N][D], dw_gate, dw_up [F][D] and dw_down [O][F] are contiguous and whole
- * outputs. saved is only read. */
+ * outputs. saved is only read; act(a) and the slopes are what it holds, so d->act is
+ * checked and has no other effect. */
 conv2d_status_t feed_forward_bwd(const feed_forward_desc_t *d, const void *dy, const void *x, const void *w_gate,
                                  const void *w_up, const void *w_down, const void *saved, void *dx, void *dw_gate,
                                  void *dw_up, void *dw_down, void *ws, void *stream);

@@ -252,3 +252,14 @@ def test_feed_forward_infinite_gradient_in_the_last_row(N, dt):
         inf = torch.isinf(w)
         assert torch.equal(torch.isnan(got), torch.isnan(w)) and torch.equal(got[inf], w[inf]), name
     assert torch.equal(dx[:-1], dx0[:-1])
+
+
+def test_feed_forward_backward_has_the_saved_activation():
+    """The slopes are those of the pass that saved them, whatever activation is named."""
+    x, wg, wu, wd, dy = _ff_case(70, 40, 72, 24, "f32")
+    _, saved = conv.feed_forward(x, wg, wu, wd, "sigmoid")
+    want = conv.feed_forward_backward(dy, x, wg, wu, wd, saved, "sigmoid")
+    for act in ("silu", "gelu", "gelu_tanh", "relu"):
+        assert all(torch.equal(a, b) for a, b in zip(conv.feed_forward_backward(dy, x, wg, wu, wd, saved, act), want))
+    with pytest.raises(ValueError, match="activation"):
+        conv.feed_forward_backward(dy, x, wg, wu, wd, saved, "tanh")
