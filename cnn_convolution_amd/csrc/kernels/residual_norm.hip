@@ -331,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void res_norm_fwd_wide_kernel(const ResNo
 
 // Workspace of the backward pass: the blocks' sums of the next norm [B][2][C], then
 // the records [B + groups][2][C] and their groups, then (wide rows) each row's two
-// means [N][2].
+// means [N][2]. Where lanes take whole groups there are B records and nothing after them.
 struct Sums {
     float *norm, *record;
     int *group;
@@ -889,18 +889,20 @@ int64_t bwd_blocks(int64_t N, int64_t C)
 // 65536 rows of 64, bf16, 65536 groups 2796 and 39, 4096 groups (half of the lanes) 196 and
 // 38; 16384 of 1024, 512 groups (half) 78 and 69; 3000 of 512, fp32, 375 groups of 8 (a
 // third) 31 and 24; 19941 of 1001, 69 groups (one lane in 15) 93 and 591.
-bool own_groups(const ResNormArgs &a, const Group &g)
+bool own_groups(int64_t N, int64_t groups, const Group &g)
 {
-    if (!g.lpr || a.groups <= 1) return false;
-    return a.rows <= 8 || 2 * a.groups >= 256 * (threads_of(g.lpr) / g.lpr);
+    if (!g.lpr || groups <= 1) return false;
+    return N / groups <= 8 || 2 * groups >= 256 * (threads_of(g.lpr) / g.lpr);
 }
 
 }  // namespace
 
 int64_t res_norm_bwd_ws_bytes(int64_t N, int64_t C, int64_t groups)
 {
-    const int64_t B = bwd_blocks(N, C), G = std::max<int64_t>(groups, 1);
-    return ((2 * B + G) * 2 * C * 4 + (B + G + 1) / 2 * 8 + (group_of(C, true).lpr ? 0 : N * 8) + 255) / 256 * 256;
+    const Group g = group_of(C, true);
+    // (lanes that take whole groups leave one record a workgroup)
+    const int64_t B = bwd_blocks(N, C), G = own_groups(N, groups, g) ? 1 : std::max<int64_t>(groups, 1);
+    return ((2 * B + G) * 2 * C * 4 + (B + G + 1) / 2 * 8 + (g.lpr ? 0 : N * 8) + 255) / 256 * 256;
 }
 
 hipError_t launch_res_norm_fwd(const ResNormArgs &a, hipStream_t s)
@@ -938,7 +940,7 @@ hipError_t launch_res_norm_bwd(const ResNormArgs &a, hipStream_t s)
     }
     const Group g = group_of(a.C, true);
     const int64_t B = bwd_blocks(a.N, a.C);
-    const bool own = own_groups(a, g);
+    const bool own = own_groups(a.N, a.groups, g);
     const hipError_t e = with_norm_types(a.dtype, a.branch_dtype, [&](auto tr, auto tb) {
         using TR = typename decltype(tr)::type;
         using TB = typename decltype(tb)::type;

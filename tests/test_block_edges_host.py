@@ -64,3 +64,15 @@ def test_launches_that_cannot_be_are_refused_before_anything_is_enqueued():
     for dtype in (_lib.F32, _lib.F16, _lib.BF16):
         d = _block.FeedForwardDesc(8192, 1 << 18, 1 << 18, 1 << 18, 0, 0, 0, 0, 0, dtype, 0, 0, 0)
         assert _block.size("feed_forward_bwd_workspace_size", d) > 0
+
+
+def test_workspaces_of_many_gates_hold_no_records_of_each():
+    """Lanes that take whole groups of rows leave one record a workgroup: at most 256 of two
+    rows of sums, twice; where a workgroup leaves one for each gate there is one for each."""
+    def size(N, C, groups):
+        d = _block.ResidualNormDesc(N, C, groups, *[0] * 8, 0, 0, 0, 1, 1e-5, 1.0, 1.0)
+        return _block.size("residual_norm_bwd_workspace_size", d)
+    for N, C, groups in ((65536, 4096, 65536), (65536, 64, 65536), (4096, 1000, 4096), (3000, 520, 1000)):
+        assert size(N, C, groups) <= 513 * 2 * C * 4 + 4096
+    assert size(19941, 1001, 69) >= (2 * 256 + 69) * 2 * 1001 * 4
+    assert size(8192, 9000, 4096) >= 4096 * 2 * 9000 * 4

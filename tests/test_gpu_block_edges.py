@@ -263,3 +263,26 @@ def test_feed_forward_backward_has_the_saved_activation():
         assert all(torch.equal(a, b) for a, b in zip(conv.feed_forward_backward(dy, x, wg, wu, wd, saved, act), want))
     with pytest.raises(ValueError, match="activation"):
         conv.feed_forward_backward(dy, x, wg, wu, wd, saved, "tanh")
+
+
+# ---- norms around a residual sum ----------------------------------------------------------
+
+@pytest.mark.parametrize("N,C,G", [(4096, 64, 4096), (2048, 512, 256), (800, 5000, 400)])
+def test_residual_norm_workspace_of_many_gates(N, C, G):
+    """Nothing behind the workspace's size is written, and what it held does not matter."""
+    gen = torch.Generator(device=DEV).manual_seed(C)
+    b, r, dy, dout = (torch.randn(N, C, generator=gen, device=DEV) for _ in range(4))
+    one = torch.ones(C, device=DEV)
+    kw = dict(gate=torch.randn(G, C, generator=gen, device=DEV), post_weight=one, weight=one)
+    out, _, st = conv.residual_norm(b, r, **kw)
+    n = conv.residual_norm_workspace_size(b, gate=kw["gate"])
+    outs = []
+    for fill in (0, 255):
+        ws = torch.full((n + 4096,), fill, dtype=torch.uint8, device=DEV)
+        g = {"d" + k: torch.empty(C, device=DEV) for k in ("post_weight", "post_bias", "weight", "bias")}
+        g["dgate"] = torch.empty(G, C, device=DEV)
+        dr, db = torch.empty_like(b), torch.empty_like(b)
+        conv.residual_norm_backward_into(dy, dout, b, out, st, dr, db, ws, **kw, **g)
+        assert bool((ws[n:] == fill).all())
+        outs.append([dr, db] + list(g.values()))
+    assert all(torch.equal(a, c) for a, c in zip(*outs))
