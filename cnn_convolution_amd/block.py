@@ -372,14 +372,25 @@ def _checked(tensors, name, sizes, dev):
 
 
 def _no_twice(pointers, name, numbers, sizes):
-    """Refuses a tensor that is in the list twice (two workgroups would update it at once)."""
-    if len(set(pointers)) == len(pointers):
-        return
+    """Refuses a tensor that is in the list twice (two workgroups would update it at once);
+    the pointers as a set."""
+    some = set(pointers)
+    if len(some) == len(pointers):
+        return some
     seen = set()
     for i, p in zip(numbers, pointers):
         if sizes[i] and p in seen:
             raise ValueError(f"{name}[{i}] is in the list twice")
         seen.add(p)
+    return some
+
+
+def _no_parameter(copies, params, numbers, codes, types, sizes):
+    """Refuses a copy in a parameter's memory, unless it is that parameter itself."""
+    at = {p: i for i, p in enumerate(params) if sizes[i]}
+    for i, c, code in zip(numbers, copies, codes):
+        if sizes[i] and c in at and (at[c] != i or types[i] != code):
+            raise ValueError(f"copies[{i}] is in the memory of params[{at[c]}]")
 
 
 def _each(value, name, count):
@@ -396,7 +407,7 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
     """Enqueue one AdamW step: every tensor of ``params`` and ``state`` (adamw_state of
     these tensors) is updated in place from ``grads``, all contiguous and each of any of
     the three types; ``copies``, where given, receive the new parameters in their own
-    types (None entries are left out).
+    types (None entries are left out). Parameters, copies and states must not overlap.
 
     step: the number of this step, from 1 on. lr, weight_decay: numbers, or one for each
     tensor. grad_scale multiplies the gradients (1 / loss scale). seed: of the numbers
@@ -412,7 +423,7 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
     table = state._entries(*_state_pointers(state, dev))
     whole, real = memoryview(table).cast("q"), memoryview(table).cast("d")
     whole[0::words] = pointers = array("q", map(_data_ptr, params))
-    _no_twice(pointers, "params", range(count), state.sizes)
+    held = _no_twice(pointers, "params", range(count), state.sizes)
     whole[9::words] = array("q", [p | g << 32 for p, g in zip(types, _checked(grads, "grads", state.sizes, dev))])
     whole[1::words] = array("q", map(_data_ptr, grads))
     if copies is not None:
@@ -423,7 +434,9 @@ def adamw(params, grads, state: AdamWState, step, lr, beta1: float = 0.9, beta2:
         codes = _checked([copies[i] for i in some], "copies", [state.sizes[i] for i in some], dev)
         for i, code in zip(some, codes):
             whole[i * words + 2], whole[i * words + 10] = copies[i].data_ptr(), code
-        _no_twice([whole[i * words + 2] for i in some], "copies", some, state.sizes)
+        to = [whole[i * words + 2] for i in some]
+        if not held.isdisjoint(_no_twice(to, "copies", some, state.sizes)):
+            _no_parameter(to, pointers, some, codes, types, state.sizes)
     real[11::words] = array("d", _each(lr, "lr", count))
     real[12::words] = array("d", _each(weight_decay, "weight_decay", count))
     step_ptr = scale_ptr = None

@@ -184,8 +184,8 @@ typedef struct {
 } adamw_desc_t;
 
 /* tensors: host array of d->count entries, read before the call returns. The
- * parameters, copies, states and scales of different tensors must not overlap
- * (gradients may: they are read). Device
+ * parameters, copies, states and scales must not overlap (gradients may overlap
+ * each other: they are read). Device
  * scalars for steps that are captured and replayed, or NULL: step_ptr (int64, t),
  * grad_scale_ptr (fp32, multiplies grad_scale), lr_ptr (fp32, multiplies every lr). */
 conv2d_status_t adamw_step(const adamw_desc_t *d, const adamw_tensor_t *tensors, const int64_t *step_ptr,

@@ -1,11 +1,16 @@
 """Block operators without a GPU: a process's first call, limits that are refused before
-anything is enqueued, workspace sizes."""
+anything is enqueued, workspace sizes, tensors in each other's memory."""
 import ctypes
 import os
 import subprocess
 import sys
 
-from cnn_convolution_amd import _block, _lib
+import pytest
+import torch
+
+import cnn_convolution_amd as conv
+from cnn_convolution_amd import _block, _lib, head
+from test_head_binding_host import DeviceTensor
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -76,3 +81,27 @@ def test_workspaces_of_many_gates_hold_no_records_of_each():
         assert size(N, C, groups) <= 513 * 2 * C * 4 + 4096
     assert size(19941, 1001, 69) >= (2 * 256 + 69) * 2 * 1001 * 4
     assert size(8192, 9000, 4096) >= 4096 * 2 * 9000 * 4
+
+
+def test_adamw_refuses_copies_in_a_parameters_memory(monkeypatch):
+    """Another tensor's workgroup, or in another type the tensor's own, would read what the copy
+    wrote; a copy that is its parameter itself changes nothing."""
+    calls = []
+    monkeypatch.setattr(_block, "call", lambda *args: calls.append(args))
+    head._torch_names()
+    monkeypatch.setattr(head, "_current_device", lambda: 1)
+    monkeypatch.setattr(head, "_raw_stream", lambda dev: 7)
+    state = conv.AdamWState([6, 4, 0], 32, "cpu")
+    for name in ("exp_avg", "exp_avg_sq"):
+        setattr(state, name, DeviceTensor(*getattr(state, name).shape))
+    p, g = ([DeviceTensor(n) for n in state.sizes] for _ in range(2))
+    wide = DeviceTensor(4)
+    half = DeviceTensor(6, dtype=torch.bfloat16)
+    half.data_ptr, wide.data_ptr = p[0].data_ptr, p[0].data_ptr
+    conv.adamw(p, g, state, 1, 1.0, copies=[p[0], None, p[2]])
+    assert len(calls) == 1
+    with pytest.raises(ValueError, match=r"copies\[0\] is in the memory of params\[0\]"):
+        conv.adamw(p, g, state, 1, 1.0, copies=[half, None, None])
+    with pytest.raises(ValueError, match=r"copies\[1\] is in the memory of params\[0\]"):
+        conv.adamw(p, g, state, 1, 1.0, copies=[None, wide, None])
+    assert len(calls) == 1
