@@ -883,16 +883,29 @@ int64_t bwd_blocks(int64_t N, int64_t C)
     return g.lpr ? blocks_of(N, g, true) : std::max<int64_t>(1, std::min(N, kColBlocks));
 }
 
-// Whether each row's lanes take whole groups of rows with a gate: where a workgroup would
-// leave sums every few rows, and groups enough to keep half of all lanes at work, or so short
-// that few rows wait for each other. us of a workgroup's rows group by group, and so:
-// 65536 rows of 64, bf16, 65536 groups 2796 and 39, 4096 groups (half of the lanes) 196 and
-// 38; 16384 of 1024, 512 groups (half) 78 and 69; 3000 of 512, fp32, 375 groups of 8 (a
-// third) 31 and 24; 19941 of 1001, 69 groups (one lane in 15) 93 and 591.
+// Whether each row's lanes take whole groups of rows with a gate: where groups are short,
+// or where a workgroup would leave sums so often that this takes longer than the lanes wait
+// which have no group, or the last ones. `share`: of the lanes' time that has a group in it.
+// us of a workgroup's rows group by group, and so:
+//   up to 256 channels (whose sums leave 8 rows' lanes after each other), from a quarter on:
+//     65536 rows of 64, bf16, 65536 groups 2796 and 39, 2048 (a quarter) 111 and 53
+//   up to 512, from three quarters on: 32768 rows of 512, 512 groups (half) 59 and 75
+//   up to 1024, from half on: 16384 rows of 1024, 512 groups (half) 73 and 65, 384 68 and 77
+//   up to 4096, from three quarters on: 16384 rows of 4096, 192 groups (three quarters) 214
+//     and 186, 128 204 and 248; of 2048, 192 118 and 118, 160 119 and 137, 2048 254 and 106
+//   up to 8192, where lanes that keep the gates' sums too have the fewest registers, with two
+//     groups to each: 8192 rows of 8192, 1024 groups 481 and 388, 512 351 and 358, 256 288
+//     and 342, 128 242 and 502; fp32, 512 715 and 541, 256 651 and 525
+//   rows <= 8: 3000 of 512, fp32, 375 groups (a third) 31 and 24; 1024 of 8192, bf16, 128
+//     groups 106 and 89, 512 rows of 64 groups 73 and 79
 bool own_groups(int64_t N, int64_t groups, const Group &g)
 {
     if (!g.lpr || groups <= 1) return false;
-    return N / groups <= 8 || 2 * groups >= 256 * (threads_of(g.lpr) / g.lpr);
+    if (N / groups <= 8) return true;
+    const int64_t units = 256 * (threads_of(g.lpr) / g.lpr), rounds = (groups + units - 1) / units;
+    if (g.lpr == 512) return groups >= 2 * units;
+    const int64_t quarters = g.lpr < 64 ? 1 : g.lpr == 64 && g.kch == 2 ? 2 : 3;
+    return 4 * groups >= quarters * units * rounds;
 }
 
 }  // namespace

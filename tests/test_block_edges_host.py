@@ -81,6 +81,11 @@ def test_workspaces_of_many_gates_hold_no_records_of_each():
         assert size(N, C, groups) <= 513 * 2 * C * 4 + 4096
     assert size(19941, 1001, 69) >= (2 * 256 + 69) * 2 * 1001 * 4
     assert size(8192, 9000, 4096) >= 4096 * 2 * 9000 * 4
+    # long groups: whole ones where they keep the lanes at work, which takes more of wide rows
+    for N, C, few, many in ((65536, 64, 1024, 2048), (32768, 512, 512, 768), (16384, 1024, 256, 512),
+                            (16384, 4096, 128, 192), (16384, 2048, 160, 256), (8192, 8192, 256, 512)):
+        assert size(N // few * few, C, few) >= (2 * 256 + few) * 2 * C * 4
+        assert size(N // many * many, C, many) <= 513 * 2 * C * 4 + 4096
 
 
 def test_adamw_refuses_copies_in_a_parameters_memory(monkeypatch):
