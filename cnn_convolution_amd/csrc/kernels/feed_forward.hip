@@ -51,21 +51,39 @@ __global__ __launch_bounds__(256) void ff_pad_kernel(const PadArgs a)
         b -= copies;
         float most = 0.f, most_x = 0.f, own = 0.f;
         bool some = false;
-        // the largest finite |value| of a row that these lanes read, and whether it has any but 0
+        // the largest finite |value| of a row that these lanes read, and whether it has any but
+        // 0, by the bits of two fp16 values at a time (as floats, one load after the other, 4097
+        // rows of 1032 took 20 us for 12)
+        typedef uint16_t half2_t __attribute__((ext_vector_type(2)));
         const auto row_max = [&](const void *p, int64_t ld, int64_t r, int64_t n, bool &any) {
-            float m = 0.f;
-            for (int64_t c = at * E; c < n; c += lanes * E) {
-                float f[E];
-                load_some<E>(static_cast<const T *>(p) + r * ld + c, n - c, f);
+            const uint16_t *row = static_cast<const uint16_t *>(p) + r * ld;
+            half2_t m = {0, 0};
+            uint32_t seen = 0;
+            const auto take = [&](uint32_t d) {
+                d &= 0x7FFF7FFFu;
+                seen |= d;
+                // (from 0x7C00 on: infinite or NaN)
+                const uint32_t no = (d + 0x04000400u) & 0x80008000u;
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(half2_t, d & ~(no | (no - (no >> 15)))));
+            };
+            if (n < E) {
+                if (at < n) take(row[at]);
+            } else {
+                // past the end the last ones again
+                for (int64_t c = at * E; c - at * E < n; c += 4 * lanes * E) {
+                    Raw<uint16_t, E> q[4];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (fabsf(f[e]) < __builtin_inff()) m = fmaxf(m, fabsf(f[e]));
-                    any = any || f[e] != 0.f;
+                    for (int i = 0; i < 4; ++i) q[i] = load_raw<uint16_t, E>(row + min(c + i * lanes * E, n - E));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < E / 2; ++e) take(q[i].d[e]);
                 }
             }
-            for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
-            any = __any(any);
-            return m;
+            any = __any(seen != 0);
+            float f = float(__builtin_bit_cast(_Float16, uint16_t(max(m[0], m[1]))));
+            for (int k = 1; k < 64; k <<= 1) f = fmaxf(f, __shfl_xor(f, k, 64));
+            return f;
         };
         for (int64_t r = few ? b : b * 4 + wave; r < a.N; r += few ? kAmaxParts : 4 * kAmaxParts) {
             bool any = false, any_x = false;
