@@ -1,6 +1,6 @@
 // One AdamW step over many tensors (im2win_block.h), states in 32 or in 8 bits, and
-// the values of 8-bit states. Bound by HBM: every element of p, g, m and v is read and
-// of p, m and v written once.
+// the values of 8-bit states. 32 bits are bound by HBM: every element of p, g, m and v is
+// read and of p, m and v written once; 8 bits by the VALU and by how launches begin and end.
 //
 // A launch takes up to kAdamTensors tensors by value, a workgroup one chunk of
 // consecutive elements of one of them, a lane 8 (8 bits: 4) consecutive ones: a wave
@@ -10,8 +10,11 @@
 // The types of p and g are a workgroup's affair: it branches once to the code for its
 // tensor's, so that all loads go out together.
 // 200 million elements, fp32 states, bf16 gradients and copies: 1091 us (5.1 TB/s). 40
-// million in 150 tensors, 8-bit states: 205 us (3.1 TB/s), for the VALU has 440
-// instructions to a wave's 256 elements, those of fp64 and the square roots the longest.
+// million with 8-bit states in one tensor: 157 us (4.0 TB/s), in which the VALU is at work at
+// least 85 % of the SIMDs' cycles (472 instructions to a wave's 256 elements, counted as 4
+// cycles each; those of fp64 and the square roots take longer). 83 registers let a SIMD have 5
+// waves, of which 3.9 are there on average. In 150 tensors 197 us: four launches of 24 to 62
+// us in turn, with 60 to 65 % in the larger ones.
 //
 // 8-bit states: m, v and the scales are formed in fp64, so that the level that an element
 // gets is the definition's but for fp64's own roundings. A value in units of its

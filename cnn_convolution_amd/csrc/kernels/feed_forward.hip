@@ -3,8 +3,8 @@
 //
 // Forward: the gate launch (ff_tiles.hip) forms both projections, the activation and
 // the product and leaves h; a plain product (ff_products.hip) leaves y. Backward: the
-// back launch leaves da and du from dy, Wd and the saved factors; then dx, dWd and
-// dWg with dWu.
+// back launch leaves da and du from dy, Wd and the saved factors, in fp16 x too as the weights'
+// gradients read it; then dx, dWd and dWg with dWu.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -73,8 +73,9 @@ __device__ __forceinline__ void activate(int act, float a, float &f, float &df)
 // a smaller one is off by at most 2^-21 of it. The weights' gradients are sums over the rows:
 // they read x times M / S, with one M for all rows, the least S times the power of two that
 // brings the largest |x| into [2^6, 2^7), so that a row whose dy is 2^-10 of the largest
-// still has x down to 2^-10 of the largest with all digits. (With da and du written twice
-// instead, times S and times the least S, 8192 x 2048 x 8192 took 6 % more for the step.)
+// still has x down to 2^-10 of the largest with all digits. x so scaled is written by
+// workgroups of the back launch: 8192 x 2048 x 8192 390 us for 375 (with da and du written
+// twice instead, times S and times the least S, 507).
 // Rows of zeros have S 2^100: neither their x nor its size is anything to the others.
 __device__ __forceinline__ float scale_of(float m)
 {

@@ -14,9 +14,13 @@
 // norm sum dy xhat(out) and sum dy: four sums per channel stay in registers over all of a
 // workgroup's rows. S1 and S2 leave at the end of each group that the workgroup sees,
 // the others at its end; a second launch adds them in a fixed order.
-// Rows wider than a group holds are read again for each pass over them.
+// Rows of more than 8192 channels are wider than a group holds and are read again for each
+// pass over them.
 // 32768 rows of 4096, bf16: forward 212 us (5.1 TB/s), backward 317 and 10 for the second
 // launch (4.9). 19941 rows of 1001, fp32 with fp16, a gate for every 289: 82 and 9 (4.0).
+// From 4097 channels on backward is no longer bound by HBM: with two chunks to each of 512
+// lanes 56 to 238 registers do not fit and go through scratch memory (8192 rows of 8192, bf16:
+// forward 115 us, 4.7 TB/s, backward 196, 4.1; fp32 217 and 533; 8192 rows of 8200 235 and 519).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -824,6 +828,7 @@ __global__ __launch_bounds__(kThreads) void res_norm_zero_kernel(const ResNormAr
 // more: 32768 rows of 4096, bf16, forward (256, 2) 214, (512, 1) 221 .. 284, (128, 4) 215;
 // backward 329, 325 and -; 19941 rows of 1001, fp32 with fp16, backward (64, 2) 103, (128, 1)
 // 133, forward 59.5 and 56.5; 65536 rows of 2048, bf16, backward (256, 1) 337, (128, 2) 358.
+// (512, 2) is there for the rows that (256, 2) does not hold.
 // lpr 0: no group holds it.
 struct Group {
     int lpr, kch;
