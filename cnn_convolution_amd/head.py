@@ -48,7 +48,7 @@ def _code(dtype) -> int:
 
 
 def _device(t, name) -> int:
-    """The device index of a device tensor; every entry point begins here."""
+    """The device index of a device tensor; every call that enqueues begins here."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if _codes is None:

@@ -106,7 +106,8 @@ conv2d_status_t feed_forward_bwd(const feed_forward_desc_t *d, const void *dy, c
  *   (post = 0: db = dp)
  *
  * y is formed from the unrounded out. Statistics, sums, gate, weights and biases
- * and their gradients are fp32; out, y, dr and db are rounded once. */
+ * and their gradients are fp32 (a row whose squares add up to more than fp32 holds, values of
+ * 10^17 and more, has rstd 0); out, y, dr and db are rounded once. */
 enum { RN_LAYER = 0, RN_RMS = 1 };
 
 typedef struct {
