@@ -316,8 +316,8 @@ hipError_t launch_back(const FfBack &a, hipStream_t s)
     const auto kernel = ff_back_kernel<T, C>;
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kernel), C::lds_bytes, allowed);
     if (e != hipSuccess) return e;
-    const int64_t groups = grid_of<C>(tm * tn, ceil_div(a.O * int64_t(sizeof(T)), 128));
     const int64_t more = std::is_same<T, _Float16>::value ? std::min<int64_t>(ceil_div(a.N, C::threads / 64), 1024) : 0;
+    const int64_t groups = std::min(grid_of<C>(tm * tn, ceil_div(a.O * int64_t(sizeof(T)), 128)), max_groups(C::threads) - more);
     hipLaunchKernelGGL(kernel, dim3(unsigned(groups + more)), dim3(C::threads), C::lds_bytes, s, a, int(tm), int(tn),
                        int(groups));
     return hipGetLastError();
